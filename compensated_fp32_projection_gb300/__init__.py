@@ -31,9 +31,29 @@ __all__ = [
     "comp_gemm_workspace_bytes",
     "comp_gemm_workspace_bytes_mnk",
     "comp_gemm_f32x16_noalloc",
+    "comp_attn_f32",
+    "comp_attn_f32x16",
+    "comp_attn_decode_f32x16",
+    "comp_kv_append_f32",
+    "comp_kv_reserve",
+    "comp_kv_fork",
+    "comp_kv_free",
+    "comp_kv_compact",
+    "comp_kv_copy_pages",
     "device_status",
     "status_string",
 ]
+
+_ATTENTION = ("comp_attn_", "comp_kv_")
+
+
+def __getattr__(name):
+    # the attention calls import torch at their module's head: loaded on first use
+    if name in __all__ and name.startswith(_ATTENTION):
+        from . import attention
+
+        return getattr(attention, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def _torch():

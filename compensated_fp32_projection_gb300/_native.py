@@ -22,6 +22,23 @@ COMP_ERR_CUDA = 6
 
 # Every symbol the header declares, with its ctypes signature.
 _i64, _int, _u32, _vp = ctypes.c_int64, ctypes.c_int, ctypes.c_uint32, ctypes.c_void_p
+_i32, _f32 = ctypes.c_int32, ctypes.c_float
+
+
+class Attn(ctypes.Structure):
+    """comp_attn_t"""
+
+    _fields_ = [(n, _i64) for n in ("n_seq", "total_q", "total_k")] + [
+        (n, _i32) for n in ("heads", "kv_heads", "head_dim", "causal")] + [("scale", _f32)] + [
+        (n, _i64) for n in ("q_token", "q_head", "k_token", "k_head", "v_token", "v_head", "out_token", "out_head")]
+
+
+class KvCache(ctypes.Structure):
+    """comp_kv_cache_t"""
+
+    _fields_ = [("k", _vp), ("v", _vp), ("pages", _i64), ("page_size", _i32), ("kv_heads", _i32), ("head_dim", _i32)]
+
+
 SIGNATURES = {
     "comp_split_f32": (_int, [_vp, _vp, _vp, _i64, _vp]),
     "comp_merge_f32": (_int, [_vp, _vp, _vp, _i64, _vp]),
@@ -37,6 +54,18 @@ SIGNATURES = {
     "comp_gemm_f32x16_epilogue": (_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp]),
     "comp_gemm_f16x2_epilogue": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp]),
     "comp_gemm_f32x16_noalloc": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp]),
+    "comp_attn_workspace_bytes": (_i64, [_vp, _int]),
+    "comp_attn_f32x16": (_int, [_vp] * 9 + [_i64, _vp]),
+    "comp_attn_f32": (_int, [_vp] * 9 + [_i64, _vp]),
+    "comp_kv_append_f32": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp]),
+    "comp_attn_decode_workspace_bytes": (_i64, [_vp, _i64, _i32, _i64, _i64]),
+    "comp_attn_decode_f32x16": (_int, [_vp, _vp, _i64, _i64, _i32, _f32, _vp, _i64, _i64, _vp, _i64, _vp, _vp, _vp,
+                                       _i64, _vp]),
+    "comp_kv_reserve": (_int, [_i64, _i32, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "comp_kv_fork": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "comp_kv_free": (_int, [_i64, _vp, _vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp]),
+    "comp_kv_compact": (_int, [_vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "comp_kv_copy_pages": (_int, [_vp, _vp, _vp, _i64, _vp]),
     "comp_device_status": (_int, [_vp, ctypes.POINTER(_u32)]),
     "comp_check_wait_timeout": (_int, [_vp]),
     "comp_check_stalled_pipeline": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp]),

@@ -15,23 +15,6 @@ constexpr int kMaxDevices = 64;
 std::atomic<int> g_dev_state[kMaxDevices];
 std::atomic<int> g_dev_sms[kMaxDevices];
 
-bool mul_ok(int64_t a, int64_t b, int64_t* out)
-{
-    if (a < 0 || b < 0)
-        return false;
-    if (a != 0 && b > INT64_MAX / a)
-        return false;
-    *out = a * b;
-    return true;
-}
-
-// Byte ranges [a, a+na) and [b, b+nb) overlap.
-bool overlap(const void* a, int64_t na, const void* b, int64_t nb)
-{
-    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
-    return na > 0 && nb > 0 && pa < pb + static_cast<uintptr_t>(nb) && pb < pa + static_cast<uintptr_t>(na);
-}
-
 }  // namespace
 
 comp_status_t current_device(DeviceInfo* info)

@@ -8,6 +8,41 @@
 
 namespace compfp32 {
 
+// a * b in *out, false if it is negative or overflows.
+inline bool mul_ok(int64_t a, int64_t b, int64_t* out)
+{
+    if (a < 0 || b < 0)
+        return false;
+    if (a != 0 && b > INT64_MAX / a)
+        return false;
+    *out = a * b;
+    return true;
+}
+
+// Byte ranges [a, a+na) and [b, b+nb) overlap.
+inline bool overlap(const void* a, int64_t na, const void* b, int64_t nb)
+{
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+    return na > 0 && nb > 0 && pa < pb + static_cast<uintptr_t>(nb) && pb < pa + static_cast<uintptr_t>(na);
+}
+
+// Bytes from the first to the last element of a [tokens, heads, dim] tensor
+// with these token and head strides (in elements of `elem` bytes; not negative).
+inline bool strided_bytes(int64_t tokens, int64_t heads, int64_t dim, int64_t token, int64_t head, int64_t elem,
+                          int64_t* bytes)
+{
+    int64_t a, b;
+    *bytes = 0;
+    if (tokens < 0 || heads < 0 || dim < 0 || token < 0 || head < 0)
+        return false;
+    if (tokens == 0 || heads == 0 || dim == 0)
+        return true;
+    if (!mul_ok(tokens - 1, token, &a) || !mul_ok(heads - 1, head, &b) || a > INT64_MAX / 64 || b > INT64_MAX / 64)
+        return false;
+    *bytes = elem * (a + b + dim);
+    return true;
+}
+
 // Properties of the current device, checked once per device.
 struct DeviceInfo {
     int device;
@@ -70,6 +105,10 @@ bool gemm_f16x2_supported(const void* hi, const void* lo, const void* W, int64_t
 comp_status_t launch_gemm_f16x2(const uint16_t* hi, const uint16_t* lo, const uint16_t* W, float* y, int64_t M,
                                 int64_t N, int64_t K, int variant, const DeviceInfo& dev, cudaStream_t stream,
                                 const Epilogue& epi = Epilogue{}, bool stall = false);
+
+// Whether a cache descriptor is one that the kernels take; the bytes of its
+// k (and of its v).
+bool kv_cache_ok(const comp_kv_cache_t* cache, int64_t* bytes);
 
 // One thread runs a bounded wait that cannot succeed (comp_check_wait_timeout).
 comp_status_t launch_check_wait_timeout(cudaStream_t stream);

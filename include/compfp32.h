@@ -320,6 +320,163 @@ comp_status_t comp_gemm_f32x16_noalloc(const float* x, const uint16_t* W, float*
                                        int64_t K, comp_stream_t stream);
 
 /*
+ * Attention.
+ *
+ * For query row (t, h) with key/value head g = h / (heads / kv_heads) and the
+ * keys j it may see:
+ *   s_j = scale * sum_d q[t,h,d] * k[j,g,d]          m = max_j s_j
+ *   lse[t,h] = m + log(sum_j exp(s_j - m))
+ *   out[t,h,d] = sum_j exp(s_j - lse) * v[j,g,d]
+ * A row that sees no key gets out = +0 and lse = -inf.  Scores, maxima, sums
+ * and outputs are binary32.  The products follow the method of the
+ * projections: a binary32 operand enters the FP16 tensor cores as two binary16
+ * values, and accumulators are FP32.  q and k must therefore stay below 65520
+ * in magnitude, and v too (larger values give NaN).  A key that a row may not see
+ * has no influence on it, whatever k and v hold there (infinities and NaN
+ * included).
+ *
+ * comp_attn_t describes whole prompts packed one after the other:
+ *   n_seq sequences; queries cu_q[i] .. cu_q[i+1]-1 of the total_q packed
+ *   query tokens attend to keys cu_k[i] .. cu_k[i+1]-1 of the total_k packed
+ *   key tokens.  cu_q and cu_k are device arrays of n_seq + 1 ascending
+ *   int32 starting at 0 (values outside 0..total are clamped); NULL for both
+ *   means one sequence.  Lengths of zero are valid.
+ *   causal != 0: query t of n sees the keys j <= t + (m - n) of its m, so the
+ *   last query sees all of them; causal == 0: every query sees all keys.
+ *   heads is a multiple of kv_heads; head_dim 1 .. 128; scale finite and > 0.
+ *   Strides count elements: q[t,h,d] = q[t*q_token + h*q_head + d], and so on
+ *   (so q, k and v may be parts of one projection's output); not negative.
+ *   The rows of out must not overlap each other.  lse is [total_q, heads], or
+ *   NULL for none.
+ */
+typedef struct comp_attn {
+    int64_t n_seq, total_q, total_k;
+    int32_t heads, kv_heads, head_dim, causal;
+    float scale;
+    int64_t q_token, q_head, k_token, k_head, v_token, v_head, out_token, out_head;
+} comp_attn_t;
+
+/*
+ * comp_attn_workspace_bytes — the workspace that comp_attn_f32 (kv_bytes 4)
+ * or comp_attn_f32x16 (kv_bytes 2) needs for `a`.  0 for a bad argument, or
+ * where none is needed.
+ */
+int64_t comp_attn_workspace_bytes(const comp_attn_t* a, int kv_bytes);
+
+/*
+ * comp_attn_f32x16 — attention of binary32 queries over binary16 keys and
+ * values, which enter the products exactly.
+ * comp_attn_f32 — the same with binary32 keys and values.
+ * Errors: COMP_ERR_INVALID_VALUE for a NULL descriptor, a size, stride or
+ * scale outside the above, a needed pointer that is NULL, only one of cu_q and
+ * cu_k, n_seq > 1 without them, a workspace that is smaller than
+ * comp_attn_workspace_bytes or not 16-byte aligned where one is needed, or
+ * out, lse or the workspace overlapping an input or each other.
+ */
+comp_status_t comp_attn_f32x16(const comp_attn_t* a, const float* q, const uint16_t* k, const uint16_t* v,
+                               const int32_t* cu_q, const int32_t* cu_k, float* out, float* lse, void* workspace,
+                               int64_t workspace_bytes, comp_stream_t stream);
+comp_status_t comp_attn_f32(const comp_attn_t* a, const float* q, const float* k, const float* v,
+                            const int32_t* cu_q, const int32_t* cu_k, float* out, float* lse, void* workspace,
+                            int64_t workspace_bytes, comp_stream_t stream);
+
+/*
+ * A paged cache of binary16 keys and values.  Each of the `pages` pages holds
+ * page_size tokens of every key/value head: k and v are
+ * [pages, kv_heads, page_size, head_dim], dense, 16-byte aligned.
+ * page_size is 16, 32, 64 or 128; head_dim a multiple of 8 up to 128.
+ * Beside it the caller keeps, in device memory:
+ *   table   [rows, width] int32: row r lists the pages of sequence r in order;
+ *           -1 where there is none;
+ *   lengths [rows] int32: the tokens of each sequence;
+ *   refs    [pages] int32: how many table entries name each page; 0 is free.
+ * Numbers of pages and rows that lie outside their range are never followed:
+ * a page that is not there reads as zeros and is not written.
+ */
+typedef struct comp_kv_cache {
+    uint16_t* k;
+    uint16_t* v;
+    int64_t pages;
+    int32_t page_size, kv_heads, head_dim;
+} comp_kv_cache_t;
+
+/*
+ * comp_kv_append_f32 — write new tokens: k and v are binary32 [total, kv_heads,
+ * head_dim] with token and head strides, rounded to binary16 (to nearest, ties
+ * to even).  Row r's tokens are cu[r] .. cu[r+1]-1 (cu NULL: total == rows, one
+ * token each) and go to positions start[r], start[r]+1, ... of its sequence,
+ * whose pages the table must already list (see comp_kv_reserve).  lengths are
+ * the caller's to advance.
+ */
+comp_status_t comp_kv_append_f32(const comp_kv_cache_t* cache, const float* k, const float* v, int64_t k_token,
+                                 int64_t k_head, int64_t v_token, int64_t v_head, int64_t total,
+                                 const int32_t* table, int64_t rows, int64_t width, const int32_t* cu,
+                                 const int32_t* start, comp_stream_t stream);
+
+/*
+ * comp_attn_decode_f32x16 — one query token for each of `batch` sequences over
+ * the paged cache: q [batch, heads, head_dim] binary32 (token and head
+ * strides), out [batch, heads, head_dim] and lse [batch, heads] (or NULL)
+ * dense.  Sequence b sees the tokens 0 .. lengths[b]-1 of table row b (its own
+ * new token among them, written before); a length is clamped to
+ * 0 .. width * page_size.
+ * The first shared_pages entries of all rows are the same pages, a prefix that
+ * the batch shares: row 0's are read, once for the whole batch.
+ * 0 shares nothing.  Workspace: comp_attn_decode_workspace_bytes, 16-byte
+ * aligned.
+ */
+int64_t comp_attn_decode_workspace_bytes(const comp_kv_cache_t* cache, int64_t batch, int32_t heads, int64_t width,
+                                         int64_t shared_pages);
+comp_status_t comp_attn_decode_f32x16(const comp_kv_cache_t* cache, const float* q, int64_t q_token, int64_t q_head,
+                                      int32_t heads, float scale, const int32_t* table, int64_t batch,
+                                      int64_t width, const int32_t* lengths, int64_t shared_pages, float* out,
+                                      float* lse, void* workspace, int64_t workspace_bytes, comp_stream_t stream);
+
+/*
+ * Page maintenance.  The *_out arrays receive the new bookkeeping; each may be
+ * the matching input itself (updated in place) or a separate array, and
+ * nothing else may overlap.  Free pages are taken lowest number first, in the
+ * order of the requests, so results never depend on timing.
+ *
+ * comp_kv_reserve — give row r the pages that want[r] tokens need, at the end
+ * of those it has (a row's pages are its leading entries that are not -1).
+ * comp_kv_fork — make row children[i] a copy of row parents[i], i < n: full
+ * pages are shared (refs + 1); a last page that is partly filled is copied to
+ * a free page, its filled tokens only.  The children's rows must be distinct,
+ * empty before, and no parents.  n is at most 32768.
+ * Both write left[0] = free pages left; where there are not enough, left[0]
+ * is minus the number missing and nothing else changes (the *_out arrays get
+ * what was there before).
+ *
+ * comp_kv_free — give back the pages of rows seqs[0..n-1] (refs - 1 for each
+ * entry, never below 0) and empty them: entries -1, length 0.
+ *
+ * comp_kv_compact — move the pages in use to the front of the cache: with
+ * live = the number of pages with refs > 0, the ones at or beyond `live`, in
+ * ascending order, go to the free pages below it, in ascending order.
+ * remap[p] is the new number of page p (-1: free), live[0] the count; table
+ * and refs are renumbered.
+ *
+ * comp_kv_copy_pages — copy page src[i] to page dst[i], i < n.  The dst are
+ * distinct and no src.
+ */
+comp_status_t comp_kv_reserve(int64_t pages, int32_t page_size, const int32_t* table, const int32_t* refs,
+                              int64_t rows, int64_t width, const int32_t* want, int32_t* table_out,
+                              int32_t* refs_out, int32_t* left, comp_stream_t stream);
+comp_status_t comp_kv_fork(const comp_kv_cache_t* cache, const int32_t* table, const int32_t* lengths,
+                           const int32_t* refs, int64_t rows, int64_t width, const int32_t* parents,
+                           const int32_t* children, int64_t n, int32_t* table_out, int32_t* lengths_out,
+                           int32_t* refs_out, int32_t* left, comp_stream_t stream);
+comp_status_t comp_kv_free(int64_t pages, const int32_t* table, const int32_t* lengths, const int32_t* refs,
+                           int64_t rows, int64_t width, const int32_t* seqs, int64_t n, int32_t* table_out,
+                           int32_t* lengths_out, int32_t* refs_out, comp_stream_t stream);
+comp_status_t comp_kv_compact(const comp_kv_cache_t* cache, const int32_t* table, const int32_t* refs, int64_t rows,
+                              int64_t width, int32_t* table_out, int32_t* refs_out, int32_t* remap, int32_t* live,
+                              comp_stream_t stream);
+comp_status_t comp_kv_copy_pages(const comp_kv_cache_t* cache, const int32_t* src, const int32_t* dst, int64_t n,
+                                 comp_stream_t stream);
+
+/*
  * comp_device_status — waits for `stream`, then reports and clears the fault
  * word that kernels of this library set when a bounded wait inside them gives
  * up (they then skip the rest of their work and exit cleanly, leaving the

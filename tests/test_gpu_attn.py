@@ -1,0 +1,338 @@
+"""Attention over packed prompts and over the paged cache, against 64-bit sums."""
+import itertools
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+from attn_check import check_attn, check_decode  # noqa: E402
+
+
+@pytest.fixture(scope="module")
+def pkg():
+    import __graft_entry__
+
+    __graft_entry__.build()
+    import compensated_fp32_projection_gb300 as p
+
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    yield p
+    assert p.device_status() == (0, 0)
+
+
+def cu_of(lens):
+    return [0] + list(itertools.accumulate(lens))
+
+
+def ints(values):
+    return torch.tensor(values, dtype=torch.int32, device="cuda")
+
+
+def case(lens_q, lens_k, heads, kv_heads, dim, kv, seed=0, q_scale=2.0):
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randn(sum(lens_q), heads, dim, generator=g) * q_scale
+    k, v = (torch.randn(sum(lens_k), kv_heads, dim, generator=g) for _ in range(2))
+    if kv == torch.float16:
+        k, v = k.half(), v.half()
+    return q.cuda(), k.cuda(), v.cuda()
+
+
+def call(pkg, q, k, v, cu_q, cu_k, causal, scale=None, **more):
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    f = pkg.comp_attn_f32 if k.dtype == torch.float32 else pkg.comp_attn_f32x16
+    out = f(q, k, v, ints(cu_q), ints(cu_k), causal=causal, scale=scale, lse=lse, **more)
+    return out, lse
+
+
+KV = [torch.float16, torch.float32]
+
+
+@pytest.mark.parametrize("kv", KV, ids=["f16", "f32"])
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+@pytest.mark.parametrize("lens_q,lens_k", [
+    ([1], [1]),
+    ([1], [300]),
+    ([127], [127]),
+    ([128, 129], [128, 129]),
+    ([0, 5, 0, 64, 1], [0, 5, 3, 64, 1]),       # sequences without tokens, and without queries
+    ([9, 20], [4, 0]),                          # more queries than keys: causal rows that see nothing; no keys at all
+    ([33, 2, 65], [200, 131, 257]),             # queries that continue a longer sequence
+    ([257], [511]),
+], ids=str)
+def test_lengths(pkg, lens_q, lens_k, causal, kv):
+    q, k, v = case(lens_q, lens_k, 4, 2, 64, kv)
+    cu_q, cu_k = cu_of(lens_q), cu_of(lens_k)
+    out, lse = call(pkg, q, k, v, cu_q, cu_k, causal)
+    check_attn(out, lse, q, k, v, cu_q, cu_k, causal, 64 ** -0.5)
+
+
+@pytest.mark.parametrize("kv", KV, ids=["f16", "f32"])
+@pytest.mark.parametrize("heads,kv_heads,dim", [(1, 1, 1), (3, 1, 17), (2, 2, 40), (6, 2, 72), (5, 5, 80), (8, 1, 96),
+                                                (4, 4, 127), (8, 2, 128), (28, 4, 128), (20, 1, 64), (7, 7, 8)])
+def test_heads(pkg, heads, kv_heads, dim, kv):
+    lens = [150, 1, 37]
+    q, k, v = case(lens, lens, heads, kv_heads, dim, kv, seed=1)
+    cu = cu_of(lens)
+    out, lse = call(pkg, q, k, v, cu, cu, True)
+    check_attn(out, lse, q, k, v, cu, cu, True, dim ** -0.5)
+
+
+@pytest.mark.parametrize("kv", KV, ids=["f16", "f32"])
+@pytest.mark.parametrize("dim", [64, 128, 60])
+def test_parts_of_one_projection(pkg, kv, dim):
+    """q, k and v side by side in one tensor, at an odd offset too; out strided."""
+    heads, kv_heads, n = 4, 2, 141
+    for pad in (0, 1, 8):
+        g = torch.Generator().manual_seed(2)
+        width = (heads + 2 * kv_heads) * dim + pad
+        x = torch.randn(n, width, generator=g).cuda()
+        at = pad
+        q = x[:, at:at + heads * dim].view(n, heads, dim)
+        kvx = x.to(kv)
+        k = kvx[:, at + heads * dim:at + (heads + kv_heads) * dim].view(n, kv_heads, dim)
+        v = kvx[:, at + (heads + kv_heads) * dim:].view(n, kv_heads, dim)
+        place = torch.full((n, heads, dim + 5), 3.0, device="cuda")
+        out, lse = call(pkg, q, k, v, [0, n], [0, n], True, out=place[:, :, :dim])
+        check_attn(out, lse, q, k, v, [0, n], [0, n], True, dim ** -0.5)
+        assert bool((place[:, :, dim:] == 3.0).all())
+        head_major = torch.empty(heads, n, dim, device="cuda")
+        again, _ = call(pkg, q, k, v, [0, n], [0, n], True, out=head_major.transpose(0, 1))
+        assert torch.equal(again, out)
+
+
+def test_one_key_head_broadcast(pkg):
+    q, k, v = case([70], [70], 4, 1, 64, torch.float16, seed=3)
+    out, lse = call(pkg, q, k.expand(70, 4, 64), v.expand(70, 4, 64), [0, 70], [0, 70], True)
+    check_attn(out, lse, q, k, v, [0, 70], [0, 70], True, 64 ** -0.5)
+
+
+@pytest.mark.parametrize("kv", KV, ids=["f16", "f32"])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_hidden_values_have_no_influence(pkg, kv, bad, dim):
+    """What a row may not see can hold anything: later tokens, and other sequences."""
+    lens = [40, 200, 90]
+    q, k, v = case(lens, lens, 4, 2, dim, kv, seed=4)
+    cu = cu_of(lens)
+    plain, plain_lse = call(pkg, q, k, v, cu, cu, True)
+    k2, v2 = k.clone(), v.clone()
+    hurt = [30, 40 + 150, 40 + 199, 240 + 13]      # a token in each sequence, and one's last
+    for j, t in enumerate(hurt):
+        k2[t, j % 2, 3] = bad
+        v2[t, j % 2, 5 * j] = bad
+    out, lse = call(pkg, q, k2, v2, cu, cu, True)
+    for j, t in enumerate(hurt):
+        start = max(a for a in cu if a <= t)
+        first = min(x for x in hurt if x >= start)
+        assert torch.equal(out[start:first], plain[start:first])
+        assert torch.equal(lse[start:first], plain_lse[start:first])
+        mine = slice(2 * (j % 2), 2 * (j % 2) + 2)
+        assert not bool(out[t, mine].isfinite().all())     # the token itself sees it
+
+
+@pytest.mark.parametrize("kv", KV, ids=["f16", "f32"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_only_the_value_is_not_finite(pkg, kv, dim):
+    """A non-finite value reaches its own column, of the rows that see it, alone."""
+    q, k, v = case([300], [300], 2, 1, dim, kv, seed=5)
+    plain, plain_lse = call(pkg, q, k, v, [0, 300], [0, 300], True)
+    v2 = v.clone()
+    v2[170, 0, 7] = math.inf
+    out, lse = call(pkg, q, k, v2, [0, 300], [0, 300], True)
+    assert torch.equal(lse, plain_lse)
+    assert torch.equal(out[:170], plain[:170])
+    keep = [d for d in range(dim) if d != 7]
+    assert torch.equal(out[:, :, keep], plain[:, :, keep])
+    assert not bool(out[170:, :, 7].isfinite().any())
+
+
+@pytest.mark.parametrize("kv", KV, ids=["f16", "f32"])
+def test_sizes_of_scores(pkg, kv):
+    """Scores from next to nothing to thousands, values over the whole range, outliers among them."""
+    for q_scale, scale in ((1e-4, 0.125), (40.0, 0.125), (300.0, 1.0), (2.0, 1e-3)):
+        q, k, v = case([260], [260], 2, 2, 64, kv, seed=6, q_scale=q_scale)
+        v = v * torch.logspace(-4, 3, 64, device="cuda").to(v.dtype)
+        k[::7] *= 8
+        out, lse = call(pkg, q, k, v, [0, 260], [0, 260], True, scale=scale)
+        check_attn(out, lse, q, k, v, [0, 260], [0, 260], True, scale)
+
+
+@pytest.mark.parametrize("kv", KV, ids=["f16", "f32"])
+@pytest.mark.parametrize("heads,kv_heads,dim,n", [(2, 1, 128, 2500), (2, 2, 64, 4100)])
+def test_long(pkg, kv, heads, kv_heads, dim, n):
+    q, k, v = case([n], [n], heads, kv_heads, dim, kv, seed=7)
+    out, lse = call(pkg, q, k, v, [0, n], [0, n], True)
+    rows = torch.arange(0, n, 97).tolist() + [n - 1]
+    from attn_check import compare, exact_rows
+
+    qc, kc, vc, oc, lc = (x.cpu() for x in (q, k, v, out, lse))
+    for h in range(heads):
+        g = h // (heads // kv_heads)
+        seen = torch.arange(n)[None] <= torch.tensor(rows)[:, None]
+        compare(oc[rows, h], lc[rows, h], *exact_rows(qc[rows, h], kc[:, g], vc[:, g], seen, dim ** -0.5))
+
+
+def test_reruns_side_stream_and_no_lse(pkg):
+    lens = [300, 77, 1024]
+    q, k, v = case(lens, lens, 8, 2, 128, torch.float16, seed=8)
+    cu = cu_of(lens)
+    out, lse = call(pkg, q, k, v, cu, cu, True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        q2 = q * 1.0
+        again = pkg.comp_attn_f32x16(q2, k, v, ints(cu), ints(cu))
+    side.synchronize()
+    assert torch.equal(again, out)
+    third = torch.empty_like(out)
+    cu_t = ints(cu)
+    torch.cuda.synchronize()
+    pkg.comp_attn_f32x16(q, k, v, cu_t, cu_t, out=third, stream=side)
+    side.synchronize()
+    assert torch.equal(third, out)
+
+
+def test_one_sequence_without_offsets(pkg):
+    q, k, v = case([50], [80], 4, 2, 64, torch.float32, seed=9)
+    out = pkg.comp_attn_f32(q, k, v)
+    want, _ = call(pkg, q, k, v, [0, 50], [0, 80], True)
+    assert torch.equal(out, want)
+
+
+# --------------------------------------------------------------------------
+# decode
+# --------------------------------------------------------------------------
+def cache_case(lengths, shared, page, heads, kv_heads, dim, seed=0, spare=3, hole=None):
+    """Shuffled pages; what lies beyond the lengths is NaN."""
+    g = torch.Generator().manual_seed(seed)
+    own = [max(0, -(-n // page) - shared) for n in lengths]
+    width = shared + max(own) + 1
+    pages = shared + sum(own) + spare
+    order = torch.randperm(pages, generator=g).tolist()
+    k, v = (torch.full((pages, kv_heads, page, dim), math.nan, dtype=torch.float16) for _ in range(2))
+    table, at = [], shared
+    for n, o in zip(lengths, own):
+        row = order[:shared] + order[at:at + o]
+        at += o
+        for i, p in enumerate(row):
+            m = max(0, min(page, max(lengths) - i * page if i < shared else n - i * page))
+            k[p, :, :m] = torch.randn(kv_heads, m, dim, generator=g).half() if i >= shared or k[p, 0, 0, 0].isnan() \
+                else k[p, :, :m]
+            v[p, :, :m] = torch.randn(kv_heads, m, dim, generator=g).half() if i >= shared or v[p, 0, 0, 0].isnan() \
+                else v[p, :, :m]
+        table.append(row + [-1] * (width - len(row)))
+    q = torch.randn(len(lengths), heads, dim, generator=g) * 2
+    return q.cuda(), k.cuda(), v.cuda(), ints(table), ints(lengths)
+
+
+def decode(pkg, q, k, v, table, lengths, shared=0, **more):
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    return pkg.comp_attn_decode_f32x16(q, k, v, table, lengths, shared=shared, lse=lse, **more), lse
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("heads,kv_heads,dim", [(4, 2, 64), (8, 1, 128), (3, 3, 80), (20, 2, 128), (2, 2, 8),
+                                                (12, 1, 96)])
+def test_decode_lengths(pkg, page, heads, kv_heads, dim):
+    lengths = [1, 0, page, page + 1, 5 * page - 1, 900, 2]
+    q, k, v, table, n = cache_case(lengths, 0, page, heads, kv_heads, dim, seed=page)
+    out, lse = decode(pkg, q, k, v, table, n)
+    check_decode(out, lse, q, k, v, table, n, dim ** -0.5)
+
+
+@pytest.mark.parametrize("shared,page,batch,heads,kv_heads,dim", [
+    (1, 16, 3, 4, 2, 64), (8, 16, 5, 8, 2, 128), (9, 64, 40, 4, 1, 128), (3, 128, 70, 16, 2, 64), (33, 32, 2, 3, 1, 96),
+    (70, 16, 260, 2, 2, 64), (2, 32, 17, 5, 5, 80), (5, 16, 9, 40, 1, 72),
+])
+def test_decode_shared_prefix(pkg, shared, page, batch, heads, kv_heads, dim):
+    lengths = [shared * page + (7 * i * i) % 150 for i in range(batch)]
+    q, k, v, table, n = cache_case(lengths, shared, page, heads, kv_heads, dim, seed=shared)
+    out, lse = decode(pkg, q, k, v, table, n, shared)
+    check_decode(out, lse, q, k, v, table, n, dim ** -0.5)
+    apart, apart_lse = decode(pkg, q, k, v, table, n, 0)
+    check_decode(apart, apart_lse, q, k, v, table, n, dim ** -0.5)
+
+
+def test_decode_sequences_shorter_than_the_prefix(pkg):
+    """A sequence may end inside the shared pages, or have nothing."""
+    lengths = [400, 256, 255, 129, 64, 1, 0, 300, -5, 10 ** 9]
+    q, k, v, table, n = cache_case([400] * 10, 8, 32, 4, 2, 64, seed=3)
+    n = ints(lengths)
+    k.nan_to_num_(0.25), v.nan_to_num_(0.25)
+    out, lse = decode(pkg, q, k, v, table, n, 8)
+    check_decode(out, lse, q, k, v, table, n, 64 ** -0.5)
+
+
+@pytest.mark.parametrize("shared", [0, 4])
+def test_decode_pages_that_are_not_there(pkg, shared):
+    """A page number outside the cache reads as zeros."""
+    q, k, v, table, n = cache_case([200, 150, 130], 4, 16, 4, 2, 64, seed=5)
+    table[0, 5], table[1, 6], table[2, 7] = -1, 10 ** 8, k.shape[0]
+    if shared:
+        table[:, 2] = -7
+    k.nan_to_num_(0.0), v.nan_to_num_(0.0)
+    out, lse = decode(pkg, q, k, v, table, n, shared)
+    check_decode(out, lse, q, k, v, table, n, 64 ** -0.5)
+
+
+def test_decode_strided_queries_and_stream(pkg):
+    q, k, v, table, n = cache_case([77, 300, 5], 0, 16, 4, 2, 64, seed=6)
+    wide = torch.randn(3, 9, 64, device="cuda")
+    wide[:, 2:6] = q
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        out, lse = decode(pkg, wide[:, 2:6], k, v, table, n)
+    side.synchronize()
+    check_decode(out, lse, q, k, v, table, n, 64 ** -0.5)
+
+
+def test_decode_long(pkg):
+    q, k, v, table, n = cache_case([20000, 3, 9000], 0, 64, 2, 1, 128, seed=7)
+    out, lse = decode(pkg, q, k, v, table, n)
+    check_decode(out, lse, q, k, v, table, n, 128 ** -0.5)
+    q, k, v, table, n = cache_case([20000, 19200, 19201, 19999], 300, 64, 2, 1, 128, seed=8)
+    out, lse = decode(pkg, q, k, v, table, n, 300)
+    check_decode(out, lse, q, k, v, table, n, 128 ** -0.5)
+
+
+# --------------------------------------------------------------------------
+# refusals of the torch binding (the C calls' own are tested without a GPU)
+# --------------------------------------------------------------------------
+def test_refusals(pkg):
+    q, k, v = case([10], [10], 4, 2, 64, torch.float16)
+    cu = ints([0, 10])
+    for bad in (dict(q=q.half()), dict(k=k.float()), dict(q=q.cpu()), dict(q=q[0]), dict(k=k[:, :, :32]),
+                dict(k=k[:5]), dict(q=q[:, :3]), dict(cu_k=None), dict(cu_q=cu.long()), dict(cu_k=ints([0, 5, 10])),
+                dict(out=torch.empty(10, 4, 64)), dict(out=torch.empty(10, 4, 63, device="cuda")),
+                dict(lse=torch.empty(10, device="cuda")), dict(q=q.transpose(1, 2).contiguous().transpose(1, 2))):
+        a = {**dict(q=q, k=k, v=v, cu_q=cu, cu_k=cu), **bad}
+        with pytest.raises((ValueError, TypeError)):
+            pkg.comp_attn_f32x16(**a)
+    for bad in (dict(scale=0.0), dict(scale=-1.0), dict(scale=math.nan), dict(out=q)):
+        with pytest.raises(pkg.CompError):
+            pkg.comp_attn_f32x16(q, k, v, cu, cu, **bad)
+    with pytest.raises(pkg.CompError):  # head_dim beyond 128
+        pkg.comp_attn_f32x16(*case([4], [4], 1, 1, 136, torch.float16))
+    with pytest.raises(pkg.CompError):  # rows of out on top of each other
+        pkg.comp_attn_f32x16(q, k, v, cu, cu, out=torch.empty(64, device="cuda").expand(10, 4, 64))
+    q, k, v, table, n = cache_case([77, 300, 5], 0, 16, 4, 2, 64)
+    for bad in (dict(shared=-1), dict(shared=table.shape[1] + 1), dict(scale=math.inf)):
+        with pytest.raises(pkg.CompError):
+            pkg.comp_attn_decode_f32x16(q, k, v, table, n, **bad)
+    with pytest.raises(pkg.CompError):  # a page size that is not offered
+        pkg.comp_attn_decode_f32x16(q, k[:, :, :8].contiguous(), v[:, :, :8].contiguous(), table, n)
+    for bad in (dict(q=q[:2]), dict(lengths=n.long()), dict(table=table[0]), dict(k_pages=k.float())):
+        with pytest.raises(ValueError):
+            pkg.comp_attn_decode_f32x16(**{**dict(q=q, k_pages=k, v_pages=v, table=table, lengths=n), **bad})
+
+
+def test_nothing_to_do(pkg):
+    q, k, v = case([0], [0], 4, 2, 64, torch.float16)
+    assert pkg.comp_attn_f32x16(q, k, v).shape == (0, 4, 64)
+    q, k, v = case([3], [0], 4, 2, 64, torch.float32)
+    lse = torch.empty(3, 4, device="cuda")
+    assert bool((pkg.comp_attn_f32(q, k, v, lse=lse) == 0).all()) and bool(lse.isneginf().all())
