@@ -54,7 +54,7 @@ SIGNATURES = {
     "comp_gemm_f32x16_epilogue": (_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp]),
     "comp_gemm_f16x2_epilogue": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp]),
     "comp_gemm_f32x16_noalloc": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp]),
-    "comp_attn_workspace_bytes": (_i64, [_vp, _int]),
+    "comp_attn_workspace_bytes": (_i64, [_vp, _int, _vp, _vp]),
     "comp_attn_f32x16": (_int, [_vp] * 9 + [_i64, _vp]),
     "comp_attn_f32": (_int, [_vp] * 9 + [_i64, _vp]),
     "comp_kv_append_f32": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp]),

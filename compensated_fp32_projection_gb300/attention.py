@@ -100,7 +100,8 @@ def _attn(name, kv_dtype, q, k, v, cu_q, cu_k, scale, causal, out, lse, workspac
     a = _native.Attn(n_seq, tokens, k.shape[0], heads, k.shape[1], dim, int(bool(causal)),
                      dim ** -0.5 if scale is None else scale, q.stride(0), q.stride(1), k.stride(0), k.stride(1),
                      v.stride(0), v.stride(1), out.stride(0), out.stride(1))
-    need = int(_native.load().comp_attn_workspace_bytes(ctypes.byref(a), k.element_size()))
+    need = int(_native.load().comp_attn_workspace_bytes(ctypes.byref(a), k.element_size(), k.data_ptr(),
+                                                        v.data_ptr()))
     workspace = _workspace(workspace, need, q)
     _native.call(name, ctypes.byref(a), q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(cu_q), _ptr(cu_k),
                  out.data_ptr(), _ptr(lse), _ptr(workspace), 0 if workspace is None else workspace.nbytes,

@@ -181,18 +181,14 @@ comp_status_t attn(const comp_attn_t* a, const float* q, const void* k, const vo
             if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n))
                 return COMP_ERR_INVALID_VALUE;
     }
-    const int64_t need = comp_attn_workspace_bytes(a, kv_bytes);
+    const int64_t need = comp_attn_workspace_bytes(a, kv_bytes, k, v);
     if (need > 0 && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0))
         return COMP_ERR_INVALID_VALUE;
     DeviceInfo dev;
     const comp_status_t st = current_device(&dev);
     if (st != COMP_OK)
         return st;
-    Rows p{q, out, lse, cu_q, cu_k, nullptr, a->n_seq, a->total_q, a->total_k, a->q_token, a->q_head, a->out_token,
-           a->out_head, a->heads, a->heads / a->kv_heads, a->head_dim, a->causal, a->scale};
-    Source s{k, v, a->k_token, a->k_head, a->v_token, a->v_head, kv_bytes == 4, nullptr, 0, 0, 0, a->kv_heads,
-             a->head_dim};
-    return launch_rows(p, s, static_cast<cudaStream_t>(stream));
+    return launch_attn(*a, q, k, v, kv_bytes, cu_q, cu_k, out, lse, workspace, dev, static_cast<cudaStream_t>(stream));
 }
 
 bool decode_ok(const comp_kv_cache_t* c, int64_t batch, int32_t heads, int64_t width, int64_t shared_pages,
@@ -210,12 +206,12 @@ using namespace compfp32;
 
 extern "C" {
 
-int64_t comp_attn_workspace_bytes(const comp_attn_t* a, int kv_bytes)
+int64_t comp_attn_workspace_bytes(const comp_attn_t* a, int kv_bytes, const void* k, const void* v)
 {
     AttnBytes b;
     if ((kv_bytes != 2 && kv_bytes != 4) || !attn_ok(a, kv_bytes, &b))
         return 0;
-    return 0;
+    return attn_stage_bytes(*a, kv_bytes, k, v);
 }
 
 comp_status_t comp_attn_f32x16(const comp_attn_t* a, const float* q, const uint16_t* k, const uint16_t* v,

@@ -1,0 +1,940 @@
+// Attention on the fifth-generation tensor cores.
+//
+// A CTA computes up to 256 query rows of one key/value head, in two halves of
+// 128 rows (the tensor cores' M).  A row is a query token and one of the
+// `group` query heads that share the key/value head, so that grouped heads
+// share the loads and a tile of a causal prompt spans few tokens.  Keys and
+// values pass once, in tiles of BN keys:
+//
+//   S  = q k^T        q is split as in the projections, hi = fp16(q) and
+//                     lo = fp16((q - hi) 1024): the lo products first, into a
+//                     fresh accumulator, then the hi products with that
+//                     accumulator scaled by 2^-10 on input.  FP32 keys are
+//                     split likewise: lo*hi, hi*lo, then hi*hi.
+//   softmax           running maximum and sum of a row in one thread, in FP32
+//                     and to base 2: p = 2^(s c - m), c = scale log2 e.
+//   P                 to two FP16 values as well.  2^14 p, at most 16384, is
+//                     split into hi = fp16(2^14 p) and lo = fp16(2^14 p - hi)
+//                     with no further scale: values so small that lo falls
+//                     among the subnormals lie 2^-24 and more below the
+//                     row's largest, so the pair is exact to 2^-39 of it, and
+//                     both halves add up in one accumulator.
+//   O' = P v          of this tile alone, into a fresh accumulator; added in
+//                     FP32 registers, o = o 2^(m_old - m_new) + O'.  The tensor
+//                     cores' own sums so never run over more than BN keys, and
+//                     rescaling costs the multiply of that addition.
+//
+// Two products for FP16 keys and values, three for FP32 ones: the floor is
+// 4 D operations for each visible pair and product, at the tensor cores' FP16
+// rate.  One half's softmax runs while the tensor cores work for the other
+// half.  S is overwritten in place by P (128 columns of 32 bits: hi and lo
+// pairs), which the second product reads from tensor memory.
+//
+// Warps: 0 loads tiles of k and v (TMA, a ring of stages), 1 issues the
+// products, 2 and 3 see to values that must not count (below), 4..7 and 8..11
+// own the rows of the two halves: thread = tensor-memory lane = row.
+//
+// Hidden keys: a score that its row may not see becomes -inf, whatever k held,
+// so p = 0.  In the product with v a zero does not silence an infinity or a
+// NaN.  Tiles that some row sees only in part are therefore looked through
+// first: what is not finite there is set to zero in shared memory, and if a
+// row of this CTA sees it, the rows that do add it afterwards, by hand.
+#include <cuda_fp16.h>
+
+#include <cmath>
+
+#include "internal.h"
+#include "ptx.cuh"
+#include "tc_util.cuh"
+
+namespace compfp32 {
+namespace {
+
+constexpr int kThreads = 384;
+// Registers a thread at launch, and after setmaxnreg: 128 x 40 + 256 x 232 is
+// the launch's 384 x 168.  The row threads hold the D output sums of a row
+// and 32 to 64 scores.  The build checks the 168.
+constexpr int kCtrlRegs = 40;
+constexpr int kRowRegs = 232;
+static_assert(128 * kCtrlRegs + 256 * kRowRegs <= kThreads * 168, "register split");
+constexpr long long kWaitLimit = 1ll << 31;  // cycles (about a second)
+constexpr float kLog2E = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kPScale = 16384.0f;  // 2^14
+
+// Fault codes of the waits.
+constexpr uint32_t kFaultAttnLoad = 0x901;
+constexpr uint32_t kFaultAttnMma = 0x902;
+constexpr uint32_t kFaultAttnValues = 0x903;
+constexpr uint32_t kFaultAttnRows = 0x904;
+
+__device__ uint32_t g_attn_fault_word;
+
+// DP: the head dimension padded to 64 or 128.  PL: planes of k and v, 1 (FP16)
+// or 2 (FP32, split).
+template <int DP_, int PL_>
+struct Cfg {
+    static constexpr int DP = DP_, PL = PL_;
+    // Keys of a tile.  With two planes at D = 128 a tile of 128 keys would take
+    // 64 KB a stage beside the 128 KB of q: 64 keys leave three stages.
+    static constexpr int BN = DP == 128 && PL == 2 ? 64 : 128;
+    static constexpr int kBoxes = DP / 64;                      // 64-wide boxes along D
+    static constexpr uint32_t kQTile = 128 * DP * 2;            // one plane of one half
+    static constexpr uint32_t kQBytes = 4 * kQTile;
+    static constexpr uint32_t kPlane = BN * DP * 2;
+    static constexpr uint32_t kStage = PL * kPlane;
+    static constexpr int NS = DP == 128 ? 3 : (PL == 2 ? 4 : 6);
+    // Buffers of O' a half: what tensor memory has left beside S (2 x 128 of
+    // 512 columns).
+    static constexpr int OB = DP == 128 ? 1 : 2;
+    static constexpr size_t kSmem = 1024 + kQBytes + NS * kStage + 1024;
+    static_assert(kSmem <= 232448, "shared memory");
+    static constexpr uint32_t kIdescS = idesc_f16_f32(128, BN);
+    static constexpr uint32_t kIdescO = idesc_f16_f32(128, DP) | kIdescBMnMajor;
+};
+
+struct Shared {
+    uint64_t full[6], empty[6];  // a stage has landed; products and warps 2, 3 are done with it
+    uint64_t qfull[2];           // a half's q planes are in shared memory
+    uint64_t sfull[2];           // S of a tile is complete
+    uint64_t pfull[2];           // P of a tile is in tensor memory (and S has been read)
+    uint64_t ofull[4], ofree[4]; // O' is complete; has been read (half * OB + buffer)
+    uint64_t checked[6];         // warps 2 and 3 are done with a stage (a barrier for each stage: they may
+                                 // be several tiles ahead of the products)
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+    int seq, block;              // this CTA's sequence and block of rows; seq < 0: none
+    int most[2], least[2];       // most and least keys that a row of a half sees
+    int hurt;                    // a looked-through tile has values that are not finite, and seen
+};
+
+struct Params {
+    const float* q;
+    float* out;
+    float* lse;
+    const int32_t* cu_q;
+    const int32_t* cu_k;
+    const void* v;                // v as the caller has it
+    int64_t v_token, v_head;
+    const int32_t* table;         // pages of the keys (page_size > 0)
+    const int32_t* lengths;       // keys that each query token sees (nullptr: by `causal`)
+    int64_t q_token, q_head, out_token, out_head;
+    int64_t out_split, lse_split; // elements between the outputs of two parts of the keys
+    int n_seq, total_q, total_k, kv_heads, group, dim, causal, splits;
+    int page_size, table_pages, pages;
+    int v_f32, vec_q, vec_out;
+    float scale;
+};
+
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, int* abort_flag, uint32_t code)
+{
+    if (mbar_try_wait(bar, parity))
+        return true;
+    const long long start = clock64();
+    while (true) {
+        if (mbar_try_wait_sleep(bar, parity, 20000))
+            return true;
+        if (*reinterpret_cast<volatile int*>(abort_flag))
+            return false;
+        if (clock64() - start > kWaitLimit) {
+            atomicCAS(&g_attn_fault_word, 0u, code);
+            *reinterpret_cast<volatile int*>(abort_flag) = 1;
+            return false;
+        }
+    }
+}
+
+// Warp-wide: lane 0 waits, and on success every lane observes the phase itself.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort_flag, uint32_t code)
+{
+    bool ok = true;
+    if ((threadIdx.x & 31) == 0)
+        ok = wait_bounded(bar, parity, abort_flag, code);
+    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+    if (ok)
+        (void)mbar_try_wait(bar, parity);
+    return ok;
+}
+
+// Wait for what was issued before the CTA exits after an abort.
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity)
+{
+    const long long start = clock64();
+    while (!mbar_try_wait(bar, parity) && clock64() - start < kWaitLimit) {
+    }
+}
+
+__device__ __forceinline__ int clampi(int x, int lo, int hi)
+{
+    return x < lo ? lo : (x > hi ? hi : x);
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t u2_bits(uint32_t a, uint32_t b)
+{
+    return static_cast<uint64_t>(a) | (static_cast<uint64_t>(b) << 32);
+}
+
+// This CTA's sequence and block of 256 rows: blocks are numbered sequence by
+// sequence.  One warp; cu_q is read 32 sequences at a time.
+__device__ __forceinline__ void find_block(const Params& p, int block, Shared* sm)
+{
+    const int lane = threadIdx.x & 31;
+    if (!p.cu_q) {
+        const int n = static_cast<int>((static_cast<int64_t>(p.total_q) * p.group + 255) / 256);
+        if (lane == 0) {
+            sm->seq = block < n ? 0 : -1;
+            sm->block = n - 1 - block;
+        }
+        return;
+    }
+    for (int s0 = 0; s0 < p.n_seq; s0 += 32) {
+        const int s = s0 + lane;
+        int n = 0;
+        if (s < p.n_seq) {
+            const int a = clampi(p.cu_q[s], 0, p.total_q), b = clampi(p.cu_q[s + 1], a, p.total_q);
+            n = static_cast<int>((static_cast<int64_t>(b - a) * p.group + 255) / 256);
+        }
+        int x = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o)
+                x += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, x > block);
+        if (hit) {
+            if (lane == __ffs(hit) - 1) {
+                sm->seq = s;
+                sm->block = x - 1 - block;  // the last block, which sees most keys, first
+            }
+            return;
+        }
+        block -= __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0)
+        sm->seq = -1;
+}
+
+template <int DP, int PL>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                   const __grid_constant__ CUtensorMap map_k_lo, const __grid_constant__ CUtensorMap map_v_lo,
+                   const Params p)
+{
+    using C = Cfg<DP, PL>;
+    constexpr int BN = C::BN, NS = C::NS, OB = C::OB;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* const stages = smem + C::kQBytes;
+    Shared* const sm = reinterpret_cast<Shared*>(stages + NS * C::kStage);
+    static_assert(sizeof(Shared) <= 1024, "barrier area");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    grid_dependency_wait();
+    const int head = blockIdx.x % p.kv_heads;
+    const int part = blockIdx.x / p.kv_heads % p.splits;
+    if (warp == 0)
+        find_block(p, blockIdx.x / p.kv_heads / p.splits, sm);
+    if (threadIdx.x == 64) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&sm->full[i], 1);
+            mbar_init(&sm->empty[i], 3);
+            mbar_init(&sm->checked[i], 2);
+        }
+        for (int h = 0; h < 2; ++h) {
+            mbar_init(&sm->qfull[h], 4);
+            mbar_init(&sm->sfull[h], 1);
+            mbar_init(&sm->pfull[h], 4);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&sm->ofull[i], 1);
+            mbar_init(&sm->ofree[i], 4);
+        }
+        mbar_init(&sm->drain, 1);
+        sm->abort = 0;
+        for (int h = 0; h < 2; ++h) {
+            sm->most[h] = 0;
+            sm->least[h] = INT32_MAX;
+        }
+        sm->hurt = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    if (sm->seq < 0)
+        return;  // the grid is an upper bound
+
+    // the sequence, and the part of its keys that this CTA goes through
+    int q0 = 0, nq = p.total_q, k0 = 0, nk = p.total_k;
+    if (p.cu_q) {
+        q0 = clampi(p.cu_q[sm->seq], 0, p.total_q);
+        nq = clampi(p.cu_q[sm->seq + 1], q0, p.total_q) - q0;
+        k0 = clampi(p.cu_k[sm->seq], 0, p.total_k);
+        nk = clampi(p.cu_k[sm->seq + 1], k0, p.total_k) - k0;
+    }
+    const int part_keys = ((nk + BN - 1) / BN + p.splits - 1) / p.splits * BN;
+    const int first = min(static_cast<int64_t>(nk), static_cast<int64_t>(part) * part_keys);
+    const int keys = min(nk - first, part_keys);
+
+    // rows: what each sees
+    int64_t q_at = 0, out_at = 0, lse_at = 0;
+    int lim = 0;
+    bool valid = false;
+    const int half = (warp >> 2) - 1;
+    if (half >= 0) {
+        const int64_t row = static_cast<int64_t>(sm->block) * 256 + (threadIdx.x - 128);
+        valid = row < static_cast<int64_t>(nq) * p.group;
+        const int t = static_cast<int>(valid ? row / p.group : 0), hq = head * p.group + static_cast<int>(row % p.group);
+        int sees = nk;
+        if (p.lengths)
+            sees = valid ? clampi(p.lengths[q0 + t], 0, nk) : 0;
+        else if (p.causal)
+            sees = static_cast<int>(min(static_cast<int64_t>(nk), max(int64_t(0), static_cast<int64_t>(t) + 1 + nk - nq)));
+        lim = clampi(sees - first, 0, keys);
+        q_at = (q0 + static_cast<int64_t>(t)) * p.q_token + hq * p.q_head;
+        out_at = (q0 + static_cast<int64_t>(t)) * p.out_token + hq * p.out_head + part * p.out_split;
+        lse_at = (q0 + static_cast<int64_t>(t)) * p.kv_heads * p.group + hq + part * p.lse_split;
+        const int hi = __reduce_max_sync(0xffffffffu, valid ? lim : 0);
+        const int lo = __reduce_min_sync(0xffffffffu, valid ? lim : INT32_MAX);
+        if (lane == 0) {
+            atomicMax(&sm->most[half], hi);
+            atomicMin(&sm->least[half], lo);
+        }
+    }
+    if (warp == 1) {
+        tmem_alloc(&sm->tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm->tmem_base;
+    const int n0 = (sm->most[0] + BN - 1) / BN, n1 = (sm->most[1] + BN - 1) / BN;
+    const int n = max(n0, n1), most = max(sm->most[0], sm->most[1]);
+    // tiles from this one on are seen only in part by some row
+    const int edge = min(n0 > 0 ? sm->least[0] : INT32_MAX, n1 > 0 ? sm->least[1] : INT32_MAX) / BN;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtrlRegs));
+        if (warp == 0) {
+            // ---------------- loads: K0, V0, K1, V1, ...
+            const int pieces = p.page_size ? BN / p.page_size : 1;
+            const int boxes = PL * C::kBoxes * pieces;
+            int i = 0;
+            for (; i < 2 * n; ++i) {
+                const int s = i % NS;
+                if (i >= NS && !warp_wait(&sm->empty[s], ((i / NS) - 1) & 1, &sm->abort, kFaultAttnLoad))
+                    break;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&sm->full[s], C::kStage);
+                __syncwarp();
+                for (int b = lane; b < boxes; b += 32) {
+                    const int piece = b % pieces, box = b / pieces % C::kBoxes, plane = b / pieces / C::kBoxes;
+                    uint8_t* const dst = stages + s * C::kStage + plane * C::kPlane + box * (BN * 128) +
+                                         piece * p.page_size * 128;
+                    const CUtensorMap* const map = plane ? ((i & 1) ? &map_v_lo : &map_k_lo) : ((i & 1) ? &map_v : &map_k);
+                    const int key = first + (i >> 1) * BN;
+                    if (p.page_size) {
+                        // a page that is not there: a place beyond the cache, which reads zeros
+                        const int at = key / p.page_size + piece;
+                        const int page = at < p.table_pages ? p.table[at] : -1;
+                        tma_load_3d(dst, map, &sm->full[s], box * 64, 0,
+                                    (page >= 0 && page < p.pages ? page : p.pages) * p.kv_heads + head);
+                    } else {
+                        tma_load_3d(dst, map, &sm->full[s], box * 64, k0 + key, head);
+                    }
+                }
+                __syncwarp();
+            }
+            if (i < 2 * n) {  // abort: what was issued lands before the CTA leaves
+                for (int j = max(0, i - NS); j < i; ++j)
+                    drain_wait(&sm->full[j % NS], (j / NS) & 1);
+            }
+        } else if (warp == 1) {
+            // ---------------- products
+            const uint32_t leader = lane == 0;
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, int phase) {
+                ok = ok && warp_wait(bar, phase & 1, &sm->abort, kFaultAttnMma);
+                tc_fence_after();
+                return ok;
+            };
+            auto scores = [&](int h, int j) {
+                const uint32_t d = tmem + h * 128;
+                const uint32_t qhi = smem_u32(smem) + h * 2 * C::kQTile, qlo = qhi + C::kQTile;
+                const uint32_t khi = smem_u32(stages) + (2 * j % NS) * C::kStage, klo = khi + C::kPlane;
+                auto chain = [&](uint32_t a, uint32_t b, int how) {  // 0 fresh, 1 add, 2 add to 2^-10 of what is there
+    #pragma unroll
+                    for (int t = 0; t < DP / 16; ++t) {
+                        const uint64_t da = sw128_kmajor_desc(a + (t / 4) * (128 * 128) + (t % 4) * 32);
+                        const uint64_t db = sw128_kmajor_desc(b + (t / 4) * (BN * 128) + (t % 4) * 32);
+                        if (t == 0 && how == 2)
+                            umma_f16_scale10_by(leader, d, da, db, C::kIdescS);
+                        else
+                            umma_f16_by(leader, d, da, db, C::kIdescS, t > 0 || how > 0);
+                    }
+                };
+                chain(qlo, khi, 0);
+                if (PL == 2)
+                    chain(qhi, klo, 1);
+                chain(qhi, khi, 2);
+                umma_commit_by(leader, &sm->sfull[h]);
+            };
+            auto values = [&](int h, int j) {
+                const uint32_t pt = tmem + h * 128, d = tmem + 256 + h * 128 + (OB == 2 ? (j & 1) * 64 : 0);
+                const uint32_t vhi = smem_u32(stages) + ((2 * j + 1) % NS) * C::kStage, vlo = vhi + C::kPlane;
+                // P of 16 keys: 8 columns of hi pairs, then 8 of lo pairs
+                auto step = [&](int t, int lo_p, uint32_t v, int how) {
+                    const uint32_t a = pt + t * 16 + lo_p * 8;
+                    const uint64_t db = sw128_mnmajor_desc(v + t * 2048, BN * 128);
+                    if (how == 2)
+                        umma_f16_ta_scale10_by(leader, d, a, db, C::kIdescO);
+                    else
+                        umma_f16_ta_by(leader, d, a, db, C::kIdescO, how);
+                };
+                if (PL == 2) {
+    #pragma unroll
+                    for (int t = 0; t < BN / 16; ++t)
+                        step(t, 0, vlo, t > 0);
+                }
+    #pragma unroll
+                for (int t = 0; t < BN / 16; ++t) {
+                    step(t, 1, vhi, t > 0 ? 1 : (PL == 2 ? 2 : 0));
+                    step(t, 0, vhi, 1);
+                }
+                umma_commit_by(leader, &sm->ofull[h * OB + (OB == 2 ? (j & 1) : 0)]);
+            };
+            if (n > 0 && wait(&sm->full[0], 0)) {
+                for (int h = 0; h < 2; ++h)
+                    if ((h ? n1 : n0) > 0 && wait(&sm->qfull[h], 0))
+                        scores(h, 0);
+                umma_commit_by(leader, &sm->empty[0]);
+            }
+            for (int j = 0; ok && j < n; ++j) {
+                const int sv = (2 * j + 1) % NS, sk = (2 * j + 2) % NS;
+                bool v_here = false, k_here = false;
+                for (int h = 0; h < 2; ++h) {
+                    const int nh = h ? n1 : n0;
+                    if (j < nh) {
+                        if (!v_here && (!wait(&sm->full[sv], (2 * j + 1) / NS) ||
+                                        (j >= edge && !wait(&sm->checked[sv], (2 * j + 1) / NS))))
+                            break;
+                        v_here = true;
+                        if (!wait(&sm->pfull[h], j))
+                            break;
+                        if (j >= OB && !wait(&sm->ofree[h * OB + j % OB], j / OB - 1))
+                            break;
+                        values(h, j);
+                        if (h == 1 || j >= n1)
+                            umma_commit_by(leader, &sm->empty[sv]);
+                    }
+                    if (j + 1 < nh) {
+                        if (!k_here && !wait(&sm->full[sk], (2 * j + 2) / NS))
+                            break;
+                        k_here = true;
+                        scores(h, j + 1);
+                        if (h == 1 || j + 1 >= n1)
+                            umma_commit_by(leader, &sm->empty[sk]);
+                    }
+                }
+            }
+            if (!ok) {
+                umma_commit_by(leader, &sm->drain);
+                drain_wait(&sm->drain, 0);
+            }
+        } else {
+            // ---------------- values that must not count
+            for (int i = 0; i < 2 * n; ++i) {
+                const int s = i % NS, j = i >> 1;
+                if (!warp_wait(&sm->full[s], (i / NS) & 1, &sm->abort, kFaultAttnValues))
+                    break;
+                if ((i & 1) && j >= edge) {
+                    uint8_t* const tile = stages + s * C::kStage;
+                    bool seen = false;
+                    for (uint32_t at = (warp - 2) * 512 + lane * 16; at < C::kStage; at += 1024) {
+                        uint4 x = *reinterpret_cast<const uint4*>(tile + at);
+                        uint32_t* const w = reinterpret_cast<uint32_t*>(&x);
+                        bool any = false;
+    #pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            // an exponent of all ones carries into the sign's place
+                            const uint32_t odd = ((w[e] & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
+                            any |= odd != 0;
+                            w[e] &= ~((odd >> 15) * 0xffffu);
+                        }
+                        if (any) {
+                            *reinterpret_cast<uint4*>(tile + at) = x;
+                            seen |= j * BN + static_cast<int>(at / 128 % BN) < most;
+                        }
+                    }
+                    if (__any_sync(0xffffffffu, seen) && lane == 0)
+                        atomicOr(&sm->hurt, 1);
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sm->checked[s]);
+                    mbar_arrive(&sm->empty[s]);
+                }
+            }
+        }
+    } else {
+        // ---------------- rows
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
+        const int nh = half ? n1 : n0, w4 = warp & 3;
+        const uint32_t lanes = static_cast<uint32_t>(w4 * 32) << 16;
+        bool ok = true;
+        // q into shared memory, split; a warp takes its 32 rows one after the other
+        if (nh > 0) {
+            uint8_t* const hi_tile = smem + half * 2 * C::kQTile;
+            constexpr int E = DP / 32;  // values of a lane
+            const int d0 = lane * E;
+#pragma unroll 4
+            for (int i = 0; i < 32; ++i) {
+                const int64_t at = __shfl_sync(0xffffffffu, q_at, i);
+                const bool there = __shfl_sync(0xffffffffu, valid ? 1 : 0, i) != 0;
+                float x[E];
+                if (there && p.vec_q && d0 + E <= p.dim) {
+                    if (E == 4) {
+                        const float4 f = __ldg(reinterpret_cast<const float4*>(p.q + at + d0));
+                        x[0] = f.x, x[1] = f.y, x[E - 2] = f.z, x[E - 1] = f.w;
+                    } else {
+                        const float2 f = __ldg(reinterpret_cast<const float2*>(p.q + at + d0));
+                        x[0] = f.x, x[1] = f.y;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        x[e] = there && d0 + e < p.dim ? __ldg(p.q + at + d0 + e) : 0.0f;
+                }
+                uint32_t hi[E / 2], lo[E / 2];
+#pragma unroll
+                for (int e = 0; e < E; e += 2)
+                    split2(x[e], x[e + 1], hi[e / 2], lo[e / 2]);
+                const uint32_t r = w4 * 32 + i;
+                const uint32_t to = (d0 / 64) * (128 * 128) + sw128(r, (d0 % 64) / 8) + (d0 % 8) * 2;
+                if (E == 4) {
+                    *reinterpret_cast<uint2*>(hi_tile + to) = make_uint2(hi[0], hi[E / 2 - 1]);
+                    *reinterpret_cast<uint2*>(hi_tile + C::kQTile + to) = make_uint2(lo[0], lo[E / 2 - 1]);
+                } else {
+                    *reinterpret_cast<uint32_t*>(hi_tile + to) = hi[0];
+                    *reinterpret_cast<uint32_t*>(hi_tile + C::kQTile + to) = lo[0];
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sm->qfull[half]);
+        }
+
+        const float c2 = p.scale * kLog2E;
+        const uint64_t c22 = f2_bits(c2, c2);
+        const uint32_t st = tmem + lanes + half * 128;
+        const int row_lim = valid ? lim : INT32_MAX;  // rows that are not there are not stored
+        float m = -INFINITY;        // the running maximum of s * c2
+        uint64_t l2 = 0;            // the running sum of 2^14 p, in two parts
+        float alpha = 0.0f;         // what the sums so far are to be scaled by with the next O'
+        uint64_t o[DP / 2];
+#pragma unroll
+        for (int i = 0; i < DP / 2; ++i)
+            o[i] = 0;
+
+        // o = o alpha + O' of tile j
+        auto take = [&](int j) {
+            const int b = half * OB + (OB == 2 ? (j & 1) : 0);
+            if (!warp_wait(&sm->ofull[b], (j / OB) & 1, &sm->abort, kFaultAttnRows))
+                return false;
+            tc_fence_after();
+            const uint64_t a2 = f2_bits(alpha, alpha);
+            const uint32_t from = tmem + lanes + 256 + half * 128 + (OB == 2 ? (j & 1) * 64 : 0);
+#pragma unroll
+            for (int c = 0; c < DP / 32; ++c) {
+                uint32_t r[32];
+                tmem_ld32(from + c * 32, r);
+                tmem_ld_wait32(r);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    o[c * 16 + i] = fma2(o[c * 16 + i], a2, u2_bits(r[2 * i], r[2 * i + 1]));
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sm->ofree[b]);
+            return true;
+        };
+
+        for (int j = 0; j < nh; ++j) {
+            if (!warp_wait(&sm->sfull[half], j & 1, &sm->abort, kFaultAttnRows)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const bool part_seen = __any_sync(0xffffffffu, row_lim < (j + 1) * BN);
+            const int left = row_lim - j * BN;  // columns below this are seen
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < BN / 32; ++c) {
+                uint32_t r[32];
+                tmem_ld32(st + c * 32, r);
+                tmem_ld_wait32(r);
+                if (part_seen) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        top[i & 3] = fmaxf(top[i & 3], c * 32 + i < left ? __uint_as_float(r[i]) : -INFINITY);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        top[i & 3] = fmaxf(top[i & 3], __uint_as_float(r[i]));
+                }
+            }
+            const float m_new = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c2);
+            const float shift = m_new == -INFINITY ? 0.0f : m_new;  // nothing seen yet: every p is 0
+            const float alpha_new = ex2(m - shift);
+            m = m_new;
+            l2 = mul2(l2, f2_bits(alpha_new, alpha_new));
+            const uint64_t s2 = f2_bits(-shift, -shift), k2 = f2_bits(kPScale, kPScale);
+            uint32_t r[2][16];
+            tmem_ld16(st, r[0]);
+#pragma unroll
+            for (int c = 0; c < BN / 16; ++c) {
+                uint32_t (&x)[16] = r[c & 1];
+                tmem_ld_wait16(x);
+                if (c + 1 < BN / 16)
+                    tmem_ld16(st + (c + 1) * 16, r[(c + 1) & 1]);
+                if (part_seen) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        x[i] = c * 16 + i < left ? x[i] : 0xff800000u;  // -inf
+                }
+                uint32_t out[16];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint64_t y = fma2(u2_bits(x[2 * i], x[2 * i + 1]), c22, s2);
+                    const uint64_t e = mul2(f2_bits(ex2(lo_f(y)), ex2(hi_f(y))), k2);
+                    l2 = add2(l2, e);
+                    const __half2 h = __floats2half2_rn(lo_f(e), hi_f(e));
+                    const float2 hf = __half22float2(h);
+                    const uint64_t rest = sub2(e, f2_bits(hf.x, hf.y));
+                    out[i] = pack_h2(h);
+                    out[8 + i] = pack_h2(__floats2half2_rn(lo_f(rest), hi_f(rest)));
+                }
+                tmem_st16(st + c * 16, out);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sm->pfull[half]);
+            if (j > 0 && !take(j - 1)) {
+                ok = false;
+                break;
+            }
+            alpha = alpha_new;
+        }
+        if (ok && nh > 0)
+            ok = take(nh - 1);
+        if (ok && valid) {
+            const float l = (lo_f(l2) + hi_f(l2)) * (1.0f / kPScale);
+            // no key seen, or none that counts beside an infinite score (NaN stays NaN)
+            const float norm = l == 0.0f ? 0.0f : (1.0f / kPScale) / l;
+            float* const out = p.out + out_at;
+#pragma unroll
+            for (int d = 0; d < DP; d += 4) {
+                const float x0 = lo_f(o[d / 2]) * norm, x1 = hi_f(o[d / 2]) * norm;
+                const float x2 = lo_f(o[d / 2 + 1]) * norm, x3 = hi_f(o[d / 2 + 1]) * norm;
+                if (p.vec_out && d + 4 <= p.dim) {
+                    *reinterpret_cast<float4*>(out + d) = make_float4(x0, x1, x2, x3);
+                } else {
+                    if (d < p.dim)
+                        out[d] = x0;
+                    if (d + 1 < p.dim)
+                        out[d + 1] = x1;
+                    if (d + 2 < p.dim)
+                        out[d + 2] = x2;
+                    if (d + 3 < p.dim)
+                        out[d + 3] = x3;
+                }
+            }
+            if (p.lse)
+                p.lse[lse_at] = l == 0.0f ? -INFINITY : fmaf(m, kLn2, logf(l));
+            // values that are not finite were taken out of the tiles from
+            // `edge` on: a row that sees one adds it (its weight is positive)
+            if (*reinterpret_cast<volatile int*>(&sm->hurt)) {
+#pragma unroll 1
+                for (int i = edge * BN; i < lim; ++i) {
+                    const int key = first + i;
+                    int64_t at = (static_cast<int64_t>(k0) + key) * p.v_token + head * p.v_head;
+                    if (p.page_size) {
+                        const int page = p.table[key / p.page_size];
+                        if (page < 0 || page >= p.pages)
+                            continue;
+                        at = ((static_cast<int64_t>(page) * p.kv_heads + head) * p.page_size + key % p.page_size) *
+                             p.dim;
+                    }
+#pragma unroll 1
+                    for (int d = 0; d < p.dim; ++d) {
+                        const float x = __half2float(p.v_f32 ? __float2half_rn(static_cast<const float*>(p.v)[at + d])
+                                                             : static_cast<const __half*>(p.v)[at + d]);
+                        if (!isfinite(x))
+                            out[d] += x;
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1)
+        tmem_dealloc(tmem, 512);
+}
+
+// FP32 keys and values as FP16 planes (hi = fp16(x), lo = fp16((x - hi) 1024)),
+// or FP16 ones that the tensor maps cannot take (addresses or strides off 16
+// bytes) as they are: rows of `dpad` values, zeros past the head dimension.
+// Each value is read once; the kernel above then reads every row once for
+// each 256 query rows.  blockIdx.y: k or v.
+struct Stage {
+    const void* src[2];
+    int64_t token[2], head[2];
+    uint16_t* hi[2];
+    uint16_t* lo[2];
+    int64_t tokens;
+    int heads, dim, dpad, f32, vec;
+};
+
+__global__ void __launch_bounds__(256) attn_stage_kernel(Stage p)
+{
+    const int w = blockIdx.y, parts = p.dpad / 8;
+    const int64_t work = p.tokens * p.heads * parts;
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; u < work;
+         u += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        const int part = static_cast<int>(u % parts);
+        const int64_t row = u / parts, at = row / p.heads * p.token[w] + row % p.heads * p.head[w] + part * 8;
+        const int64_t to = row * p.dpad + part * 8;
+        if (p.f32) {
+            const float* const src = static_cast<const float*>(p.src[w]) + at;
+            float x[8];
+            if (p.vec && part * 8 + 8 <= p.dim) {
+                const float4 a = *reinterpret_cast<const float4*>(src), b = *reinterpret_cast<const float4*>(src + 4);
+                x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    x[i] = part * 8 + i < p.dim ? src[i] : 0.0f;
+            }
+            uint4 hi, lo;
+            split2(x[0], x[1], hi.x, lo.x);
+            split2(x[2], x[3], hi.y, lo.y);
+            split2(x[4], x[5], hi.z, lo.z);
+            split2(x[6], x[7], hi.w, lo.w);
+            *reinterpret_cast<uint4*>(p.hi[w] + to) = hi;
+            *reinterpret_cast<uint4*>(p.lo[w] + to) = lo;
+        } else {
+            const uint16_t* const src = static_cast<const uint16_t*>(p.src[w]) + at;
+            uint32_t x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t a = part * 8 + 2 * i < p.dim ? src[2 * i] : 0;
+                const uint32_t b = part * 8 + 2 * i + 1 < p.dim ? src[2 * i + 1] : 0;
+                x[i] = a | (b << 16);
+            }
+            *reinterpret_cast<uint4*>(p.hi[w] + to) = make_uint4(x[0], x[1], x[2], x[3]);
+        }
+    }
+}
+
+// [heads][rows][dim] FP16 as boxes of box_rows x 64.  A dimension of extent 1
+// may have any stride.
+bool encode_kv(CUtensorMap* map, const void* base, int64_t dim, int64_t rows, int64_t heads, int64_t row_stride,
+               int64_t head_stride, int box_rows)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn)
+        return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(rows),
+                                static_cast<cuuint64_t>(heads)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(rows > 1 ? row_stride * 2 : 256),
+                                   static_cast<cuuint64_t>(heads > 1 ? head_stride * 2 : 256)};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Whether a tensor map can describe [tokens, heads] rows with these strides.
+bool map_legal(int64_t tokens, int64_t heads, int64_t token, int64_t head)
+{
+    const auto ok = [](int64_t extent, int64_t stride) {
+        return extent <= 1 || (stride > 0 && stride % 8 == 0 && stride < (1ll << 38));
+    };
+    return ok(tokens, token) && ok(heads, head);
+}
+
+template <int DP, int PL>
+comp_status_t launch_t(const CUtensorMap (&maps)[4], const Params& p, int64_t grid, const DeviceInfo& dev,
+                       cudaStream_t stream)
+{
+    using C = Cfg<DP, PL>;
+    static std::mutex mu;
+    static bool done[64] = {};
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (dev.device < 0 || dev.device >= 64)
+            return COMP_ERR_CUDA;
+        if (!done[dev.device]) {
+            if (cudaFuncSetAttribute(attn_tc_kernel<DP, PL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     static_cast<int>(C::kSmem)) != cudaSuccess) {
+                (void)cudaGetLastError();
+                return COMP_ERR_CUDA;
+            }
+            done[dev.device] = true;
+        }
+    }
+    return launch_pdl(attn_tc_kernel<DP, PL>, static_cast<int>(grid), kThreads, C::kSmem, stream, maps[0], maps[1],
+                      maps[2], maps[3], p);
+}
+
+int64_t pad8(int64_t d)
+{
+    return (d + 7) / 8 * 8;
+}
+
+}  // namespace
+
+// Planes that a call stages: k and v, two each if they are FP32; 0 if the
+// caller's own FP16 rows can be loaded.
+int64_t attn_stage_bytes(const comp_attn_t& a, int kv_bytes, const void* k, const void* v)
+{
+    if (a.total_k == 0)
+        return 0;
+    if (kv_bytes == 2 && aligned16(k) && aligned16(v) && map_legal(a.total_k, a.kv_heads, a.k_token, a.k_head) &&
+        map_legal(a.total_k, a.kv_heads, a.v_token, a.v_head))
+        return 0;
+    return (kv_bytes == 4 ? 4 : 2) * 2 * a.total_k * a.kv_heads * pad8(a.head_dim);
+}
+
+comp_status_t launch_attn(const comp_attn_t& a, const float* q, const void* k, const void* v, int kv_bytes,
+                          const int32_t* cu_q, const int32_t* cu_k, float* out, float* lse, void* workspace,
+                          const DeviceInfo& dev, cudaStream_t stream)
+{
+    Params p{};
+    p.q = q;
+    p.out = out;
+    p.lse = lse;
+    p.cu_q = cu_q;
+    p.cu_k = cu_k;
+    p.v = v;
+    p.v_token = a.v_token;
+    p.v_head = a.v_head;
+    p.q_token = a.q_token;
+    p.q_head = a.q_head;
+    p.out_token = a.out_token;
+    p.out_head = a.out_head;
+    p.n_seq = static_cast<int>(a.n_seq);
+    p.total_q = static_cast<int>(a.total_q);
+    p.total_k = static_cast<int>(a.total_k);
+    p.kv_heads = a.kv_heads;
+    p.group = a.heads / a.kv_heads;
+    p.dim = a.head_dim;
+    p.causal = a.causal;
+    p.splits = 1;
+    p.v_f32 = kv_bytes == 4;
+    p.scale = a.scale;
+    const int lane_values = a.head_dim <= 64 ? 2 : 4;
+    p.vec_q = a.q_token % lane_values == 0 && a.q_head % lane_values == 0 && aligned16(q);
+    p.vec_out = a.out_token % 4 == 0 && a.out_head % 4 == 0 && aligned16(out);
+
+    CUtensorMap maps[4] = {};
+    const int box_rows = a.head_dim > 64 && kv_bytes == 4 ? 64 : 128;  // Cfg::BN
+    if (a.total_k > 0) {
+        const void* planes[4] = {k, v, nullptr, nullptr};
+        int64_t token[2] = {a.k_token, a.v_token}, head[2] = {a.k_head, a.v_head}, dim = a.head_dim;
+        if (attn_stage_bytes(a, kv_bytes, k, v) > 0) {
+            const int64_t dpad = pad8(a.head_dim), plane = a.total_k * a.kv_heads * dpad;
+            uint16_t* const ws = static_cast<uint16_t*>(workspace);
+            Stage s{{k, v}, {a.k_token, a.v_token}, {a.k_head, a.v_head}, {ws, ws + plane},
+                    {ws + 2 * plane, ws + 3 * plane}, a.total_k, a.kv_heads, a.head_dim, static_cast<int>(dpad),
+                    kv_bytes == 4, 0};
+            s.vec = aligned16(k) && aligned16(v) && a.k_token % 4 == 0 && a.v_token % 4 == 0 && a.k_head % 4 == 0 &&
+                    a.v_head % 4 == 0;
+            const int64_t work = a.total_k * a.kv_heads * (dpad / 8), most = dev.sm_count * 8;
+            const int64_t blocks = (work + 255) / 256;
+            attn_stage_kernel<<<dim3(static_cast<unsigned>(blocks < most ? blocks : most), 2), 256, 0, stream>>>(s);
+            if (launch_status() != COMP_OK)
+                return COMP_ERR_LAUNCH;
+            for (int i = 0; i < 2; ++i) {
+                planes[i] = s.hi[i];
+                planes[2 + i] = s.lo[i];
+                token[i] = a.kv_heads * dpad;
+                head[i] = dpad;
+            }
+            dim = dpad;
+        }
+        for (int i = 0; i < (kv_bytes == 4 ? 4 : 2); ++i)
+            if (!encode_kv(&maps[i], planes[i], dim, a.total_k, a.kv_heads, token[i % 2], head[i % 2], box_rows))
+                return COMP_ERR_CUDA;
+    }
+    const int64_t rows = a.total_q * p.group;
+    const int64_t grid = (cu_q ? rows / 256 + a.n_seq : (rows + 255) / 256) * a.kv_heads;
+    if (grid > INT32_MAX)
+        return COMP_ERR_INVALID_VALUE;
+    if (a.head_dim <= 64)
+        return kv_bytes == 4 ? launch_t<64, 2>(maps, p, grid, dev, stream) : launch_t<64, 1>(maps, p, grid, dev, stream);
+    return kv_bytes == 4 ? launch_t<128, 2>(maps, p, grid, dev, stream) : launch_t<128, 1>(maps, p, grid, dev, stream);
+}
+
+comp_status_t read_and_clear_attn_fault(cudaStream_t stream, uint32_t* where)
+{
+    uint32_t word = 0;
+    const uint32_t zero = 0;
+    if (cudaMemcpyFromSymbolAsync(&word, g_attn_fault_word, sizeof(word), 0, cudaMemcpyDeviceToHost, stream) !=
+            cudaSuccess ||
+        cudaMemcpyToSymbolAsync(g_attn_fault_word, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, stream) !=
+            cudaSuccess ||
+        cudaStreamSynchronize(stream) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return COMP_ERR_CUDA;
+    }
+    if (word != 0 && where)
+        *where = word;
+    return word == 0 ? COMP_OK : COMP_ERR_TIMEOUT;
+}
+
+}  // namespace compfp32

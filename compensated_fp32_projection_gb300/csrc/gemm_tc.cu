@@ -56,6 +56,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "tc_util.cuh"
 
 namespace compfp32 {
 namespace {
@@ -185,113 +186,6 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity)
     const long long start = clock64();
     while (!mbar_try_wait(bar, parity) && clock64() - start < kWaitLimit) {
     }
-}
-
-// 16-byte load from shared memory at a 32-bit shared-window address.
-__device__ __forceinline__ float4 lds128(uint32_t addr)
-{
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
-    return v;
-}
-
-__device__ __forceinline__ uint32_t pack_h2(__half2 h)
-{
-    return *reinterpret_cast<uint32_t*>(&h);
-}
-
-// Byte offset of 16-byte chunk `chunk` of row `row` in a tile of 128-byte rows
-// with the 128-byte swizzle (tile base 1024-byte aligned).
-__device__ __forceinline__ uint32_t sw128(uint32_t row, uint32_t chunk)
-{
-    return row * 128u + ((chunk ^ (row & 7u)) << 4);
-}
-
-__device__ __forceinline__ uint64_t f2_bits(float a, float b)
-{
-    return static_cast<uint64_t>(__float_as_uint(a)) | (static_cast<uint64_t>(__float_as_uint(b)) << 32);
-}
-
-__device__ __forceinline__ float lo_f(uint64_t v)
-{
-    return __uint_as_float(static_cast<uint32_t>(v));
-}
-
-__device__ __forceinline__ float hi_f(uint64_t v)
-{
-    return __uint_as_float(static_cast<uint32_t>(v >> 32));
-}
-
-// Split two consecutive values (a first): packed FP16 pairs hi and lo.
-// The residual (a - hi) * 1024 is computed on both lanes at once, each
-// operation rounded to nearest even and never fused (exact here: the
-// difference and the scaling by a power of two are representable).
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo)
-{
-    const __half2 h = __floats2half2_rn(a, b);
-    const float2 hf = __half22float2(h);
-    uint64_t d, r;
-    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(f2_bits(a, b)), "l"(f2_bits(hf.x, hf.y)));
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(d), "l"(f2_bits(1024.0f, 1024.0f)));
-    hi = pack_h2(h);
-    lo = pack_h2(__floats2half2_rn(lo_f(r), hi_f(r)));
-}
-
-// Two element-wise RNE FP32 additions: r0 += v0, r1 += v1.
-__device__ __forceinline__ void add2(float& r0, float& r1, uint32_t v0, uint32_t v1)
-{
-    uint64_t s;
-    asm("add.rn.f32x2 %0, %1, %2;"
-        : "=l"(s)
-        : "l"(f2_bits(r0, r1)), "l"(f2_bits(__uint_as_float(v0), __uint_as_float(v1))));
-    r0 = lo_f(s);
-    r1 = hi_f(s);
-}
-
-// Warp-wide: 32 TMEM lanes x 16 consecutive 32-bit columns.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
-
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-
-__device__ __forceinline__ void tmem_st_wait()
-{
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-// D (+)= A * B^T with A (128 x 16 FP16) in tensor memory and B in shared memory.
-__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-// D = A * B^T + D * 2^-10 (accumulator input scaled by 2^-10), A in tensor memory.
-__device__ __forceinline__ void umma_f16_ta_scale10(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, 1, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p, 10;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc)
-        : "memory");
 }
 
 struct Problem {
@@ -2605,27 +2499,6 @@ __global__ void __cluster_dims__(KS, 1, 1) __launch_bounds__(swp::kThreads, 1)
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn()
-{
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-        else
-            (void)cudaGetLastError();
-    });
-    return fn;
-}
-
 // A 2-D row-major tensor (inner extent `inner` contiguous, `outer` rows) as a
 // tensor map with box_inner x box_outer boxes and the 128-byte swizzle.
 bool encode_2d(CUtensorMap* map, CUtensorMapDataType dtype, size_t elem, const void* base, int64_t inner,
@@ -2698,11 +2571,6 @@ int pick_bn(int64_t M, int64_t N, int sms)
     return best;
 }
 
-inline bool aligned16(const void* p)
-{
-    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
-}
-
 template <bool kVec>
 comp_status_t dispatch(int bn, const CUtensorMap& tw, const CUtensorMap& tx, const Problem& P, const DeviceInfo& dev,
                        cudaStream_t s)
@@ -2769,30 +2637,6 @@ comp_status_t launch_gemm_tc(const float* x, const uint16_t* W, float* y, int64_
 }
 
 namespace {
-
-// Launch with programmatic stream serialisation: the kernel's set-up overlaps
-// the end of the previous kernel on the stream; its producer waits
-// (griddepcontrol.wait) before it reads what that kernel wrote.
-template <typename... KArgs, typename... Args>
-comp_status_t launch_pdl(void (*kernel)(KArgs...), int grid, int threads, size_t smem, cudaStream_t stream,
-                         Args&&... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return COMP_ERR_LAUNCH;
-    }
-    return COMP_OK;
-}
 
 // Clusters of KS CTAs of the split-K instance that run at once on the device
 // (the occupancy API's count: clusters must fit inside one GPC, so it can be

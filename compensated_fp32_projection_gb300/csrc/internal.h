@@ -116,6 +116,15 @@ comp_status_t launch_check_wait_timeout(cudaStream_t stream);
 // Reads and clears the fault word of the tensor-core kernels (after the stream
 // has been synchronised).
 comp_status_t read_and_clear_fault(cudaStream_t stream, uint32_t* where);
+// The same of the attention kernels; `where` is written only if there is a fault.
+comp_status_t read_and_clear_attn_fault(cudaStream_t stream, uint32_t* where);
+
+// Packed attention (arguments validated; sizes > 0 but total_k) and the
+// workspace it needs for k and v.
+int64_t attn_stage_bytes(const comp_attn_t& a, int kv_bytes, const void* k, const void* v);
+comp_status_t launch_attn(const comp_attn_t& a, const float* q, const void* k, const void* v, int kv_bytes,
+                          const int32_t* cu_q, const int32_t* cu_k, float* out, float* lse, void* workspace,
+                          const DeviceInfo& dev, cudaStream_t stream);
 
 inline comp_status_t launch_status()
 {

@@ -358,10 +358,12 @@ typedef struct comp_attn {
 
 /*
  * comp_attn_workspace_bytes — the workspace that comp_attn_f32 (kv_bytes 4)
- * or comp_attn_f32x16 (kv_bytes 2) needs for `a`.  0 for a bad argument, or
- * where none is needed.
+ * or comp_attn_f32x16 (kv_bytes 2) needs for `a` with these k and v.  0 for a
+ * bad argument, or where none is needed: FP16 keys and values at 16-byte
+ * aligned addresses with strides of multiples of 8 are read where they are,
+ * others are laid out there first (FP32 ones split into two planes each).
  */
-int64_t comp_attn_workspace_bytes(const comp_attn_t* a, int kv_bytes);
+int64_t comp_attn_workspace_bytes(const comp_attn_t* a, int kv_bytes, const void* k, const void* v);
 
 /*
  * comp_attn_f32x16 — attention of binary32 queries over binary16 keys and

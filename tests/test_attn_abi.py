@@ -49,8 +49,18 @@ def test_attn_pointers(lib):
         assert call(lib, attn(), **bad) == INVALID, bad
     assert call(lib, None) == INVALID
     assert call(lib, attn(total_q=0)) == 0   # nothing to do
-    assert lib.comp_attn_workspace_bytes(attn(head_dim=500), 4) == 0
-    assert lib.comp_attn_workspace_bytes(attn(), 3) == 0
+
+
+def test_attn_workspace(lib):
+    need = lambda a, size, k=MB, v=2 * MB: lib.comp_attn_workspace_bytes(a, size, P(k), P(v))  # noqa: E731
+    assert need(attn(head_dim=500), 4) == 0 and need(attn(), 3) == 0   # bad arguments
+    planes = 12 * 2 * 64 * 2
+    assert need(attn(), 2) == 0
+    assert need(attn(), 2, k=MB + 2) == need(attn(k_token=129), 2) == need(attn(v_head=0), 2) == 2 * planes
+    assert need(attn(), 4) == 4 * planes
+    assert call(lib, attn(), f32=True, ws_bytes=4 * planes - 1) == INVALID
+    assert call(lib, attn(), f32=True, ws=8 * MB + 8) == INVALID
+    assert call(lib, attn(), f32=True, ws=None, ws_bytes=0) == INVALID
 
 
 def cache(**change):
