@@ -1,0 +1,686 @@
+// Attention of single tokens over a paged FP16 cache: each key and value of a
+// sequence is read once for the query heads that share it, 4 D bytes for 4 D
+// operations a head, so the bound is HBM.
+//
+// Tensor cores.  The m16n8k16 product has room for 16 rows; up to eight query
+// heads of a key/value head come in twice, rows 0..7 hi = fp16(x) and rows
+// 8..15 lo.  One product so does both halves of the compensated form, and a
+// thread finds a row's hi sum and lo sum side by side in its own registers:
+//   s = S_hi + 2^-10 S_lo        with q split as in the projections;
+//   O' = O'_hi + O'_lo           with 2^14 p split into hi and lo (no scale on
+//                                lo: see the packed kernel).
+// O' of a tile is added to o = o 2^(m_old - m_new) + O' in FP32 registers, as
+// in the packed kernel.  Memory, not these products, is the bound here, so the
+// older warp-wide instructions serve: tcgen05's 128 rows would be empty.
+//
+// Work.  The tiles of all (sequence, key/value head) rows stand in one line
+// that is cut into equal pieces, one for each CTA: the lengths may differ as
+// they like and no CTA waits for the longest.  A CTA computes its piece row
+// by row; a row that lies wholly in one piece is written to the output, the
+// parts of a row that was cut go to the workspace and are joined by a second
+// launch, in order, as are the parts of a shared prefix (computed for the
+// whole batch by the packed kernel).
+//
+// In a CTA, a warp loads (TMA, one box for each page) and four warps compute:
+// each takes 16 of a tile's 64 keys with its own maximum and sums; they are
+// joined in shared memory at the end of a row.
+#include <cuda_fp16.h>
+
+#include <cmath>
+
+#include "attn.h"
+#include "internal.h"
+#include "ptx.cuh"
+#include "tc_util.cuh"
+
+namespace compfp32 {
+namespace {
+
+constexpr int kTile = 64;       // keys of a tile
+constexpr int kWarps = 4;       // computing warps
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr uint32_t kFaultDecodeLoad = 0xA01;
+constexpr uint32_t kFaultDecodeRows = 0xA02;
+
+// DP: head dimension padded to 64 or 128; NB: blocks of eight query heads.
+template <int DP, int NB>
+struct Cfg {
+    static constexpr int kBoxes = DP / 64;
+    static constexpr uint32_t kPlane = kTile * DP * 2;
+    static constexpr uint32_t kStage = 2 * kPlane;          // k, v
+    static constexpr int NS = DP == 128 ? 3 : 6;            // 96 KB: with NB = 1 two CTAs fit an SM
+    static constexpr uint32_t kJoin = (kWarps - 1) * NB * 8 * DP * 4;
+    static constexpr size_t kSmem = 1024 + NS * kStage + kJoin + 1024;
+};
+
+struct Shared {
+    uint64_t full[6], empty[6];
+    float m[kWarps][16], l[kWarps][16];
+    int abort;
+};
+
+struct Params {
+    const float* q;
+    float* out;
+    float* lse;             // [batch, heads] (nullptr: none)
+    float* part_o;          // [2 * ctas][NB * 8][dim]
+    float* part_lse;        // [2 * ctas][NB * 8]
+    const int32_t* table;
+    const int32_t* lengths;
+    int64_t q_token, q_head;
+    int64_t width, pages;
+    int batch, heads, kv_heads, group, row_blocks, dim, page_size, shared, ctas, vec_q;
+    float scale;
+};
+
+// Tiles of a sequence beyond the shared pages.
+__device__ __forceinline__ int tiles_of(const Params& p, int b, int* own)
+{
+    int64_t n = p.lengths[b];
+    const int64_t most = p.width * p.page_size;
+    n = n < 0 ? 0 : (n > most ? most : n);
+    n -= static_cast<int64_t>(p.shared) * p.page_size;
+    n = n < 0 ? 0 : n;
+    if (own)
+        *own = static_cast<int>(n);
+    return static_cast<int>((n + kTile - 1) / kTile);
+}
+
+// Sum of tiles_of over b in [0, end) by one warp.
+__device__ __forceinline__ int64_t sum_tiles(const Params& p, int end)
+{
+    int64_t n = 0;
+    for (int b = threadIdx.x & 31; b < end; b += 32)
+        n += tiles_of(p, b, nullptr);
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        n += __shfl_xor_sync(0xffffffffu, n, o);
+    return n;
+}
+
+// CTAs that have a piece of the line: each has one tile at least.
+__device__ __forceinline__ int64_t working_ctas(const Params& p, int64_t total)
+{
+    return total < p.ctas ? total : p.ctas;
+}
+
+// The line of tiles: sequence by sequence, within one head unit by head unit
+// (a key/value head and a block of its query heads).  A position in it.
+struct Place {
+    int b, unit, tile;  // tile of the row
+    int tiles, own;     // the row's tiles and keys
+};
+
+// One warp; `at` is below the total.
+__device__ __forceinline__ Place find_place(const Params& p, int64_t at)
+{
+    const int units = p.kv_heads * p.row_blocks, lane = threadIdx.x & 31;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        int own = 0;
+        const int n = b0 + lane < p.batch ? tiles_of(p, b0 + lane, &own) : 0;
+        int64_t x = static_cast<int64_t>(n) * units;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o)
+                x += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, x > at);
+        if (hit) {
+            const int src = __ffs(hit) - 1;
+            const int64_t before = __shfl_sync(0xffffffffu, x, src) -
+                                   static_cast<int64_t>(__shfl_sync(0xffffffffu, n, src)) * units;
+            Place r;
+            r.b = b0 + src;
+            r.tiles = __shfl_sync(0xffffffffu, n, src);
+            r.own = __shfl_sync(0xffffffffu, own, src);
+            r.unit = static_cast<int>((at - before) / r.tiles);
+            r.tile = static_cast<int>((at - before) % r.tiles);
+            return r;
+        }
+        at -= __shfl_sync(0xffffffffu, x, 31);
+    }
+    return Place{p.batch, 0, 0, 0, 0};
+}
+
+// The next row with tiles after r's.
+__device__ __forceinline__ void next_row(const Params& p, Place& r)
+{
+    r.tile = 0;
+    if (++r.unit < p.kv_heads * p.row_blocks)
+        return;
+    r.unit = 0;
+    do {
+        ++r.b;
+        r.tiles = r.b < p.batch ? tiles_of(p, r.b, &r.own) : 0;
+    } while (r.tiles == 0 && r.b < p.batch);
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// c += a b: a 16 x 16, b 16 x 8, FP16 in, FP32 sums.
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int DP, int NB>
+__global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
+    attn_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                       const Params p)
+{
+    using C = Cfg<DP, NB>;
+    constexpr int NS = C::NS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* const stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float* const join = reinterpret_cast<float*>(stages + NS * C::kStage);
+    Shared* const sm = reinterpret_cast<Shared*>(stages + NS * C::kStage + C::kJoin);
+    static_assert(sizeof(Shared) <= 1024, "shared area");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&sm->full[i], 1);
+            mbar_init(&sm->empty[i], kWarps);
+        }
+        sm->abort = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    grid_dependency_wait();
+
+    const int64_t total = sum_tiles(p, p.batch) * p.kv_heads * p.row_blocks;
+    const int64_t ctas = working_ctas(p, total);
+    if (blockIdx.x >= ctas)
+        return;
+    const int64_t begin = total * blockIdx.x / ctas, end = total * (blockIdx.x + 1) / ctas;
+    Place r = find_place(p, begin);
+
+    if (warp == kWarps) {
+        // ---------------- loads
+        const int box_rows = p.page_size < kTile ? p.page_size : kTile;
+        const int pieces = kTile / box_rows, boxes = 2 * C::kBoxes * pieces;
+        int i = 0;
+        bool ok = true;
+        for (int64_t at = begin; ok && at < end; ++at, ++i) {
+            const int s = i % NS;
+            if (i >= NS && !attn_warp_wait(&sm->empty[s], ((i / NS) - 1) & 1, &sm->abort, kFaultDecodeLoad)) {
+                ok = false;
+                break;
+            }
+            if (lane == 0)
+                mbar_arrive_expect_tx(&sm->full[s], C::kStage);
+            __syncwarp();
+            const int head = r.unit / p.row_blocks;
+            for (int b = lane; b < boxes; b += 32) {
+                const int piece = b % pieces, box = b / pieces % C::kBoxes, is_v = b / pieces / C::kBoxes;
+                // r.tile < tiles: the first key of a piece may lie past the length, not past the row's last tile
+                const int64_t key = static_cast<int64_t>(p.shared) * p.page_size + static_cast<int64_t>(r.tile) * kTile +
+                                    piece * box_rows;
+                const int64_t col = key / p.page_size;
+                const int page = col < p.width ? p.table[r.b * p.width + col] : -1;
+                // a page that is not there: a place beyond the cache, which reads zeros
+                tma_load_3d(stages + s * C::kStage + is_v * C::kPlane + box * (kTile * 128) + piece * box_rows * 128,
+                            is_v ? &map_v : &map_k, &sm->full[s], box * 64, static_cast<int>(key % p.page_size),
+                            static_cast<int>((page >= 0 && page < p.pages ? page : p.pages) * p.kv_heads + head));
+            }
+            __syncwarp();
+            if (++r.tile == r.tiles)
+                next_row(p, r);
+        }
+        if (!ok)
+            for (int j = i - NS > 0 ? i - NS : 0; j < i; ++j)
+                attn_drain_wait(&sm->full[j % NS], (j / NS) & 1);
+    } else {
+        // ---------------- rows
+        const int g = lane >> 2, quad = lane & 3;
+        const float c2 = p.scale * kAttnLog2E;
+        bool ok = true;
+        int i = 0, fragment = 0;
+        for (int64_t at = begin; at < end; ++fragment) {
+            const int n = static_cast<int>(r.tiles - r.tile < end - at ? r.tiles - r.tile : end - at);
+            const int head = r.unit / p.row_blocks, first_head = r.unit % p.row_blocks * (NB * 8);
+            // the query heads' values, split: rows 0..7 hi, 8..15 lo
+            uint32_t q[NB][DP / 16][4];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                const int hg = first_head + nb * 8 + g;
+                const float* const src = p.q + r.b * p.q_token + (head * p.group + hg) * p.q_head;
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int d = k * 16 + e * 8 + quad * 2;
+                        float2 x = make_float2(0.0f, 0.0f);
+                        if (hg < p.group) {
+                            if (p.vec_q && d + 2 <= p.dim) {
+                                x = __ldg(reinterpret_cast<const float2*>(src + d));
+                            } else {
+                                x.x = d < p.dim ? __ldg(src + d) : 0.0f;
+                                x.y = d + 1 < p.dim ? __ldg(src + d + 1) : 0.0f;
+                            }
+                        }
+                        split2(x.x, x.y, q[nb][k][2 * e], q[nb][k][2 * e + 1]);
+                    }
+            }
+            float m[NB];
+            uint64_t l2[NB], o[NB][DP / 8];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                m[nb] = -INFINITY;
+                l2[nb] = 0;
+#pragma unroll
+                for (int t = 0; t < DP / 8; ++t)
+                    o[nb][t] = 0;
+            }
+            for (int t = 0; t < n; ++t, ++i) {
+                const int s = i % NS;
+                ok = ok && attn_warp_wait(&sm->full[s], (i / NS) & 1, &sm->abort, kFaultDecodeRows);
+                if (!ok)
+                    continue;  // the joins below still take place, so that no warp waits for another
+                uint8_t* const kt = stages + s * C::kStage;
+                uint8_t* const vt = kt + C::kPlane;
+                const int left = r.own - (r.tile + t) * kTile - warp * 16;  // keys of this warp's 16 that count
+                if (left > 0) {
+                    if (left < 16) {
+                        // beyond the sequence's end v may hold anything: 0 times that must be 0
+#pragma unroll
+                        for (int x = 0; x < C::kBoxes; ++x)
+                            for (int u = lane; u < 16 * 8; u += 32)
+                                if (u / 8 >= left)
+                                    *reinterpret_cast<uint4*>(vt + x * (kTile * 128) + (warp * 16 + u / 8) * 128 +
+                                                              u % 8 * 16) = make_uint4(0, 0, 0, 0);
+                        __syncwarp();
+                    }
+                    float c[NB][2][4] = {};
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt) {
+                        const uint32_t row = warp * 16 + nt * 8 + (lane & 7);
+#pragma unroll
+                        for (int k = 0; k < DP / 16; k += 2) {
+                            uint32_t b[4];
+                            ldmatrix4(smem_u32(kt) + (k / 4) * (kTile * 128) + sw128(row, (k % 4) * 2 + (lane >> 3)), b);
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb) {
+                                mma16816(c[nb][nt], q[nb][k], b[0], b[1]);
+                                mma16816(c[nb][nt], q[nb][k + 1], b[2], b[3]);
+                            }
+                        }
+                    }
+                    uint32_t pa[NB][4];
+                    uint64_t a2[NB];
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        float x[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = (e >> 1) * 8 + quad * 2 + (e & 1);
+                            x[e] = fmaf(c[nb][e >> 1][2 + (e & 1)], 0x1p-10f, c[nb][e >> 1][e & 1]);
+                            x[e] = key < left ? x[e] : -INFINITY;
+                        }
+                        float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * c2;
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                        const float m_new = fmaxf(m[nb], top), shift = m_new == -INFINITY ? 0.0f : m_new;
+                        const float alpha = ex2(m[nb] - shift);
+                        m[nb] = m_new;
+                        a2[nb] = f2_bits(alpha, alpha);
+                        uint64_t e2[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            e2[e] = mul2(f2_bits(ex2(fmaf(x[2 * e], c2, -shift)),
+                                                      ex2(fmaf(x[2 * e + 1], c2, -shift))),
+                                              f2_bits(kAttnPScale, kAttnPScale));
+                            split_p(e2[e], pa[nb][2 * e], pa[nb][2 * e + 1]);
+                        }
+                        l2[nb] = fma2(l2[nb], a2[nb], add2(e2[0], e2[1]));
+                    }
+#pragma unroll
+                    for (int d = 0; d < DP / 16; ++d) {
+                        uint32_t b[4];
+                        const uint32_t row = warp * 16 + (lane & 15);
+                        ldmatrix4_trans(smem_u32(vt) + (d / 4) * (kTile * 128) + sw128(row, (d % 4) * 2 + (lane >> 4)), b);
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float y[4] = {};
+                                mma16816(y, pa[nb], b[2 * e], b[2 * e + 1]);
+                                o[nb][2 * d + e] = fma2(o[nb][2 * d + e], a2[nb],
+                                                             add2(f2_bits(y[0], y[1]), f2_bits(y[2], y[3])));
+                            }
+                    }
+                    if (left < 16)
+                        fence_proxy_async_smem();  // the zeros, before the next load into this stage
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sm->empty[s]);
+            }
+
+            // join the four warps' sums of this row
+            float l[NB];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                l[nb] = lo_f(l2[nb]) + hi_f(l2[nb]);
+                l[nb] += __shfl_xor_sync(0xffffffffu, l[nb], 1);
+                l[nb] += __shfl_xor_sync(0xffffffffu, l[nb], 2);
+            }
+            asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");  // warp 0 has read the last row's
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                if (quad == 0) {
+                    sm->m[warp][nb * 8 + g] = m[nb];
+                    sm->l[warp][nb * 8 + g] = l[nb];
+                }
+                if (warp > 0) {
+                    float* const to = join + (((warp - 1) * NB + nb) * 8 + g) * DP + quad * 2;
+#pragma unroll
+                    for (int t = 0; t < DP / 8; ++t)
+                        *reinterpret_cast<uint64_t*>(to + t * 8) = o[nb][t];
+                }
+            }
+            asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+            if (warp == 0 && ok) {
+                const bool whole = n == r.tiles;
+                const int64_t slot = 2 * blockIdx.x + (fragment > 0 ? 1 : 0);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    const int row = nb * 8 + g, hg = first_head + row;
+                    float top = m[nb];
+#pragma unroll
+                    for (int w = 1; w < kWarps; ++w)
+                        top = fmaxf(top, sm->m[w][row]);
+                    const float shift = top == -INFINITY ? 0.0f : top;
+                    const float w0 = ex2(m[nb] - shift);
+                    float sum = l[nb] * w0;
+                    uint64_t f = f2_bits(w0, w0);
+#pragma unroll
+                    for (int t = 0; t < DP / 8; ++t)
+                        o[nb][t] = mul2(o[nb][t], f);
+#pragma unroll
+                    for (int w = 1; w < kWarps; ++w) {
+                        const float wf = ex2(sm->m[w][row] - shift);
+                        sum = fmaf(sm->l[w][row], wf, sum);
+                        f = f2_bits(wf, wf);
+                        const float* const from = join + (((w - 1) * NB + nb) * 8 + g) * DP + quad * 2;
+#pragma unroll
+                        for (int t = 0; t < DP / 8; ++t)
+                            o[nb][t] = fma2(*reinterpret_cast<const uint64_t*>(from + t * 8), f, o[nb][t]);
+                    }
+                    if (hg >= p.group)
+                        continue;
+                    const int64_t at_row = static_cast<int64_t>(r.b) * p.heads + head * p.group + hg;
+                    float* const to = whole ? p.out + at_row * p.dim : p.part_o + (slot * (NB * 8) + row) * p.dim;
+                    const float lsum = sum * (1.0f / kAttnPScale);
+                    const float norm = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+                    for (int t = 0; t < DP / 8; ++t) {
+                        const int d = t * 8 + quad * 2;  // the head dimension is a multiple of 8
+                        if (t * 8 < p.dim)
+                            *reinterpret_cast<float2*>(to + d) = make_float2(lo_f(o[nb][t]) * norm, hi_f(o[nb][t]) * norm);
+                    }
+                    const float lse = sum == 0.0f ? -INFINITY : fmaf(top, kAttnLn2, logf(lsum));
+                    if (quad == 0) {
+                        if (!whole)
+                            p.part_lse[slot * (NB * 8) + row] = lse;
+                        else if (p.lse)
+                            p.lse[at_row] = lse;
+                    }
+                }
+            }
+            at += n;
+            r.tile += n - 1;  // next_row begins at the row's last tile
+            next_row(p, r);
+        }
+    }
+}
+
+// The parts of each row joined: the prefix's (splits of them), then those of
+// the sequence's own keys, in order.  One warp for each row, four values of
+// the head dimension a lane.
+struct Join {
+    const float* pre_o;     // [splits][batch * heads][dim]
+    const float* pre_lse;   // [splits][batch * heads]
+    float* lse_out;         // the caller's (nullptr: none)
+    int splits, rows_a_unit;
+};
+
+__global__ void __launch_bounds__(256) attn_join_kernel(Params p, Join x)
+{
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int64_t rows = static_cast<int64_t>(p.batch) * p.heads;
+    if (row >= rows)
+        return;
+    const int b = static_cast<int>(row / p.heads), h = static_cast<int>(row % p.heads);
+    const int head = h / p.group, block = h % p.group / x.rows_a_unit, in_block = h % p.group % x.rows_a_unit;
+    const int units = p.kv_heads * p.row_blocks;
+    int own;
+    const int tiles = tiles_of(p, b, &own);
+    // the CTAs that have this row's tiles
+    int64_t c0 = 0, c1 = -1, total = 0;
+    bool whole = false;
+    if (tiles > 0) {
+        total = sum_tiles(p, p.batch) * units;
+        const int64_t t0 = sum_tiles(p, b) * units + (head * p.row_blocks + block) * static_cast<int64_t>(tiles);
+        const int64_t ctas = working_ctas(p, total);
+        // the last CTA whose piece begins at or before a tile
+        c0 = ((t0 + 1) * ctas - 1) / total;
+        c1 = ((t0 + tiles) * ctas - 1) / total;
+        whole = c0 == c1;
+        if (whole && x.splits == 0)
+            return;  // the output is there
+        // the first part is its CTA's second one if that CTA begins before it
+        c0 = 2 * c0 + (total * c0 / ctas < t0 ? 1 : 0);
+        c1 = 2 * c1;
+        if (c1 < c0)
+            c1 = c0;
+    }
+    const int parts = x.splits + (tiles == 0 ? 0 : (whole ? 1 : static_cast<int>((c1 - c0 + 1) / 2) + 1));
+    // slots of a row's parts: c0, then 2 (c0 / 2 + 1), 2 (c0 / 2 + 2), ...
+    auto find = [&](int i, const float*& o) {
+        if (i < x.splits) {
+            o = x.pre_o + (static_cast<int64_t>(i) * rows + row) * p.dim;
+            return x.pre_lse[static_cast<int64_t>(i) * rows + row];
+        }
+        if (whole) {
+            o = p.out + row * p.dim;
+            return p.lse[row];
+        }
+        const int64_t slot = i == x.splits ? c0 : 2 * (c0 / 2 + i - x.splits);
+        o = p.part_o + (slot * x.rows_a_unit + in_block) * p.dim;
+        return p.part_lse[slot * x.rows_a_unit + in_block];
+    };
+    float top = -INFINITY;
+    for (int i = lane; i < parts; i += 32) {
+        const float* o;
+        const float y = find(i, o);
+        top = isnan(y) ? y : fmaxf(top, y);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float shift = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f, acc[4] = {};
+    for (int i = 0; i < parts; ++i) {
+        const float* o;
+        const float y = find(i, o);
+        if (y == -INFINITY)
+            continue;  // sees nothing there
+        const float w = expf(y - shift);
+        sum += w;
+        if (lane * 4 < p.dim) {
+            const float4 v = *reinterpret_cast<const float4*>(o + lane * 4);
+            acc[0] = fmaf(v.x, w, acc[0]);
+            acc[1] = fmaf(v.y, w, acc[1]);
+            acc[2] = fmaf(v.z, w, acc[2]);
+            acc[3] = fmaf(v.w, w, acc[3]);
+        }
+    }
+    const float norm = sum == 0.0f ? 0.0f : 1.0f / sum;
+    if (lane * 4 < p.dim)
+        *reinterpret_cast<float4*>(p.out + row * p.dim + lane * 4) =
+            make_float4(acc[0] * norm, acc[1] * norm, acc[2] * norm, acc[3] * norm);
+    if (x.lse_out && lane == 0)
+        x.lse_out[row] = sum == 0.0f ? -INFINITY : shift + logf(sum);
+}
+
+template <int DP, int NB>
+comp_status_t launch_t(const CUtensorMap& mk, const CUtensorMap& mv, const Params& p, const DeviceInfo& dev,
+                       cudaStream_t stream)
+{
+    using C = Cfg<DP, NB>;
+    static std::mutex mu;
+    static bool done[64] = {};
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (dev.device < 0 || dev.device >= 64)
+            return COMP_ERR_CUDA;
+        if (!done[dev.device]) {
+            if (cudaFuncSetAttribute(attn_decode_kernel<DP, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     static_cast<int>(C::kSmem)) != cudaSuccess) {
+                (void)cudaGetLastError();
+                return COMP_ERR_CUDA;
+            }
+            done[dev.device] = true;
+        }
+    }
+    return launch_pdl(attn_decode_kernel<DP, NB>, p.ctas, kThreads, C::kSmem, stream, mk, mv, p);
+}
+
+// CTAs of the line of tiles: two an SM.  The workspace's size must not depend
+// on the device, so their number is bounded.
+constexpr int kMostCtas = 320;
+
+// Parts that the shared pages' keys are split into, so that about one wave of
+// the packed kernel's CTAs works on them; a part has at least four tiles of
+// 128 keys.
+int prefix_splits(int64_t keys, int64_t batch, int heads, int kv_heads, int sms)
+{
+    const int64_t tiles = (keys + 127) / 128;
+    const int64_t ctas = (batch * (heads / kv_heads) + 255) / 256 * kv_heads;
+    int64_t n = sms / ctas;
+    n = n > tiles / 4 ? tiles / 4 : n;
+    return static_cast<int>(n < 1 ? 1 : n);
+}
+
+constexpr int kMostSms = 160;
+
+// Floats of the workspace: parts of rows, the prefix's parts, the rows' lse.
+struct Layout {
+    int64_t part_o, part_lse, pre_o, pre_lse, lse, total;
+};
+
+Layout layout_of(const comp_kv_cache_t& c, int64_t batch, int heads, int splits)
+{
+    const int group = heads / c.kv_heads;
+    const int64_t slots = 2 * kMostCtas * (group > 8 ? 16 : 8), rows = batch * heads;
+    Layout l;
+    l.part_o = 0;
+    l.part_lse = l.part_o + slots * c.head_dim;
+    l.lse = l.part_lse + slots;
+    l.pre_lse = l.lse + (rows + 3) / 4 * 4;
+    l.pre_o = l.pre_lse + (splits * rows + 3) / 4 * 4;
+    l.total = l.pre_o + splits * rows * c.head_dim;
+    return l;
+}
+
+// Sharing pays from two sequences on.
+int64_t effective_shared(int64_t batch, int64_t shared_pages)
+{
+    return batch > 1 ? shared_pages : 0;
+}
+
+}  // namespace
+
+int64_t attn_decode_bytes(const comp_kv_cache_t& cache, int64_t batch, int heads, int64_t shared_pages)
+{
+    const int64_t shared = effective_shared(batch, shared_pages);
+    const int splits = shared > 0 ? prefix_splits(shared * cache.page_size, batch, heads, cache.kv_heads, kMostSms) : 0;
+    return 4 * layout_of(cache, batch, heads, splits).total;
+}
+
+comp_status_t launch_attn_decode(const comp_kv_cache_t& cache, const float* q, int64_t q_token, int64_t q_head,
+                                 int heads, float scale, const int32_t* table, int64_t batch, int64_t width,
+                                 const int32_t* lengths, int64_t shared_pages, float* out, float* lse,
+                                 void* workspace, const DeviceInfo& dev, cudaStream_t stream)
+{
+    const int64_t shared = effective_shared(batch, shared_pages);
+    const int group = heads / cache.kv_heads;
+    const int splits = shared > 0 ? prefix_splits(shared * cache.page_size, batch, heads, cache.kv_heads,
+                                                  dev.sm_count < kMostSms ? dev.sm_count : kMostSms)
+                                  : 0;
+    const Layout at = layout_of(cache, batch, heads, splits);
+    float* const ws = static_cast<float*>(workspace);
+    if (splits > 0) {
+        const comp_status_t st = launch_attn_prefix(cache, q, q_token, q_head, heads, scale, table, batch, lengths,
+                                                    shared, splits, ws + at.pre_o, ws + at.pre_lse, dev, stream);
+        if (st != COMP_OK)
+            return st;
+    }
+    const int nb = group > 8 ? 2 : 1;
+    Params p{};
+    p.q = q;
+    p.out = out;
+    p.lse = splits > 0 ? ws + at.lse : lse;
+    p.part_o = ws + at.part_o;
+    p.part_lse = ws + at.part_lse;
+    p.table = table;
+    p.lengths = lengths;
+    p.q_token = q_token;
+    p.q_head = q_head;
+    p.width = width;
+    p.pages = cache.pages;
+    p.batch = static_cast<int>(batch);
+    p.heads = heads;
+    p.kv_heads = cache.kv_heads;
+    p.group = group;
+    p.row_blocks = (group + 8 * nb - 1) / (8 * nb);
+    p.dim = cache.head_dim;
+    p.page_size = cache.page_size;
+    p.shared = static_cast<int>(shared);
+    p.ctas = 2 * dev.sm_count < kMostCtas ? 2 * dev.sm_count : kMostCtas;
+    p.vec_q = (reinterpret_cast<uintptr_t>(q) & 7u) == 0 && q_token % 2 == 0 && q_head % 2 == 0;
+    p.scale = scale;
+    CUtensorMap mk{}, mv{};
+    if (width > 0) {  // otherwise there are no tiles
+        const int box = cache.page_size < kTile ? cache.page_size : kTile;
+        if (!encode_pages(&mk, cache.k, cache, box) || !encode_pages(&mv, cache.v, cache, box))
+            return COMP_ERR_CUDA;
+    }
+    comp_status_t st;
+    if (cache.head_dim <= 64)
+        st = nb == 1 ? launch_t<64, 1>(mk, mv, p, dev, stream) : launch_t<64, 2>(mk, mv, p, dev, stream);
+    else
+        st = nb == 1 ? launch_t<128, 1>(mk, mv, p, dev, stream) : launch_t<128, 2>(mk, mv, p, dev, stream);
+    if (st != COMP_OK)
+        return st;
+    const Join x{ws + at.pre_o, ws + at.pre_lse, lse, splits, 8 * nb};
+    return launch_pdl(attn_join_kernel, static_cast<int>((batch * heads + 7) / 8), 256, 0, stream, p, x);
+}
+
+comp_status_t read_and_clear_decode_fault(cudaStream_t stream, uint32_t* where)
+{
+    return read_and_clear_word(&g_attn_fault_word, stream, where);
+}
+
+}  // namespace compfp32

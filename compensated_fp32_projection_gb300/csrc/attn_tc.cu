@@ -43,6 +43,7 @@
 
 #include <cmath>
 
+#include "attn.h"
 #include "internal.h"
 #include "ptx.cuh"
 #include "tc_util.cuh"
@@ -57,18 +58,12 @@ constexpr int kThreads = 384;
 constexpr int kCtrlRegs = 40;
 constexpr int kRowRegs = 232;
 static_assert(128 * kCtrlRegs + 256 * kRowRegs <= kThreads * 168, "register split");
-constexpr long long kWaitLimit = 1ll << 31;  // cycles (about a second)
-constexpr float kLog2E = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kPScale = 16384.0f;  // 2^14
 
 // Fault codes of the waits.
 constexpr uint32_t kFaultAttnLoad = 0x901;
 constexpr uint32_t kFaultAttnMma = 0x902;
 constexpr uint32_t kFaultAttnValues = 0x903;
 constexpr uint32_t kFaultAttnRows = 0x904;
-
-__device__ uint32_t g_attn_fault_word;
 
 // DP: the head dimension padded to 64 or 128.  PL: planes of k and v, 1 (FP16)
 // or 2 (FP32, split).
@@ -127,87 +122,9 @@ struct Params {
     float scale;
 };
 
-__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, int* abort_flag, uint32_t code)
-{
-    if (mbar_try_wait(bar, parity))
-        return true;
-    const long long start = clock64();
-    while (true) {
-        if (mbar_try_wait_sleep(bar, parity, 20000))
-            return true;
-        if (*reinterpret_cast<volatile int*>(abort_flag))
-            return false;
-        if (clock64() - start > kWaitLimit) {
-            atomicCAS(&g_attn_fault_word, 0u, code);
-            *reinterpret_cast<volatile int*>(abort_flag) = 1;
-            return false;
-        }
-    }
-}
-
-// Warp-wide: lane 0 waits, and on success every lane observes the phase itself.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort_flag, uint32_t code)
-{
-    bool ok = true;
-    if ((threadIdx.x & 31) == 0)
-        ok = wait_bounded(bar, parity, abort_flag, code);
-    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-    if (ok)
-        (void)mbar_try_wait(bar, parity);
-    return ok;
-}
-
-// Wait for what was issued before the CTA exits after an abort.
-__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity)
-{
-    const long long start = clock64();
-    while (!mbar_try_wait(bar, parity) && clock64() - start < kWaitLimit) {
-    }
-}
-
 __device__ __forceinline__ int clampi(int x, int lo, int hi)
 {
     return x < lo ? lo : (x > hi ? hi : x);
-}
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
-__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
-__device__ __forceinline__ uint64_t u2_bits(uint32_t a, uint32_t b)
-{
-    return static_cast<uint64_t>(a) | (static_cast<uint64_t>(b) << 32);
 }
 
 // This CTA's sequence and block of 256 rows: blocks are numbered sequence by
@@ -358,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int i = 0;
             for (; i < 2 * n; ++i) {
                 const int s = i % NS;
-                if (i >= NS && !warp_wait(&sm->empty[s], ((i / NS) - 1) & 1, &sm->abort, kFaultAttnLoad))
+                if (i >= NS && !attn_warp_wait(&sm->empty[s], ((i / NS) - 1) & 1, &sm->abort, kFaultAttnLoad))
                     break;
                 if (lane == 0)
                     mbar_arrive_expect_tx(&sm->full[s], C::kStage);
@@ -383,14 +300,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (i < 2 * n) {  // abort: what was issued lands before the CTA leaves
                 for (int j = max(0, i - NS); j < i; ++j)
-                    drain_wait(&sm->full[j % NS], (j / NS) & 1);
+                    attn_drain_wait(&sm->full[j % NS], (j / NS) & 1);
             }
         } else if (warp == 1) {
             // ---------------- products
             const uint32_t leader = lane == 0;
             bool ok = true;
             auto wait = [&](uint64_t* bar, int phase) {
-                ok = ok && warp_wait(bar, phase & 1, &sm->abort, kFaultAttnMma);
+                ok = ok && attn_warp_wait(bar, phase & 1, &sm->abort, kFaultAttnMma);
                 tc_fence_after();
                 return ok;
             };
@@ -475,13 +392,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) {
                 umma_commit_by(leader, &sm->drain);
-                drain_wait(&sm->drain, 0);
+                attn_drain_wait(&sm->drain, 0);
             }
         } else {
             // ---------------- values that must not count
             for (int i = 0; i < 2 * n; ++i) {
                 const int s = i % NS, j = i >> 1;
-                if (!warp_wait(&sm->full[s], (i / NS) & 1, &sm->abort, kFaultAttnValues))
+                if (!attn_warp_wait(&sm->full[s], (i / NS) & 1, &sm->abort, kFaultAttnValues))
                     break;
                 if ((i & 1) && j >= edge) {
                     uint8_t* const tile = stages + s * C::kStage;
@@ -562,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&sm->qfull[half]);
         }
 
-        const float c2 = p.scale * kLog2E;
+        const float c2 = p.scale * kAttnLog2E;
         const uint64_t c22 = f2_bits(c2, c2);
         const uint32_t st = tmem + lanes + half * 128;
         const int row_lim = valid ? lim : INT32_MAX;  // rows that are not there are not stored
@@ -577,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // o = o alpha + O' of tile j
         auto take = [&](int j) {
             const int b = half * OB + (OB == 2 ? (j & 1) : 0);
-            if (!warp_wait(&sm->ofull[b], (j / OB) & 1, &sm->abort, kFaultAttnRows))
+            if (!attn_warp_wait(&sm->ofull[b], (j / OB) & 1, &sm->abort, kFaultAttnRows))
                 return false;
             tc_fence_after();
             const uint64_t a2 = f2_bits(alpha, alpha);
@@ -599,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
 
         for (int j = 0; j < nh; ++j) {
-            if (!warp_wait(&sm->sfull[half], j & 1, &sm->abort, kFaultAttnRows)) {
+            if (!attn_warp_wait(&sm->sfull[half], j & 1, &sm->abort, kFaultAttnRows)) {
                 ok = false;
                 break;
             }
@@ -627,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float alpha_new = ex2(m - shift);
             m = m_new;
             l2 = mul2(l2, f2_bits(alpha_new, alpha_new));
-            const uint64_t s2 = f2_bits(-shift, -shift), k2 = f2_bits(kPScale, kPScale);
+            const uint64_t s2 = f2_bits(-shift, -shift), k2 = f2_bits(kAttnPScale, kAttnPScale);
             uint32_t r[2][16];
             tmem_ld16(st, r[0]);
 #pragma unroll
@@ -647,11 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint64_t y = fma2(u2_bits(x[2 * i], x[2 * i + 1]), c22, s2);
                     const uint64_t e = mul2(f2_bits(ex2(lo_f(y)), ex2(hi_f(y))), k2);
                     l2 = add2(l2, e);
-                    const __half2 h = __floats2half2_rn(lo_f(e), hi_f(e));
-                    const float2 hf = __half22float2(h);
-                    const uint64_t rest = sub2(e, f2_bits(hf.x, hf.y));
-                    out[i] = pack_h2(h);
-                    out[8 + i] = pack_h2(__floats2half2_rn(lo_f(rest), hi_f(rest)));
+                    split_p(e, out[i], out[8 + i]);
                 }
                 tmem_st16(st + c * 16, out);
             }
@@ -669,9 +582,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && nh > 0)
             ok = take(nh - 1);
         if (ok && valid) {
-            const float l = (lo_f(l2) + hi_f(l2)) * (1.0f / kPScale);
+            const float l = (lo_f(l2) + hi_f(l2)) * (1.0f / kAttnPScale);
             // no key seen, or none that counts beside an infinite score (NaN stays NaN)
-            const float norm = l == 0.0f ? 0.0f : (1.0f / kPScale) / l;
+            const float norm = l == 0.0f ? 0.0f : (1.0f / kAttnPScale) / l;
             float* const out = p.out + out_at;
 #pragma unroll
             for (int d = 0; d < DP; d += 4) {
@@ -691,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (p.lse)
-                p.lse[lse_at] = l == 0.0f ? -INFINITY : fmaf(m, kLn2, logf(l));
+                p.lse[lse_at] = l == 0.0f ? -INFINITY : fmaf(m, kAttnLn2, logf(l));
             // values that are not finite were taken out of the tiles from
             // `edge` on: a row that sees one adds it (its weight is positive)
             if (*reinterpret_cast<volatile int*>(&sm->hurt)) {
@@ -777,25 +690,6 @@ __global__ void __launch_bounds__(256) attn_stage_kernel(Stage p)
             *reinterpret_cast<uint4*>(p.hi[w] + to) = make_uint4(x[0], x[1], x[2], x[3]);
         }
     }
-}
-
-// [heads][rows][dim] FP16 as boxes of box_rows x 64.  A dimension of extent 1
-// may have any stride.
-bool encode_kv(CUtensorMap* map, const void* base, int64_t dim, int64_t rows, int64_t heads, int64_t row_stride,
-               int64_t head_stride, int box_rows)
-{
-    EncodeTiledFn fn = encode_fn();
-    if (!fn)
-        return false;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(rows),
-                                static_cast<cuuint64_t>(heads)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(rows > 1 ? row_stride * 2 : 256),
-                                   static_cast<cuuint64_t>(heads > 1 ? head_stride * 2 : 256)};
-    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Whether a tensor map can describe [tokens, heads] rows with these strides.
@@ -908,7 +802,7 @@ comp_status_t launch_attn(const comp_attn_t& a, const float* q, const void* k, c
             dim = dpad;
         }
         for (int i = 0; i < (kv_bytes == 4 ? 4 : 2); ++i)
-            if (!encode_kv(&maps[i], planes[i], dim, a.total_k, a.kv_heads, token[i % 2], head[i % 2], box_rows))
+            if (!encode_rows(&maps[i], planes[i], dim, a.total_k, a.kv_heads, token[i % 2], head[i % 2], box_rows))
                 return COMP_ERR_CUDA;
     }
     const int64_t rows = a.total_q * p.group;
@@ -920,21 +814,52 @@ comp_status_t launch_attn(const comp_attn_t& a, const float* q, const void* k, c
     return kv_bytes == 4 ? launch_t<128, 2>(maps, p, grid, dev, stream) : launch_t<128, 1>(maps, p, grid, dev, stream);
 }
 
+comp_status_t launch_attn_prefix(const comp_kv_cache_t& cache, const float* q, int64_t q_token, int64_t q_head,
+                                 int heads, float scale, const int32_t* table, int64_t batch, const int32_t* lengths,
+                                 int64_t shared, int splits, float* out, float* lse, const DeviceInfo& dev,
+                                 cudaStream_t stream)
+{
+    Params p{};
+    p.q = q;
+    p.out = out;
+    p.lse = lse;
+    p.v = cache.v;
+    p.table = table;
+    p.lengths = lengths;
+    p.q_token = q_token;
+    p.q_head = q_head;
+    p.out_token = static_cast<int64_t>(heads) * cache.head_dim;
+    p.out_head = cache.head_dim;
+    p.lse_split = batch * heads;
+    p.out_split = p.lse_split * cache.head_dim;
+    p.n_seq = 1;
+    p.total_q = static_cast<int>(batch);
+    p.total_k = static_cast<int>(shared * cache.page_size);
+    p.kv_heads = cache.kv_heads;
+    p.group = heads / cache.kv_heads;
+    p.dim = cache.head_dim;
+    p.splits = splits;
+    p.page_size = cache.page_size;
+    p.table_pages = static_cast<int>(shared);
+    p.pages = static_cast<int>(cache.pages);
+    p.scale = scale;
+    const int lane_values = cache.head_dim <= 64 ? 2 : 4;
+    p.vec_q = q_token % lane_values == 0 && q_head % lane_values == 0 && aligned16(q);
+    p.vec_out = 1;
+    CUtensorMap maps[4] = {};
+    if (!encode_pages(&maps[0], cache.k, cache, cache.page_size) ||
+        !encode_pages(&maps[1], cache.v, cache, cache.page_size))
+        return COMP_ERR_CUDA;
+    const int64_t grid = (batch * p.group + 255) / 256 * cache.kv_heads * splits;
+    if (grid > INT32_MAX)
+        return COMP_ERR_INVALID_VALUE;
+    return cache.head_dim <= 64 ? launch_t<64, 1>(maps, p, grid, dev, stream)
+                                : launch_t<128, 1>(maps, p, grid, dev, stream);
+}
+
 comp_status_t read_and_clear_attn_fault(cudaStream_t stream, uint32_t* where)
 {
-    uint32_t word = 0;
-    const uint32_t zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&word, g_attn_fault_word, sizeof(word), 0, cudaMemcpyDeviceToHost, stream) !=
-            cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_attn_fault_word, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, stream) !=
-            cudaSuccess ||
-        cudaStreamSynchronize(stream) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return COMP_ERR_CUDA;
-    }
-    if (word != 0 && where)
-        *where = word;
-    return word == 0 ? COMP_OK : COMP_ERR_TIMEOUT;
+    return read_and_clear_word(&g_attn_fault_word, stream, where);
 }
 
 }  // namespace compfp32

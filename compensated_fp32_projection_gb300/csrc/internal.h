@@ -110,6 +110,13 @@ comp_status_t launch_gemm_f16x2(const uint16_t* hi, const uint16_t* lo, const ui
 // k (and of its v).
 bool kv_cache_ok(const comp_kv_cache_t* cache, int64_t* bytes);
 
+// Attention of single tokens over a cache (arguments validated; batch > 0).
+int64_t attn_decode_bytes(const comp_kv_cache_t& cache, int64_t batch, int heads, int64_t shared_pages);
+comp_status_t launch_attn_decode(const comp_kv_cache_t& cache, const float* q, int64_t q_token, int64_t q_head,
+                                 int heads, float scale, const int32_t* table, int64_t batch, int64_t width,
+                                 const int32_t* lengths, int64_t shared_pages, float* out, float* lse,
+                                 void* workspace, const DeviceInfo& dev, cudaStream_t stream);
+
 // One thread runs a bounded wait that cannot succeed (comp_check_wait_timeout).
 comp_status_t launch_check_wait_timeout(cudaStream_t stream);
 
@@ -118,6 +125,7 @@ comp_status_t launch_check_wait_timeout(cudaStream_t stream);
 comp_status_t read_and_clear_fault(cudaStream_t stream, uint32_t* where);
 // The same of the attention kernels; `where` is written only if there is a fault.
 comp_status_t read_and_clear_attn_fault(cudaStream_t stream, uint32_t* where);
+comp_status_t read_and_clear_decode_fault(cudaStream_t stream, uint32_t* where);
 
 // Packed attention (arguments validated; sizes > 0 but total_k) and the
 // workspace it needs for k and v.

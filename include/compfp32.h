@@ -425,7 +425,7 @@ comp_status_t comp_kv_append_f32(const comp_kv_cache_t* cache, const float* k, c
  * The first shared_pages entries of all rows are the same pages, a prefix that
  * the batch shares: row 0's are read, once for the whole batch.
  * 0 shares nothing.  Workspace: comp_attn_decode_workspace_bytes, 16-byte
- * aligned.
+ * aligned.  A cache without pages takes only a table of width 0.
  */
 int64_t comp_attn_decode_workspace_bytes(const comp_kv_cache_t* cache, int64_t batch, int32_t heads, int64_t width,
                                          int64_t shared_pages);
