@@ -52,11 +52,11 @@ namespace compfp32 {
 namespace {
 
 constexpr int kThreads = 384;
-// Registers a thread at launch, and after setmaxnreg: 128 x 40 + 256 x 232 is
+// Registers a thread at launch, and after setmaxnreg: 128 x 56 + 256 x 224 is
 // the launch's 384 x 168.  The row threads hold the D output sums of a row
-// and 32 to 64 scores.  The build checks the 168.
-constexpr int kCtrlRegs = 40;
-constexpr int kRowRegs = 232;
+// and 32 scores.  The build checks the 168.
+constexpr int kCtrlRegs = 56;
+constexpr int kRowRegs = 224;
 static_assert(128 * kCtrlRegs + 256 * kRowRegs <= kThreads * 168, "register split");
 
 // Fault codes of the waits.
@@ -125,6 +125,16 @@ struct Params {
 __device__ __forceinline__ int clampi(int x, int lo, int hi)
 {
     return x < lo ? lo : (x > hi ? hi : x);
+}
+
+// The high half of every shared-memory descriptor here: 1024 bytes between
+// groups of eight rows, version 1, 128-byte swizzle; and the low half: address
+// and leading-dimension offset.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+__device__ __forceinline__ uint32_t desc_lo(uint32_t smem_addr, uint32_t leading)
+{
+    return ((smem_addr & 0x3FFFFu) >> 4) | ((leading >> 4) << 16);
 }
 
 // This CTA's sequence and block of 256 rows: blocks are numbered sequence by
@@ -304,70 +314,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp == 1) {
             // ---------------- products
+            // Each is issued from one place: the code of a tile must stay in
+            // the instruction caches beside the row warps' own.  Descriptors are
+            // their low 32 bits (address, leading offset); the high ones (stride
+            // 1024, version, swizzle) are the same for all operands.
             const uint32_t leader = lane == 0;
+            const uint32_t q_lo32 = desc_lo(smem_u32(smem), 16), k_lo32 = desc_lo(smem_u32(stages), 16);
+            const uint32_t v_lo32 = desc_lo(smem_u32(stages), BN * 128);
+            constexpr uint32_t kQPlane = C::kQTile >> 4, kKvPlane = C::kPlane >> 4, kKvStage = C::kStage >> 4;
             bool ok = true;
             auto wait = [&](uint64_t* bar, int phase) {
                 ok = ok && attn_warp_wait(bar, phase & 1, &sm->abort, kFaultAttnMma);
                 tc_fence_after();
                 return ok;
             };
-            auto scores = [&](int h, int j) {
-                const uint32_t d = tmem + h * 128;
-                const uint32_t qhi = smem_u32(smem) + h * 2 * C::kQTile, qlo = qhi + C::kQTile;
-                const uint32_t khi = smem_u32(stages) + (2 * j % NS) * C::kStage, klo = khi + C::kPlane;
-                auto chain = [&](uint32_t a, uint32_t b, int how) {  // 0 fresh, 1 add, 2 add to 2^-10 of what is there
-    #pragma unroll
-                    for (int t = 0; t < DP / 16; ++t) {
-                        const uint64_t da = sw128_kmajor_desc(a + (t / 4) * (128 * 128) + (t % 4) * 32);
-                        const uint64_t db = sw128_kmajor_desc(b + (t / 4) * (BN * 128) + (t % 4) * 32);
-                        if (t == 0 && how == 2)
-                            umma_f16_scale10_by(leader, d, da, db, C::kIdescS);
-                        else
-                            umma_f16_by(leader, d, da, db, C::kIdescS, t > 0 || how > 0);
-                    }
-                };
-                chain(qlo, khi, 0);
-                if (PL == 2)
-                    chain(qhi, klo, 1);
-                chain(qhi, khi, 2);
-                umma_commit_by(leader, &sm->sfull[h]);
-            };
-            auto values = [&](int h, int j) {
-                const uint32_t pt = tmem + h * 128, d = tmem + 256 + h * 128 + (OB == 2 ? (j & 1) * 64 : 0);
-                const uint32_t vhi = smem_u32(stages) + ((2 * j + 1) % NS) * C::kStage, vlo = vhi + C::kPlane;
-                // P of 16 keys: 8 columns of hi pairs, then 8 of lo pairs
-                auto step = [&](int t, int lo_p, uint32_t v, int how) {
-                    const uint32_t a = pt + t * 16 + lo_p * 8;
-                    const uint64_t db = sw128_mnmajor_desc(v + t * 2048, BN * 128);
-                    if (how == 2)
-                        umma_f16_ta_scale10_by(leader, d, a, db, C::kIdescO);
+            // S: a and b at q's and k's planes; how: 0 fresh, 1 added, 2 added to 2^-10 of what is there
+            auto chain = [&](uint32_t d, uint32_t qd, uint32_t kd, int how) {
+#pragma unroll
+                for (int t = 0; t < DP / 16; ++t) {
+                    const uint32_t da = qd + (t / 4) * (128 * 128 >> 4) + (t % 4) * 2;
+                    const uint32_t db = kd + (t / 4) * (BN * 128 >> 4) + (t % 4) * 2;
+                    if (t == 0 && how == 2)
+                        umma_w_scale10_by(leader, d, da, db, kDescHi, C::kIdescS);
                     else
-                        umma_f16_ta_by(leader, d, a, db, C::kIdescO, how);
-                };
-                if (PL == 2) {
-    #pragma unroll
-                    for (int t = 0; t < BN / 16; ++t)
-                        step(t, 0, vlo, t > 0);
+                        umma_w_by(leader, d, da, db, kDescHi, C::kIdescS, t > 0 || how > 0);
                 }
-    #pragma unroll
-                for (int t = 0; t < BN / 16; ++t) {
-                    step(t, 1, vhi, t > 0 ? 1 : (PL == 2 ? 2 : 0));
-                    step(t, 0, vhi, 1);
-                }
-                umma_commit_by(leader, &sm->ofull[h * OB + (OB == 2 ? (j & 1) : 0)]);
             };
-            if (n > 0 && wait(&sm->full[0], 0)) {
-                for (int h = 0; h < 2; ++h)
-                    if ((h ? n1 : n0) > 0 && wait(&sm->qfull[h], 0))
-                        scores(h, 0);
-                umma_commit_by(leader, &sm->empty[0]);
-            }
-            for (int j = 0; ok && j < n; ++j) {
+            for (int j = -1; ok && j < n; ++j) {
                 const int sv = (2 * j + 1) % NS, sk = (2 * j + 2) % NS;
                 bool v_here = false, k_here = false;
+#pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
                     const int nh = h ? n1 : n0;
-                    if (j < nh) {
+                    if (j >= 0 && j < nh) {
                         if (!v_here && (!wait(&sm->full[sv], (2 * j + 1) / NS) ||
                                         (j >= edge && !wait(&sm->checked[sv], (2 * j + 1) / NS))))
                             break;
@@ -376,7 +355,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                             break;
                         if (j >= OB && !wait(&sm->ofree[h * OB + j % OB], j / OB - 1))
                             break;
-                        values(h, j);
+                        // P of 16 keys: 8 columns of hi pairs, then 8 of lo pairs
+                        const uint32_t pt = tmem + h * 128, d = tmem + 256 + h * 128 + (OB == 2 ? (j & 1) * 64 : 0);
+                        const uint32_t vhi = v_lo32 + sv * kKvStage, vlo = vhi + kKvPlane;
+                        if (PL == 2) {
+#pragma unroll
+                            for (int t = 0; t < BN / 16; ++t)
+                                umma_ta_w_by(leader, d, pt + t * 16, vlo + t * 128, kDescHi, C::kIdescO, t > 0);
+                        }
+#pragma unroll
+                        for (int t = 0; t < BN / 16; ++t) {
+                            if (t == 0 && PL == 2)
+                                umma_ta_w_scale10_by(leader, d, pt + t * 16 + 8, vhi + t * 128, kDescHi, C::kIdescO);
+                            else
+                                umma_ta_w_by(leader, d, pt + t * 16 + 8, vhi + t * 128, kDescHi, C::kIdescO, t > 0);
+                            umma_ta_w_by(leader, d, pt + t * 16, vhi + t * 128, kDescHi, C::kIdescO, 1);
+                        }
+                        umma_commit_by(leader, &sm->ofull[h * OB + (OB == 2 ? (j & 1) : 0)]);
                         if (h == 1 || j >= n1)
                             umma_commit_by(leader, &sm->empty[sv]);
                     }
@@ -384,7 +379,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!k_here && !wait(&sm->full[sk], (2 * j + 2) / NS))
                             break;
                         k_here = true;
-                        scores(h, j + 1);
+                        if (j < 0 && !wait(&sm->qfull[h], 0))
+                            break;
+                        const uint32_t d = tmem + h * 128, qhi = q_lo32 + h * 2 * kQPlane, khi = k_lo32 + sk * kKvStage;
+                        chain(d, qhi + kQPlane, khi, 0);
+                        if (PL == 2)
+                            chain(d, qhi, khi + kKvPlane, 1);
+                        chain(d, qhi, khi, 2);
+                        umma_commit_by(leader, &sm->sfull[h]);
                         if (h == 1 || j + 1 >= n1)
                             umma_commit_by(leader, &sm->empty[sk]);
                     }
@@ -441,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t* const hi_tile = smem + half * 2 * C::kQTile;
             constexpr int E = DP / 32;  // values of a lane
             const int d0 = lane * E;
-#pragma unroll 4
+#pragma unroll 16
             for (int i = 0; i < 32; ++i) {
                 const int64_t at = __shfl_sync(0xffffffffu, q_at, i);
                 const bool there = __shfl_sync(0xffffffffu, valid ? 1 : 0, i) != 0;
@@ -491,96 +493,106 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < DP / 2; ++i)
             o[i] = 0;
 
-        // o = o alpha + O' of tile j
-        auto take = [&](int j) {
-            const int b = half * OB + (OB == 2 ? (j & 1) : 0);
-            if (!attn_warp_wait(&sm->ofull[b], (j / OB) & 1, &sm->abort, kFaultAttnRows))
-                return false;
-            tc_fence_after();
-            const uint64_t a2 = f2_bits(alpha, alpha);
-            const uint32_t from = tmem + lanes + 256 + half * 128 + (OB == 2 ? (j & 1) * 64 : 0);
-#pragma unroll
-            for (int c = 0; c < DP / 32; ++c) {
-                uint32_t r[32];
-                tmem_ld32(from + c * 32, r);
-                tmem_ld_wait32(r);
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    o[c * 16 + i] = fma2(o[c * 16 + i], a2, u2_bits(r[2 * i], r[2 * i + 1]));
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&sm->ofree[b]);
-            return true;
-        };
-
-        for (int j = 0; j < nh; ++j) {
-            if (!attn_warp_wait(&sm->sfull[half], j & 1, &sm->abort, kFaultAttnRows)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            const bool part_seen = __any_sync(0xffffffffu, row_lim < (j + 1) * BN);
-            const int left = row_lim - j * BN;  // columns below this are seen
-            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int c = 0; c < BN / 32; ++c) {
-                uint32_t r[32];
-                tmem_ld32(st + c * 32, r);
-                tmem_ld_wait32(r);
-                if (part_seen) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        top[i & 3] = fmaxf(top[i & 3], c * 32 + i < left ? __uint_as_float(r[i]) : -INFINITY);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        top[i & 3] = fmaxf(top[i & 3], __uint_as_float(r[i]));
+        // Tile j's scores become P; then O' of the tile before is taken, while
+        // the tensor cores go on.  One place for each, as above.
+#pragma unroll 1
+        for (int j = 0; j <= nh && nh > 0; ++j) {
+            float alpha_new = 0.0f;
+            if (j < nh) {
+                if (!attn_warp_wait(&sm->sfull[half], j & 1, &sm->abort, kFaultAttnRows)) {
+                    ok = false;
+                    break;
                 }
-            }
-            const float m_new = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c2);
-            const float shift = m_new == -INFINITY ? 0.0f : m_new;  // nothing seen yet: every p is 0
-            const float alpha_new = ex2(m - shift);
-            m = m_new;
-            l2 = mul2(l2, f2_bits(alpha_new, alpha_new));
-            const uint64_t s2 = f2_bits(-shift, -shift), k2 = f2_bits(kAttnPScale, kAttnPScale);
-            uint32_t r[2][16];
-            tmem_ld16(st, r[0]);
+                tc_fence_after();
+                if (__any_sync(0xffffffffu, row_lim < (j + 1) * BN)) {
+                    // hidden scores to -inf, in place
+                    const int left = row_lim - j * BN;
+#pragma unroll 1
+                    for (int c = 0; c < BN; c += 16) {
+                        uint32_t r[16];
+                        tmem_ld16(st + c, r);
+                        tmem_ld_wait16(r);
 #pragma unroll
-            for (int c = 0; c < BN / 16; ++c) {
-                uint32_t (&x)[16] = r[c & 1];
-                tmem_ld_wait16(x);
-                if (c + 1 < BN / 16)
-                    tmem_ld16(st + (c + 1) * 16, r[(c + 1) & 1]);
-                if (part_seen) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        x[i] = c * 16 + i < left ? x[i] : 0xff800000u;  // -inf
+                        for (int i = 0; i < 16; ++i)
+                            r[i] = c + i < left ? r[i] : 0xff800000u;
+                        tmem_st16(st + c, r);
+                    }
+                    tmem_st_wait();
                 }
-                uint32_t out[16];
+                uint32_t r[2][16];
+                tmem_ld16(st, r[0]);
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint64_t y = fma2(u2_bits(x[2 * i], x[2 * i + 1]), c22, s2);
-                    const uint64_t e = mul2(f2_bits(ex2(lo_f(y)), ex2(hi_f(y))), k2);
-                    l2 = add2(l2, e);
-                    split_p(e, out[i], out[8 + i]);
+                for (int c = 0; c < BN / 16; ++c) {
+                    uint32_t (&x)[16] = r[c & 1];
+                    tmem_ld_wait16(x);
+                    tmem_ld16(st + (c + 1) % (BN / 16) * 16, r[(c + 1) & 1]);
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2)
+                        top[i / 2 & 3] = fmaxf(top[i / 2 & 3], fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
                 }
-                tmem_st16(st + c * 16, out);
+                const float m_new = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c2);
+                const float shift = m_new == -INFINITY ? 0.0f : m_new;  // nothing seen yet: every p is 0
+                alpha_new = ex2(m - shift);
+                m = m_new;
+                l2 = mul2(l2, f2_bits(alpha_new, alpha_new));
+                const uint64_t s2 = f2_bits(-shift, -shift), k2 = f2_bits(kAttnPScale, kAttnPScale);
+                // r[0] holds the first 16 scores again
+#pragma unroll 1
+                for (int c = 0; c < BN; c += 32) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t (&x)[16] = r[e];
+                        tmem_ld_wait16(x);
+                        // the last of these reads P, and is not used
+                        tmem_ld16(st + (c + e * 16 + 16) % BN, r[1 - e]);
+                        uint32_t out[16];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint64_t y = fma2(u2_bits(x[2 * i], x[2 * i + 1]), c22, s2);
+                            const uint64_t w = mul2(f2_bits(ex2(lo_f(y)), ex2(hi_f(y))), k2);
+                            l2 = add2(l2, w);
+                            split_p(w, out[i], out[8 + i]);
+                        }
+                        tmem_st16(st + c + e * 16, out);
+                    }
+                }
+                tmem_ld_wait16(r[0]);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sm->pfull[half]);
             }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&sm->pfull[half]);
-            if (j > 0 && !take(j - 1)) {
-                ok = false;
-                break;
+            if (j > 0) {
+                // o = o alpha + O' of tile j - 1
+                const int b = OB == 2 ? (j - 1) & 1 : 0;
+                if (!attn_warp_wait(&sm->ofull[half * OB + b], ((j - 1) / OB) & 1, &sm->abort, kFaultAttnRows)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t a2 = f2_bits(alpha, alpha);
+                const uint32_t from = tmem + lanes + 256 + half * 128 + b * 64;
+                uint32_t r[2][16];
+                tmem_ld16(from, r[0]);
+#pragma unroll
+                for (int c = 0; c < DP / 16; ++c) {
+                    uint32_t (&x)[16] = r[c & 1];
+                    tmem_ld_wait16(x);
+                    if (c + 1 < DP / 16)
+                        tmem_ld16(from + (c + 1) * 16, r[(c + 1) & 1]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        o[c * 8 + i] = fma2(o[c * 8 + i], a2, u2_bits(x[2 * i], x[2 * i + 1]));
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sm->ofree[half * OB + b]);
             }
             alpha = alpha_new;
         }
-        if (ok && nh > 0)
-            ok = take(nh - 1);
         if (ok && valid) {
             const float l = (lo_f(l2) + hi_f(l2)) * (1.0f / kAttnPScale);
             // no key seen, or none that counts beside an infinite score (NaN stays NaN)

@@ -193,28 +193,60 @@ __device__ __forceinline__ void umma_f16_scale10_by(uint32_t leader, uint32_t d_
         : "memory");
 }
 
-// The same two with A (128 x 16 FP16) in tensor memory.
-__device__ __forceinline__ void umma_f16_ta_by(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                               uint32_t idesc, uint32_t accumulate)
+// The same with both descriptors as their low 32-bit words and one common high
+// word, which makes advancing one a 32-bit addition; and with A (128 x 16 FP16)
+// in tensor memory.
+__device__ __forceinline__ void umma_w_by(uint32_t leader, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
+                                          uint32_t desc_hi, uint32_t idesc, uint32_t accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %3};\n\t"
+        "mov.b64 db, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "setp.ne.b32 q, %6, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(desc_hi), "r"(idesc), "r"(accumulate), "r"(leader)
         : "memory");
 }
 
-__device__ __forceinline__ void umma_f16_ta_scale10_by(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem,
-                                                       uint64_t b_desc, uint32_t idesc)
+__device__ __forceinline__ void umma_w_scale10_by(uint32_t leader, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
+                                                  uint32_t desc_hi, uint32_t idesc)
 {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %3};\n\t"
+        "mov.b64 db, {%2, %3};\n\t"
         "setp.ne.b32 p, 1, 0;\n\t"
-        "setp.ne.b32 q, %4, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p, 10;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(leader)
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p, 10;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(desc_hi), "r"(idesc), "r"(leader)
+        : "memory");
+}
+
+__device__ __forceinline__ void umma_ta_w_by(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                             uint32_t desc_hi, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\t"
+        "mov.b64 db, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "setp.ne.b32 q, %6, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(desc_hi), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+
+__device__ __forceinline__ void umma_ta_w_scale10_by(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                                     uint32_t desc_hi, uint32_t idesc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\t"
+        "mov.b64 db, {%2, %3};\n\t"
+        "setp.ne.b32 p, 1, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p, 10;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(desc_hi), "r"(idesc), "r"(leader)
         : "memory");
 }
 
@@ -255,22 +287,6 @@ __device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t smem_addr)
     return d;
 }
 
-// The descriptor of an operand whose M/N extent is the contiguous one, 128-byte
-// swizzled: rows of 64 FP16 along M/N (128 bytes), one for each k; 8 of them an
-// atom of 1024 bytes.  Leading-dimension offset: bytes between blocks of 64
-// along M/N (`block`); stride-dimension offset: 1024 bytes between groups of
-// eight k.  Advancing K by 16 is done by adding 2048 bytes to the start address.
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint32_t block)
-{
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>(block >> 4) << 16;
-    d |= static_cast<uint64_t>(1024u >> 4) << 32;
-    d |= static_cast<uint64_t>(1u) << 46;
-    d |= static_cast<uint64_t>(2u) << 61;
-    return d;
-}
-
 // Instruction descriptor for tcgen05.mma kind::f16 with FP16 A and B, FP32
 // accumulator, both operands K-major, no negation, dense:
 // D format (bits 4-5) = 1 (F32); A format (bits 7-9) = 0 (F16); B format
@@ -280,7 +296,11 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n)
     return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-// The bit that makes B the operand of sw128_mnmajor_desc.
+// The bit that makes B an operand whose N extent is the contiguous one.  Its
+// descriptor, 128-byte swizzled: rows of 64 FP16 along N (128 bytes), one for
+// each k, 8 of them an atom of 1024 bytes; the leading-dimension offset is the
+// bytes between blocks of 64 along N, the stride-dimension offset the 1024
+// bytes between groups of eight k.  Advancing K by 16 adds 2048 bytes.
 constexpr uint32_t kIdescBMnMajor = 1u << 16;
 
 
