@@ -31,8 +31,9 @@
 // pairs), which the second product reads from tensor memory.
 //
 // Warps: 0 loads tiles of k and v (TMA, a ring of stages), 1 issues the
-// products, 2 and 3 see to values that must not count (below), 4..7 and 8..11
-// own the rows of the two halves: thread = tensor-memory lane = row.
+// products, 2 waits for what they need, 3 sees to values that must not count
+// (below), 4..7 and 8..11 own the rows of the two halves: thread =
+// tensor-memory lane = row.
 //
 // Hidden keys: a score that its row may not see becomes -inf, whatever k held,
 // so p = 0.  In the product with v a zero does not silence an infinity or a
@@ -64,6 +65,7 @@ constexpr uint32_t kFaultAttnLoad = 0x901;
 constexpr uint32_t kFaultAttnMma = 0x902;
 constexpr uint32_t kFaultAttnValues = 0x903;
 constexpr uint32_t kFaultAttnRows = 0x904;
+constexpr uint32_t kFaultAttnTmem = 0x905;
 
 // DP: the head dimension padded to 64 or 128.  PL: planes of k and v, 1 (FP16)
 // or 2 (FP32, split).
@@ -89,13 +91,12 @@ struct Cfg {
 };
 
 struct Shared {
-    uint64_t full[6], empty[6];  // a stage has landed; products and warps 2, 3 are done with it
+    uint64_t full[6], empty[6];  // a stage has landed; the products and warp 3 are done with it
+    uint64_t checked[6];         // warp 3 has looked through a stage (a barrier for each stage: it may be
+                                 // several tiles ahead of the products)
     uint64_t qfull[2];           // a half's q planes are in shared memory
-    uint64_t sfull[2];           // S of a tile is complete
-    uint64_t pfull[2];           // P of a tile is in tensor memory (and S has been read)
-    uint64_t ofull[4], ofree[4]; // O' is complete; has been read (half * OB + buffer)
-    uint64_t checked[6];         // warps 2 and 3 are done with a stage (a barrier for each stage: they may
-                                 // be several tiles ahead of the products)
+    uint64_t sfull[2];           // a half's S of a tile, and O' of the tile before, are complete
+    uint64_t pfull[2];           // a half's P of a tile is in tensor memory, and an O' buffer is free for it
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
@@ -201,17 +202,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 64) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(&sm->full[i], 1);
-            mbar_init(&sm->empty[i], 3);
-            mbar_init(&sm->checked[i], 2);
+            mbar_init(&sm->empty[i], 2);
+            mbar_init(&sm->checked[i], 1);
         }
         for (int h = 0; h < 2; ++h) {
             mbar_init(&sm->qfull[h], 4);
             mbar_init(&sm->sfull[h], 1);
             mbar_init(&sm->pfull[h], 4);
-        }
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(&sm->ofull[i], 1);
-            mbar_init(&sm->ofree[i], 4);
         }
         mbar_init(&sm->drain, 1);
         sm->abort = 0;
@@ -270,7 +267,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sm->tmem_base;
+    // All 512 columns are this CTA's, so they begin at 0: tensor-memory addresses
+    // are constants to the issuing warp.
+    const bool at_zero = sm->tmem_base == 0;
     const int n0 = (sm->most[0] + BN - 1) / BN, n1 = (sm->most[1] + BN - 1) / BN;
     const int n = max(n0, n1), most = max(sm->most[0], sm->most[1]);
     // tiles from this one on are seen only in part by some row
@@ -278,7 +277,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtrlRegs));
-        if (warp == 0) {
+        if (!at_zero) {
+            if (threadIdx.x == 0) {
+                atomicCAS(&g_attn_fault_word, 0u, kFaultAttnTmem);
+                *reinterpret_cast<volatile int*>(&sm->abort) = 1;
+            }
+        } else if (warp == 0) {
             // ---------------- loads: K0, V0, K1, V1, ...
             const int pieces = p.page_size ? BN / p.page_size : 1;
             const int boxes = PL * C::kBoxes * pieces;
@@ -314,20 +318,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp == 1) {
             // ---------------- products
-            // Each is issued from one place: the code of a tile must stay in
-            // the instruction caches beside the row warps' own.  Descriptors are
-            // their low 32 bits (address, leading offset); the high ones (stride
-            // 1024, version, swizzle) are the same for all operands.
+            // This warp only issues: warp 2 waits for what a step needs and hands
+            // the step over at a named barrier (a test of an mbarrier takes hundreds
+            // of cycles while the tensor cores stream operands from shared memory).
+            // Each product is issued from one place, so that a tile's code stays
+            // in the instruction caches.  Descriptors are their low 32 bits
+            // (address, leading offset); the high ones are the same for all.
             const uint32_t leader = lane == 0;
             const uint32_t q_lo32 = desc_lo(smem_u32(smem), 16), k_lo32 = desc_lo(smem_u32(stages), 16);
             const uint32_t v_lo32 = desc_lo(smem_u32(stages), BN * 128);
             constexpr uint32_t kQPlane = C::kQTile >> 4, kKvPlane = C::kPlane >> 4, kKvStage = C::kStage >> 4;
-            bool ok = true;
-            auto wait = [&](uint64_t* bar, int phase) {
-                ok = ok && attn_warp_wait(bar, phase & 1, &sm->abort, kFaultAttnMma);
-                tc_fence_after();
-                return ok;
-            };
             // S: a and b at q's and k's planes; how: 0 fresh, 1 added, 2 added to 2^-10 of what is there
             auto chain = [&](uint32_t d, uint32_t qd, uint32_t kd, int how) {
 #pragma unroll
@@ -340,23 +340,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                         umma_w_by(leader, d, da, db, kDescHi, C::kIdescS, t > 0 || how > 0);
                 }
             };
+            bool ok = true;
+            int step = 0, sk = 0, sv = NS - 1;  // stages of K of tile j + 1 and V of tile j
             for (int j = -1; ok && j < n; ++j) {
-                const int sv = (2 * j + 1) % NS, sk = (2 * j + 2) % NS;
-                bool v_here = false, k_here = false;
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
                     const int nh = h ? n1 : n0;
-                    if (j >= 0 && j < nh) {
-                        if (!v_here && (!wait(&sm->full[sv], (2 * j + 1) / NS) ||
-                                        (j >= edge && !wait(&sm->checked[sv], (2 * j + 1) / NS))))
-                            break;
-                        v_here = true;
-                        if (!wait(&sm->pfull[h], j))
-                            break;
-                        if (j >= OB && !wait(&sm->ofree[h * OB + j % OB], j / OB - 1))
-                            break;
+                    const bool has_v = j >= 0 && j < nh, has_k = j + 1 < nh;
+                    if (!has_v && !has_k)
+                        continue;
+                    ok = bar_red_and(2 + (step++ & 1), 64, true);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    if (has_v) {
                         // P of 16 keys: 8 columns of hi pairs, then 8 of lo pairs
-                        const uint32_t pt = tmem + h * 128, d = tmem + 256 + h * 128 + (OB == 2 ? (j & 1) * 64 : 0);
+                        const uint32_t pt = h * 128, d = 256 + h * 128 + (OB == 2 ? (j & 1) * 64 : 0);
                         const uint32_t vhi = v_lo32 + sv * kKvStage, vlo = vhi + kKvPlane;
                         if (PL == 2) {
 #pragma unroll
@@ -371,30 +370,64 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 umma_ta_w_by(leader, d, pt + t * 16 + 8, vhi + t * 128, kDescHi, C::kIdescO, t > 0);
                             umma_ta_w_by(leader, d, pt + t * 16, vhi + t * 128, kDescHi, C::kIdescO, 1);
                         }
-                        umma_commit_by(leader, &sm->ofull[h * OB + (OB == 2 ? (j & 1) : 0)]);
                         if (h == 1 || j >= n1)
                             umma_commit_by(leader, &sm->empty[sv]);
                     }
-                    if (j + 1 < nh) {
-                        if (!k_here && !wait(&sm->full[sk], (2 * j + 2) / NS))
-                            break;
-                        k_here = true;
-                        if (j < 0 && !wait(&sm->qfull[h], 0))
-                            break;
-                        const uint32_t d = tmem + h * 128, qhi = q_lo32 + h * 2 * kQPlane, khi = k_lo32 + sk * kKvStage;
+                    if (has_k) {
+                        const uint32_t d = h * 128, qhi = q_lo32 + h * 2 * kQPlane, khi = k_lo32 + sk * kKvStage;
                         chain(d, qhi + kQPlane, khi, 0);
                         if (PL == 2)
                             chain(d, qhi, khi + kKvPlane, 1);
                         chain(d, qhi, khi, 2);
-                        umma_commit_by(leader, &sm->sfull[h]);
-                        if (h == 1 || j + 1 >= n1)
-                            umma_commit_by(leader, &sm->empty[sk]);
                     }
+                    umma_commit_by(leader, &sm->sfull[h]);
+                    if (has_k && (h == 1 || j + 1 >= n1))
+                        umma_commit_by(leader, &sm->empty[sk]);
                 }
+                sk = sk + 2 >= NS ? sk + 2 - NS : sk + 2;
+                sv = sv + 2 >= NS ? sv + 2 - NS : sv + 2;
             }
             if (!ok) {
                 umma_commit_by(leader, &sm->drain);
                 attn_drain_wait(&sm->drain, 0);
+            }
+        } else if (warp == 2) {
+            // ---------------- waits for the products, step by step
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, int phase) {
+                if (ok && lane == 0)
+                    ok = attn_wait(bar, phase & 1, &sm->abort, kFaultAttnMma);
+            };
+            int step = 0;
+            for (int j = -1; ok && j < n; ++j) {
+                const int iv = 2 * j + 1, ik = 2 * j + 2;  // loads of V of tile j and K of tile j + 1
+                bool v_here = false, k_here = false;
+                for (int h = 0; h < 2; ++h) {
+                    const int nh = h ? n1 : n0;
+                    const bool has_v = j >= 0 && j < nh, has_k = j + 1 < nh;
+                    if (!has_v && !has_k)
+                        continue;
+                    if (has_v) {
+                        if (!v_here) {
+                            wait(&sm->full[iv % NS], iv / NS);
+                            if (j >= edge)
+                                wait(&sm->checked[iv % NS], iv / NS);
+                            v_here = true;
+                        }
+                        wait(&sm->pfull[h], j);
+                    }
+                    if (has_k) {
+                        if (!k_here)
+                            wait(&sm->full[ik % NS], ik / NS);
+                        k_here = true;
+                        if (j < 0)
+                            wait(&sm->qfull[h], 0);
+                    }
+                    // lane 0's observations reach the issuing warp through the barrier
+                    ok = bar_red_and(2 + (step++ & 1), 64, ok);
+                    if (!ok)
+                        break;
+                }
             }
         } else {
             // ---------------- values that must not count
@@ -405,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if ((i & 1) && j >= edge) {
                     uint8_t* const tile = stages + s * C::kStage;
                     bool seen = false;
-                    for (uint32_t at = (warp - 2) * 512 + lane * 16; at < C::kStage; at += 1024) {
+                    for (uint32_t at = lane * 16; at < C::kStage; at += 512) {
                         uint4 x = *reinterpret_cast<const uint4*>(tile + at);
                         uint32_t* const w = reinterpret_cast<uint32_t*>(&x);
                         bool any = false;
@@ -483,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
         const float c2 = p.scale * kAttnLog2E;
         const uint64_t c22 = f2_bits(c2, c2);
-        const uint32_t st = tmem + lanes + half * 128;
+        const uint32_t st = lanes + half * 128;
         const int row_lim = valid ? lim : INT32_MAX;  // rows that are not there are not stored
         float m = -INFINITY;        // the running maximum of s * c2
         uint64_t l2 = 0;            // the running sum of 2^14 p, in two parts
@@ -493,17 +526,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < DP / 2; ++i)
             o[i] = 0;
 
-        // Tile j's scores become P; then O' of the tile before is taken, while
-        // the tensor cores go on.  One place for each, as above.
+        // o = o alpha + O' of tile j
+        auto take = [&](int j) {
+            const uint64_t a2 = f2_bits(alpha, alpha);
+            const uint32_t from = lanes + 256 + half * 128 + (OB == 2 ? (j & 1) * 64 : 0);
+            uint32_t r[2][16];
+            tmem_ld16(from, r[0]);
+#pragma unroll
+            for (int c = 0; c < DP / 16; ++c) {
+                uint32_t (&x)[16] = r[c & 1];
+                tmem_ld_wait16(x);
+                if (c + 1 < DP / 16)
+                    tmem_ld16(from + (c + 1) * 16, r[(c + 1) & 1]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    o[c * 8 + i] = fma2(o[c * 8 + i], a2, u2_bits(x[2 * i], x[2 * i + 1]));
+            }
+        };
+
+        // Tile j's scores become P, and O' of the tile before is taken: first
+        // where there is one buffer for it (P's arrival frees it), else last,
+        // while the tensor cores go on.
 #pragma unroll 1
         for (int j = 0; j <= nh && nh > 0; ++j) {
-            float alpha_new = 0.0f;
-            if (j < nh) {
-                if (!attn_warp_wait(&sm->sfull[half], j & 1, &sm->abort, kFaultAttnRows)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
+            if (!attn_warp_wait(&sm->sfull[half], j & 1, &sm->abort, kFaultAttnRows)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            if (j > 0 && (OB == 1 || j == nh))
+                take(j - 1);
+            if (j == nh)
+                break;
+            {
                 if (__any_sync(0xffffffffu, row_lim < (j + 1) * BN)) {
                     // hidden scores to -inf, in place
                     const int left = row_lim - j * BN;
@@ -533,10 +588,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const float m_new = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c2);
                 const float shift = m_new == -INFINITY ? 0.0f : m_new;  // nothing seen yet: every p is 0
-                alpha_new = ex2(m - shift);
+                const float alpha_new = ex2(m - shift);
                 m = m_new;
                 l2 = mul2(l2, f2_bits(alpha_new, alpha_new));
-                const uint64_t s2 = f2_bits(-shift, -shift), k2 = f2_bits(kAttnPScale, kAttnPScale);
+                // 2^14 p in one operation: the sum's rounding, at most 2^-21 of 14,
+                // is of the size of the scores' own
+                const uint64_t s2 = f2_bits(14.0f - shift, 14.0f - shift);
                 // r[0] holds the first 16 scores again
 #pragma unroll 1
                 for (int c = 0; c < BN; c += 32) {
@@ -550,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const uint64_t y = fma2(u2_bits(x[2 * i], x[2 * i + 1]), c22, s2);
-                            const uint64_t w = mul2(f2_bits(ex2(lo_f(y)), ex2(hi_f(y))), k2);
+                            const uint64_t w = f2_bits(ex2(lo_f(y)), ex2(hi_f(y)));
                             l2 = add2(l2, w);
                             split_p(w, out[i], out[8 + i]);
                         }
@@ -563,35 +620,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&sm->pfull[half]);
+                if (OB == 2 && j > 0)
+                    take(j - 1);
+                alpha = alpha_new;
             }
-            if (j > 0) {
-                // o = o alpha + O' of tile j - 1
-                const int b = OB == 2 ? (j - 1) & 1 : 0;
-                if (!attn_warp_wait(&sm->ofull[half * OB + b], ((j - 1) / OB) & 1, &sm->abort, kFaultAttnRows)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint64_t a2 = f2_bits(alpha, alpha);
-                const uint32_t from = tmem + lanes + 256 + half * 128 + b * 64;
-                uint32_t r[2][16];
-                tmem_ld16(from, r[0]);
-#pragma unroll
-                for (int c = 0; c < DP / 16; ++c) {
-                    uint32_t (&x)[16] = r[c & 1];
-                    tmem_ld_wait16(x);
-                    if (c + 1 < DP / 16)
-                        tmem_ld16(from + (c + 1) * 16, r[(c + 1) & 1]);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        o[c * 8 + i] = fma2(o[c * 8 + i], a2, u2_bits(x[2 * i], x[2 * i + 1]));
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&sm->ofree[half * OB + b]);
-            }
-            alpha = alpha_new;
         }
         if (ok && valid) {
             const float l = (lo_f(l2) + hi_f(l2)) * (1.0f / kAttnPScale);
@@ -646,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 1)
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(sm->tmem_base, 512);
 }
 
 // FP32 keys and values as FP16 planes (hi = fp16(x), lo = fp16((x - hi) 1024)),
