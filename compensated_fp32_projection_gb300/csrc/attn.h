@@ -48,6 +48,16 @@ __device__ __forceinline__ bool attn_warp_wait(uint64_t* bar, uint32_t parity, i
     return ok;
 }
 
+// Lane 0 waits for the warp; for loads from tensor memory, which
+// tcgen05.fence::after_thread_sync orders after this.
+__device__ __forceinline__ bool attn_lane0_wait(uint64_t* bar, uint32_t parity, int* abort_flag, uint32_t code)
+{
+    bool ok = true;
+    if ((threadIdx.x & 31) == 0)
+        ok = attn_wait(bar, parity, abort_flag, code);
+    return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+
 // Wait for what was issued before the CTA exits after an abort.
 __device__ __forceinline__ void attn_drain_wait(uint64_t* bar, uint32_t parity)
 {
@@ -85,13 +95,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     return d;
 }
 
-__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
 __device__ __forceinline__ uint64_t u2_bits(uint32_t a, uint32_t b)
 {
     return static_cast<uint64_t>(a) | (static_cast<uint64_t>(b) << 32);
@@ -101,13 +104,19 @@ __device__ __forceinline__ uint64_t u2_bits(uint32_t a, uint32_t b)
 // hi + lo = 2^14 p: lo = fp16(2^14 p - hi), unscaled.  hi is at most 16384 and
 // lo has FP16's subnormals down to 2^-24, so what is lost of a weight is at
 // most 2^-22 of it or 2^-39 of the largest possible one.
-__device__ __forceinline__ void split_p(uint64_t p, uint32_t& hi, uint32_t& lo)
+// p - hi is exact, and one operation on the packed hi (an FP16 factor of -1).
+__device__ __forceinline__ void split_p(float p0, float p1, uint32_t& hi, uint32_t& lo)
 {
-    const __half2 h = __floats2half2_rn(lo_f(p), hi_f(p));
-    const float2 hf = __half22float2(h);
-    const uint64_t rest = sub2(p, f2_bits(hf.x, hf.y));
-    hi = pack_h2(h);
-    lo = pack_h2(__floats2half2_rn(lo_f(rest), hi_f(rest)));
+    hi = pack_h2(__floats2half2_rn(p0, p1));
+    float r0, r1;
+    asm("{\n\t.reg .b16 a, b, m;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "mov.b16 m, 0xbc00;\n\t"
+        "fma.rn.f32.f16 %0, a, m, %3;\n\t"
+        "fma.rn.f32.f16 %1, b, m, %4;\n\t}"
+        : "=f"(r0), "=f"(r1)
+        : "r"(hi), "f"(p0), "f"(p1));
+    lo = pack_h2(__floats2half2_rn(r0, r1));
 }
 
 // FP16 [heads][rows][dim] as boxes of box_rows x 64 values, 128-byte swizzled.

@@ -345,10 +345,9 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
                         uint64_t e2[2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            e2[e] = mul2(f2_bits(ex2(fmaf(x[2 * e], c2, -shift)),
-                                                      ex2(fmaf(x[2 * e + 1], c2, -shift))),
-                                              f2_bits(kAttnPScale, kAttnPScale));
-                            split_p(e2[e], pa[nb][2 * e], pa[nb][2 * e + 1]);
+                            e2[e] = f2_bits(ex2(fmaf(x[2 * e], c2, 14.0f - shift)),
+                                            ex2(fmaf(x[2 * e + 1], c2, 14.0f - shift)));  // 2^14 p
+                            split_p(lo_f(e2[e]), hi_f(e2[e]), pa[nb][2 * e], pa[nb][2 * e + 1]);
                         }
                         l2[nb] = fma2(l2[nb], a2[nb], add2(e2[0], e2[1]));
                     }

@@ -30,8 +30,8 @@
 // half.  S is overwritten in place by P (128 columns of 32 bits: hi and lo
 // pairs), which the second product reads from tensor memory.
 //
-// Warps: 0 loads tiles of k and v (TMA, a ring of stages), 1 issues the
-// products, 2 waits for what they need, 3 sees to values that must not count
+// Warps: 0 loads tiles of k and v (TMA, a ring of stages), 1 and 2 issue the
+// products of the two halves in turns, 3 sees to values that must not count
 // (below), 4..7 and 8..11 own the rows of the two halves: thread =
 // tensor-memory lane = row.
 //
@@ -91,13 +91,14 @@ struct Cfg {
 };
 
 struct Shared {
-    uint64_t full[6], empty[6];  // a stage has landed; the products and warp 3 are done with it
+    uint64_t full[6], empty[6];  // a stage has landed; both halves' products and warp 3 are done with it
     uint64_t checked[6];         // warp 3 has looked through a stage (a barrier for each stage: it may be
                                  // several tiles ahead of the products)
     uint64_t qfull[2];           // a half's q planes are in shared memory
     uint64_t sfull[2];           // a half's S of a tile, and O' of the tile before, are complete
-    uint64_t pfull[2];           // a half's P of a tile is in tensor memory, and an O' buffer is free for it
-    uint64_t drain;
+    uint64_t pfull[2][2];        // the first and second half of the keys of a half's P are in tensor memory,
+                                 // and an O' buffer is free
+    uint64_t drain[2];
     uint32_t tmem_base;
     int abort;
     int seq, block;              // this CTA's sequence and block of rows; seq < 0: none
@@ -192,7 +193,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* const stages = smem + C::kQBytes;
     Shared* const sm = reinterpret_cast<Shared*>(stages + NS * C::kStage);
     static_assert(sizeof(Shared) <= 1024, "barrier area");
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // warp-uniform to the compiler, so that roles and loop counts stay in uniform registers
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     grid_dependency_wait();
     const int head = blockIdx.x % p.kv_heads;
@@ -202,15 +204,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 64) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(&sm->full[i], 1);
-            mbar_init(&sm->empty[i], 2);
+            mbar_init(&sm->empty[i], 3);
             mbar_init(&sm->checked[i], 1);
         }
         for (int h = 0; h < 2; ++h) {
             mbar_init(&sm->qfull[h], 4);
             mbar_init(&sm->sfull[h], 1);
-            mbar_init(&sm->pfull[h], 4);
+            mbar_init(&sm->pfull[h][0], 4);
+            mbar_init(&sm->pfull[h][1], 4);
         }
-        mbar_init(&sm->drain, 1);
+        mbar_init(&sm->drain[0], 1);
+        mbar_init(&sm->drain[1], 1);
         sm->abort = 0;
         for (int h = 0; h < 2; ++h) {
             sm->most[h] = 0;
@@ -270,10 +274,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // All 512 columns are this CTA's, so they begin at 0: tensor-memory addresses
     // are constants to the issuing warp.
     const bool at_zero = sm->tmem_base == 0;
-    const int n0 = (sm->most[0] + BN - 1) / BN, n1 = (sm->most[1] + BN - 1) / BN;
+    const int n0 = __shfl_sync(0xffffffffu, (sm->most[0] + BN - 1) / BN, 0);
+    const int n1 = __shfl_sync(0xffffffffu, (sm->most[1] + BN - 1) / BN, 0);
     const int n = max(n0, n1), most = max(sm->most[0], sm->most[1]);
     // tiles from this one on are seen only in part by some row
-    const int edge = min(n0 > 0 ? sm->least[0] : INT32_MAX, n1 > 0 ? sm->least[1] : INT32_MAX) / BN;
+    const int edge = __shfl_sync(
+        0xffffffffu, min(n0 > 0 ? sm->least[0] : INT32_MAX, n1 > 0 ? sm->least[1] : INT32_MAX) / BN, 0);
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtrlRegs));
@@ -316,119 +322,118 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = max(0, i - NS); j < i; ++j)
                     attn_drain_wait(&sm->full[j % NS], (j / NS) & 1);
             }
-        } else if (warp == 1) {
-            // ---------------- products
-            // This warp only issues: warp 2 waits for what a step needs and hands
-            // the step over at a named barrier (a test of an mbarrier takes hundreds
-            // of cycles while the tensor cores stream operands from shared memory).
-            // Each product is issued from one place, so that a tile's code stays
-            // in the instruction caches.  Descriptors are their low 32 bits
-            // (address, leading offset); the high ones are the same for all.
-            const uint32_t leader = lane == 0;
-            const uint32_t q_lo32 = desc_lo(smem_u32(smem), 16), k_lo32 = desc_lo(smem_u32(stages), 16);
-            const uint32_t v_lo32 = desc_lo(smem_u32(stages), BN * 128);
-            constexpr uint32_t kQPlane = C::kQTile >> 4, kKvPlane = C::kPlane >> 4, kKvStage = C::kStage >> 4;
+        } else if (warp < 3) {
+            // ---------------- products: warp 1 issues those of the first half, warp 2 of the second
+            // One lane issues in a branch of its own with constant accumulator
+            // addresses: 65 cycles for a 128 x 128 x 16 product, the tensor
+            // cores' rate (measured; 73 with the whole warp predicated, which
+            // does not keep them busy).  The halves take turns, step by step
+            // (named barriers 2 and 3): products of both mixed would leave the
+            // two softmaxes at the same time, and the tensor cores idle then.
+            const int h = warp - 1, nh = h ? n1 : n0;
+            const uint32_t qhi = desc_lo(smem_u32(smem), 16) + h * 2 * (C::kQTile >> 4), qlo = qhi + (C::kQTile >> 4);
+            const uint32_t k_lo32 = desc_lo(smem_u32(stages), 16), v_lo32 = desc_lo(smem_u32(stages), BN * 128);
+            constexpr uint32_t kKvPlane = C::kPlane >> 4, kKvStage = C::kStage >> 4;
+            const uint32_t ds = h * 128;
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, int phase) {
+                ok = ok && attn_wait(bar, phase & 1, &sm->abort, kFaultAttnMma);
+            };
             // S: a and b at q's and k's planes; how: 0 fresh, 1 added, 2 added to 2^-10 of what is there
-            auto chain = [&](uint32_t d, uint32_t qd, uint32_t kd, int how) {
+            auto chain = [&](uint32_t qd, uint32_t kd, int how) {
 #pragma unroll
                 for (int t = 0; t < DP / 16; ++t) {
                     const uint32_t da = qd + (t / 4) * (128 * 128 >> 4) + (t % 4) * 2;
                     const uint32_t db = kd + (t / 4) * (BN * 128 >> 4) + (t % 4) * 2;
                     if (t == 0 && how == 2)
-                        umma_w_scale10_by(leader, d, da, db, kDescHi, C::kIdescS);
+                        umma_w_scale10_by(1, ds, da, db, kDescHi, C::kIdescS);
                     else
-                        umma_w_by(leader, d, da, db, kDescHi, C::kIdescS, t > 0 || how > 0);
+                        umma_w_by(1, ds, da, db, kDescHi, C::kIdescS, t > 0 || how > 0);
                 }
             };
-            bool ok = true;
-            int step = 0, sk = 0, sv = NS - 1;  // stages of K of tile j + 1 and V of tile j
-            for (int j = -1; ok && j < n; ++j) {
+            int sk = 0, sv = NS - 1;  // stages of K of tile j + 1 and V of tile j
 #pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    const int nh = h ? n1 : n0;
-                    const bool has_v = j >= 0 && j < nh, has_k = j + 1 < nh;
-                    if (!has_v && !has_k)
-                        continue;
-                    ok = bar_red_and(2 + (step++ & 1), 64, true);
-                    if (!ok)
-                        break;
-                    tc_fence_after();
+            for (int j = -1; j < n; ++j) {
+                const int iv = 2 * j + 1, ik = 2 * j + 2;  // their loads
+                const bool has_v = j >= 0 && j < nh, has_k = j + 1 < nh;
+                if (elect_one()) {
                     if (has_v) {
-                        // P of 16 keys: 8 columns of hi pairs, then 8 of lo pairs
-                        const uint32_t pt = h * 128, d = 256 + h * 128 + (OB == 2 ? (j & 1) * 64 : 0);
+                        wait(&sm->full[sv], iv / NS);
+                        if (j >= edge)
+                            wait(&sm->checked[sv], iv / NS);
+                    }
+                    if (has_v)
+                        wait(&sm->pfull[h][0], j);
+                    else if (has_k)
+                        wait(&sm->qfull[h], 0);
+                }
+                __syncwarp();
+                // the turn: the second half waits for the first half's step, the first for the second's before
+                if (h == 1 || j >= 0)
+                    asm volatile("bar.sync %0, 64;" ::"r"(3 - h) : "memory");
+                if (elect_one()) {
+                    tc_fence_after();
+                    if (has_v && ok) {
+                        // P of 16 keys: 8 columns of hi pairs, then 8 of lo pairs.
+                        // The first half of the keys, then, as soon as its P is
+                        // there, the second.
+                        constexpr int kSteps = BN / 32;
+                        const uint32_t d = 256 + h * 128 + (OB == 2 ? (j & 1) * 64 : 0);
                         const uint32_t vhi = v_lo32 + sv * kKvStage, vlo = vhi + kKvPlane;
+                        auto part = [&](int t0) {
+#pragma unroll
+                            for (int t = t0; t < t0 + kSteps; ++t) {
+                                if (PL == 1) {
+                                    umma_ta_w_by(1, d, ds + t * 16 + 8, vhi + t * 128, kDescHi, C::kIdescO, t > 0);
+                                    umma_ta_w_by(1, d, ds + t * 16, vhi + t * 128, kDescHi, C::kIdescO, 1);
+                                } else {  // hi P with lo v, over all keys before the accumulator is scaled
+                                    umma_ta_w_by(1, d, ds + t * 16, vlo + t * 128, kDescHi, C::kIdescO, t > 0);
+                                }
+                            }
+                        };
+                        part(0);
+                        wait(&sm->pfull[h][1], j);
+                        tc_fence_after();
+                        part(kSteps);
                         if (PL == 2) {
 #pragma unroll
-                            for (int t = 0; t < BN / 16; ++t)
-                                umma_ta_w_by(leader, d, pt + t * 16, vlo + t * 128, kDescHi, C::kIdescO, t > 0);
+                            for (int t = 0; t < 2 * kSteps; ++t) {
+                                if (t == 0)
+                                    umma_ta_w_scale10_by(1, d, ds + 8, vhi, kDescHi, C::kIdescO);
+                                else
+                                    umma_ta_w_by(1, d, ds + t * 16 + 8, vhi + t * 128, kDescHi, C::kIdescO, 1);
+                                umma_ta_w_by(1, d, ds + t * 16, vhi + t * 128, kDescHi, C::kIdescO, 1);
+                            }
                         }
-#pragma unroll
-                        for (int t = 0; t < BN / 16; ++t) {
-                            if (t == 0 && PL == 2)
-                                umma_ta_w_scale10_by(leader, d, pt + t * 16 + 8, vhi + t * 128, kDescHi, C::kIdescO);
-                            else
-                                umma_ta_w_by(leader, d, pt + t * 16 + 8, vhi + t * 128, kDescHi, C::kIdescO, t > 0);
-                            umma_ta_w_by(leader, d, pt + t * 16, vhi + t * 128, kDescHi, C::kIdescO, 1);
-                        }
-                        if (h == 1 || j >= n1)
-                            umma_commit_by(leader, &sm->empty[sv]);
                     }
-                    if (has_k) {
-                        const uint32_t d = h * 128, qhi = q_lo32 + h * 2 * kQPlane, khi = k_lo32 + sk * kKvStage;
-                        chain(d, qhi + kQPlane, khi, 0);
+                    if (j >= 0)
+                        umma_commit_by(1, &sm->empty[sv]);
+                    if (has_k)
+                        wait(&sm->full[sk], ik / NS);
+                    if (has_k && ok) {
+                        tc_fence_after();
+                        const uint32_t khi = k_lo32 + sk * kKvStage;
+                        chain(qlo, khi, 0);
                         if (PL == 2)
-                            chain(d, qhi, khi + kKvPlane, 1);
-                        chain(d, qhi, khi, 2);
+                            chain(qhi, khi + kKvPlane, 1);
+                        chain(qhi, khi, 2);
                     }
-                    umma_commit_by(leader, &sm->sfull[h]);
-                    if (has_k && (h == 1 || j + 1 >= n1))
-                        umma_commit_by(leader, &sm->empty[sk]);
+                    if ((has_v || has_k) && ok)
+                        umma_commit_by(1, &sm->sfull[h]);
+                    if (j + 1 < n)
+                        umma_commit_by(1, &sm->empty[sk]);
                 }
+                __syncwarp();
+                if (h == 0 || j + 1 < n)
+                    asm volatile("bar.arrive %0, 64;" ::"r"(2 + h) : "memory");
                 sk = sk + 2 >= NS ? sk + 2 - NS : sk + 2;
                 sv = sv + 2 >= NS ? sv + 2 - NS : sv + 2;
             }
-            if (!ok) {
-                umma_commit_by(leader, &sm->drain);
-                attn_drain_wait(&sm->drain, 0);
+            if (elect_one() && *reinterpret_cast<volatile int*>(&sm->abort)) {
+                umma_commit_by(1, &sm->drain[h]);
+                attn_drain_wait(&sm->drain[h], 0);
             }
-        } else if (warp == 2) {
-            // ---------------- waits for the products, step by step
-            bool ok = true;
-            auto wait = [&](uint64_t* bar, int phase) {
-                if (ok && lane == 0)
-                    ok = attn_wait(bar, phase & 1, &sm->abort, kFaultAttnMma);
-            };
-            int step = 0;
-            for (int j = -1; ok && j < n; ++j) {
-                const int iv = 2 * j + 1, ik = 2 * j + 2;  // loads of V of tile j and K of tile j + 1
-                bool v_here = false, k_here = false;
-                for (int h = 0; h < 2; ++h) {
-                    const int nh = h ? n1 : n0;
-                    const bool has_v = j >= 0 && j < nh, has_k = j + 1 < nh;
-                    if (!has_v && !has_k)
-                        continue;
-                    if (has_v) {
-                        if (!v_here) {
-                            wait(&sm->full[iv % NS], iv / NS);
-                            if (j >= edge)
-                                wait(&sm->checked[iv % NS], iv / NS);
-                            v_here = true;
-                        }
-                        wait(&sm->pfull[h], j);
-                    }
-                    if (has_k) {
-                        if (!k_here)
-                            wait(&sm->full[ik % NS], ik / NS);
-                        k_here = true;
-                        if (j < 0)
-                            wait(&sm->qfull[h], 0);
-                    }
-                    // lane 0's observations reach the issuing warp through the barrier
-                    ok = bar_red_and(2 + (step++ & 1), 64, ok);
-                    if (!ok)
-                        break;
-                }
-            }
+            __syncwarp();
         } else {
             // ---------------- values that must not count
             for (int i = 0; i < 2 * n; ++i) {
@@ -530,17 +535,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto take = [&](int j) {
             const uint64_t a2 = f2_bits(alpha, alpha);
             const uint32_t from = lanes + 256 + half * 128 + (OB == 2 ? (j & 1) * 64 : 0);
-            uint32_t r[2][16];
-            tmem_ld16(from, r[0]);
+            uint32_t r[2][32];
+            tmem_ld32(from, r[0]);
 #pragma unroll
-            for (int c = 0; c < DP / 16; ++c) {
-                uint32_t (&x)[16] = r[c & 1];
-                tmem_ld_wait16(x);
-                if (c + 1 < DP / 16)
-                    tmem_ld16(from + (c + 1) * 16, r[(c + 1) & 1]);
+            for (int c = 0; c < DP / 32; ++c) {
+                uint32_t (&x)[32] = r[c & 1];
+                tmem_ld_wait32(x);
+                if (c + 1 < DP / 32)
+                    tmem_ld32(from + (c + 1) * 32, r[(c + 1) & 1]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    o[c * 8 + i] = fma2(o[c * 8 + i], a2, u2_bits(x[2 * i], x[2 * i + 1]));
+                for (int i = 0; i < 16; ++i)
+                    o[c * 16 + i] = fma2(o[c * 16 + i], a2, u2_bits(x[2 * i], x[2 * i + 1]));
             }
         };
 
@@ -549,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // while the tensor cores go on.
 #pragma unroll 1
         for (int j = 0; j <= nh && nh > 0; ++j) {
-            if (!attn_warp_wait(&sm->sfull[half], j & 1, &sm->abort, kFaultAttnRows)) {
+            if (!attn_lane0_wait(&sm->sfull[half], j & 1, &sm->abort, kFaultAttnRows)) {
                 ok = false;
                 break;
             }
@@ -574,18 +579,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tmem_st_wait();
                 }
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                {
+                    uint32_t r[2][32];
+                    tmem_ld32(st, r[0]);
+#pragma unroll
+                    for (int c = 0; c < BN / 32; ++c) {
+                        uint32_t (&x)[32] = r[c & 1];
+                        tmem_ld_wait32(x);
+                        if (c + 1 < BN / 32)
+                            tmem_ld32(st + (c + 1) * 32, r[(c + 1) & 1]);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2)
+                            top[i / 2 & 3] =
+                                fmaxf(top[i / 2 & 3], fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
+                    }
+                }
                 uint32_t r[2][16];
                 tmem_ld16(st, r[0]);
-                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int c = 0; c < BN / 16; ++c) {
-                    uint32_t (&x)[16] = r[c & 1];
-                    tmem_ld_wait16(x);
-                    tmem_ld16(st + (c + 1) % (BN / 16) * 16, r[(c + 1) & 1]);
-#pragma unroll
-                    for (int i = 0; i < 16; i += 2)
-                        top[i / 2 & 3] = fmaxf(top[i / 2 & 3], fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
-                }
                 const float m_new = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c2);
                 const float shift = m_new == -INFINITY ? 0.0f : m_new;  // nothing seen yet: every p is 0
                 const float alpha_new = ex2(m - shift);
@@ -594,7 +605,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // 2^14 p in one operation: the sum's rounding, at most 2^-21 of 14,
                 // is of the size of the scores' own
                 const uint64_t s2 = f2_bits(14.0f - shift, 14.0f - shift);
-                // r[0] holds the first 16 scores again
 #pragma unroll 1
                 for (int c = 0; c < BN; c += 32) {
 #pragma unroll
@@ -607,19 +617,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const uint64_t y = fma2(u2_bits(x[2 * i], x[2 * i + 1]), c22, s2);
-                            const uint64_t w = f2_bits(ex2(lo_f(y)), ex2(hi_f(y)));
-                            l2 = add2(l2, w);
-                            split_p(w, out[i], out[8 + i]);
+                            const float w0 = ex2(lo_f(y)), w1 = ex2(hi_f(y));
+                            l2 = add2(l2, f2_bits(w0, w1));
+                            split_p(w0, w1, out[i], out[8 + i]);
                         }
                         tmem_st16(st + c + e * 16, out);
                     }
+                    if (c == BN / 2 - 32 || c == BN - 32) {
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(&sm->pfull[half][c >= BN / 2]);
+                    }
                 }
                 tmem_ld_wait16(r[0]);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&sm->pfull[half]);
                 if (OB == 2 && j > 0)
                     take(j - 1);
                 alpha = alpha_new;
