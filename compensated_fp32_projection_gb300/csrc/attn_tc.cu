@@ -96,8 +96,6 @@ struct Shared {
                                  // several tiles ahead of the products)
     uint64_t qfull[2];           // a half's q planes are in shared memory
     uint64_t sfull[2];           // a half's S of a tile, and O' of the tile before, are complete
-    uint64_t pfull[2][2];        // the first and second half of the keys of a half's P are in tensor memory,
-                                 // and an O' buffer is free
     uint64_t drain[2];
     uint32_t tmem_base;
     int abort;
@@ -137,6 +135,17 @@ constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_lo(uint32_t smem_addr, uint32_t leading)
 {
     return ((smem_addr & 0x3FFFFu) >> 4) | ((leading >> 4) << 16);
+}
+
+// Named barriers of a half's four row warps and its issuing warp.
+__device__ __forceinline__ void rows_sync(int id)
+{
+    asm volatile("bar.sync %0, 160;" ::"r"(id) : "memory");
+}
+
+__device__ __forceinline__ void rows_arrive(int id)
+{
+    asm volatile("bar.arrive %0, 160;" ::"r"(id) : "memory");
 }
 
 // This CTA's sequence and block of 256 rows: blocks are numbered sequence by
@@ -210,8 +219,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int h = 0; h < 2; ++h) {
             mbar_init(&sm->qfull[h], 4);
             mbar_init(&sm->sfull[h], 1);
-            mbar_init(&sm->pfull[h][0], 4);
-            mbar_init(&sm->pfull[h][1], 4);
         }
         mbar_init(&sm->drain[0], 1);
         mbar_init(&sm->drain[1], 1);
@@ -274,8 +281,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // All 512 columns are this CTA's, so they begin at 0: tensor-memory addresses
     // are constants to the issuing warp.
     const bool at_zero = sm->tmem_base == 0;
-    const int n0 = __shfl_sync(0xffffffffu, (sm->most[0] + BN - 1) / BN, 0);
-    const int n1 = __shfl_sync(0xffffffffu, (sm->most[1] + BN - 1) / BN, 0);
+    if (!at_zero && threadIdx.x == 0)
+        atomicCAS(&g_attn_fault_word, 0u, kFaultAttnTmem);
+    const int n0 = __shfl_sync(0xffffffffu, at_zero ? (sm->most[0] + BN - 1) / BN : 0, 0);
+    const int n1 = __shfl_sync(0xffffffffu, at_zero ? (sm->most[1] + BN - 1) / BN : 0, 0);
     const int n = max(n0, n1), most = max(sm->most[0], sm->most[1]);
     // tiles from this one on are seen only in part by some row
     const int edge = __shfl_sync(
@@ -283,12 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtrlRegs));
-        if (!at_zero) {
-            if (threadIdx.x == 0) {
-                atomicCAS(&g_attn_fault_word, 0u, kFaultAttnTmem);
-                *reinterpret_cast<volatile int*>(&sm->abort) = 1;
-            }
-        } else if (warp == 0) {
+        if (warp == 0) {
             // ---------------- loads: K0, V0, K1, V1, ...
             const int pieces = p.page_size ? BN / p.page_size : 1;
             const int boxes = PL * C::kBoxes * pieces;
@@ -330,6 +334,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // does not keep them busy).  The halves take turns, step by step
             // (named barriers 2 and 3): products of both mixed would leave the
             // two softmaxes at the same time, and the tensor cores idle then.
+            // P arrives by named barriers too (4 to 7: half and part): a test of an
+            // mbarrier takes hundreds of cycles while operands stream from shared
+            // memory.  After an abort every warp still goes through its barriers.
             const int h = warp - 1, nh = h ? n1 : n0;
             const uint32_t qhi = desc_lo(smem_u32(smem), 16) + h * 2 * (C::kQTile >> 4), qlo = qhi + (C::kQTile >> 4);
             const uint32_t k_lo32 = desc_lo(smem_u32(stages), 16), v_lo32 = desc_lo(smem_u32(stages), BN * 128);
@@ -362,38 +369,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (j >= edge)
                             wait(&sm->checked[sv], iv / NS);
                     }
-                    if (has_v)
-                        wait(&sm->pfull[h][0], j);
-                    else if (has_k)
+                    if (has_k && !has_v)
                         wait(&sm->qfull[h], 0);
                 }
                 __syncwarp();
+                if (has_v)
+                    rows_sync(4 + 2 * h);
                 // the turn: the second half waits for the first half's step, the first for the second's before
                 if (h == 1 || j >= 0)
                     asm volatile("bar.sync %0, 64;" ::"r"(3 - h) : "memory");
-                if (elect_one()) {
+                // P of 16 keys: 8 columns of hi pairs, then 8 of lo pairs.  The first
+                // half of the keys, then, as soon as its P is there, the second.
+                constexpr int kSteps = BN / 32;
+                const uint32_t d = 256 + h * 128 + (OB == 2 ? (j & 1) * 64 : 0);
+                const uint32_t vhi = v_lo32 + sv * kKvStage, vlo = vhi + kKvPlane;
+                auto part = [&](int t0) {
                     tc_fence_after();
-                    if (has_v && ok) {
-                        // P of 16 keys: 8 columns of hi pairs, then 8 of lo pairs.
-                        // The first half of the keys, then, as soon as its P is
-                        // there, the second.
-                        constexpr int kSteps = BN / 32;
-                        const uint32_t d = 256 + h * 128 + (OB == 2 ? (j & 1) * 64 : 0);
-                        const uint32_t vhi = v_lo32 + sv * kKvStage, vlo = vhi + kKvPlane;
-                        auto part = [&](int t0) {
 #pragma unroll
-                            for (int t = t0; t < t0 + kSteps; ++t) {
-                                if (PL == 1) {
-                                    umma_ta_w_by(1, d, ds + t * 16 + 8, vhi + t * 128, kDescHi, C::kIdescO, t > 0);
-                                    umma_ta_w_by(1, d, ds + t * 16, vhi + t * 128, kDescHi, C::kIdescO, 1);
-                                } else {  // hi P with lo v, over all keys before the accumulator is scaled
-                                    umma_ta_w_by(1, d, ds + t * 16, vlo + t * 128, kDescHi, C::kIdescO, t > 0);
-                                }
-                            }
-                        };
+                    for (int t = t0; t < t0 + kSteps; ++t) {
+                        if (PL == 1) {
+                            umma_ta_w_by(1, d, ds + t * 16 + 8, vhi + t * 128, kDescHi, C::kIdescO, t > 0);
+                            umma_ta_w_by(1, d, ds + t * 16, vhi + t * 128, kDescHi, C::kIdescO, 1);
+                        } else {  // hi P with lo v, over all keys before the accumulator is scaled
+                            umma_ta_w_by(1, d, ds + t * 16, vlo + t * 128, kDescHi, C::kIdescO, t > 0);
+                        }
+                    }
+                };
+                if (has_v) {
+                    if (elect_one() && ok)
                         part(0);
-                        wait(&sm->pfull[h][1], j);
-                        tc_fence_after();
+                    __syncwarp();
+                    rows_sync(5 + 2 * h);
+                }
+                if (elect_one()) {
+                    if (has_v && ok) {
                         part(kSteps);
                         if (PL == 2) {
 #pragma unroll
@@ -420,12 +429,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if ((has_v || has_k) && ok)
                         umma_commit_by(1, &sm->sfull[h]);
-                    if (j + 1 < n)
-                        umma_commit_by(1, &sm->empty[sk]);
                 }
                 __syncwarp();
                 if (h == 0 || j + 1 < n)
                     asm volatile("bar.arrive %0, 64;" ::"r"(2 + h) : "memory");
+                if (elect_one() && j + 1 < n)
+                    umma_commit_by(1, &sm->empty[sk]);
+                __syncwarp();
                 sk = sk + 2 >= NS ? sk + 2 - NS : sk + 2;
                 sv = sv + 2 >= NS ? sv + 2 - NS : sv + 2;
             }
@@ -556,6 +566,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j <= nh && nh > 0; ++j) {
             if (!attn_lane0_wait(&sm->sfull[half], j & 1, &sm->abort, kFaultAttnRows)) {
                 ok = false;
+                for (; j < nh; ++j) {  // the issuing warp waits for the rest of P
+                    rows_sync(4 + 2 * half);
+                    rows_sync(5 + 2 * half);
+                }
                 break;
             }
             tc_fence_after();
@@ -595,8 +609,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 fmaxf(top[i / 2 & 3], fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
                     }
                 }
-                uint32_t r[2][16];
-                tmem_ld16(st, r[0]);
+                uint32_t x[32];
+                tmem_ld32(st, x);
                 const float m_new = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c2);
                 const float shift = m_new == -INFINITY ? 0.0f : m_new;  // nothing seen yet: every p is 0
                 const float alpha_new = ex2(m - shift);
@@ -605,20 +619,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // 2^14 p in one operation: the sum's rounding, at most 2^-21 of 14,
                 // is of the size of the scores' own
                 const uint64_t s2 = f2_bits(14.0f - shift, 14.0f - shift);
+                uint64_t l3 = 0;
 #pragma unroll 1
                 for (int c = 0; c < BN; c += 32) {
+                    float w[32];
+                    tmem_ld_wait32(x);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const uint64_t y = fma2(u2_bits(x[2 * i], x[2 * i + 1]), c22, s2);
+                        w[2 * i] = ex2(lo_f(y));
+                        w[2 * i + 1] = ex2(hi_f(y));
+                    }
+                    // the last of these reads P, and is not used
+                    tmem_ld32(st + (c + 32) % BN, x);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        uint32_t (&x)[16] = r[e];
-                        tmem_ld_wait16(x);
-                        // the last of these reads P, and is not used
-                        tmem_ld16(st + (c + e * 16 + 16) % BN, r[1 - e]);
                         uint32_t out[16];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const uint64_t y = fma2(u2_bits(x[2 * i], x[2 * i + 1]), c22, s2);
-                            const float w0 = ex2(lo_f(y)), w1 = ex2(hi_f(y));
-                            l2 = add2(l2, f2_bits(w0, w1));
+                            const float w0 = w[e * 16 + 2 * i], w1 = w[e * 16 + 2 * i + 1];
+                            (e ? l3 : l2) = add2(e ? l3 : l2, f2_bits(w0, w1));
                             split_p(w0, w1, out[i], out[8 + i]);
                         }
                         tmem_st16(st + c + e * 16, out);
@@ -626,12 +646,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (c == BN / 2 - 32 || c == BN - 32) {
                         tmem_st_wait();
                         tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(&sm->pfull[half][c >= BN / 2]);
+                        rows_arrive(4 + 2 * half + (c >= BN / 2));
                     }
                 }
-                tmem_ld_wait16(r[0]);
+                l2 = add2(l2, l3);
+                tmem_ld_wait32(x);
                 if (OB == 2 && j > 0)
                     take(j - 1);
                 alpha = alpha_new;
