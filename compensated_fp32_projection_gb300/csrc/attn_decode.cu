@@ -49,7 +49,7 @@ struct Cfg {
     static constexpr uint32_t kPlane = kTile * DP * 2;
     static constexpr uint32_t kStage = 2 * kPlane;          // k, v
     static constexpr int NS = DP == 128 ? 3 : 6;            // 96 KB: with NB = 1 two CTAs fit an SM
-    static constexpr uint32_t kJoin = (kWarps - 1) * NB * 8 * DP * 4;
+    static constexpr uint32_t kJoin = (kWarps - 1) * NB * 8 * DP * 4;  // three quarters of four warps' sums
     static constexpr size_t kSmem = 1024 + NS * kStage + kJoin + 1024;
 };
 
@@ -57,6 +57,8 @@ struct Shared {
     uint64_t full[6], empty[6];
     float m[kWarps][16], l[kWarps][16];
     int abort;
+    int begin, end;      // this CTA's piece of the line
+    int b, unit, tile;   // where it begins
 };
 
 struct Params {
@@ -67,83 +69,62 @@ struct Params {
     float* part_lse;        // [2 * ctas][NB * 8]
     const int32_t* table;
     const int32_t* lengths;
-    int64_t q_token, q_head;
-    int64_t width, pages;
-    int batch, heads, kv_heads, group, row_blocks, dim, page_size, shared, ctas, vec_q;
+    int64_t q_token, q_head, width;
+    int batch, heads, kv_heads, group, row_blocks, dim, page_shift, pages, shared_keys, most_keys, ctas, vec_q;
     float scale;
 };
 
-// Tiles of a sequence beyond the shared pages.
-__device__ __forceinline__ int tiles_of(const Params& p, int b, int* own)
+// Keys of a sequence beyond the shared pages, and their tiles.
+__device__ __forceinline__ int own_keys(const Params& p, int b)
 {
-    int64_t n = p.lengths[b];
-    const int64_t most = p.width * p.page_size;
-    n = n < 0 ? 0 : (n > most ? most : n);
-    n -= static_cast<int64_t>(p.shared) * p.page_size;
-    n = n < 0 ? 0 : n;
-    if (own)
-        *own = static_cast<int>(n);
-    return static_cast<int>((n + kTile - 1) / kTile);
+    const int n = p.lengths[b];
+    return max(0, min(n, p.most_keys) - p.shared_keys);
 }
 
-// Sum of tiles_of over b in [0, end) by one warp.
-__device__ __forceinline__ int64_t sum_tiles(const Params& p, int end)
+__device__ __forceinline__ int tiles_of(int own)
 {
-    int64_t n = 0;
+    return (own + kTile - 1) / kTile;
+}
+
+// Sum of the tiles of the sequences before `end` by one warp.
+__device__ __forceinline__ int sum_tiles(const Params& p, int end)
+{
+    int n = 0;
+#pragma unroll 4
     for (int b = threadIdx.x & 31; b < end; b += 32)
-        n += tiles_of(p, b, nullptr);
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-        n += __shfl_xor_sync(0xffffffffu, n, o);
-    return n;
-}
-
-// CTAs that have a piece of the line: each has one tile at least.
-__device__ __forceinline__ int64_t working_ctas(const Params& p, int64_t total)
-{
-    return total < p.ctas ? total : p.ctas;
+        n += tiles_of(own_keys(p, b));
+    return __reduce_add_sync(0xffffffffu, n);
 }
 
 // The line of tiles: sequence by sequence, within one head unit by head unit
-// (a key/value head and a block of its query heads).  A position in it.
-struct Place {
-    int b, unit, tile;  // tile of the row
-    int tiles, own;     // the row's tiles and keys
+// (a key/value head and a block of its query heads), cut into pieces that
+// differ by at most one tile: the first `rest` have one more.
+struct Cut {
+    int ctas, each, rest;
+    __device__ __forceinline__ Cut(const Params& p, int total)
+        : ctas(min(total, p.ctas)), each(ctas > 0 ? total / ctas : 0), rest(ctas > 0 ? total % ctas : 0)
+    {
+    }
+    __device__ __forceinline__ int begin(int cta) const { return cta * each + min(cta, rest); }
+    __device__ __forceinline__ int cta_of(int tile) const
+    {
+        const int big = rest * (each + 1);
+        return tile < big ? tile / (each + 1) : rest + (tile - big) / each;
+    }
 };
 
-// One warp; `at` is below the total.
-__device__ __forceinline__ Place find_place(const Params& p, int64_t at)
+// A row of the line, and a tile of it.
+struct Place {
+    int b, unit, tile, own, tiles;
+};
+
+__device__ __forceinline__ void set_row(const Params& p, Place& r)
 {
-    const int units = p.kv_heads * p.row_blocks, lane = threadIdx.x & 31;
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
-        int own = 0;
-        const int n = b0 + lane < p.batch ? tiles_of(p, b0 + lane, &own) : 0;
-        int64_t x = static_cast<int64_t>(n) * units;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o)
-                x += y;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, x > at);
-        if (hit) {
-            const int src = __ffs(hit) - 1;
-            const int64_t before = __shfl_sync(0xffffffffu, x, src) -
-                                   static_cast<int64_t>(__shfl_sync(0xffffffffu, n, src)) * units;
-            Place r;
-            r.b = b0 + src;
-            r.tiles = __shfl_sync(0xffffffffu, n, src);
-            r.own = __shfl_sync(0xffffffffu, own, src);
-            r.unit = static_cast<int>((at - before) / r.tiles);
-            r.tile = static_cast<int>((at - before) % r.tiles);
-            return r;
-        }
-        at -= __shfl_sync(0xffffffffu, x, 31);
-    }
-    return Place{p.batch, 0, 0, 0, 0};
+    r.own = r.b < p.batch ? own_keys(p, r.b) : 0;
+    r.tiles = tiles_of(r.own);
 }
 
-// The next row with tiles after r's.
+// The next row that has tiles.
 __device__ __forceinline__ void next_row(const Params& p, Place& r)
 {
     r.tile = 0;
@@ -152,8 +133,44 @@ __device__ __forceinline__ void next_row(const Params& p, Place& r)
     r.unit = 0;
     do {
         ++r.b;
-        r.tiles = r.b < p.batch ? tiles_of(p, r.b, &r.own) : 0;
+        set_row(p, r);
     } while (r.tiles == 0 && r.b < p.batch);
+}
+
+// One warp: this CTA's piece, and where it begins.
+__device__ __forceinline__ void find_piece(const Params& p, Shared* sm)
+{
+    const int units = p.kv_heads * p.row_blocks, lane = threadIdx.x & 31;
+    const Cut cut(p, sum_tiles(p, p.batch) * units);
+    const int cta = blockIdx.x;
+    int at = cut.begin(cta);
+    if (lane == 0) {
+        sm->begin = cta < cut.ctas ? at : 0;
+        sm->end = cta < cut.ctas ? cut.begin(cta + 1) : 0;
+    }
+    if (cta >= cut.ctas)
+        return;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        const int n = b0 + lane < p.batch ? tiles_of(own_keys(p, b0 + lane)) : 0;
+        int x = n * units;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o)
+                x += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, x > at);
+        if (hit) {
+            if (lane == __ffs(hit) - 1) {
+                at -= x - n * units;
+                sm->b = b0 + lane;
+                sm->unit = at / n;
+                sm->tile = at % n;
+            }
+            return;
+        }
+        at -= __shfl_sync(0xffffffffu, x, 31);
+    }
 }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4])
@@ -182,6 +199,20 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Where warp `from` leaves its sums of warp `to`'s quarter of the head
+// dimension (pairs of values; the next eight values are four pairs on).
+template <int DP, int NB>
+__device__ __forceinline__ uint64_t* join_place(float* join, int to, int from, int nb, int g, int quad)
+{
+    const int slot = to * (kWarps - 1) + (from < to ? from : from - 1);
+    return reinterpret_cast<uint64_t*>(join) + ((slot * NB + nb) * 8 + g) * (DP / kWarps / 2) + quad;
+}
+
+__device__ __forceinline__ void bar_sync_rows()
+{
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+}
+
 template <int DP, int NB>
 __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
     attn_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
@@ -203,24 +234,42 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
         sm->abort = 0;
         fence_mbar_init();
     }
-    __syncthreads();
+    grid_dependency_launch();
     grid_dependency_wait();
-
-    const int64_t total = sum_tiles(p, p.batch) * p.kv_heads * p.row_blocks;
-    const int64_t ctas = working_ctas(p, total);
-    if (blockIdx.x >= ctas)
+    if (warp == kWarps)
+        find_piece(p, sm);
+    __syncthreads();
+    const int begin = sm->begin, end = sm->end;
+    if (begin == end)
         return;
-    const int64_t begin = total * blockIdx.x / ctas, end = total * (blockIdx.x + 1) / ctas;
-    Place r = find_place(p, begin);
+    Place r{sm->b, sm->unit, sm->tile, 0, 0};
+    set_row(p, r);
 
     if (warp == kWarps) {
-        // ---------------- loads
-        const int box_rows = p.page_size < kTile ? p.page_size : kTile;
-        const int pieces = kTile / box_rows, boxes = 2 * C::kBoxes * pieces;
-        int i = 0;
+        // ---------------- loads: a lane has one box of every tile
+        const int box_rows = min(1 << p.page_shift, kTile), pieces = kTile / box_rows;
+        const int piece = lane % pieces, box = lane / pieces % C::kBoxes, is_v = lane / pieces / C::kBoxes;
+        const bool mine = is_v < 2;
+        const uint32_t to = is_v * C::kPlane + box * (kTile * 128) + piece * box_rows * 128;
+        const CUtensorMap* const map = is_v ? &map_v : &map_k;
+        // the page of this lane's box; one that is not there: a place beyond the
+        // cache, which reads zeros
+        auto page_of = [&](int& slot) {
+            const int key = p.shared_keys + r.tile * kTile + piece * box_rows;
+            const int col = key >> p.page_shift;
+            slot = key & ((1 << p.page_shift) - 1);
+            const int page = mine && r.b < p.batch && col < p.width ? p.table[r.b * p.width + col] : -1;
+            return (page >= 0 && page < p.pages ? page : p.pages) * p.kv_heads + r.unit / p.row_blocks;
+        };
+        int slot, page = page_of(slot), i = 0;
         bool ok = true;
-        for (int64_t at = begin; ok && at < end; ++at, ++i) {
-            const int s = i % NS;
+        for (int at = begin; at < end; ++at, ++i) {
+            const int s = i % NS, now_slot = slot, now_page = page;
+            // the next tile's page is on its way while this one waits
+            if (++r.tile == r.tiles)
+                next_row(p, r);
+            if (at + 1 < end)
+                page = page_of(slot);
             if (i >= NS && !attn_warp_wait(&sm->empty[s], ((i / NS) - 1) & 1, &sm->abort, kFaultDecodeLoad)) {
                 ok = false;
                 break;
@@ -228,25 +277,12 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
             if (lane == 0)
                 mbar_arrive_expect_tx(&sm->full[s], C::kStage);
             __syncwarp();
-            const int head = r.unit / p.row_blocks;
-            for (int b = lane; b < boxes; b += 32) {
-                const int piece = b % pieces, box = b / pieces % C::kBoxes, is_v = b / pieces / C::kBoxes;
-                // r.tile < tiles: the first key of a piece may lie past the length, not past the row's last tile
-                const int64_t key = static_cast<int64_t>(p.shared) * p.page_size + static_cast<int64_t>(r.tile) * kTile +
-                                    piece * box_rows;
-                const int64_t col = key / p.page_size;
-                const int page = col < p.width ? p.table[r.b * p.width + col] : -1;
-                // a page that is not there: a place beyond the cache, which reads zeros
-                tma_load_3d(stages + s * C::kStage + is_v * C::kPlane + box * (kTile * 128) + piece * box_rows * 128,
-                            is_v ? &map_v : &map_k, &sm->full[s], box * 64, static_cast<int>(key % p.page_size),
-                            static_cast<int>((page >= 0 && page < p.pages ? page : p.pages) * p.kv_heads + head));
-            }
+            if (mine)
+                tma_load_3d(stages + s * C::kStage + to, map, &sm->full[s], box * 64, now_slot, now_page);
             __syncwarp();
-            if (++r.tile == r.tiles)
-                next_row(p, r);
         }
         if (!ok)
-            for (int j = i - NS > 0 ? i - NS : 0; j < i; ++j)
+            for (int j = max(0, i - NS); j < i; ++j)
                 attn_drain_wait(&sm->full[j % NS], (j / NS) & 1);
     } else {
         // ---------------- rows
@@ -254,32 +290,50 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
         const float c2 = p.scale * kAttnLog2E;
         bool ok = true;
         int i = 0, fragment = 0;
-        for (int64_t at = begin; at < end; ++fragment) {
-            const int n = static_cast<int>(r.tiles - r.tile < end - at ? r.tiles - r.tile : end - at);
-            const int head = r.unit / p.row_blocks, first_head = r.unit % p.row_blocks * (NB * 8);
-            // the query heads' values, split: rows 0..7 hi, 8..15 lo
-            uint32_t q[NB][DP / 16][4];
+        // The query heads of a row, split: rows 0..7 of a block hi, 8..15 lo.
+        // The next row's values are loaded while this row's tiles are computed.
+        float2 raw[NB][DP / 16][2];
+        auto load_q = [&](const Place& at) {
+            const int head = at.unit / p.row_blocks, first_head = at.unit % p.row_blocks * (NB * 8);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
                 const int hg = first_head + nb * 8 + g;
-                const float* const src = p.q + r.b * p.q_token + (head * p.group + hg) * p.q_head;
+                const float* const src = p.q + at.b * p.q_token + (head * p.group + hg) * p.q_head;
+                const bool there = hg < p.group && at.b < p.batch;
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int d = k * 16 + e * 8 + quad * 2;
+                        const int d = k * 16 + e * 8 + quad * 2;  // the head dimension is a multiple of 8
                         float2 x = make_float2(0.0f, 0.0f);
-                        if (hg < p.group) {
-                            if (p.vec_q && d + 2 <= p.dim) {
+                        if (there && d < p.dim) {
+                            if (p.vec_q) {
                                 x = __ldg(reinterpret_cast<const float2*>(src + d));
                             } else {
-                                x.x = d < p.dim ? __ldg(src + d) : 0.0f;
-                                x.y = d + 1 < p.dim ? __ldg(src + d + 1) : 0.0f;
+                                x.x = __ldg(src + d);
+                                x.y = __ldg(src + d + 1);
                             }
                         }
-                        split2(x.x, x.y, q[nb][k][2 * e], q[nb][k][2 * e + 1]);
+                        raw[nb][k][e] = x;
                     }
             }
+        };
+        load_q(r);
+        for (int at = begin; at < end; ++fragment) {
+            const int n = min(r.tiles - r.tile, end - at);
+            const int head = r.unit / p.row_blocks, first_head = r.unit % p.row_blocks * (NB * 8);
+            uint32_t q[NB][DP / 16][4];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        split2(raw[nb][k][e].x, raw[nb][k][e].y, q[nb][k][2 * e], q[nb][k][2 * e + 1]);
+            Place next = r;
+            next_row(p, next);
+            if (NB == 1 && at + n < end)  // with two blocks the registers do not suffice
+                load_q(next);
             float m[NB];
             uint64_t l2[NB], o[NB][DP / 8];
 #pragma unroll
@@ -382,62 +436,74 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
                 l[nb] += __shfl_xor_sync(0xffffffffu, l[nb], 1);
                 l[nb] += __shfl_xor_sync(0xffffffffu, l[nb], 2);
             }
-            asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");  // warp 0 has read the last row's
+            // each warp joins a quarter of the head dimension and gets the others' sums for it
+            constexpr int kQuarter = DP / 8 / kWarps;
+            bar_sync_rows();  // the last row's have been read
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
                 if (quad == 0) {
                     sm->m[warp][nb * 8 + g] = m[nb];
                     sm->l[warp][nb * 8 + g] = l[nb];
                 }
-                if (warp > 0) {
-                    float* const to = join + (((warp - 1) * NB + nb) * 8 + g) * DP + quad * 2;
 #pragma unroll
-                    for (int t = 0; t < DP / 8; ++t)
-                        *reinterpret_cast<uint64_t*>(to + t * 8) = o[nb][t];
-                }
+                for (int w = 0; w < kWarps; ++w)
+                    if (w != warp) {
+                        uint64_t* const to = join_place<DP, NB>(join, w, warp, nb, g, quad);
+#pragma unroll
+                        for (int t = 0; t < kQuarter; ++t)
+                            to[t * 4] = o[nb][w * kQuarter + t];
+                    }
             }
-            asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
-            if (warp == 0 && ok) {
+            bar_sync_rows();
+            if (ok) {
                 const bool whole = n == r.tiles;
-                const int64_t slot = 2 * blockIdx.x + (fragment > 0 ? 1 : 0);
+                const int slot = 2 * blockIdx.x + (fragment > 0 ? 1 : 0);
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
                     const int row = nb * 8 + g, hg = first_head + row;
-                    float top = m[nb];
+                    float mw[kWarps], top = -INFINITY;
 #pragma unroll
-                    for (int w = 1; w < kWarps; ++w)
-                        top = fmaxf(top, sm->m[w][row]);
+                    for (int w = 0; w < kWarps; ++w) {
+                        mw[w] = sm->m[w][row];
+                        top = fmaxf(top, mw[w]);
+                    }
                     const float shift = top == -INFINITY ? 0.0f : top;
-                    const float w0 = ex2(m[nb] - shift);
-                    float sum = l[nb] * w0;
-                    uint64_t f = f2_bits(w0, w0);
+                    float sum = 0.0f;
+                    uint64_t y[kQuarter] = {};
 #pragma unroll
-                    for (int t = 0; t < DP / 8; ++t)
-                        o[nb][t] = mul2(o[nb][t], f);
+                    for (int w = 0; w < kWarps; ++w) {
+                        const float f = ex2(mw[w] - shift);
+                        sum = fmaf(sm->l[w][row], f, sum);
+                        const uint64_t f2 = f2_bits(f, f);
+                        const uint64_t* const from = join_place<DP, NB>(join, warp, w, nb, g, quad);
 #pragma unroll
-                    for (int w = 1; w < kWarps; ++w) {
-                        const float wf = ex2(sm->m[w][row] - shift);
-                        sum = fmaf(sm->l[w][row], wf, sum);
-                        f = f2_bits(wf, wf);
-                        const float* const from = join + (((w - 1) * NB + nb) * 8 + g) * DP + quad * 2;
+                        for (int t = 0; t < kQuarter; ++t) {
+                            uint64_t x = 0;
+                            if (w != warp) {
+                                x = from[t * 4];
+                            } else {
 #pragma unroll
-                        for (int t = 0; t < DP / 8; ++t)
-                            o[nb][t] = fma2(*reinterpret_cast<const uint64_t*>(from + t * 8), f, o[nb][t]);
+                                for (int v = 0; v < kWarps; ++v)
+                                    x = v == warp ? o[nb][v * kQuarter + t] : x;
+                            }
+                            y[t] = fma2(x, f2, y[t]);
+                        }
                     }
                     if (hg >= p.group)
                         continue;
                     const int64_t at_row = static_cast<int64_t>(r.b) * p.heads + head * p.group + hg;
-                    float* const to = whole ? p.out + at_row * p.dim : p.part_o + (slot * (NB * 8) + row) * p.dim;
-                    const float lsum = sum * (1.0f / kAttnPScale);
+                    float* const to = whole ? p.out + at_row * p.dim
+                                            : p.part_o + (static_cast<int64_t>(slot) * (NB * 8) + row) * p.dim;
                     const float norm = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-                    for (int t = 0; t < DP / 8; ++t) {
-                        const int d = t * 8 + quad * 2;  // the head dimension is a multiple of 8
-                        if (t * 8 < p.dim)
-                            *reinterpret_cast<float2*>(to + d) = make_float2(lo_f(o[nb][t]) * norm, hi_f(o[nb][t]) * norm);
+                    for (int t = 0; t < kQuarter; ++t) {
+                        const int d = (warp * kQuarter + t) * 8 + quad * 2;  // the head dimension is a multiple of 8
+                        if (d < p.dim)
+                            *reinterpret_cast<float2*>(to + d) = make_float2(lo_f(y[t]) * norm, hi_f(y[t]) * norm);
                     }
-                    const float lse = sum == 0.0f ? -INFINITY : fmaf(top, kAttnLn2, logf(lsum));
-                    if (quad == 0) {
+                    if (quad == 0 && warp == 0) {
+                        const float lse =
+                            sum == 0.0f ? -INFINITY : fmaf(top, kAttnLn2, logf(sum * (1.0f / kAttnPScale)));
                         if (!whole)
                             p.part_lse[slot * (NB * 8) + row] = lse;
                         else if (p.lse)
@@ -446,8 +512,9 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
                 }
             }
             at += n;
-            r.tile += n - 1;  // next_row begins at the row's last tile
-            next_row(p, r);
+            r = next;
+            if (NB > 1 && at < end)
+                load_q(r);
         }
     }
 }
@@ -464,6 +531,7 @@ struct Join {
 
 __global__ void __launch_bounds__(256) attn_join_kernel(Params p, Join x)
 {
+    grid_dependency_launch();
     grid_dependency_wait();
     const int lane = threadIdx.x & 31;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -472,30 +540,22 @@ __global__ void __launch_bounds__(256) attn_join_kernel(Params p, Join x)
         return;
     const int b = static_cast<int>(row / p.heads), h = static_cast<int>(row % p.heads);
     const int head = h / p.group, block = h % p.group / x.rows_a_unit, in_block = h % p.group % x.rows_a_unit;
-    const int units = p.kv_heads * p.row_blocks;
-    int own;
-    const int tiles = tiles_of(p, b, &own);
+    const int units = p.kv_heads * p.row_blocks, tiles = tiles_of(own_keys(p, b));
     // the CTAs that have this row's tiles
-    int64_t c0 = 0, c1 = -1, total = 0;
+    int first_slot = 0, own_parts = 0;
     bool whole = false;
     if (tiles > 0) {
-        total = sum_tiles(p, p.batch) * units;
-        const int64_t t0 = sum_tiles(p, b) * units + (head * p.row_blocks + block) * static_cast<int64_t>(tiles);
-        const int64_t ctas = working_ctas(p, total);
-        // the last CTA whose piece begins at or before a tile
-        c0 = ((t0 + 1) * ctas - 1) / total;
-        c1 = ((t0 + tiles) * ctas - 1) / total;
+        const Cut cut(p, sum_tiles(p, p.batch) * units);
+        const int t0 = sum_tiles(p, b) * units + (head * p.row_blocks + block) * tiles;
+        const int c0 = cut.cta_of(t0), c1 = cut.cta_of(t0 + tiles - 1);
         whole = c0 == c1;
         if (whole && x.splits == 0)
             return;  // the output is there
-        // the first part is its CTA's second one if that CTA begins before it
-        c0 = 2 * c0 + (total * c0 / ctas < t0 ? 1 : 0);
-        c1 = 2 * c1;
-        if (c1 < c0)
-            c1 = c0;
+        own_parts = c1 - c0 + 1;
+        first_slot = 2 * c0 + (cut.begin(c0) < t0 ? 1 : 0);  // its CTA begins with another row
     }
-    const int parts = x.splits + (tiles == 0 ? 0 : (whole ? 1 : static_cast<int>((c1 - c0 + 1) / 2) + 1));
-    // slots of a row's parts: c0, then 2 (c0 / 2 + 1), 2 (c0 / 2 + 2), ...
+    const int parts = x.splits + own_parts;
+    // part i: its lse and where its sums are; slots first_slot, then 2 (c0 + 1), 2 (c0 + 2), ...
     auto find = [&](int i, const float*& o) {
         if (i < x.splits) {
             o = x.pre_o + (static_cast<int64_t>(i) * rows + row) * p.dim;
@@ -505,34 +565,44 @@ __global__ void __launch_bounds__(256) attn_join_kernel(Params p, Join x)
             o = p.out + row * p.dim;
             return p.lse[row];
         }
-        const int64_t slot = i == x.splits ? c0 : 2 * (c0 / 2 + i - x.splits);
+        const int64_t slot = i == x.splits ? first_slot : 2 * (first_slot / 2 + i - x.splits);
         o = p.part_o + (slot * x.rows_a_unit + in_block) * p.dim;
         return p.part_lse[slot * x.rows_a_unit + in_block];
     };
-    float top = -INFINITY;
-    for (int i = lane; i < parts; i += 32) {
-        const float* o;
-        const float y = find(i, o);
-        top = isnan(y) ? y : fmaxf(top, y);
-    }
+    float top = -INFINITY, acc[4] = {}, sum = 0.0f;
+    for (int i0 = 0; i0 < parts; i0 += 32) {  // a lane has one part's lse, all lanes share the sums
+        const float* mine = nullptr;
+        const float y = i0 + lane < parts ? find(i0 + lane, mine) : -INFINITY;
+        float t = y;
 #pragma unroll
-    for (int o = 16; o; o >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float shift = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f, acc[4] = {};
-    for (int i = 0; i < parts; ++i) {
-        const float* o;
-        const float y = find(i, o);
-        if (y == -INFINITY)
-            continue;  // sees nothing there
-        const float w = expf(y - shift);
-        sum += w;
-        if (lane * 4 < p.dim) {
-            const float4 v = *reinterpret_cast<const float4*>(o + lane * 4);
-            acc[0] = fmaf(v.x, w, acc[0]);
-            acc[1] = fmaf(v.y, w, acc[1]);
-            acc[2] = fmaf(v.z, w, acc[2]);
-            acc[3] = fmaf(v.w, w, acc[3]);
+        for (int o = 16; o; o >>= 1)
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+        t = fmaxf(top, t);
+        const float shift = t == -INFINITY ? 0.0f : t, a = expf(top - shift);
+        top = t;
+        const float w = expf(y - shift);  // a part that sees nothing weighs nothing; NaN stays NaN
+        float s = w;
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+            s += __shfl_xor_sync(0xffffffffu, s, o);
+        sum = fmaf(sum, a, s);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            acc[e] *= a;
+        const int n = min(32, parts - i0);
+#pragma unroll 8
+        for (int i = 0; i < n; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, w, i);
+            const float* const o = reinterpret_cast<const float*>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), i));
+            if (lane * 4 < p.dim) {
+                const float4 v = *reinterpret_cast<const float4*>(o + lane * 4);
+                // where nothing was seen the sums are 0
+                acc[0] = fmaf(v.x, wi, acc[0]);
+                acc[1] = fmaf(v.y, wi, acc[1]);
+                acc[2] = fmaf(v.z, wi, acc[2]);
+                acc[3] = fmaf(v.w, wi, acc[3]);
+            }
         }
     }
     const float norm = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -540,7 +610,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(Params p, Join x)
         *reinterpret_cast<float4*>(p.out + row * p.dim + lane * 4) =
             make_float4(acc[0] * norm, acc[1] * norm, acc[2] * norm, acc[3] * norm);
     if (x.lse_out && lane == 0)
-        x.lse_out[row] = sum == 0.0f ? -INFINITY : shift + logf(sum);
+        x.lse_out[row] = sum == 0.0f ? -INFINITY : top + logf(sum);
 }
 
 template <int DP, int NB>
@@ -648,15 +718,20 @@ comp_status_t launch_attn_decode(const comp_kv_cache_t& cache, const float* q, i
     p.q_token = q_token;
     p.q_head = q_head;
     p.width = width;
-    p.pages = cache.pages;
+    p.pages = static_cast<int>(cache.pages);
     p.batch = static_cast<int>(batch);
     p.heads = heads;
     p.kv_heads = cache.kv_heads;
     p.group = group;
     p.row_blocks = (group + 8 * nb - 1) / (8 * nb);
     p.dim = cache.head_dim;
-    p.page_size = cache.page_size;
-    p.shared = static_cast<int>(shared);
+    while ((1 << p.page_shift) < cache.page_size)
+        ++p.page_shift;
+    p.shared_keys = static_cast<int>(shared * cache.page_size);
+    p.most_keys = static_cast<int>(width * cache.page_size);
+    // the line of tiles is counted in ints
+    if ((width * cache.page_size / kTile + 1) * batch > INT32_MAX / (p.kv_heads * p.row_blocks))
+        return COMP_ERR_INVALID_VALUE;
     p.ctas = 2 * dev.sm_count < kMostCtas ? 2 * dev.sm_count : kMostCtas;
     p.vec_q = (reinterpret_cast<uintptr_t>(q) & 7u) == 0 && q_token % 2 == 0 && q_head % 2 == 0;
     p.scale = scale;

@@ -205,6 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // warp-uniform to the compiler, so that roles and loop counts stay in uniform registers
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
+    grid_dependency_launch();
     grid_dependency_wait();
     const int head = blockIdx.x % p.kv_heads;
     const int part = blockIdx.x / p.kv_heads % p.splits;
@@ -728,6 +729,7 @@ struct Stage {
 
 __global__ void __launch_bounds__(256) attn_stage_kernel(Stage p)
 {
+    grid_dependency_launch();
     const int w = blockIdx.y, parts = p.dpad / 8;
     const int64_t work = p.tokens * p.heads * parts;
     for (int64_t u = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; u < work;

@@ -12,6 +12,7 @@
 #include <cuda_fp16.h>
 
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace compfp32 {
 namespace {
@@ -467,6 +468,7 @@ __global__ void __launch_bounds__(kCopyThreads) append_kernel(comp_kv_cache_t ca
                                                               int64_t rows, int64_t width, const int32_t* cu,
                                                               const int32_t* start)
 {
+    grid_dependency_launch();
     const int parts = cache.head_dim / 8;
     const int64_t work = total * cache.kv_heads * parts;
     for (int64_t u = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; u < work;

@@ -508,6 +508,11 @@ __device__ __forceinline__ void grid_dependency_wait()
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+__device__ __forceinline__ void grid_dependency_launch()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---------------------------------------------------------------------------
 // Exchanges of generic data between the CTAs of a cluster (distributed shared
 // memory): stores into another CTA's shared memory, published by an arrival
