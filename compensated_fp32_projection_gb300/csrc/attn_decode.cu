@@ -14,16 +14,15 @@
 // older warp-wide instructions serve: tcgen05's 128 rows would be empty.
 //
 // Work.  The tiles of all (sequence, key/value head) rows stand in one line
-// that is cut into equal pieces, one for each CTA: the lengths may differ as
-// they like and no CTA waits for the longest.  A CTA computes its piece row
-// by row; a row that lies wholly in one piece is written to the output, the
-// parts of a row that was cut go to the workspace and are joined by a second
-// launch, in order, as are the parts of a shared prefix (computed for the
-// whole batch by the packed kernel).
-//
-// In a CTA, a warp loads (TMA, one box for each page) and four warps compute:
-// each takes 16 of a tile's 64 keys with its own maximum and sums; they are
-// joined in shared memory at the end of a row.
+// that is cut into equal pieces, one for each warp: the lengths may differ as
+// they like and no warp waits for the longest, nor for any other.  A warp
+// goes through its piece row by row; a row that lies wholly in one piece is
+// written to the output, the parts of a row that was cut go to the workspace
+// and are joined by a second launch, in order, as are the parts of a shared
+// prefix (computed for the whole batch by the packed kernel).  A warp loads
+// its own tiles of 16 keys (TMA, a ring of stages).  An earlier form, four
+// warps sharing tiles of 64 keys of a row and joining at its end, spent more
+// on the joins than on the tiles where rows are short.
 #include <cuda_fp16.h>
 
 #include <cmath>
@@ -36,11 +35,11 @@
 namespace compfp32 {
 namespace {
 
-constexpr int kTile = 64;       // keys of a tile
-constexpr int kWarps = 4;       // computing warps
-constexpr int kThreads = 32 * (kWarps + 1);
-constexpr uint32_t kFaultDecodeLoad = 0xA01;
-constexpr uint32_t kFaultDecodeRows = 0xA02;
+constexpr int kTile = 16;       // keys of a tile, the k of a product
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kLeast = 4;
+constexpr uint32_t kFaultDecode = 0xA01;
 
 // DP: head dimension padded to 64 or 128; NB: blocks of eight query heads.
 template <int DP, int NB>
@@ -48,29 +47,20 @@ struct Cfg {
     static constexpr int kBoxes = DP / 64;
     static constexpr uint32_t kPlane = kTile * DP * 2;
     static constexpr uint32_t kStage = 2 * kPlane;          // k, v
-    static constexpr int NS = DP == 128 ? 3 : 6;            // 96 KB: with NB = 1 two CTAs fit an SM
-    static constexpr uint32_t kJoin = (kWarps - 1) * NB * 8 * DP * 4;  // three quarters of four warps' sums
-    static constexpr size_t kSmem = 1024 + NS * kStage + kJoin + 1024;
-};
-
-struct Shared {
-    uint64_t full[6], empty[6];
-    float m[kWarps][16], l[kWarps][16];
-    int abort;
-    int begin, end;      // this CTA's piece of the line
-    int b, unit, tile;   // where it begins
+    static constexpr int NS = DP == 128 ? 3 : 6;            // 24 KB a warp
+    static constexpr size_t kSmem = 1024 + kWarps * NS * kStage;
 };
 
 struct Params {
     const float* q;
     float* out;
     float* lse;             // [batch, heads] (nullptr: none)
-    float* part_o;          // [2 * ctas][NB * 8][dim]
-    float* part_lse;        // [2 * ctas][NB * 8]
+    float* part_o;          // [2 * pieces][NB * 8][dim]
+    float* part_lse;        // [2 * pieces][NB * 8]
     const int32_t* table;
     const int32_t* lengths;
     int64_t q_token, q_head, width;
-    int batch, heads, kv_heads, group, row_blocks, dim, page_shift, pages, shared_keys, most_keys, ctas, vec_q;
+    int batch, heads, kv_heads, group, row_blocks, dim, page_shift, pages, shared_keys, most_keys, pieces, vec_q;
     float scale;
 };
 
@@ -98,15 +88,16 @@ __device__ __forceinline__ int sum_tiles(const Params& p, int end)
 
 // The line of tiles: sequence by sequence, within one head unit by head unit
 // (a key/value head and a block of its query heads), cut into pieces that
-// differ by at most one tile: the first `rest` have one more.
+// differ by at most one tile: the first `rest` have one more.  A piece has about
+// kLeast tiles at least: a part of a row costs its join more than a tile costs.
 struct Cut {
-    int ctas, each, rest;
+    int pieces, each, rest;
     __device__ __forceinline__ Cut(const Params& p, int total)
-        : ctas(min(total, p.ctas)), each(ctas > 0 ? total / ctas : 0), rest(ctas > 0 ? total % ctas : 0)
+        : pieces(min((total + kLeast - 1) / kLeast, p.pieces)), each(pieces > 0 ? total / pieces : 0), rest(pieces > 0 ? total % pieces : 0)
     {
     }
-    __device__ __forceinline__ int begin(int cta) const { return cta * each + min(cta, rest); }
-    __device__ __forceinline__ int cta_of(int tile) const
+    __device__ __forceinline__ int begin(int piece) const { return piece * each + min(piece, rest); }
+    __device__ __forceinline__ int piece_of(int tile) const
     {
         const int big = rest * (each + 1);
         return tile < big ? tile / (each + 1) : rest + (tile - big) / each;
@@ -137,40 +128,48 @@ __device__ __forceinline__ void next_row(const Params& p, Place& r)
     } while (r.tiles == 0 && r.b < p.batch);
 }
 
-// One warp: this CTA's piece, and where it begins.
-__device__ __forceinline__ void find_piece(const Params& p, Shared* sm)
+// A warp's piece of the line and the place where it begins; false if there is
+// none.  A lane sums the tiles of consecutive sequences.
+__device__ __forceinline__ bool find_piece(const Params& p, int piece, int& begin, int& end, Place& r)
 {
     const int units = p.kv_heads * p.row_blocks, lane = threadIdx.x & 31;
-    const Cut cut(p, sum_tiles(p, p.batch) * units);
-    const int cta = blockIdx.x;
-    int at = cut.begin(cta);
-    if (lane == 0) {
-        sm->begin = cta < cut.ctas ? at : 0;
-        sm->end = cta < cut.ctas ? cut.begin(cta + 1) : 0;
-    }
-    if (cta >= cut.ctas)
-        return;
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
-        const int n = b0 + lane < p.batch ? tiles_of(own_keys(p, b0 + lane)) : 0;
-        int x = n * units;
+    const int each = (p.batch + 31) / 32, first = lane * each, last = min(first + each, p.batch);
+    int mine = 0;
+#pragma unroll 8
+    for (int b = first; b < last; ++b)
+        mine += tiles_of(own_keys(p, b));
+    int x = mine;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o)
-                x += y;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, x > at);
-        if (hit) {
-            if (lane == __ffs(hit) - 1) {
-                at -= x - n * units;
-                sm->b = b0 + lane;
-                sm->unit = at / n;
-                sm->tile = at % n;
-            }
-            return;
-        }
-        at -= __shfl_sync(0xffffffffu, x, 31);
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o)
+            x += y;
     }
+    const Cut cut(p, __shfl_sync(0xffffffffu, x, 31) * units);
+    if (piece >= cut.pieces)
+        return false;
+    begin = cut.begin(piece);
+    end = cut.begin(piece + 1);
+    int at = begin - (x - mine) * units;
+    r = Place{0, 0, 0, 0, 0};
+    const bool here = at >= 0 && at < mine * units;
+    if (here) {
+        for (r.b = first;; ++r.b) {
+            set_row(p, r);
+            if (at < r.tiles * units)
+                break;
+            at -= r.tiles * units;
+        }
+        r.unit = at / r.tiles;
+        r.tile = at % r.tiles;
+    }
+    const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+    r.b = __shfl_sync(0xffffffffu, r.b, src);
+    r.unit = __shfl_sync(0xffffffffu, r.unit, src);
+    r.tile = __shfl_sync(0xffffffffu, r.tile, src);
+    r.own = __shfl_sync(0xffffffffu, r.own, src);
+    r.tiles = __shfl_sync(0xffffffffu, r.tiles, src);
+    return true;
 }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4])
@@ -199,20 +198,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Where warp `from` leaves its sums of warp `to`'s quarter of the head
-// dimension (pairs of values; the next eight values are four pairs on).
-template <int DP, int NB>
-__device__ __forceinline__ uint64_t* join_place(float* join, int to, int from, int nb, int g, int quad)
-{
-    const int slot = to * (kWarps - 1) + (from < to ? from : from - 1);
-    return reinterpret_cast<uint64_t*>(join) + ((slot * NB + nb) * 8 + g) * (DP / kWarps / 2) + quad;
-}
-
-__device__ __forceinline__ void bar_sync_rows()
-{
-    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
-}
-
 template <int DP, int NB>
 __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
     attn_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
@@ -221,302 +206,244 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
     using C = Cfg<DP, NB>;
     constexpr int NS = C::NS;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* const stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float* const join = reinterpret_cast<float*>(stages + NS * C::kStage);
-    Shared* const sm = reinterpret_cast<Shared*>(stages + NS * C::kStage + C::kJoin);
-    static_assert(sizeof(Shared) <= 1024, "shared area");
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(&sm->full[i], 1);
-            mbar_init(&sm->empty[i], kWarps);
-        }
-        sm->abort = 0;
+    __shared__ uint64_t full_of[kWarps][NS];
+    __shared__ int abort_flag[kWarps];
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    uint8_t* const stages =
+        reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023)) +
+        warp * (NS * C::kStage);
+    uint64_t* const full = full_of[warp];
+    if (lane == 0) {
+        for (int i = 0; i < NS; ++i)
+            mbar_init(&full[i], 1);
+        abort_flag[warp] = 0;
         fence_mbar_init();
     }
+    __syncwarp();
     grid_dependency_launch();
     grid_dependency_wait();
-    if (warp == kWarps)
-        find_piece(p, sm);
-    __syncthreads();
-    const int begin = sm->begin, end = sm->end;
-    if (begin == end)
-        return;
-    Place r{sm->b, sm->unit, sm->tile, 0, 0};
-    set_row(p, r);
 
-    if (warp == kWarps) {
-        // ---------------- loads: a lane has one box of every tile
-        const int box_rows = min(1 << p.page_shift, kTile), pieces = kTile / box_rows;
-        const int piece = lane % pieces, box = lane / pieces % C::kBoxes, is_v = lane / pieces / C::kBoxes;
-        const bool mine = is_v < 2;
-        const uint32_t to = is_v * C::kPlane + box * (kTile * 128) + piece * box_rows * 128;
-        const CUtensorMap* const map = is_v ? &map_v : &map_k;
-        // the page of this lane's box; one that is not there: a place beyond the
-        // cache, which reads zeros
-        auto page_of = [&](int& slot) {
-            const int key = p.shared_keys + r.tile * kTile + piece * box_rows;
-            const int col = key >> p.page_shift;
-            slot = key & ((1 << p.page_shift) - 1);
-            const int page = mine && r.b < p.batch && col < p.width ? p.table[r.b * p.width + col] : -1;
-            return (page >= 0 && page < p.pages ? page : p.pages) * p.kv_heads + r.unit / p.row_blocks;
-        };
-        int slot, page = page_of(slot), i = 0;
-        bool ok = true;
-        for (int at = begin; at < end; ++at, ++i) {
-            const int s = i % NS, now_slot = slot, now_page = page;
-            // the next tile's page is on its way while this one waits
-            if (++r.tile == r.tiles)
-                next_row(p, r);
-            if (at + 1 < end)
-                page = page_of(slot);
-            if (i >= NS && !attn_warp_wait(&sm->empty[s], ((i / NS) - 1) & 1, &sm->abort, kFaultDecodeLoad)) {
+    // this warp's piece; consecutive ones are on different SMs
+    const int piece = warp * gridDim.x + blockIdx.x;
+    int begin, end;
+    Place r;
+    if (!find_piece(p, piece, begin, end, r))
+        return;
+
+    // Rows.  The query heads split: rows 0..7 of a block hi, 8..15 lo.
+    const int g = lane >> 2, quad = lane & 3;
+    const float c2 = p.scale * kAttnLog2E;
+    bool ok = true;
+    int i = 0, fragment = 0;
+    float2 raw[NB][DP / 16][2];
+    auto load_q = [&](const Place& at) {
+        const int head = at.unit / p.row_blocks, first_head = at.unit % p.row_blocks * (NB * 8);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            const int hg = first_head + nb * 8 + g;
+            const float* const src = p.q + at.b * p.q_token + (head * p.group + hg) * p.q_head;
+            const bool there = hg < p.group && at.b < p.batch;
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int d = k * 16 + e * 8 + quad * 2;  // the head dimension is a multiple of 8
+                    float2 x = make_float2(0.0f, 0.0f);
+                    if (there && d < p.dim) {
+                        if (p.vec_q) {
+                            x = __ldg(reinterpret_cast<const float2*>(src + d));
+                        } else {
+                            x.x = __ldg(src + d);
+                            x.y = __ldg(src + d + 1);
+                        }
+                    }
+                    raw[nb][k][e] = x;
+                }
+        }
+    };
+    // Loads run NS tiles ahead: lanes 0 .. 2 kBoxes - 1 have a box of each.  The
+    // lanes hold the page numbers of 32 tiles of a row, fetched when the row
+    // is new; one that is not there: a place beyond the cache, which reads
+    // zeros.
+    Place next = r;
+    const int box = lane % C::kBoxes, is_v = lane / C::kBoxes;
+    const bool mine = is_v < 2;
+    const uint32_t to = is_v * C::kPlane + box * (kTile * 128);
+    const CUtensorMap* const map = is_v ? &map_v : &map_k;
+    int pages = 0, page_tile = 0, loads = 0;
+    auto look_up = [&] {
+        page_tile = next.tile;
+        const int col = (p.shared_keys + (next.tile + lane) * kTile) >> p.page_shift;
+        pages = next.tile + lane < next.tiles && col < p.width ? p.table[next.b * p.width + col] : -1;
+    };
+    auto load = [&] {
+        const int s = loads % NS, at = __shfl_sync(0xffffffffu, pages, next.tile - page_tile);
+        const int slot = (p.shared_keys + next.tile * kTile) & ((1 << p.page_shift) - 1);
+        if (lane == 0)
+            mbar_arrive_expect_tx(&full[s], C::kStage);
+        __syncwarp();
+        if (mine)
+            tma_load_3d(stages + s * C::kStage + to, map, &full[s], box * 64, slot,
+                        (at >= 0 && at < p.pages ? at : p.pages) * p.kv_heads + next.unit / p.row_blocks);
+        if (begin + ++loads < end) {
+            if (++next.tile == next.tiles) {
+                next_row(p, next);
+                look_up();
+            } else if (next.tile == page_tile + 32) {
+                look_up();
+            }
+        }
+    };
+    look_up();
+    load_q(r);
+    for (int i = 0; i < NS && begin + i < end; ++i)
+        load();
+
+    for (int at = begin; ok && at < end; ++fragment) {
+        const int n = min(r.tiles - r.tile, end - at);
+        const int head = r.unit / p.row_blocks, first_head = r.unit % p.row_blocks * (NB * 8);
+        uint32_t q[NB][DP / 16][4];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    split2(raw[nb][k][e].x, raw[nb][k][e].y, q[nb][k][2 * e], q[nb][k][2 * e + 1]);
+        Place after = r;
+        if (at + n < end) {
+            next_row(p, after);
+            if (NB == 1)  // with two blocks the registers do not suffice
+                load_q(after);
+        }
+        float m[NB];
+        uint64_t l2[NB], o[NB][DP / 8];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            m[nb] = -INFINITY;
+            l2[nb] = 0;
+#pragma unroll
+            for (int t = 0; t < DP / 8; ++t)
+                o[nb][t] = 0;
+        }
+        for (int t = 0; t < n; ++t, ++i) {
+            const int s = i % NS;
+            if (!attn_warp_wait(&full[s], (i / NS) & 1, &abort_flag[warp], kFaultDecode)) {
                 ok = false;
                 break;
             }
-            if (lane == 0)
-                mbar_arrive_expect_tx(&sm->full[s], C::kStage);
-            __syncwarp();
-            if (mine)
-                tma_load_3d(stages + s * C::kStage + to, map, &sm->full[s], box * 64, now_slot, now_page);
-            __syncwarp();
-        }
-        if (!ok)
-            for (int j = max(0, i - NS); j < i; ++j)
-                attn_drain_wait(&sm->full[j % NS], (j / NS) & 1);
-    } else {
-        // ---------------- rows
-        const int g = lane >> 2, quad = lane & 3;
-        const float c2 = p.scale * kAttnLog2E;
-        bool ok = true;
-        int i = 0, fragment = 0;
-        // The query heads of a row, split: rows 0..7 of a block hi, 8..15 lo.
-        // The next row's values are loaded while this row's tiles are computed.
-        float2 raw[NB][DP / 16][2];
-        auto load_q = [&](const Place& at) {
-            const int head = at.unit / p.row_blocks, first_head = at.unit % p.row_blocks * (NB * 8);
+            uint8_t* const kt = stages + s * C::kStage;
+            uint8_t* const vt = kt + C::kPlane;
+            const int left = r.own - (r.tile + t) * kTile;  // keys of the tile that count
+            if (left < kTile) {
+                // beyond the sequence's end v may hold anything: 0 times that must be 0
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                const int hg = first_head + nb * 8 + g;
-                const float* const src = p.q + at.b * p.q_token + (head * p.group + hg) * p.q_head;
-                const bool there = hg < p.group && at.b < p.batch;
-#pragma unroll
-                for (int k = 0; k < DP / 16; ++k)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int d = k * 16 + e * 8 + quad * 2;  // the head dimension is a multiple of 8
-                        float2 x = make_float2(0.0f, 0.0f);
-                        if (there && d < p.dim) {
-                            if (p.vec_q) {
-                                x = __ldg(reinterpret_cast<const float2*>(src + d));
-                            } else {
-                                x.x = __ldg(src + d);
-                                x.y = __ldg(src + d + 1);
-                            }
-                        }
-                        raw[nb][k][e] = x;
-                    }
+                for (int x = 0; x < C::kBoxes; ++x)
+                    for (int u = lane; u < kTile * 8; u += 32)
+                        if (u / 8 >= left)
+                            *reinterpret_cast<uint4*>(vt + x * (kTile * 128) + u * 16) = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();  // before the next load into this stage
+                __syncwarp();
             }
-        };
-        load_q(r);
-        for (int at = begin; at < end; ++fragment) {
-            const int n = min(r.tiles - r.tile, end - at);
-            const int head = r.unit / p.row_blocks, first_head = r.unit % p.row_blocks * (NB * 8);
-            uint32_t q[NB][DP / 16][4];
+            // two chains for each eight keys, the even and the odd steps of the head dimension
+            float c[NB][2][2][4] = {};
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+            for (int k = 0; k < DP / 16; k += 2)
 #pragma unroll
-                for (int k = 0; k < DP / 16; ++k)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        split2(raw[nb][k][e].x, raw[nb][k][e].y, q[nb][k][2 * e], q[nb][k][2 * e + 1]);
-            Place next = r;
-            next_row(p, next);
-            if (NB == 1 && at + n < end)  // with two blocks the registers do not suffice
-                load_q(next);
-            float m[NB];
-            uint64_t l2[NB], o[NB][DP / 8];
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                m[nb] = -INFINITY;
-                l2[nb] = 0;
-#pragma unroll
-                for (int t = 0; t < DP / 8; ++t)
-                    o[nb][t] = 0;
-            }
-            for (int t = 0; t < n; ++t, ++i) {
-                const int s = i % NS;
-                ok = ok && attn_warp_wait(&sm->full[s], (i / NS) & 1, &sm->abort, kFaultDecodeRows);
-                if (!ok)
-                    continue;  // the joins below still take place, so that no warp waits for another
-                uint8_t* const kt = stages + s * C::kStage;
-                uint8_t* const vt = kt + C::kPlane;
-                const int left = r.own - (r.tile + t) * kTile - warp * 16;  // keys of this warp's 16 that count
-                if (left > 0) {
-                    if (left < 16) {
-                        // beyond the sequence's end v may hold anything: 0 times that must be 0
-#pragma unroll
-                        for (int x = 0; x < C::kBoxes; ++x)
-                            for (int u = lane; u < 16 * 8; u += 32)
-                                if (u / 8 >= left)
-                                    *reinterpret_cast<uint4*>(vt + x * (kTile * 128) + (warp * 16 + u / 8) * 128 +
-                                                              u % 8 * 16) = make_uint4(0, 0, 0, 0);
-                        __syncwarp();
-                    }
-                    float c[NB][2][4] = {};
-#pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        const uint32_t row = warp * 16 + nt * 8 + (lane & 7);
-#pragma unroll
-                        for (int k = 0; k < DP / 16; k += 2) {
-                            uint32_t b[4];
-                            ldmatrix4(smem_u32(kt) + (k / 4) * (kTile * 128) + sw128(row, (k % 4) * 2 + (lane >> 3)), b);
-#pragma unroll
-                            for (int nb = 0; nb < NB; ++nb) {
-                                mma16816(c[nb][nt], q[nb][k], b[0], b[1]);
-                                mma16816(c[nb][nt], q[nb][k + 1], b[2], b[3]);
-                            }
-                        }
-                    }
-                    uint32_t pa[NB][4];
-                    uint64_t a2[NB];
+                for (int nt = 0; nt < 2; ++nt) {
+                    uint32_t b[4];
+                    ldmatrix4(smem_u32(kt) + (k / 4) * (kTile * 128) + sw128(nt * 8 + (lane & 7), (k % 4) * 2 + (lane >> 3)),
+                              b);
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb) {
-                        float x[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int key = (e >> 1) * 8 + quad * 2 + (e & 1);
-                            x[e] = fmaf(c[nb][e >> 1][2 + (e & 1)], 0x1p-10f, c[nb][e >> 1][e & 1]);
-                            x[e] = key < left ? x[e] : -INFINITY;
-                        }
-                        float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * c2;
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                        const float m_new = fmaxf(m[nb], top), shift = m_new == -INFINITY ? 0.0f : m_new;
-                        const float alpha = ex2(m[nb] - shift);
-                        m[nb] = m_new;
-                        a2[nb] = f2_bits(alpha, alpha);
-                        uint64_t e2[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            e2[e] = f2_bits(ex2(fmaf(x[2 * e], c2, 14.0f - shift)),
-                                            ex2(fmaf(x[2 * e + 1], c2, 14.0f - shift)));  // 2^14 p
-                            split_p(lo_f(e2[e]), hi_f(e2[e]), pa[nb][2 * e], pa[nb][2 * e + 1]);
-                        }
-                        l2[nb] = fma2(l2[nb], a2[nb], add2(e2[0], e2[1]));
+                        mma16816(c[nb][nt][0], q[nb][k], b[0], b[1]);
+                        mma16816(c[nb][nt][1], q[nb][k + 1], b[2], b[3]);
                     }
-#pragma unroll
-                    for (int d = 0; d < DP / 16; ++d) {
-                        uint32_t b[4];
-                        const uint32_t row = warp * 16 + (lane & 15);
-                        ldmatrix4_trans(smem_u32(vt) + (d / 4) * (kTile * 128) + sw128(row, (d % 4) * 2 + (lane >> 4)), b);
-#pragma unroll
-                        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                float y[4] = {};
-                                mma16816(y, pa[nb], b[2 * e], b[2 * e + 1]);
-                                o[nb][2 * d + e] = fma2(o[nb][2 * d + e], a2[nb],
-                                                             add2(f2_bits(y[0], y[1]), f2_bits(y[2], y[3])));
-                            }
-                    }
-                    if (left < 16)
-                        fence_proxy_async_smem();  // the zeros, before the next load into this stage
                 }
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&sm->empty[s]);
-            }
-
-            // join the four warps' sums of this row
-            float l[NB];
+            uint32_t pa[NB][4];
+            uint64_t a2[NB];
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-                l[nb] = lo_f(l2[nb]) + hi_f(l2[nb]);
-                l[nb] += __shfl_xor_sync(0xffffffffu, l[nb], 1);
-                l[nb] += __shfl_xor_sync(0xffffffffu, l[nb], 2);
-            }
-            // each warp joins a quarter of the head dimension and gets the others' sums for it
-            constexpr int kQuarter = DP / 8 / kWarps;
-            bar_sync_rows();  // the last row's have been read
+                float x[4];
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                if (quad == 0) {
-                    sm->m[warp][nb * 8 + g] = m[nb];
-                    sm->l[warp][nb * 8 + g] = l[nb];
+                for (int e = 0; e < 4; ++e) {
+                    const int nt = e >> 1, col = e & 1, key = nt * 8 + quad * 2 + col;
+                    x[e] = fmaf(c[nb][nt][0][2 + col] + c[nb][nt][1][2 + col], 0x1p-10f,
+                                c[nb][nt][0][col] + c[nb][nt][1][col]);
+                    x[e] = key < left ? x[e] : -INFINITY;
                 }
+                float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * c2;
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const float m_new = fmaxf(m[nb], top), shift = m_new == -INFINITY ? 0.0f : m_new;
+                const float alpha = ex2(m[nb] - shift);
+                m[nb] = m_new;
+                a2[nb] = f2_bits(alpha, alpha);
+                float w[4];  // 2^14 p
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w)
-                    if (w != warp) {
-                        uint64_t* const to = join_place<DP, NB>(join, w, warp, nb, g, quad);
+                for (int e = 0; e < 4; ++e)
+                    w[e] = ex2(fmaf(x[e], c2, 14.0f - shift));
+                split_p(w[0], w[1], pa[nb][0], pa[nb][1]);
+                split_p(w[2], w[3], pa[nb][2], pa[nb][3]);
+                l2[nb] = fma2(l2[nb], a2[nb], add2(f2_bits(w[0], w[1]), f2_bits(w[2], w[3])));
+            }
 #pragma unroll
-                        for (int t = 0; t < kQuarter; ++t)
-                            to[t * 4] = o[nb][w * kQuarter + t];
+            for (int d = 0; d < DP / 16; ++d) {
+                uint32_t b[4];
+                ldmatrix4_trans(smem_u32(vt) + (d / 4) * (kTile * 128) + sw128(lane & 15, (d % 4) * 2 + (lane >> 4)), b);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float y[4] = {};
+                        mma16816(y, pa[nb], b[2 * e], b[2 * e + 1]);
+                        o[nb][2 * d + e] = fma2(o[nb][2 * d + e], a2[nb], add2(f2_bits(y[0], y[1]), f2_bits(y[2], y[3])));
                     }
             }
-            bar_sync_rows();
-            if (ok) {
-                const bool whole = n == r.tiles;
-                const int slot = 2 * blockIdx.x + (fragment > 0 ? 1 : 0);
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    const int row = nb * 8 + g, hg = first_head + row;
-                    float mw[kWarps], top = -INFINITY;
-#pragma unroll
-                    for (int w = 0; w < kWarps; ++w) {
-                        mw[w] = sm->m[w][row];
-                        top = fmaxf(top, mw[w]);
-                    }
-                    const float shift = top == -INFINITY ? 0.0f : top;
-                    float sum = 0.0f;
-                    uint64_t y[kQuarter] = {};
-#pragma unroll
-                    for (int w = 0; w < kWarps; ++w) {
-                        const float f = ex2(mw[w] - shift);
-                        sum = fmaf(sm->l[w][row], f, sum);
-                        const uint64_t f2 = f2_bits(f, f);
-                        const uint64_t* const from = join_place<DP, NB>(join, warp, w, nb, g, quad);
-#pragma unroll
-                        for (int t = 0; t < kQuarter; ++t) {
-                            uint64_t x = 0;
-                            if (w != warp) {
-                                x = from[t * 4];
-                            } else {
-#pragma unroll
-                                for (int v = 0; v < kWarps; ++v)
-                                    x = v == warp ? o[nb][v * kQuarter + t] : x;
-                            }
-                            y[t] = fma2(x, f2, y[t]);
-                        }
-                    }
-                    if (hg >= p.group)
-                        continue;
-                    const int64_t at_row = static_cast<int64_t>(r.b) * p.heads + head * p.group + hg;
-                    float* const to = whole ? p.out + at_row * p.dim
-                                            : p.part_o + (static_cast<int64_t>(slot) * (NB * 8) + row) * p.dim;
-                    const float norm = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-                    for (int t = 0; t < kQuarter; ++t) {
-                        const int d = (warp * kQuarter + t) * 8 + quad * 2;  // the head dimension is a multiple of 8
-                        if (d < p.dim)
-                            *reinterpret_cast<float2*>(to + d) = make_float2(lo_f(y[t]) * norm, hi_f(y[t]) * norm);
-                    }
-                    if (quad == 0 && warp == 0) {
-                        const float lse =
-                            sum == 0.0f ? -INFINITY : fmaf(top, kAttnLn2, logf(sum * (1.0f / kAttnPScale)));
-                        if (!whole)
-                            p.part_lse[slot * (NB * 8) + row] = lse;
-                        else if (p.lse)
-                            p.lse[at_row] = lse;
-                    }
-                }
-            }
-            at += n;
-            r = next;
-            if (NB > 1 && at < end)
-                load_q(r);
+            __syncwarp();  // all lanes have read the stage
+            if (begin + loads < end)
+                load();
         }
+
+        // the row, or this warp's part of it
+        if (ok) {
+            const bool whole = n == r.tiles;
+            const int part = 2 * piece + (fragment > 0 ? 1 : 0);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                float sum = lo_f(l2[nb]) + hi_f(l2[nb]);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                const int row = nb * 8 + g, hg = first_head + row;
+                if (hg >= p.group)
+                    continue;
+                const int64_t at_row = static_cast<int64_t>(r.b) * p.heads + head * p.group + hg;
+                float* const dst = whole ? p.out + at_row * p.dim
+                                         : p.part_o + (static_cast<int64_t>(part) * (NB * 8) + row) * p.dim;
+                const float norm = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+                for (int t = 0; t < DP / 8; ++t)
+                    if (t * 8 < p.dim)
+                        *reinterpret_cast<float2*>(dst + t * 8 + quad * 2) =
+                            make_float2(lo_f(o[nb][t]) * norm, hi_f(o[nb][t]) * norm);
+                if (quad == 0) {
+                    const float lse =
+                        sum == 0.0f ? -INFINITY : fmaf(m[nb], kAttnLn2, logf(sum * (1.0f / kAttnPScale)));
+                    if (!whole)
+                        p.part_lse[part * (NB * 8) + row] = lse;
+                    else if (p.lse)
+                        p.lse[at_row] = lse;
+                }
+            }
+        }
+        at += n;
+        r = after;
+        if (NB > 1 && at < end)
+            load_q(r);
     }
+    if (!ok)  // what was issued lands before the warp leaves
+        for (int j = i; j < loads; ++j)
+            attn_drain_wait(&full[j % NS], (j / NS) & 1);
 }
 
 // The parts of each row joined: the prefix's (splits of them), then those of
@@ -541,18 +468,18 @@ __global__ void __launch_bounds__(256) attn_join_kernel(Params p, Join x)
     const int b = static_cast<int>(row / p.heads), h = static_cast<int>(row % p.heads);
     const int head = h / p.group, block = h % p.group / x.rows_a_unit, in_block = h % p.group % x.rows_a_unit;
     const int units = p.kv_heads * p.row_blocks, tiles = tiles_of(own_keys(p, b));
-    // the CTAs that have this row's tiles
+    // the pieces that have this row's tiles
     int first_slot = 0, own_parts = 0;
     bool whole = false;
     if (tiles > 0) {
         const Cut cut(p, sum_tiles(p, p.batch) * units);
         const int t0 = sum_tiles(p, b) * units + (head * p.row_blocks + block) * tiles;
-        const int c0 = cut.cta_of(t0), c1 = cut.cta_of(t0 + tiles - 1);
+        const int c0 = cut.piece_of(t0), c1 = cut.piece_of(t0 + tiles - 1);
         whole = c0 == c1;
         if (whole && x.splits == 0)
             return;  // the output is there
         own_parts = c1 - c0 + 1;
-        first_slot = 2 * c0 + (cut.begin(c0) < t0 ? 1 : 0);  // its CTA begins with another row
+        first_slot = 2 * c0 + (cut.begin(c0) < t0 ? 1 : 0);  // that piece begins with another row
     }
     const int parts = x.splits + own_parts;
     // part i: its lse and where its sums are; slots first_slot, then 2 (c0 + 1), 2 (c0 + 2), ...
@@ -590,7 +517,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(Params p, Join x)
         for (int e = 0; e < 4; ++e)
             acc[e] *= a;
         const int n = min(32, parts - i0);
-#pragma unroll 8
+#pragma unroll 16
         for (int i = 0; i < n; ++i) {
             const float wi = __shfl_sync(0xffffffffu, w, i);
             const float* const o = reinterpret_cast<const float*>(
@@ -633,12 +560,12 @@ comp_status_t launch_t(const CUtensorMap& mk, const CUtensorMap& mv, const Param
             done[dev.device] = true;
         }
     }
-    return launch_pdl(attn_decode_kernel<DP, NB>, p.ctas, kThreads, C::kSmem, stream, mk, mv, p);
+    return launch_pdl(attn_decode_kernel<DP, NB>, p.pieces / kWarps, kThreads, C::kSmem, stream, mk, mv, p);
 }
 
-// CTAs of the line of tiles: two an SM.  The workspace's size must not depend
-// on the device, so their number is bounded.
-constexpr int kMostCtas = 320;
+// Pieces of the line of tiles: one for each warp of two CTAs an SM.  The
+// workspace's size must not depend on the device, so their number is bounded.
+constexpr int kMostPieces = 320 * kWarps;
 
 // Parts that the shared pages' keys are split into, so that about one wave of
 // the packed kernel's CTAs works on them; a part has at least four tiles of
@@ -662,7 +589,7 @@ struct Layout {
 Layout layout_of(const comp_kv_cache_t& c, int64_t batch, int heads, int splits)
 {
     const int group = heads / c.kv_heads;
-    const int64_t slots = 2 * kMostCtas * (group > 8 ? 16 : 8), rows = batch * heads;
+    const int64_t slots = 2 * kMostPieces * (group > 8 ? 16 : 8), rows = batch * heads;
     Layout l;
     l.part_o = 0;
     l.part_lse = l.part_o + slots * c.head_dim;
@@ -732,13 +659,12 @@ comp_status_t launch_attn_decode(const comp_kv_cache_t& cache, const float* q, i
     // the line of tiles is counted in ints
     if ((width * cache.page_size / kTile + 1) * batch > INT32_MAX / (p.kv_heads * p.row_blocks))
         return COMP_ERR_INVALID_VALUE;
-    p.ctas = 2 * dev.sm_count < kMostCtas ? 2 * dev.sm_count : kMostCtas;
+    p.pieces = 2 * dev.sm_count * kWarps < kMostPieces ? 2 * dev.sm_count * kWarps : kMostPieces;
     p.vec_q = (reinterpret_cast<uintptr_t>(q) & 7u) == 0 && q_token % 2 == 0 && q_head % 2 == 0;
     p.scale = scale;
     CUtensorMap mk{}, mv{};
     if (width > 0) {  // otherwise there are no tiles
-        const int box = cache.page_size < kTile ? cache.page_size : kTile;
-        if (!encode_pages(&mk, cache.k, cache, box) || !encode_pages(&mv, cache.v, cache, box))
+        if (!encode_pages(&mk, cache.k, cache, kTile) || !encode_pages(&mv, cache.v, cache, kTile))
             return COMP_ERR_CUDA;
     }
     comp_status_t st;
