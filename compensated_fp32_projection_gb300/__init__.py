@@ -52,7 +52,8 @@ def __getattr__(name):
     if name in __all__ and name.startswith(_ATTENTION):
         from . import attention
 
-        return getattr(attention, name)
+        globals().update((n, getattr(attention, n)) for n in attention.__all__)
+        return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 

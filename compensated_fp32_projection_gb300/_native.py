@@ -86,6 +86,8 @@ class CompError(RuntimeError):
 def load() -> ctypes.CDLL:
     """The loaded library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
