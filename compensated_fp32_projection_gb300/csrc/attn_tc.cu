@@ -94,7 +94,6 @@ struct Shared {
     uint64_t full[6], empty[6];  // a stage has landed; both halves' products and warp 3 are done with it
     uint64_t checked[6];         // warp 3 has looked through a stage (a barrier for each stage: it may be
                                  // several tiles ahead of the products)
-    uint64_t qfull[2];           // a half's q planes are in shared memory
     uint64_t sfull[2];           // a half's S of a tile, and O' of the tile before, are complete
     uint64_t drain[2];
     uint32_t tmem_base;
@@ -135,6 +134,13 @@ constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_lo(uint32_t smem_addr, uint32_t leading)
 {
     return ((smem_addr & 0x3FFFFu) >> 4) | ((leading >> 4) << 16);
+}
+
+// The sign bits of the FP16 values of a pair that are infinite or NaN: an
+// exponent of all ones carries into the sign's place.
+__device__ __forceinline__ uint32_t not_finite(uint32_t pair)
+{
+    return ((pair & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
 }
 
 // Named barriers of a half's four row warps and its issuing warp.
@@ -218,7 +224,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm->checked[i], 1);
         }
         for (int h = 0; h < 2; ++h) {
-            mbar_init(&sm->qfull[h], 4);
             mbar_init(&sm->sfull[h], 1);
         }
         mbar_init(&sm->drain[0], 1);
@@ -253,18 +258,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool valid = false;
     const int half = (warp >> 2) - 1;
     if (half >= 0) {
-        const int64_t row = static_cast<int64_t>(sm->block) * 256 + (threadIdx.x - 128);
-        valid = row < static_cast<int64_t>(nq) * p.group;
-        const int t = static_cast<int>(valid ? row / p.group : 0), hq = head * p.group + static_cast<int>(row % p.group);
+        // total_q * heads is an int
+        const unsigned row = static_cast<unsigned>(sm->block) * 256u + (threadIdx.x - 128);
+        const unsigned group = static_cast<unsigned>(p.group);
+        valid = row < static_cast<unsigned>(nq) * group;
+        const int t = static_cast<int>(valid ? row / group : 0u), hq = head * p.group + static_cast<int>(row % group);
         int sees = nk;
         if (p.lengths)
             sees = valid ? clampi(p.lengths[q0 + t], 0, nk) : 0;
         else if (p.causal)
-            sees = static_cast<int>(min(static_cast<int64_t>(nk), max(int64_t(0), static_cast<int64_t>(t) + 1 + nk - nq)));
+            sees = clampi(t + 1 - nq + nk, 0, nk);  // t < nq: no overflow
         lim = clampi(sees - first, 0, keys);
-        q_at = (q0 + static_cast<int64_t>(t)) * p.q_token + hq * p.q_head;
-        out_at = (q0 + static_cast<int64_t>(t)) * p.out_token + hq * p.out_head + part * p.out_split;
-        lse_at = (q0 + static_cast<int64_t>(t)) * p.kv_heads * p.group + hq + part * p.lse_split;
+        const int64_t token = q0 + static_cast<int64_t>(t);
+        q_at = token * p.q_token + hq * p.q_head;
+        out_at = token * p.out_token + hq * p.out_head + part * p.out_split;
+        lse_at = token * (p.kv_heads * p.group) + hq + part * p.lse_split;
         const int hi = __reduce_max_sync(0xffffffffu, valid ? lim : 0);
         const int lo = __reduce_min_sync(0xffffffffu, valid ? lim : INT32_MAX);
         if (lane == 0) {
@@ -335,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // does not keep them busy).  The halves take turns, step by step
             // (named barriers 2 and 3): products of both mixed would leave the
             // two softmaxes at the same time, and the tensor cores idle then.
-            // P arrives by named barriers too (4 to 7: half and part): a test of an
+            // q and P arrive by named barriers too (4 to 7: half and part): a test of an
             // mbarrier takes hundreds of cycles while operands stream from shared
             // memory.  After an abort every warp still goes through its barriers.
             const int h = warp - 1, nh = h ? n1 : n0;
@@ -370,11 +378,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (j >= edge)
                             wait(&sm->checked[sv], iv / NS);
                     }
-                    if (has_k && !has_v)
-                        wait(&sm->qfull[h], 0);
                 }
                 __syncwarp();
-                if (has_v)
+                if (has_v || has_k)  // P's first half, before the first tile q
                     rows_sync(4 + 2 * h);
                 // the turn: the second half waits for the first half's step, the first for the second's before
                 if (h == 1 || j >= 0)
@@ -454,20 +460,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if ((i & 1) && j >= edge) {
                     uint8_t* const tile = stages + s * C::kStage;
                     bool seen = false;
-                    for (uint32_t at = lane * 16; at < C::kStage; at += 512) {
-                        uint4 x = *reinterpret_cast<const uint4*>(tile + at);
-                        uint32_t* const w = reinterpret_cast<uint32_t*>(&x);
-                        bool any = false;
-    #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            // an exponent of all ones carries into the sign's place
-                            const uint32_t odd = ((w[e] & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
-                            any |= odd != 0;
-                            w[e] &= ~((odd >> 15) * 0xffffu);
+                    constexpr int kBatch = 8;  // loads in flight a lane
+#pragma unroll 1
+                    for (uint32_t at = lane * 16; at < C::kStage; at += kBatch * 512) {
+                        uint4 x[kBatch];
+                        uint32_t odd = 0;
+#pragma unroll
+                        for (int b = 0; b < kBatch; ++b) {
+                            x[b] = *reinterpret_cast<const uint4*>(tile + at + b * 512);
+                            odd |= not_finite(x[b].x) | not_finite(x[b].y) | not_finite(x[b].z) | not_finite(x[b].w);
                         }
-                        if (any) {
-                            *reinterpret_cast<uint4*>(tile + at) = x;
-                            seen |= j * BN + static_cast<int>(at / 128 % BN) < most;
+                        if (odd != 0) {
+#pragma unroll
+                            for (int b = 0; b < kBatch; ++b) {
+                                uint32_t* const w = reinterpret_cast<uint32_t*>(&x[b]);
+                                uint32_t here = 0;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const uint32_t f = not_finite(w[e]);
+                                    here |= f;
+                                    w[e] &= ~((f >> 15) * 0xffffu);
+                                }
+                                if (here) {
+                                    *reinterpret_cast<uint4*>(tile + at + b * 512) = x[b];
+                                    seen |= j * BN + static_cast<int>((at + b * 512) / 128 % BN) < most;
+                                }
+                            }
                         }
                     }
                     if (__any_sync(0xffffffffu, seen) && lane == 0)
@@ -490,44 +508,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         // q into shared memory, split; a warp takes its 32 rows one after the other
         if (nh > 0) {
             uint8_t* const hi_tile = smem + half * 2 * C::kQTile;
-            constexpr int E = DP / 32;  // values of a lane
-            const int d0 = lane * E;
-#pragma unroll 16
-            for (int i = 0; i < 32; ++i) {
-                const int64_t at = __shfl_sync(0xffffffffu, q_at, i);
-                const bool there = __shfl_sync(0xffffffffu, valid ? 1 : 0, i) != 0;
-                float x[E];
-                if (there && p.vec_q && d0 + E <= p.dim) {
-                    if (E == 4) {
-                        const float4 f = __ldg(reinterpret_cast<const float4*>(p.q + at + d0));
-                        x[0] = f.x, x[1] = f.y, x[E - 2] = f.z, x[E - 1] = f.w;
-                    } else {
-                        const float2 f = __ldg(reinterpret_cast<const float2*>(p.q + at + d0));
-                        x[0] = f.x, x[1] = f.y;
-                    }
-                } else {
+            constexpr int kLanes = DP / 4, kAtOnce = 32 / kLanes;  // lanes of a row, rows a load
+            const int d0 = lane % kLanes * 4, sub = lane / kLanes;
+            const unsigned rows_there = __ballot_sync(0xffffffffu, valid);
+            auto split_row = [&](int i, float4 f) {
+                if (!((rows_there >> i) & 1))
+                    f = float4{};
+                uint2 hi, lo;
+                split2(f.x, f.y, hi.x, lo.x);
+                split2(f.z, f.w, hi.y, lo.y);
+                const uint32_t to = (d0 / 64) * (128 * 128) + sw128(w4 * 32 + i, (d0 % 64) / 8) + (d0 % 8) * 2;
+                *reinterpret_cast<uint2*>(hi_tile + to) = hi;
+                *reinterpret_cast<uint2*>(hi_tile + C::kQTile + to) = lo;
+            };
+            if (p.vec_q) {
+                // all of the warp's rows on their way at once; rows that are not
+                // there have the address of one that is
+                float4 x[32 / kAtOnce];
 #pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        x[e] = there && d0 + e < p.dim ? __ldg(p.q + at + d0 + e) : 0.0f;
+                for (int i = 0; i < 32 / kAtOnce; ++i) {
+                    const int64_t at = __shfl_sync(0xffffffffu, q_at, i * kAtOnce + sub);
+                    x[i] = __ldg(reinterpret_cast<const float4*>(p.q + at + (d0 < p.dim ? d0 : 0)));
                 }
-                uint32_t hi[E / 2], lo[E / 2];
 #pragma unroll
-                for (int e = 0; e < E; e += 2)
-                    split2(x[e], x[e + 1], hi[e / 2], lo[e / 2]);
-                const uint32_t r = w4 * 32 + i;
-                const uint32_t to = (d0 / 64) * (128 * 128) + sw128(r, (d0 % 64) / 8) + (d0 % 8) * 2;
-                if (E == 4) {
-                    *reinterpret_cast<uint2*>(hi_tile + to) = make_uint2(hi[0], hi[E / 2 - 1]);
-                    *reinterpret_cast<uint2*>(hi_tile + C::kQTile + to) = make_uint2(lo[0], lo[E / 2 - 1]);
-                } else {
-                    *reinterpret_cast<uint32_t*>(hi_tile + to) = hi[0];
-                    *reinterpret_cast<uint32_t*>(hi_tile + C::kQTile + to) = lo[0];
+                for (int i = 0; i < 32 / kAtOnce; ++i)
+                    split_row(i * kAtOnce + sub, d0 < p.dim ? x[i] : float4{});
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < 32 / kAtOnce; ++i) {
+                    const float* const src = p.q + __shfl_sync(0xffffffffu, q_at, i * kAtOnce + sub) + d0;
+                    float4 f{};
+                    f.x = d0 < p.dim ? __ldg(src) : 0.0f;
+                    f.y = d0 + 1 < p.dim ? __ldg(src + 1) : 0.0f;
+                    f.z = d0 + 2 < p.dim ? __ldg(src + 2) : 0.0f;
+                    f.w = d0 + 3 < p.dim ? __ldg(src + 3) : 0.0f;
+                    split_row(i * kAtOnce + sub, f);
                 }
             }
             fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&sm->qfull[half]);
+            rows_arrive(4 + 2 * half);
         }
 
         const float c2 = p.scale * kAttnLog2E;
@@ -657,33 +676,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                 alpha = alpha_new;
             }
         }
-        if (ok && valid) {
-            const float l = (lo_f(l2) + hi_f(l2)) * (1.0f / kAttnPScale);
-            // no key seen, or none that counts beside an infinite score (NaN stays NaN)
-            const float norm = l == 0.0f ? 0.0f : (1.0f / kAttnPScale) / l;
-            float* const out = p.out + out_at;
+        // out, row by row through shared memory (this warp's share of q's planes,
+        // which the products of this half have read): a thread holds a row, and
+        // rows are written 512 or 256 bytes at a time
+        const float l = (lo_f(l2) + hi_f(l2)) * (1.0f / kAttnPScale);
+        // no key seen, or none that counts beside an infinite score (NaN stays NaN)
+        const float norm = l == 0.0f ? 0.0f : (1.0f / kAttnPScale) / l;
+        if (ok) {
+            constexpr int kChunks = DP / 4;  // 16 bytes each
+            ulonglong2* const tile = reinterpret_cast<ulonglong2*>(smem + half * 2 * C::kQTile) + w4 * 32 * kChunks;
 #pragma unroll
-            for (int d = 0; d < DP; d += 4) {
-                const float x0 = lo_f(o[d / 2]) * norm, x1 = hi_f(o[d / 2]) * norm;
-                const float x2 = lo_f(o[d / 2 + 1]) * norm, x3 = hi_f(o[d / 2 + 1]) * norm;
+            for (int c = 0; c < kChunks; ++c)
+                tile[lane * kChunks + (c ^ (lane & 7))] = make_ulonglong2(o[2 * c], o[2 * c + 1]);
+            __syncwarp();
+            constexpr int kRows = 32 / kChunks;  // rows a warp writes at once
+            const int chunk = lane % kChunks, d = chunk * 4;
+#pragma unroll 4
+            for (int i0 = 0; i0 < 32; i0 += kRows) {
+                const int i = i0 + lane / kChunks;
+                float* const to = p.out + __shfl_sync(0xffffffffu, out_at, i) + d;
+                const float f = __shfl_sync(0xffffffffu, norm, i);
+                const bool there = __shfl_sync(0xffffffffu, valid ? 1 : 0, i) != 0;
+                const float4 x = reinterpret_cast<const float4*>(tile)[i * kChunks + (chunk ^ (i & 7))];
+                if (!there)
+                    continue;
                 if (p.vec_out && d + 4 <= p.dim) {
-                    *reinterpret_cast<float4*>(out + d) = make_float4(x0, x1, x2, x3);
+                    *reinterpret_cast<float4*>(to) = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
                 } else {
                     if (d < p.dim)
-                        out[d] = x0;
+                        to[0] = x.x * f;
                     if (d + 1 < p.dim)
-                        out[d + 1] = x1;
+                        to[1] = x.y * f;
                     if (d + 2 < p.dim)
-                        out[d + 2] = x2;
+                        to[2] = x.z * f;
                     if (d + 3 < p.dim)
-                        out[d + 3] = x3;
+                        to[3] = x.w * f;
                 }
             }
+            __syncwarp();  // the rows are written before values are added below
+        }
+        if (ok && valid) {
             if (p.lse)
                 p.lse[lse_at] = l == 0.0f ? -INFINITY : fmaf(m, kAttnLn2, logf(l));
             // values that are not finite were taken out of the tiles from
             // `edge` on: a row that sees one adds it (its weight is positive)
             if (*reinterpret_cast<volatile int*>(&sm->hurt)) {
+                float* const out = p.out + out_at;
 #pragma unroll 1
                 for (int i = edge * BN; i < lim; ++i) {
                     const int key = first + i;
@@ -848,8 +886,7 @@ comp_status_t launch_attn(const comp_attn_t& a, const float* q, const void* k, c
     p.splits = 1;
     p.v_f32 = kv_bytes == 4;
     p.scale = a.scale;
-    const int lane_values = a.head_dim <= 64 ? 2 : 4;
-    p.vec_q = a.q_token % lane_values == 0 && a.q_head % lane_values == 0 && aligned16(q);
+    p.vec_q = a.q_token % 4 == 0 && a.q_head % 4 == 0 && a.head_dim % 4 == 0 && aligned16(q);
     p.vec_out = a.out_token % 4 == 0 && a.out_head % 4 == 0 && aligned16(out);
 
     CUtensorMap maps[4] = {};
@@ -920,8 +957,7 @@ comp_status_t launch_attn_prefix(const comp_kv_cache_t& cache, const float* q, i
     p.table_pages = static_cast<int>(shared);
     p.pages = static_cast<int>(cache.pages);
     p.scale = scale;
-    const int lane_values = cache.head_dim <= 64 ? 2 : 4;
-    p.vec_q = q_token % lane_values == 0 && q_head % lane_values == 0 && aligned16(q);
+    p.vec_q = q_token % 4 == 0 && q_head % 4 == 0 && aligned16(q);
     p.vec_out = 1;
     CUtensorMap maps[4] = {};
     if (!encode_pages(&maps[0], cache.k, cache, cache.page_size) ||
