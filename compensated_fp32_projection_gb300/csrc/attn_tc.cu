@@ -94,6 +94,7 @@ struct Shared {
     uint64_t full[6], empty[6];  // a stage has landed; both halves' products and warp 3 are done with it
     uint64_t checked[6];         // warp 3 has looked through a stage (a barrier for each stage: it may be
                                  // several tiles ahead of the products)
+    uint64_t qload[2];           // a half's q has landed, FP32
     uint64_t sfull[2];           // a half's S of a tile, and O' of the tile before, are complete
     uint64_t drain[2];
     uint32_t tmem_base;
@@ -118,6 +119,7 @@ struct Params {
     int n_seq, total_q, total_k, kv_heads, group, dim, causal, splits;
     int page_size, table_pages, pages;
     int v_f32, vec_q, vec_out;
+    int q_tokens;                 // query tokens of a half, if q can be loaded by tensor map; else 0
     float scale;
 };
 
@@ -199,7 +201,7 @@ template <int DP, int PL>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                    const __grid_constant__ CUtensorMap map_k_lo, const __grid_constant__ CUtensorMap map_v_lo,
-                   const Params p)
+                   const __grid_constant__ CUtensorMap map_q, const Params p)
 {
     using C = Cfg<DP, PL>;
     constexpr int BN = C::BN, NS = C::NS, OB = C::OB;
@@ -224,6 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm->checked[i], 1);
         }
         for (int h = 0; h < 2; ++h) {
+            mbar_init(&sm->qload[h], 1);
             mbar_init(&sm->sfull[h], 1);
         }
         mbar_init(&sm->drain[0], 1);
@@ -521,18 +524,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<uint2*>(hi_tile + to) = hi;
                 *reinterpret_cast<uint2*>(hi_tile + C::kQTile + to) = lo;
             };
-            if (p.vec_q) {
-                // all of the warp's rows on their way at once; rows that are not
-                // there have the address of one that is
+            if (p.q_tokens > 0) {
+                // one load brings the half's rows, FP32, to where the planes will be
+                // (tokens past the sequence's end too: rows that are not there); the
+                // warps read them all before one of them writes a plane.  Loads by
+                // the threads would wait for each other in the small L1 that 227 KB
+                // of shared memory leave.
+                if (w4 == 0 && lane == 0) {
+                    mbar_arrive_expect_tx(&sm->qload[half], 128 * p.dim * 4);
+                    tma_load_3d(hi_tile, &map_q, &sm->qload[half], 0, head * p.group,
+                                q0 + sm->block * (2 * p.q_tokens) + half * p.q_tokens);
+                }
+                __syncwarp();
+                ok = attn_warp_wait(&sm->qload[half], 0, &sm->abort, kFaultAttnRows);
                 float4 x[32 / kAtOnce];
 #pragma unroll
-                for (int i = 0; i < 32 / kAtOnce; ++i) {
-                    const int64_t at = __shfl_sync(0xffffffffu, q_at, i * kAtOnce + sub);
-                    x[i] = __ldg(reinterpret_cast<const float4*>(p.q + at + (d0 < p.dim ? d0 : 0)));
-                }
+                for (int i = 0; i < 32 / kAtOnce; ++i)
+                    x[i] = d0 < p.dim ? *reinterpret_cast<const float4*>(
+                                            hi_tile + ((w4 * 32 + i * kAtOnce + sub) * p.dim + d0) * 4)
+                                      : float4{};
+                asm volatile("bar.sync %0, 128;" ::"r"(8 + half) : "memory");
 #pragma unroll
                 for (int i = 0; i < 32 / kAtOnce; ++i)
-                    split_row(i * kAtOnce + sub, d0 < p.dim ? x[i] : float4{});
+                    split_row(i * kAtOnce + sub, x[i]);
+            } else if (p.vec_q) {
+                // rows that are not there have the address of one that is
+#pragma unroll 1
+                for (int i0 = 0; i0 < 32; i0 += 8 * kAtOnce) {
+                    float4 x[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int64_t at = __shfl_sync(0xffffffffu, q_at, i0 + i * kAtOnce + sub);
+                        x[i] = __ldg(reinterpret_cast<const float4*>(p.q + at + (d0 < p.dim ? d0 : 0)));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        split_row(i0 + i * kAtOnce + sub, d0 < p.dim ? x[i] : float4{});
+                }
             } else {
 #pragma unroll 1
                 for (int i = 0; i < 32 / kAtOnce; ++i) {
@@ -691,18 +719,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             constexpr int kRows = 32 / kChunks;  // rows a warp writes at once
             const int chunk = lane % kChunks, d = chunk * 4;
-#pragma unroll 4
-            for (int i0 = 0; i0 < 32; i0 += kRows) {
-                const int i = i0 + lane / kChunks;
-                float* const to = p.out + __shfl_sync(0xffffffffu, out_at, i) + d;
-                const float f = __shfl_sync(0xffffffffu, norm, i);
-                const bool there = __shfl_sync(0xffffffffu, valid ? 1 : 0, i) != 0;
-                const float4 x = reinterpret_cast<const float4*>(tile)[i * kChunks + (chunk ^ (i & 7))];
-                if (!there)
-                    continue;
-                if (p.vec_out && d + 4 <= p.dim) {
-                    *reinterpret_cast<float4*>(to) = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
-                } else {
+            const unsigned rows_there = __ballot_sync(0xffffffffu, valid);
+            if (p.vec_out) {  // no branch but the store's own predicate: the rows overlap
+#pragma unroll 8
+                for (int i0 = 0; i0 < 32; i0 += kRows) {
+                    const int i = i0 + lane / kChunks;
+                    float* const to = p.out + __shfl_sync(0xffffffffu, out_at, i) + d;
+                    const float f = __shfl_sync(0xffffffffu, norm, i);
+                    const float4 x = reinterpret_cast<const float4*>(tile)[i * kChunks + (chunk ^ (i & 7))];
+                    if (((rows_there >> i) & 1) && d < p.dim)
+                        *reinterpret_cast<float4*>(to) = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
+                }
+            } else {
+#pragma unroll 1
+                for (int i0 = 0; i0 < 32; i0 += kRows) {
+                    const int i = i0 + lane / kChunks;
+                    float* const to = p.out + __shfl_sync(0xffffffffu, out_at, i) + d;
+                    const float f = __shfl_sync(0xffffffffu, norm, i);
+                    const float4 x = reinterpret_cast<const float4*>(tile)[i * kChunks + (chunk ^ (i & 7))];
+                    if (!((rows_there >> i) & 1))
+                        continue;
                     if (d < p.dim)
                         to[0] = x.x * f;
                     if (d + 1 < p.dim)
@@ -816,8 +852,32 @@ bool map_legal(int64_t tokens, int64_t heads, int64_t token, int64_t head)
     return ok(tokens, token) && ok(heads, head);
 }
 
+// q as boxes of one half's rows, where they are whole tokens: `group` heads of
+// `tokens` tokens, dense.  0 if it is not to be loaded so.
+int encode_q(CUtensorMap* map, const float* q, int dim, int heads, int group, int64_t tokens, int64_t token,
+             int64_t head, bool vec)
+{
+    const auto ok = [](int64_t extent, int64_t stride) {
+        return extent <= 1 || (stride > 0 && stride % 4 == 0 && stride < (1ll << 37));
+    };
+    EncodeTiledFn fn = encode_fn();
+    if (!fn || !vec || 128 % group != 0 || !ok(tokens, token) || !ok(heads, head))
+        return 0;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads),
+                                static_cast<cuuint64_t>(tokens)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(heads > 1 ? head * 4 : 512),
+                                   static_cast<cuuint64_t>(tokens > 1 ? token * 4 : 512)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(dim), static_cast<cuuint32_t>(group),
+                               static_cast<cuuint32_t>(128 / group)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const bool done = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<float*>(q), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return done ? 128 / group : 0;
+}
+
 template <int DP, int PL>
-comp_status_t launch_t(const CUtensorMap (&maps)[4], const Params& p, int64_t grid, const DeviceInfo& dev,
+comp_status_t launch_t(const CUtensorMap (&maps)[5], const Params& p, int64_t grid, const DeviceInfo& dev,
                        cudaStream_t stream)
 {
     using C = Cfg<DP, PL>;
@@ -837,7 +897,7 @@ comp_status_t launch_t(const CUtensorMap (&maps)[4], const Params& p, int64_t gr
         }
     }
     return launch_pdl(attn_tc_kernel<DP, PL>, static_cast<int>(grid), kThreads, C::kSmem, stream, maps[0], maps[1],
-                      maps[2], maps[3], p);
+                      maps[2], maps[3], maps[4], p);
 }
 
 int64_t pad8(int64_t d)
@@ -887,9 +947,9 @@ comp_status_t launch_attn(const comp_attn_t& a, const float* q, const void* k, c
     p.v_f32 = kv_bytes == 4;
     p.scale = a.scale;
     p.vec_q = a.q_token % 4 == 0 && a.q_head % 4 == 0 && a.head_dim % 4 == 0 && aligned16(q);
-    p.vec_out = a.out_token % 4 == 0 && a.out_head % 4 == 0 && aligned16(out);
+    p.vec_out = a.out_token % 4 == 0 && a.out_head % 4 == 0 && a.head_dim % 4 == 0 && aligned16(out);
 
-    CUtensorMap maps[4] = {};
+    CUtensorMap maps[5] = {};
     const int box_rows = a.head_dim > 64 && kv_bytes == 4 ? 64 : 128;  // Cfg::BN
     if (a.total_k > 0) {
         const void* planes[4] = {k, v, nullptr, nullptr};
@@ -919,6 +979,7 @@ comp_status_t launch_attn(const comp_attn_t& a, const float* q, const void* k, c
             if (!encode_rows(&maps[i], planes[i], dim, a.total_k, a.kv_heads, token[i % 2], head[i % 2], box_rows))
                 return COMP_ERR_CUDA;
     }
+    p.q_tokens = encode_q(&maps[4], q, p.dim, a.heads, p.group, a.total_q, a.q_token, a.q_head, p.vec_q);
     const int64_t rows = a.total_q * p.group;
     const int64_t grid = (cu_q ? rows / 256 + a.n_seq : (rows + 255) / 256) * a.kv_heads;
     if (grid > INT32_MAX)
@@ -959,10 +1020,11 @@ comp_status_t launch_attn_prefix(const comp_kv_cache_t& cache, const float* q, i
     p.scale = scale;
     p.vec_q = q_token % 4 == 0 && q_head % 4 == 0 && aligned16(q);
     p.vec_out = 1;
-    CUtensorMap maps[4] = {};
+    CUtensorMap maps[5] = {};
     if (!encode_pages(&maps[0], cache.k, cache, cache.page_size) ||
         !encode_pages(&maps[1], cache.v, cache, cache.page_size))
         return COMP_ERR_CUDA;
+    p.q_tokens = encode_q(&maps[4], q, p.dim, heads, p.group, batch, q_token, q_head, p.vec_q);
     const int64_t grid = (batch * p.group + 255) / 256 * cache.kv_heads * splits;
     if (grid > INT32_MAX)
         return COMP_ERR_INVALID_VALUE;
