@@ -99,7 +99,8 @@ struct Shared {
     uint64_t drain[2];
     uint32_t tmem_base;
     int abort;
-    int seq, block;              // this CTA's sequence and block of rows; seq < 0: none
+    int block;                   // this CTA's block of rows; < 0: none
+    int q0, nq, k0, nk;          // its sequence's queries and keys
     int most[2], least[2];       // most and least keys that a row of a half sees
     int hurt;                    // a looked-through tile has values that are not finite, and seen
 };
@@ -157,24 +158,27 @@ __device__ __forceinline__ void rows_arrive(int id)
 }
 
 // This CTA's sequence and block of 256 rows: blocks are numbered sequence by
-// sequence.  One warp; cu_q is read 32 sequences at a time.
+// sequence, the last of one, which sees most keys, first.  One warp; the
+// offsets are read 32 sequences at a time.
 __device__ __forceinline__ void find_block(const Params& p, int block, Shared* sm)
 {
     const int lane = threadIdx.x & 31;
     if (!p.cu_q) {
-        const int n = static_cast<int>((static_cast<int64_t>(p.total_q) * p.group + 255) / 256);
         if (lane == 0) {
-            sm->seq = block < n ? 0 : -1;
-            sm->block = n - 1 - block;
+            sm->block = static_cast<int>((static_cast<int64_t>(p.total_q) * p.group + 255) / 256) - 1 - block;
+            sm->q0 = sm->k0 = 0;
+            sm->nq = p.total_q;
+            sm->nk = p.total_k;
         }
         return;
     }
     for (int s0 = 0; s0 < p.n_seq; s0 += 32) {
         const int s = s0 + lane;
-        int n = 0;
+        int n = 0, a = 0, b = 0, c = 0, d = 0;
         if (s < p.n_seq) {
-            const int a = clampi(p.cu_q[s], 0, p.total_q), b = clampi(p.cu_q[s + 1], a, p.total_q);
-            n = static_cast<int>((static_cast<int64_t>(b - a) * p.group + 255) / 256);
+            a = clampi(p.cu_q[s], 0, p.total_q), b = clampi(p.cu_q[s + 1], a, p.total_q);
+            c = clampi(p.cu_k[s], 0, p.total_k), d = clampi(p.cu_k[s + 1], c, p.total_k);
+            n = static_cast<int>((static_cast<unsigned>(b - a) * static_cast<unsigned>(p.group) + 255u) / 256u);
         }
         int x = n;
 #pragma unroll
@@ -186,15 +190,18 @@ __device__ __forceinline__ void find_block(const Params& p, int block, Shared* s
         const unsigned hit = __ballot_sync(0xffffffffu, x > block);
         if (hit) {
             if (lane == __ffs(hit) - 1) {
-                sm->seq = s;
-                sm->block = x - 1 - block;  // the last block, which sees most keys, first
+                sm->block = x - 1 - block;
+                sm->q0 = a;
+                sm->nq = b - a;
+                sm->k0 = c;
+                sm->nk = d - c;
             }
             return;
         }
         block -= __shfl_sync(0xffffffffu, x, 31);
     }
     if (lane == 0)
-        sm->seq = -1;
+        sm->block = -1;
 }
 
 template <int DP, int PL>
@@ -240,17 +247,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbar_init();
     }
     __syncthreads();
-    if (sm->seq < 0)
+    if (sm->block < 0)
         return;  // the grid is an upper bound
 
-    // the sequence, and the part of its keys that this CTA goes through
-    int q0 = 0, nq = p.total_q, k0 = 0, nk = p.total_k;
-    if (p.cu_q) {
-        q0 = clampi(p.cu_q[sm->seq], 0, p.total_q);
-        nq = clampi(p.cu_q[sm->seq + 1], q0, p.total_q) - q0;
-        k0 = clampi(p.cu_k[sm->seq], 0, p.total_k);
-        nk = clampi(p.cu_k[sm->seq + 1], k0, p.total_k) - k0;
+    const int half = (warp >> 2) - 1;
+    // One load brings a half's rows of q, FP32, to where its planes will be
+    // (tokens past the sequence's end too: rows that are not there).  Loads by
+    // the threads would wait for each other in the small L1 that 227 KB of
+    // shared memory leave.
+    if (p.q_tokens > 0 && (warp == 4 || warp == 8) && lane == 0) {
+        mbar_arrive_expect_tx(&sm->qload[half], 128 * p.dim * 4);
+        tma_load_3d(smem + half * 2 * C::kQTile, &map_q, &sm->qload[half], 0, head * p.group,
+                    sm->q0 + (2 * sm->block + half) * p.q_tokens);
     }
+
+    // the part of its sequence's keys that this CTA goes through
+    const int q0 = sm->q0, nq = sm->nq, k0 = sm->k0, nk = sm->nk;
     const int part_keys = ((nk + BN - 1) / BN + p.splits - 1) / p.splits * BN;
     const int first = min(static_cast<int64_t>(nk), static_cast<int64_t>(part) * part_keys);
     const int keys = min(nk - first, part_keys);
@@ -259,7 +271,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     int64_t q_at = 0, out_at = 0, lse_at = 0;
     int lim = 0;
     bool valid = false;
-    const int half = (warp >> 2) - 1;
     if (half >= 0) {
         // total_q * heads is an int
         const unsigned row = static_cast<unsigned>(sm->block) * 256u + (threadIdx.x - 128);
@@ -525,17 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<uint2*>(hi_tile + C::kQTile + to) = lo;
             };
             if (p.q_tokens > 0) {
-                // one load brings the half's rows, FP32, to where the planes will be
-                // (tokens past the sequence's end too: rows that are not there); the
-                // warps read them all before one of them writes a plane.  Loads by
-                // the threads would wait for each other in the small L1 that 227 KB
-                // of shared memory leave.
-                if (w4 == 0 && lane == 0) {
-                    mbar_arrive_expect_tx(&sm->qload[half], 128 * p.dim * 4);
-                    tma_load_3d(hi_tile, &map_q, &sm->qload[half], 0, head * p.group,
-                                q0 + sm->block * (2 * p.q_tokens) + half * p.q_tokens);
-                }
-                __syncwarp();
+                // the warps read all rows before one of them writes a plane
                 ok = attn_warp_wait(&sm->qload[half], 0, &sm->abort, kFaultAttnRows);
                 float4 x[32 / kAtOnce];
 #pragma unroll
@@ -713,40 +714,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) {
             constexpr int kChunks = DP / 4;  // 16 bytes each
             ulonglong2* const tile = reinterpret_cast<ulonglong2*>(smem + half * 2 * C::kQTile) + w4 * 32 * kChunks;
+            const uint64_t norm2 = f2_bits(norm, norm);
 #pragma unroll
             for (int c = 0; c < kChunks; ++c)
-                tile[lane * kChunks + (c ^ (lane & 7))] = make_ulonglong2(o[2 * c], o[2 * c + 1]);
+                tile[lane * kChunks + (c ^ (lane & 7))] = make_ulonglong2(mul2(o[2 * c], norm2), mul2(o[2 * c + 1], norm2));
             __syncwarp();
             constexpr int kRows = 32 / kChunks;  // rows a warp writes at once
             const int chunk = lane % kChunks, d = chunk * 4;
             const unsigned rows_there = __ballot_sync(0xffffffffu, valid);
-            if (p.vec_out) {  // no branch but the store's own predicate: the rows overlap
+            if (p.vec_out && p.q_tokens > 0) {
+                // rows are whole tokens of a power of two of heads: addresses by shifts
+                // (exchanges between lanes queue behind the other half's operands)
+                const int shift = 31 - __clz(p.group);
+                float* const base = p.out + (static_cast<int64_t>(q0) + (2 * sm->block + half) * p.q_tokens) * p.out_token +
+                                    static_cast<int64_t>(head) * p.group * p.out_head + part * p.out_split + d;
 #pragma unroll 8
                 for (int i0 = 0; i0 < 32; i0 += kRows) {
-                    const int i = i0 + lane / kChunks;
-                    float* const to = p.out + __shfl_sync(0xffffffffu, out_at, i) + d;
-                    const float f = __shfl_sync(0xffffffffu, norm, i);
+                    const int i = i0 + lane / kChunks, row = w4 * 32 + i;
+                    float* const to = base + (row >> shift) * p.out_token + (row & (p.group - 1)) * p.out_head;
                     const float4 x = reinterpret_cast<const float4*>(tile)[i * kChunks + (chunk ^ (i & 7))];
                     if (((rows_there >> i) & 1) && d < p.dim)
-                        *reinterpret_cast<float4*>(to) = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
+                        *reinterpret_cast<float4*>(to) = x;
                 }
             } else {
 #pragma unroll 1
                 for (int i0 = 0; i0 < 32; i0 += kRows) {
                     const int i = i0 + lane / kChunks;
                     float* const to = p.out + __shfl_sync(0xffffffffu, out_at, i) + d;
-                    const float f = __shfl_sync(0xffffffffu, norm, i);
                     const float4 x = reinterpret_cast<const float4*>(tile)[i * kChunks + (chunk ^ (i & 7))];
                     if (!((rows_there >> i) & 1))
                         continue;
+                    if (p.vec_out && d < p.dim) {
+                        *reinterpret_cast<float4*>(to) = x;
+                        continue;
+                    }
                     if (d < p.dim)
-                        to[0] = x.x * f;
+                        to[0] = x.x;
                     if (d + 1 < p.dim)
-                        to[1] = x.y * f;
+                        to[1] = x.y;
                     if (d + 2 < p.dim)
-                        to[2] = x.z * f;
+                        to[2] = x.z;
                     if (d + 3 < p.dim)
-                        to[3] = x.w * f;
+                        to[3] = x.w;
                 }
             }
             __syncwarp();  // the rows are written before values are added below
