@@ -12,6 +12,8 @@ import threading
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libcompfp32.so")
 
+BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_attn_binding.so")
+
 COMP_OK = 0
 COMP_ERR_INVALID_VALUE = 1
 COMP_ERR_MISALIGNED = 2  # reserved, never returned

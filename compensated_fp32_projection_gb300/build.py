@@ -1,7 +1,9 @@
 """Builds the CUDA library ``libcompfp32.so`` in place (nvcc, sm_103a only).
 
 Each ``csrc/*.cu`` is compiled in parallel to an object under ``_build/`` and
-the objects are linked into one shared library next to this file.  The CUDA
+the objects are linked into one shared library next to this file.
+``csrc/attn_binding.cpp`` is compiled with the host compiler at the same time
+and becomes ``_attn_binding.so``, the torch binding of the attention calls.  The CUDA
 runtime is linked statically, so the library needs only the NVIDIA driver at
 run time (and loads, without running anything, on a machine with no GPU).
 
@@ -10,10 +12,12 @@ No fast-math and no flush-to-zero: the split and merge must be bit-exact.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +25,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libcompfp32.so")
+BINDING = os.path.join(PKG, "_attn_binding.so")
+BINDING_SRC = os.path.join(CSRC, "attn_binding.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
@@ -53,15 +59,15 @@ def _sources():
 
 
 def _deps():
-    return _sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + [
+    return _sources() + [BINDING_SRC] + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + [
         os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)
     ] + [os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -72,6 +78,35 @@ def _compile(src: str) -> tuple[str, str]:
     if p.returncode != 0:
         raise RuntimeError(f"nvcc failed for {src}:\n{' '.join(cmd)}\n{p.stdout}\n{p.stderr}")
     return obj, p.stderr
+
+
+def _cuda_include() -> str:
+    return os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+
+
+def _compile_binding() -> str:
+    """The torch binding's object; torch's headers are found without importing it."""
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    obj = os.path.join(BUILD, "attn_binding.o")
+    inc = [INCLUDE, os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], _cuda_include()]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-c", BINDING_SRC, "-o", obj,
+           *[a for d in inc for a in ("-isystem" if d != INCLUDE else "-I", d)]]
+    p = subprocess.run(cmd, capture_output=True, text=True)
+    if p.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for {BINDING_SRC}:\n{' '.join(cmd)}\n{p.stdout}\n{p.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    lib = os.path.join(importlib.util.find_spec("torch").submodule_search_locations[0], "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", obj, "-o", tmp, "-L", PKG, "-l:libcompfp32.so", "-L", lib,
+           "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    p = subprocess.run(cmd, capture_output=True, text=True)
+    if p.returncode != 0:
+        raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{p.stdout}\n{p.stderr}")
+    os.replace(tmp, BINDING)
 
 
 # Kernels that move registers between warpgroups with setmaxnreg assume this
@@ -100,8 +135,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        binding = ex.submit(_compile_binding)
         results = list(ex.map(_compile, srcs))
+        binding_obj = binding.result()
     with open(os.path.join(BUILD, "ptxas.txt"), "w") as f:
         for (obj, log), src in zip(results, srcs):
             f.write(f"== {os.path.basename(src)}\n{log}\n")
@@ -112,6 +149,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if p.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{p.stdout}\n{p.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding_obj)
     if verbose:
         print(open(os.path.join(BUILD, "ptxas.txt")).read())
     return LIB
