@@ -121,6 +121,7 @@ struct Params {
     int page_size, table_pages, pages;
     int v_f32, vec_q, vec_out;
     int q_tokens;                 // query tokens of a half, if q can be loaded by tensor map; else 0
+    int out_tokens, out_part;     // query tokens of a warp's rows, if out can be written so, else 0; and of a part
     float scale;
 };
 
@@ -208,7 +209,8 @@ template <int DP, int PL>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                    const __grid_constant__ CUtensorMap map_k_lo, const __grid_constant__ CUtensorMap map_v_lo,
-                   const __grid_constant__ CUtensorMap map_q, const Params p)
+                   const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_out,
+                   const Params p)
 {
     using C = Cfg<DP, PL>;
     constexpr int BN = C::BN, NS = C::NS, OB = C::OB;
@@ -705,24 +707,44 @@ __global__ void __launch_bounds__(kThreads, 1)
                 alpha = alpha_new;
             }
         }
-        // out, row by row through shared memory (this warp's share of q's planes,
-        // which the products of this half have read): a thread holds a row, and
-        // rows are written 512 or 256 bytes at a time
+        // out, through shared memory (this warp's share of q's planes, which the
+        // products of this half have read): a thread holds a row
         const float l = (lo_f(l2) + hi_f(l2)) * (1.0f / kAttnPScale);
         // no key seen, or none that counts beside an infinite score (NaN stays NaN)
         const float norm = l == 0.0f ? 0.0f : (1.0f / kAttnPScale) / l;
         if (ok) {
+            // Boxes of 32 values of the warp's 32 rows, 128-byte swizzled as the
+            // tensor map wants them (and as free of bank conflicts either way).
             constexpr int kChunks = DP / 4;  // 16 bytes each
-            ulonglong2* const tile = reinterpret_cast<ulonglong2*>(smem + half * 2 * C::kQTile) + w4 * 32 * kChunks;
+            uint8_t* const tile = smem + half * 2 * C::kQTile + w4 * (32 * DP * 4);
             const uint64_t norm2 = f2_bits(norm, norm);
 #pragma unroll
             for (int c = 0; c < kChunks; ++c)
-                tile[lane * kChunks + (c ^ (lane & 7))] = make_ulonglong2(mul2(o[2 * c], norm2), mul2(o[2 * c + 1], norm2));
-            __syncwarp();
+                *reinterpret_cast<ulonglong2*>(tile + (c / 8) * 4096 + sw128(lane, c % 8)) =
+                    make_ulonglong2(mul2(o[2 * c], norm2), mul2(o[2 * c + 1], norm2));
             constexpr int kRows = 32 / kChunks;  // rows a warp writes at once
             const int chunk = lane % kChunks, d = chunk * 4;
             const unsigned rows_there = __ballot_sync(0xffffffffu, valid);
-            if (p.vec_out && p.q_tokens > 0) {
+            if (p.out_tokens > 0 && rows_there == 0xffffffffu) {
+                // whole tokens, all there: by tensor map
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    const int token = part * p.out_part + q0 + ((2 * sm->block + half) * 4 + w4) * p.out_tokens;
+#pragma unroll
+                    for (int x = 0; x < DP / 32; ++x)
+                        if (x * 32 < p.dim)
+                            tma_store_3d(&map_out, tile + x * 4096, x * 32, head * p.group, token);
+                    bulk_commit_group();
+                    if (sm->hurt) {  // written before values are added below
+                        bulk_wait_group0();
+                        asm volatile("fence.proxy.async.global;" ::: "memory");
+                    } else {
+                        bulk_wait_group_read0();
+                    }
+                }
+                __syncwarp();
+            } else if (__syncwarp(), p.vec_out && p.q_tokens > 0) {
                 // rows are whole tokens of a power of two of heads: addresses by shifts
                 // (exchanges between lanes queue behind the other half's operands)
                 const int shift = 31 - __clz(p.group);
@@ -732,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i0 = 0; i0 < 32; i0 += kRows) {
                     const int i = i0 + lane / kChunks, row = w4 * 32 + i;
                     float* const to = base + (row >> shift) * p.out_token + (row & (p.group - 1)) * p.out_head;
-                    const float4 x = reinterpret_cast<const float4*>(tile)[i * kChunks + (chunk ^ (i & 7))];
+                    const float4 x = *reinterpret_cast<const float4*>(tile + (chunk / 8) * 4096 + sw128(i, chunk % 8));
                     if (((rows_there >> i) & 1) && d < p.dim)
                         *reinterpret_cast<float4*>(to) = x;
                 }
@@ -741,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i0 = 0; i0 < 32; i0 += kRows) {
                     const int i = i0 + lane / kChunks;
                     float* const to = p.out + __shfl_sync(0xffffffffu, out_at, i) + d;
-                    const float4 x = reinterpret_cast<const float4*>(tile)[i * kChunks + (chunk ^ (i & 7))];
+                    const float4 x = *reinterpret_cast<const float4*>(tile + (chunk / 8) * 4096 + sw128(i, chunk % 8));
                     if (!((rows_there >> i) & 1))
                         continue;
                     if (p.vec_out && d < p.dim) {
@@ -861,32 +883,34 @@ bool map_legal(int64_t tokens, int64_t heads, int64_t token, int64_t head)
     return ok(tokens, token) && ok(heads, head);
 }
 
-// q as boxes of one half's rows, where they are whole tokens: `group` heads of
-// `tokens` tokens, dense.  0 if it is not to be loaded so.
-int encode_q(CUtensorMap* map, const float* q, int dim, int heads, int group, int64_t tokens, int64_t token,
-             int64_t head, bool vec)
+// FP32 [tokens, heads, dim] as boxes of `rows` rows that are whole tokens of
+// `group` heads, `width` values of each: q's halves (dense) or out's warps (32
+// values, 128-byte swizzled).  The box's tokens, or 0 if there is no such map.
+int encode_tokens(CUtensorMap* map, const float* base, int dim, int heads, int group, int64_t tokens, int64_t token,
+                  int64_t head, int rows, int width, bool vec)
 {
     const auto ok = [](int64_t extent, int64_t stride) {
         return extent <= 1 || (stride > 0 && stride % 4 == 0 && stride < (1ll << 37));
     };
     EncodeTiledFn fn = encode_fn();
-    if (!fn || !vec || 128 % group != 0 || !ok(tokens, token) || !ok(heads, head))
+    if (!fn || !vec || rows % group != 0 || !ok(tokens, token) || !ok(heads, head))
         return 0;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads),
                                 static_cast<cuuint64_t>(tokens)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(heads > 1 ? head * 4 : 512),
                                    static_cast<cuuint64_t>(tokens > 1 ? token * 4 : 512)};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(dim), static_cast<cuuint32_t>(group),
-                               static_cast<cuuint32_t>(128 / group)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(width), static_cast<cuuint32_t>(group),
+                               static_cast<cuuint32_t>(rows / group)};
     const cuuint32_t estr[3] = {1, 1, 1};
-    const bool done = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<float*>(q), dims, strides, box, estr,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+    const bool done = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<float*>(base), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         rows == 128 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-    return done ? 128 / group : 0;
+    return done ? rows / group : 0;
 }
 
 template <int DP, int PL>
-comp_status_t launch_t(const CUtensorMap (&maps)[5], const Params& p, int64_t grid, const DeviceInfo& dev,
+comp_status_t launch_t(const CUtensorMap (&maps)[6], const Params& p, int64_t grid, const DeviceInfo& dev,
                        cudaStream_t stream)
 {
     using C = Cfg<DP, PL>;
@@ -906,7 +930,7 @@ comp_status_t launch_t(const CUtensorMap (&maps)[5], const Params& p, int64_t gr
         }
     }
     return launch_pdl(attn_tc_kernel<DP, PL>, static_cast<int>(grid), kThreads, C::kSmem, stream, maps[0], maps[1],
-                      maps[2], maps[3], maps[4], p);
+                      maps[2], maps[3], maps[4], maps[5], p);
 }
 
 int64_t pad8(int64_t d)
@@ -958,7 +982,7 @@ comp_status_t launch_attn(const comp_attn_t& a, const float* q, const void* k, c
     p.vec_q = a.q_token % 4 == 0 && a.q_head % 4 == 0 && a.head_dim % 4 == 0 && aligned16(q);
     p.vec_out = a.out_token % 4 == 0 && a.out_head % 4 == 0 && a.head_dim % 4 == 0 && aligned16(out);
 
-    CUtensorMap maps[5] = {};
+    CUtensorMap maps[6] = {};
     const int box_rows = a.head_dim > 64 && kv_bytes == 4 ? 64 : 128;  // Cfg::BN
     if (a.total_k > 0) {
         const void* planes[4] = {k, v, nullptr, nullptr};
@@ -988,7 +1012,10 @@ comp_status_t launch_attn(const comp_attn_t& a, const float* q, const void* k, c
             if (!encode_rows(&maps[i], planes[i], dim, a.total_k, a.kv_heads, token[i % 2], head[i % 2], box_rows))
                 return COMP_ERR_CUDA;
     }
-    p.q_tokens = encode_q(&maps[4], q, p.dim, a.heads, p.group, a.total_q, a.q_token, a.q_head, p.vec_q);
+    p.q_tokens = encode_tokens(&maps[4], q, p.dim, a.heads, p.group, a.total_q, a.q_token, a.q_head, 128, p.dim,
+                               p.vec_q);
+    p.out_tokens = encode_tokens(&maps[5], out, p.dim, a.heads, p.group, a.total_q, a.out_token, a.out_head, 32, 32,
+                                 p.vec_out);
     const int64_t rows = a.total_q * p.group;
     const int64_t grid = (cu_q ? rows / 256 + a.n_seq : (rows + 255) / 256) * a.kv_heads;
     if (grid > INT32_MAX)
@@ -1029,11 +1056,14 @@ comp_status_t launch_attn_prefix(const comp_kv_cache_t& cache, const float* q, i
     p.scale = scale;
     p.vec_q = q_token % 4 == 0 && q_head % 4 == 0 && aligned16(q);
     p.vec_out = 1;
-    CUtensorMap maps[5] = {};
+    CUtensorMap maps[6] = {};
     if (!encode_pages(&maps[0], cache.k, cache, cache.page_size) ||
         !encode_pages(&maps[1], cache.v, cache, cache.page_size))
         return COMP_ERR_CUDA;
-    p.q_tokens = encode_q(&maps[4], q, p.dim, heads, p.group, batch, q_token, q_head, p.vec_q);
+    p.q_tokens = encode_tokens(&maps[4], q, p.dim, heads, p.group, batch, q_token, q_head, 128, p.dim, p.vec_q);
+    p.out_tokens = encode_tokens(&maps[5], out, p.dim, heads, p.group, batch * splits, p.out_token, p.out_head, 32,
+                                 32, true);
+    p.out_part = static_cast<int>(batch);
     const int64_t grid = (batch * p.group + 255) / 256 * cache.kv_heads * splits;
     if (grid > INT32_MAX)
         return COMP_ERR_INVALID_VALUE;
