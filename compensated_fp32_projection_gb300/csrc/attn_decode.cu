@@ -60,7 +60,7 @@ struct Params {
     const int32_t* table;
     const int32_t* lengths;
     int64_t q_token, q_head, width;
-    int batch, heads, kv_heads, group, row_blocks, dim, page_shift, pages, shared_keys, most_keys, pieces, vec_q;
+    int batch, heads, kv_heads, group, row_blocks, dim, page_shift, pages, shared_keys, most_keys, pieces, vec_q, after_prefix;
     float scale;
 };
 
@@ -221,14 +221,22 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
     }
     __syncwarp();
     grid_dependency_launch();
-    grid_dependency_wait();
+    // After a prefix's kernel this one need not wait for it, only for what came
+    // before, which that kernel has waited for before it let this one start: the
+    // SMs it leaves free, and those it is done with, work here meanwhile.  What
+    // follows this kernel follows both, so its first CTA waits at its end.
+    if (!p.after_prefix)
+        grid_dependency_wait();
 
     // this warp's piece; consecutive ones are on different SMs
     const int piece = warp * gridDim.x + blockIdx.x;
     int begin, end;
     Place r;
-    if (!find_piece(p, piece, begin, end, r))
+    if (!find_piece(p, piece, begin, end, r)) {
+        if (blockIdx.x == 0)
+            grid_dependency_wait();
         return;
+    }
 
     // Rows.  The query heads split: rows 0..7 of a block hi, 8..15 lo.
     const int g = lane >> 2, quad = lane & 3;
@@ -444,6 +452,8 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
     if (!ok)  // what was issued lands before the warp leaves
         for (int j = i; j < loads; ++j)
             attn_drain_wait(&full[j % NS], (j / NS) & 1);
+    if (blockIdx.x == 0)
+        grid_dependency_wait();
 }
 
 // The parts of each row joined: the prefix's (splits of them), then those of
@@ -662,6 +672,7 @@ comp_status_t launch_attn_decode(const comp_kv_cache_t& cache, const float* q, i
     p.pieces = 2 * dev.sm_count * kWarps < kMostPieces ? 2 * dev.sm_count * kWarps : kMostPieces;
     p.vec_q = (reinterpret_cast<uintptr_t>(q) & 7u) == 0 && q_token % 2 == 0 && q_head % 2 == 0;
     p.scale = scale;
+    p.after_prefix = splits > 0;
     CUtensorMap mk{}, mv{};
     if (width > 0) {  // otherwise there are no tiles
         if (!encode_pages(&mk, cache.k, cache, kTile) || !encode_pages(&mv, cache.v, cache, kTile))

@@ -222,8 +222,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // warp-uniform to the compiler, so that roles and loop counts stay in uniform registers
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
-    grid_dependency_launch();
+    // A dependent that starts early finds what this kernel waited for complete
+    // (the decode kernel relies on it).
     grid_dependency_wait();
+    grid_dependency_launch();
     const int head = blockIdx.x % p.kv_heads;
     const int part = blockIdx.x / p.kv_heads % p.splits;
     if (warp == 0)
