@@ -523,7 +523,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nh = half ? n1 : n0, w4 = warp & 3;
         const uint32_t lanes = static_cast<uint32_t>(w4 * 32) << 16;
         bool ok = true;
-        // q into shared memory, split; a warp takes its 32 rows one after the other
+        // q has landed before anything else is done where it goes, and before the
+        // CTA leaves
+        if (p.q_tokens > 0)
+            ok = attn_warp_wait(&sm->qload[half], 0, &sm->abort, kFaultAttnRows);
+        // q's planes: a warp splits its 32 rows
         if (nh > 0) {
             uint8_t* const hi_tile = smem + half * 2 * C::kQTile;
             constexpr int kLanes = DP / 4, kAtOnce = 32 / kLanes;  // lanes of a row, rows a load
@@ -541,7 +545,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             if (p.q_tokens > 0) {
                 // the warps read all rows before one of them writes a plane
-                ok = attn_warp_wait(&sm->qload[half], 0, &sm->abort, kFaultAttnRows);
                 float4 x[32 / kAtOnce];
 #pragma unroll
                 for (int i = 0; i < 32 / kAtOnce; ++i)
