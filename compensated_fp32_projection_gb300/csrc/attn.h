@@ -36,6 +36,22 @@ __device__ __forceinline__ bool attn_wait(uint64_t* bar, uint32_t parity, int* a
     }
 }
 
+// The same for a barrier that the other CTA of a cluster arrives on too.
+__device__ __forceinline__ bool attn_wait_cluster(uint64_t* bar, uint32_t parity, int* abort_flag, uint32_t code)
+{
+    const long long start = clock64();
+    while (!mbar_try_wait_acquire_cluster(bar, parity)) {
+        if (*reinterpret_cast<volatile int*>(abort_flag))
+            return false;
+        if (clock64() - start > kAttnWaitLimit) {
+            atomicCAS(&g_attn_fault_word, 0u, code);
+            *reinterpret_cast<volatile int*>(abort_flag) = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
 // Warp-wide: lane 0 waits, and on success every lane observes the phase itself.
 __device__ __forceinline__ bool attn_warp_wait(uint64_t* bar, uint32_t parity, int* abort_flag, uint32_t code)
 {

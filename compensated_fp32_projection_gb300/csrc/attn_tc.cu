@@ -68,26 +68,36 @@ constexpr uint32_t kFaultAttnRows = 0x904;
 constexpr uint32_t kFaultAttnTmem = 0x905;
 
 // DP: the head dimension padded to 64 or 128.  PL: planes of k and v, 1 (FP16)
-// or 2 (FP32, split).
-template <int DP_, int PL_>
+// or 2 (FP32, split).  PAIR: two CTAs of a cluster work on the same keys, 512
+// rows together: their products are issued as one (cta_group::2, M = 256), and
+// each holds half of every tile, half the keys of k and half the head
+// dimension of v.
+template <int DP_, int PL_, bool PAIR_>
 struct Cfg {
     static constexpr int DP = DP_, PL = PL_;
+    static constexpr int R = PAIR_ ? 2 : 1;                     // CTAs that share a tile
     // Keys of a tile.  With two planes at D = 128 a tile of 128 keys would take
-    // 64 KB a stage beside the 128 KB of q: 64 keys leave three stages.
-    static constexpr int BN = DP == 128 && PL == 2 ? 64 : 128;
+    // 64 KB a stage beside the 128 KB of q: 64 keys leave three stages to one
+    // CTA.  Products of 64 columns are bound by the shared memory that feeds
+    // them (49 cycles instead of 32), so that a pair, which has room for 128,
+    // takes 304 us where one CTA takes 341 (4096 FP32 tokens, 16 heads of 128;
+    // causal, 32 heads: 349 against 366).  Its blocks of 512 rows want long
+    // sequences: it is used from 1024 rows on average on.
+    static constexpr int BN = DP == 128 && PL == 2 && !PAIR_ ? 64 : 128;
     static constexpr int kBoxes = DP / 64;                      // 64-wide boxes along D
     static constexpr uint32_t kQTile = 128 * DP * 2;            // one plane of one half
     static constexpr uint32_t kQBytes = 4 * kQTile;
-    static constexpr uint32_t kPlane = BN * DP * 2;
+    static constexpr uint32_t kPlane = BN * DP * 2 / R;
     static constexpr uint32_t kStage = PL * kPlane;
+    static constexpr uint32_t kKBox = BN / R * 128;             // bytes of 64 values of a stage's keys
     static constexpr int NS = DP == 128 ? 3 : (PL == 2 ? 4 : 6);
     // Buffers of O' a half: what tensor memory has left beside S (2 x 128 of
     // 512 columns).
     static constexpr int OB = DP == 128 ? 1 : 2;
     static constexpr size_t kSmem = 1024 + kQBytes + NS * kStage + 1024;
     static_assert(kSmem <= 232448, "shared memory");
-    static constexpr uint32_t kIdescS = idesc_f16_f32(128, BN);
-    static constexpr uint32_t kIdescO = idesc_f16_f32(128, DP) | kIdescBMnMajor;
+    static constexpr uint32_t kIdescS = idesc_f16_f32(128 * R, BN);
+    static constexpr uint32_t kIdescO = idesc_f16_f32(128 * R, DP) | kIdescBMnMajor;
 };
 
 struct Shared {
@@ -96,12 +106,14 @@ struct Shared {
                                  // several tiles ahead of the products)
     uint64_t qload[2];           // a half's q has landed, FP32
     uint64_t sfull[2];           // a half's S of a tile, and O' of the tile before, are complete
+    uint64_t pfull[2][2];        // pairs: q, then the first part of each P, and the second, of both CTAs
     uint64_t drain[2];
     uint32_t tmem_base;
     int abort;
     int block;                   // this CTA's block of rows; < 0: none
     int q0, nq, k0, nk;          // its sequence's queries and keys
     int most[2], least[2];       // most and least keys that a row of a half sees
+    int other[4];                // pairs: the other CTA's
     int hurt;                    // a looked-through tile has values that are not finite, and seen
 };
 
@@ -158,15 +170,16 @@ __device__ __forceinline__ void rows_arrive(int id)
     asm volatile("bar.arrive %0, 160;" ::"r"(id) : "memory");
 }
 
-// This CTA's sequence and block of 256 rows: blocks are numbered sequence by
+// This CTA's (or pair's) sequence and block of kRows rows: blocks are numbered sequence by
 // sequence, the last of one, which sees most keys, first.  One warp; the
 // offsets are read 32 sequences at a time.
+template <int kRows>
 __device__ __forceinline__ void find_block(const Params& p, int block, Shared* sm)
 {
     const int lane = threadIdx.x & 31;
     if (!p.cu_q) {
         if (lane == 0) {
-            sm->block = static_cast<int>((static_cast<int64_t>(p.total_q) * p.group + 255) / 256) - 1 - block;
+            sm->block = static_cast<int>((static_cast<int64_t>(p.total_q) * p.group + kRows - 1) / kRows) - 1 - block;
             sm->q0 = sm->k0 = 0;
             sm->nq = p.total_q;
             sm->nk = p.total_k;
@@ -179,7 +192,7 @@ __device__ __forceinline__ void find_block(const Params& p, int block, Shared* s
         if (s < p.n_seq) {
             a = clampi(p.cu_q[s], 0, p.total_q), b = clampi(p.cu_q[s + 1], a, p.total_q);
             c = clampi(p.cu_k[s], 0, p.total_k), d = clampi(p.cu_k[s + 1], c, p.total_k);
-            n = static_cast<int>((static_cast<unsigned>(b - a) * static_cast<unsigned>(p.group) + 255u) / 256u);
+            n = static_cast<int>((static_cast<unsigned>(b - a) * static_cast<unsigned>(p.group) + (kRows - 1u)) / kRows);
         }
         int x = n;
 #pragma unroll
@@ -205,15 +218,15 @@ __device__ __forceinline__ void find_block(const Params& p, int block, Shared* s
         sm->block = -1;
 }
 
-template <int DP, int PL>
+template <int DP, int PL, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                    const __grid_constant__ CUtensorMap map_k_lo, const __grid_constant__ CUtensorMap map_v_lo,
                    const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_out,
                    const Params p)
 {
-    using C = Cfg<DP, PL>;
-    constexpr int BN = C::BN, NS = C::NS, OB = C::OB;
+    using C = Cfg<DP, PL, PAIR>;
+    constexpr int BN = C::BN, NS = C::NS, OB = C::OB, R = C::R;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* const stages = smem + C::kQBytes;
@@ -226,19 +239,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (the decode kernel relies on it).
     grid_dependency_wait();
     grid_dependency_launch();
-    const int head = blockIdx.x % p.kv_heads;
-    const int part = blockIdx.x / p.kv_heads % p.splits;
+    const uint32_t rank = PAIR ? cluster_ctarank() : 0;
+    const int item = blockIdx.x / R, head = item % p.kv_heads;
+    const int part = item / p.kv_heads % p.splits;
     if (warp == 0)
-        find_block(p, blockIdx.x / p.kv_heads / p.splits, sm);
+        find_block<256 * R>(p, item / p.kv_heads / p.splits, sm);
     if (threadIdx.x == 64) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(&sm->full[i], 1);
             mbar_init(&sm->empty[i], 3);
-            mbar_init(&sm->checked[i], 1);
+            mbar_init(&sm->checked[i], R);
         }
         for (int h = 0; h < 2; ++h) {
             mbar_init(&sm->qload[h], 1);
             mbar_init(&sm->sfull[h], 1);
+            mbar_init(&sm->pfull[h][0], 4 * R);
+            mbar_init(&sm->pfull[h][1], 4 * R);
         }
         mbar_init(&sm->drain[0], 1);
         mbar_init(&sm->drain[1], 1);
@@ -254,7 +270,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (sm->block < 0)
         return;  // the grid is an upper bound
 
-    const int half = (warp >> 2) - 1;
+    // A half's rows in blocks of 128: this CTA's block of them.
+    const int half = (warp >> 2) - 1, rows128 = (2 * sm->block + half) * R + static_cast<int>(rank);
     // One load brings a half's rows of q, FP32, to where its planes will be
     // (tokens past the sequence's end too: rows that are not there).  Loads by
     // the threads would wait for each other in the small L1 that 227 KB of
@@ -262,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (p.q_tokens > 0 && (warp == 4 || warp == 8) && lane == 0) {
         mbar_arrive_expect_tx(&sm->qload[half], 128 * p.dim * 4);
         tma_load_3d(smem + half * 2 * C::kQTile, &map_q, &sm->qload[half], 0, head * p.group,
-                    sm->q0 + (2 * sm->block + half) * p.q_tokens);
+                    sm->q0 + rows128 * p.q_tokens);
     }
 
     // the part of its sequence's keys that this CTA goes through
@@ -277,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool valid = false;
     if (half >= 0) {
         // total_q * heads is an int
-        const unsigned row = static_cast<unsigned>(sm->block) * 256u + (threadIdx.x - 128);
+        const unsigned row = static_cast<unsigned>(rows128) * 128u + (threadIdx.x & 127);
         const unsigned group = static_cast<unsigned>(p.group);
         valid = row < static_cast<unsigned>(nq) * group;
         const int t = static_cast<int>(valid ? row / group : 0u), hq = head * p.group + static_cast<int>(row % group);
@@ -299,10 +316,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     if (warp == 1) {
-        tmem_alloc(&sm->tmem_base, 512);
-        tmem_relinquish();
+        if (PAIR) {
+            tmem_alloc_pair(&sm->tmem_base, 512);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(&sm->tmem_base, 512);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
+    if (PAIR) {
+        // what the rows of either CTA see decides on the tiles of both
+        cluster_sync();
+        if (threadIdx.x < 4)
+            st_cluster(mapa_shared(&sm->other[threadIdx.x], rank ^ 1),
+                       threadIdx.x < 2 ? sm->most[threadIdx.x] : sm->least[threadIdx.x - 2]);
+        cluster_sync();
+        if (threadIdx.x < 2) {
+            sm->most[threadIdx.x] = max(sm->most[threadIdx.x], sm->other[threadIdx.x]);
+            sm->least[threadIdx.x] = min(sm->least[threadIdx.x], sm->other[threadIdx.x + 2]);
+        }
+    }
     __syncthreads();
     tc_fence_after();
     // All 512 columns are this CTA's, so they begin at 0: tensor-memory addresses
@@ -331,6 +365,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0)
                     mbar_arrive_expect_tx(&sm->full[s], C::kStage);
                 __syncwarp();
+                if (PAIR) {
+                    // this CTA's half: keys of k in boxes along the head dimension, 64
+                    // values of v in boxes of 64 keys
+                    if (lane < 2 * PL) {
+                        const int plane = lane / 2, sub = lane % 2, is_v = i & 1;
+                        const CUtensorMap* const map = plane ? (is_v ? &map_v_lo : &map_k_lo) : (is_v ? &map_v : &map_k);
+                        const int key = k0 + first + (i >> 1) * BN;
+                        tma_load_3d(stages + s * C::kStage + plane * C::kPlane + sub * 8192, map, &sm->full[s],
+                                    (is_v ? rank : sub) * 64, key + (is_v ? sub : rank) * 64, head);
+                    }
+                    __syncwarp();
+                    continue;
+                }
                 for (int b = lane; b < boxes; b += 32) {
                     const int piece = b % pieces, box = b / pieces % C::kBoxes, plane = b / pieces / C::kBoxes;
                     uint8_t* const dst = stages + s * C::kStage + plane * C::kPlane + box * (BN * 128) +
@@ -353,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = max(0, i - NS); j < i; ++j)
                     attn_drain_wait(&sm->full[j % NS], (j / NS) & 1);
             }
-        } else if (warp < 3) {
+        } else if (warp < 3 && rank == 0) {
             // ---------------- products: warp 1 issues those of the first half, warp 2 of the second
             // One lane issues in a branch of its own with constant accumulator
             // addresses: 65 cycles for a 128 x 128 x 16 product, the tensor
@@ -373,16 +420,49 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto wait = [&](uint64_t* bar, int phase) {
                 ok = ok && attn_wait(bar, phase & 1, &sm->abort, kFaultAttnMma);
             };
+            auto wait_cluster = [&](uint64_t* bar, int phase) {
+                ok = ok && attn_wait_cluster(bar, phase & 1, &sm->abort, kFaultAttnMma);
+            };
+            // a stage's tile, in a pair both CTAs' halves of it (which pass their warps 3)
+            auto wait_tile = [&](int s, int load, bool looked_through) {
+                if (PAIR && looked_through) {
+                    wait_cluster(&sm->checked[s], load / NS);
+                } else if (PAIR) {
+                    wait(&sm->checked[s], load / NS);
+                } else {
+                    wait(&sm->full[s], load / NS);
+                    if (looked_through)
+                        wait(&sm->checked[s], load / NS);
+                }
+            };
+            auto commit = [&](uint64_t* bar) {
+                if (PAIR)
+                    umma_commit_pair_by(1, bar, 0x3);
+                else
+                    umma_commit_by(1, bar);
+            };
+            auto pv = [&](uint32_t d, uint32_t a, uint32_t b, uint32_t add) {
+                if (PAIR)
+                    umma_pair_ta_w_by(1, d, a, b, kDescHi, C::kIdescO, add);
+                else
+                    umma_ta_w_by(1, d, a, b, kDescHi, C::kIdescO, add);
+            };
             // S: a and b at q's and k's planes; how: 0 fresh, 1 added, 2 added to 2^-10 of what is there
             auto chain = [&](uint32_t qd, uint32_t kd, int how) {
 #pragma unroll
                 for (int t = 0; t < DP / 16; ++t) {
                     const uint32_t da = qd + (t / 4) * (128 * 128 >> 4) + (t % 4) * 2;
-                    const uint32_t db = kd + (t / 4) * (BN * 128 >> 4) + (t % 4) * 2;
-                    if (t == 0 && how == 2)
-                        umma_w_scale10_by(1, ds, da, db, kDescHi, C::kIdescS);
-                    else
+                    const uint32_t db = kd + (t / 4) * (C::kKBox >> 4) + (t % 4) * 2;
+                    if (t == 0 && how == 2) {
+                        if (PAIR)
+                            umma_pair_w_scale10_by(1, ds, da, db, kDescHi, C::kIdescS);
+                        else
+                            umma_w_scale10_by(1, ds, da, db, kDescHi, C::kIdescS);
+                    } else if (PAIR) {
+                        umma_pair_w_by(1, ds, da, db, kDescHi, C::kIdescS, t > 0 || how > 0);
+                    } else {
                         umma_w_by(1, ds, da, db, kDescHi, C::kIdescS, t > 0 || how > 0);
+                    }
                 }
             };
             int sk = 0, sv = NS - 1;  // stages of K of tile j + 1 and V of tile j
@@ -391,14 +471,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int iv = 2 * j + 1, ik = 2 * j + 2;  // their loads
                 const bool has_v = j >= 0 && j < nh, has_k = j + 1 < nh;
                 if (elect_one()) {
-                    if (has_v) {
-                        wait(&sm->full[sv], iv / NS);
-                        if (j >= edge)
-                            wait(&sm->checked[sv], iv / NS);
-                    }
+                    if (has_v)
+                        wait_tile(sv, iv, j >= edge);
+                    if (PAIR && j < 0 && has_k)
+                        wait_cluster(&sm->pfull[h][0], 0);
+                    else if (PAIR && has_v)
+                        wait(&sm->pfull[h][0], j + 1);
                 }
                 __syncwarp();
-                if (has_v || has_k)  // P's first half, before the first tile q
+                if (!PAIR && (has_v || has_k))  // P's first half, before the first tile q
                     rows_sync(4 + 2 * h);
                 // the turn: the second half waits for the first half's step, the first for the second's before
                 if (h == 1 || j >= 0)
@@ -413,10 +494,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int t = t0; t < t0 + kSteps; ++t) {
                         if (PL == 1) {
-                            umma_ta_w_by(1, d, ds + t * 16 + 8, vhi + t * 128, kDescHi, C::kIdescO, t > 0);
-                            umma_ta_w_by(1, d, ds + t * 16, vhi + t * 128, kDescHi, C::kIdescO, 1);
+                            pv(d, ds + t * 16 + 8, vhi + t * 128, t > 0);
+                            pv(d, ds + t * 16, vhi + t * 128, 1);
                         } else {  // hi P with lo v, over all keys before the accumulator is scaled
-                            umma_ta_w_by(1, d, ds + t * 16, vlo + t * 128, kDescHi, C::kIdescO, t > 0);
+                            pv(d, ds + t * 16, vlo + t * 128, t > 0);
                         }
                     }
                 };
@@ -424,26 +505,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (elect_one() && ok)
                         part(0);
                     __syncwarp();
-                    rows_sync(5 + 2 * h);
+                    if (!PAIR)
+                        rows_sync(5 + 2 * h);
                 }
                 if (elect_one()) {
+                    if (PAIR && has_v)
+                        wait(&sm->pfull[h][1], j);
                     if (has_v && ok) {
                         part(kSteps);
                         if (PL == 2) {
 #pragma unroll
                             for (int t = 0; t < 2 * kSteps; ++t) {
-                                if (t == 0)
-                                    umma_ta_w_scale10_by(1, d, ds + 8, vhi, kDescHi, C::kIdescO);
+                                if (t > 0)
+                                    pv(d, ds + t * 16 + 8, vhi + t * 128, 1);
+                                else if (PAIR)
+                                    umma_pair_ta_w_scale10_by(1, d, ds + 8, vhi, kDescHi, C::kIdescO);
                                 else
-                                    umma_ta_w_by(1, d, ds + t * 16 + 8, vhi + t * 128, kDescHi, C::kIdescO, 1);
-                                umma_ta_w_by(1, d, ds + t * 16, vhi + t * 128, kDescHi, C::kIdescO, 1);
+                                    umma_ta_w_scale10_by(1, d, ds + 8, vhi, kDescHi, C::kIdescO);
+                                pv(d, ds + t * 16, vhi + t * 128, 1);
                             }
                         }
                     }
                     if (j >= 0)
-                        umma_commit_by(1, &sm->empty[sv]);
+                        commit(&sm->empty[sv]);
                     if (has_k)
-                        wait(&sm->full[sk], ik / NS);
+                        wait_tile(sk, ik, false);
                     if (has_k && ok) {
                         tc_fence_after();
                         const uint32_t khi = k_lo32 + sk * kKvStage;
@@ -453,23 +539,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                         chain(qhi, khi, 2);
                     }
                     if ((has_v || has_k) && ok)
-                        umma_commit_by(1, &sm->sfull[h]);
+                        commit(&sm->sfull[h]);
                 }
                 __syncwarp();
                 if (h == 0 || j + 1 < n)
                     asm volatile("bar.arrive %0, 64;" ::"r"(2 + h) : "memory");
                 if (elect_one() && j + 1 < n)
-                    umma_commit_by(1, &sm->empty[sk]);
+                    commit(&sm->empty[sk]);
                 __syncwarp();
                 sk = sk + 2 >= NS ? sk + 2 - NS : sk + 2;
                 sv = sv + 2 >= NS ? sv + 2 - NS : sv + 2;
             }
             if (elect_one() && *reinterpret_cast<volatile int*>(&sm->abort)) {
-                umma_commit_by(1, &sm->drain[h]);
+                if (PAIR)
+                    umma_commit_pair_by(1, &sm->drain[h], 0x1);
+                else
+                    umma_commit_by(1, &sm->drain[h]);
                 attn_drain_wait(&sm->drain[h], 0);
             }
             __syncwarp();
-        } else {
+        } else if (warp == 3) {
             // ---------------- values that must not count
             for (int i = 0; i < 2 * n; ++i) {
                 const int s = i % NS, j = i >> 1;
@@ -506,13 +595,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     }
-                    if (__any_sync(0xffffffffu, seen) && lane == 0)
-                        atomicOr(&sm->hurt, 1);
+                    if (__any_sync(0xffffffffu, seen) && lane == 0) {
+                        *reinterpret_cast<volatile int*>(&sm->hurt) = 1;
+                        if (PAIR)  // v's columns are the other CTA's rows' too
+                            st_cluster(mapa_shared(&sm->hurt, rank ^ 1), 1);
+                    }
                     fence_proxy_async_smem();
                 }
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&sm->checked[s]);
+                    // a pair's other CTA learns here that the load has landed; only what
+                    // this warp wrote itself needs a release over the cluster
+                    if (!PAIR)
+                        mbar_arrive(&sm->checked[s]);
+                    else if ((i & 1) && j >= edge)
+                        mbar_arrive_release_cluster(mapa_shared(&sm->checked[s], 0));
+                    else
+                        mbar_arrive_cluster(mapa_shared(&sm->checked[s], 0));
                     mbar_arrive(&sm->empty[s]);
                 }
             }
@@ -523,10 +622,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nh = half ? n1 : n0, w4 = warp & 3;
         const uint32_t lanes = static_cast<uint32_t>(w4 * 32) << 16;
         bool ok = true;
-        // q has landed before anything else is done where it goes, and before the
-        // CTA leaves
-        if (p.q_tokens > 0)
-            ok = attn_warp_wait(&sm->qload[half], 0, &sm->abort, kFaultAttnRows);
+        // q, or a part of P, to the issuing warp (a pair's is in its first CTA)
+        auto hand_over = [&](int part_of_p, bool planes) {
+            if (PAIR) {
+                __syncwarp();
+                const uint32_t to = mapa_shared(&sm->pfull[half][part_of_p], 0);
+                if (lane == 0) {
+                    // q's planes are shared memory; P is tensor memory, ordered by
+                    // tcgen05's own fences, and a release over the cluster costs a
+                    // thousand cycles a tile
+                    if (planes)
+                        mbar_arrive_release_cluster(to);
+                    else
+                        mbar_arrive_cluster(to);
+                }
+            } else {
+                rows_arrive(4 + 2 * half + part_of_p);
+            }
+        };
         // q's planes: a warp splits its 32 rows
         if (nh > 0) {
             uint8_t* const hi_tile = smem + half * 2 * C::kQTile;
@@ -545,6 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             if (p.q_tokens > 0) {
                 // the warps read all rows before one of them writes a plane
+                ok = attn_warp_wait(&sm->qload[half], 0, &sm->abort, kFaultAttnRows);
                 float4 x[32 / kAtOnce];
 #pragma unroll
                 for (int i = 0; i < 32 / kAtOnce; ++i)
@@ -582,7 +696,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             fence_proxy_async_smem();
-            rows_arrive(4 + 2 * half);
+            hand_over(0, true);
+        } else if (p.q_tokens > 0) {
+            // q lands before anything else is done where it goes, and before the CTA leaves
+            ok = attn_warp_wait(&sm->qload[half], 0, &sm->abort, kFaultAttnRows);
         }
 
         const float c2 = p.scale * kAttnLog2E;
@@ -622,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j <= nh && nh > 0; ++j) {
             if (!attn_lane0_wait(&sm->sfull[half], j & 1, &sm->abort, kFaultAttnRows)) {
                 ok = false;
-                for (; j < nh; ++j) {  // the issuing warp waits for the rest of P
+                for (; !PAIR && j < nh; ++j) {  // the issuing warp waits for the rest of P
                     rows_sync(4 + 2 * half);
                     rows_sync(5 + 2 * half);
                 }
@@ -702,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (c == BN / 2 - 32 || c == BN - 32) {
                         tmem_st_wait();
                         tc_fence_before();
-                        rows_arrive(4 + 2 * half + (c >= BN / 2));
+                        hand_over(c >= BN / 2, false);
                     }
                 }
                 l2 = add2(l2, l3);
@@ -735,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    const int token = part * p.out_part + q0 + ((2 * sm->block + half) * 4 + w4) * p.out_tokens;
+                    const int token = part * p.out_part + q0 + (rows128 * 4 + w4) * p.out_tokens;
 #pragma unroll
                     for (int x = 0; x < DP / 32; ++x)
                         if (x * 32 < p.dim)
@@ -753,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // rows are whole tokens of a power of two of heads: addresses by shifts
                 // (exchanges between lanes queue behind the other half's operands)
                 const int shift = 31 - __clz(p.group);
-                float* const base = p.out + (static_cast<int64_t>(q0) + (2 * sm->block + half) * p.q_tokens) * p.out_token +
+                float* const base = p.out + (static_cast<int64_t>(q0) + rows128 * p.q_tokens) * p.out_token +
                                     static_cast<int64_t>(head) * p.group * p.out_head + part * p.out_split + d;
 #pragma unroll 8
                 for (int i0 = 0; i0 < 32; i0 += kRows) {
@@ -817,15 +934,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     tc_fence_before();
-    __syncthreads();
+    if (PAIR)
+        cluster_sync();  // neither CTA leaves while the other's products may read it or arrive on it
+    else
+        __syncthreads();
     tc_fence_after();
-    if (warp == 1)
-        tmem_dealloc(sm->tmem_base, 512);
+    if (warp == 1) {
+        if (PAIR)
+            tmem_dealloc_pair(sm->tmem_base, 512);
+        else
+            tmem_dealloc(sm->tmem_base, 512);
+    }
 }
 
 // FP32 keys and values as FP16 planes (hi = fp16(x), lo = fp16((x - hi) 1024)),
 // or FP16 ones that the tensor maps cannot take (addresses or strides off 16
-// bytes) as they are: rows of `dpad` values, zeros past the head dimension.
+// bytes) as they are: rows of `dpad` values, zeros past the head dimension,
+// head by head, so that a tile is one run of memory.
 // Each value is read once; the kernel above then reads every row once for
 // each 256 query rows.  blockIdx.y: k or v.
 struct Stage {
@@ -846,7 +971,7 @@ __global__ void __launch_bounds__(256) attn_stage_kernel(Stage p)
          u += static_cast<int64_t>(gridDim.x) * blockDim.x) {
         const int part = static_cast<int>(u % parts);
         const int64_t row = u / parts, at = row / p.heads * p.token[w] + row % p.heads * p.head[w] + part * 8;
-        const int64_t to = row * p.dpad + part * 8;
+        const int64_t to = (row % p.heads * p.tokens + row / p.heads) * p.dpad + part * 8;
         if (p.f32) {
             const float* const src = static_cast<const float*>(p.src[w]) + at;
             float x[8];
@@ -914,11 +1039,11 @@ int encode_tokens(CUtensorMap* map, const float* base, int dim, int heads, int g
     return done ? rows / group : 0;
 }
 
-template <int DP, int PL>
+template <int DP, int PL, bool PAIR = false>
 comp_status_t launch_t(const CUtensorMap (&maps)[6], const Params& p, int64_t grid, const DeviceInfo& dev,
                        cudaStream_t stream)
 {
-    using C = Cfg<DP, PL>;
+    using C = Cfg<DP, PL, PAIR>;
     static std::mutex mu;
     static bool done[64] = {};
     {
@@ -926,7 +1051,7 @@ comp_status_t launch_t(const CUtensorMap (&maps)[6], const Params& p, int64_t gr
         if (dev.device < 0 || dev.device >= 64)
             return COMP_ERR_CUDA;
         if (!done[dev.device]) {
-            if (cudaFuncSetAttribute(attn_tc_kernel<DP, PL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            if (cudaFuncSetAttribute(attn_tc_kernel<DP, PL, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      static_cast<int>(C::kSmem)) != cudaSuccess) {
                 (void)cudaGetLastError();
                 return COMP_ERR_CUDA;
@@ -934,8 +1059,8 @@ comp_status_t launch_t(const CUtensorMap (&maps)[6], const Params& p, int64_t gr
             done[dev.device] = true;
         }
     }
-    return launch_pdl(attn_tc_kernel<DP, PL>, static_cast<int>(grid), kThreads, C::kSmem, stream, maps[0], maps[1],
-                      maps[2], maps[3], maps[4], maps[5], p);
+    return launch_pdl_cluster(attn_tc_kernel<DP, PL, PAIR>, C::R, static_cast<int>(grid) * C::R, kThreads, C::kSmem,
+                              stream, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], p);
 }
 
 int64_t pad8(int64_t d)
@@ -1008,8 +1133,8 @@ comp_status_t launch_attn(const comp_attn_t& a, const float* q, const void* k, c
             for (int i = 0; i < 2; ++i) {
                 planes[i] = s.hi[i];
                 planes[2 + i] = s.lo[i];
-                token[i] = a.kv_heads * dpad;
-                head[i] = dpad;
+                token[i] = dpad;
+                head[i] = a.total_k * dpad;
             }
             dim = dpad;
         }
@@ -1022,9 +1147,14 @@ comp_status_t launch_attn(const comp_attn_t& a, const float* q, const void* k, c
     p.out_tokens = encode_tokens(&maps[5], out, p.dim, a.heads, p.group, a.total_q, a.out_token, a.out_head, 32, 32,
                                  p.vec_out);
     const int64_t rows = a.total_q * p.group;
-    const int64_t grid = (cu_q ? rows / 256 + a.n_seq : (rows + 255) / 256) * a.kv_heads;
-    if (grid > INT32_MAX)
+    // pairs of CTAs where the sequences fill their 512 rows on average (Cfg)
+    const bool pair = a.head_dim > 64 && kv_bytes == 4 && rows / a.n_seq >= 1024;
+    const int64_t block = pair ? 512 : 256;
+    const int64_t grid = (cu_q ? rows / block + a.n_seq : (rows + block - 1) / block) * a.kv_heads;
+    if (grid > INT32_MAX / 2)
         return COMP_ERR_INVALID_VALUE;
+    if (pair)
+        return launch_t<128, 2, true>(maps, p, grid, dev, stream);
     if (a.head_dim <= 64)
         return kv_bytes == 4 ? launch_t<64, 2>(maps, p, grid, dev, stream) : launch_t<64, 1>(maps, p, grid, dev, stream);
     return kv_bytes == 4 ? launch_t<128, 2>(maps, p, grid, dev, stream) : launch_t<128, 1>(maps, p, grid, dev, stream);

@@ -415,6 +415,33 @@ __device__ __forceinline__ void umma_pair_w_scale10_by(uint32_t leader, uint32_t
         : "memory");
 }
 
+// The same two with A (each CTA's 128 rows) in the CTAs' tensor memory.
+__device__ __forceinline__ void umma_pair_ta_w_by(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                                  uint32_t desc_hi, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\t"
+        "mov.b64 db, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "setp.ne.b32 q, %6, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(desc_hi), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+
+__device__ __forceinline__ void umma_pair_ta_w_scale10_by(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem,
+                                                          uint32_t b_lo, uint32_t desc_hi, uint32_t idesc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\t"
+        "mov.b64 db, {%2, %3};\n\t"
+        "setp.ne.b32 p, 1, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], db, %4, p, 10;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(desc_hi), "r"(idesc), "r"(leader)
+        : "memory");
+}
+
 // Named-barrier reduction: blocks until `count` threads of the CTA have
 // arrived at barrier `id`, and returns the AND of their predicates.
 __device__ __forceinline__ bool bar_red_and(uint32_t id, uint32_t count, bool v)
@@ -539,6 +566,11 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t cluster_addr, float a, fl
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "f"(a), "f"(b), "f"(c),
                  "f"(d)
                  : "memory");
+}
+
+__device__ __forceinline__ void st_cluster(uint32_t cluster_addr, int v)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
 
 // Asynchronous 16-byte store into the shared memory of another CTA of the

@@ -200,25 +200,37 @@ inline bool aligned16(const void* p)
 // Launch with programmatic stream serialisation: the kernel's set-up overlaps
 // the end of the previous kernel on the stream; its producer waits
 // (griddepcontrol.wait) before it reads what that kernel wrote.
+// launch_pdl_cluster: in clusters of `cluster` CTAs.
 template <typename... KArgs, typename... Args>
-comp_status_t launch_pdl(void (*kernel)(KArgs...), int grid, int threads, size_t smem, cudaStream_t stream,
-                         Args&&... args)
+comp_status_t launch_pdl_cluster(void (*kernel)(KArgs...), int cluster, int grid, int threads, size_t smem,
+                                 cudaStream_t stream, Args&&... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
     cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...) != cudaSuccess) {
         (void)cudaGetLastError();
         return COMP_ERR_LAUNCH;
     }
     return COMP_OK;
+}
+
+template <typename... KArgs, typename... Args>
+comp_status_t launch_pdl(void (*kernel)(KArgs...), int grid, int threads, size_t smem, cudaStream_t stream,
+                         Args&&... args)
+{
+    return launch_pdl_cluster(kernel, 1, grid, threads, smem, stream, std::forward<Args>(args)...);
 }
 
 }  // namespace compfp32

@@ -175,6 +175,63 @@ def test_long(pkg, kv, heads, kv_heads, dim, n):
         compare(oc[rows, h], lc[rows, h], *exact_rows(qc[rows, h], kc[:, g], vc[:, g], seen, dim ** -0.5))
 
 
+def sampled(out, lse, q, k, v, cu, causal, every):
+    """check_attn on some rows of each sequence (its first and last among them)."""
+    from attn_check import compare, exact_rows
+
+    out, lse, q, k, v = (x.cpu() for x in (out, lse, q, k, v))
+    group = q.shape[1] // k.shape[1]
+    for a, b in zip(cu, cu[1:]):
+        n = b - a
+        rows = sorted({0, n // 2, n - 1, *range(0, n, every)})
+        seen = torch.arange(n)[None] <= torch.tensor(rows)[:, None] if causal else torch.ones(len(rows), n,
+                                                                                              dtype=torch.bool)
+        at = [a + r for r in rows]
+        for h in range(q.shape[1]):
+            compare(out[at, h], lse[at, h], *exact_rows(q[at, h], k[a:b, h // group], v[a:b, h // group], seen,
+                                                        q.shape[2] ** -0.5))
+
+
+@pytest.mark.parametrize("kv", KV, ids=["f16", "f32"])
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+@pytest.mark.parametrize("lens,heads,kv_heads,dim", [
+    ([1100, 1, 1535, 1600], 2, 2, 128),      # sequences that fill blocks of 512 rows, and ones that do not
+    ([513, 700, 130], 9, 3, 72),             # three heads to a key head: blocks end inside a token
+    ([2048, 511], 4, 1, 128),
+    ([1030], 5, 5, 100),
+], ids=str)
+def test_long_packed(pkg, lens, heads, kv_heads, dim, causal, kv):
+    q, k, v = case(lens, lens, heads, kv_heads, dim, kv, seed=10)
+    cu = cu_of(lens)
+    out, lse = call(pkg, q, k, v, cu, cu, causal)
+    sampled(out, lse, q, k, v, cu, causal, 229)
+    again, lse2 = call(pkg, q, k, v, cu, cu, causal)
+    assert torch.equal(again, out) and torch.equal(lse2, lse)
+
+
+@pytest.mark.parametrize("kv", KV, ids=["f16", "f32"])
+@pytest.mark.parametrize("column", [3, 100])
+def test_long_hidden_values(pkg, kv, column):
+    """As test_only_the_value_is_not_finite, in blocks of 512 rows; and what follows a sequence."""
+    lens = [1300, 1200]
+    q, k, v = case(lens, lens, 2, 2, 128, kv, seed=11)
+    cu = cu_of(lens)
+    plain, plain_lse = call(pkg, q, k, v, cu, cu, True)
+    v2, k2 = v.clone(), k.clone()
+    v2[777, 1, column] = math.nan
+    v2[1300 + 600, 0, column] = math.inf
+    k2[1300 + 1199, :, 5] = math.nan
+    out, lse = call(pkg, q, k2, v2, cu, cu, True)
+    keep = torch.ones(2500, 2, 128, dtype=torch.bool, device="cuda")
+    keep[777:1300, 1, column] = False
+    keep[1900:, 0, column] = False
+    keep[2499] = False
+    assert torch.equal(out[keep], plain[keep])
+    assert not bool(out[777:1300, 1, column].isfinite().any())
+    assert not bool(out[1900:, 0, column].isfinite().any())
+    assert torch.equal(lse[:2499], plain_lse[:2499])
+
+
 def test_reruns_side_stream_and_no_lse(pkg):
     lens = [300, 77, 1024]
     q, k, v = case(lens, lens, 8, 2, 128, torch.float16, seed=8)
