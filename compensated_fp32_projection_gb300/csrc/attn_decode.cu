@@ -60,7 +60,8 @@ struct Params {
     const int32_t* table;
     const int32_t* lengths;
     int64_t q_token, q_head, width;
-    int batch, heads, kv_heads, group, row_blocks, dim, page_shift, pages, shared_keys, most_keys, pieces, vec_q, after_prefix;
+    int batch, heads, kv_heads, group, row_blocks, dim;
+    int page_shift, pages, shared_keys, most_keys, pieces, vec_q, after_prefix;
     float scale;
 };
 
@@ -93,7 +94,8 @@ __device__ __forceinline__ int sum_tiles(const Params& p, int end)
 struct Cut {
     int pieces, each, rest;
     __device__ __forceinline__ Cut(const Params& p, int total)
-        : pieces(min((total + kLeast - 1) / kLeast, p.pieces)), each(pieces > 0 ? total / pieces : 0), rest(pieces > 0 ? total % pieces : 0)
+        : pieces(min((total + kLeast - 1) / kLeast, p.pieces)), each(pieces > 0 ? total / pieces : 0),
+          rest(pieces > 0 ? total % pieces : 0)
     {
     }
     __device__ __forceinline__ int begin(int piece) const { return piece * each + min(piece, rest); }
@@ -360,7 +362,8 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
 #pragma unroll
                 for (int nt = 0; nt < 2; ++nt) {
                     uint32_t b[4];
-                    ldmatrix4(smem_u32(kt) + (k / 4) * (kTile * 128) + sw128(nt * 8 + (lane & 7), (k % 4) * 2 + (lane >> 3)),
+                    ldmatrix4(smem_u32(kt) + (k / 4) * (kTile * 128) +
+                                  sw128(nt * 8 + (lane & 7), (k % 4) * 2 + (lane >> 3)),
                               b);
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb) {
@@ -398,14 +401,16 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
 #pragma unroll
             for (int d = 0; d < DP / 16; ++d) {
                 uint32_t b[4];
-                ldmatrix4_trans(smem_u32(vt) + (d / 4) * (kTile * 128) + sw128(lane & 15, (d % 4) * 2 + (lane >> 4)), b);
+                ldmatrix4_trans(
+                    smem_u32(vt) + (d / 4) * (kTile * 128) + sw128(lane & 15, (d % 4) * 2 + (lane >> 4)), b);
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         float y[4] = {};
                         mma16816(y, pa[nb], b[2 * e], b[2 * e + 1]);
-                        o[nb][2 * d + e] = fma2(o[nb][2 * d + e], a2[nb], add2(f2_bits(y[0], y[1]), f2_bits(y[2], y[3])));
+                        const uint64_t both = add2(f2_bits(y[0], y[1]), f2_bits(y[2], y[3]));
+                        o[nb][2 * d + e] = fma2(o[nb][2 * d + e], a2[nb], both);
                     }
             }
             __syncwarp();  // all lanes have read the stage
