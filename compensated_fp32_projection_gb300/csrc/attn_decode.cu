@@ -39,6 +39,7 @@ constexpr int kTile = 16;       // keys of a tile, the k of a product
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kLeast = 4;
+constexpr int kLong = 8;
 constexpr uint32_t kFaultDecode = 0xA01;
 
 // DP: head dimension padded to 64 or 128; NB: blocks of eight query heads.
@@ -61,7 +62,7 @@ struct Params {
     const int32_t* lengths;
     int64_t q_token, q_head, width;
     int batch, heads, kv_heads, group, row_blocks, dim;
-    int page_shift, pages, shared_keys, most_keys, pieces, vec_q, after_prefix;
+    int page_shift, pages, shared_keys, most_keys, pieces, waves, vec_q, after_prefix;
     float scale;
 };
 
@@ -91,10 +92,13 @@ __device__ __forceinline__ int sum_tiles(const Params& p, int end)
 // (a key/value head and a block of its query heads), cut into pieces that
 // differ by at most one tile: the first `rest` have one more.  A piece has about
 // kLeast tiles at least: a part of a row costs its join more than a tile costs.
+// There are `waves` times as many pieces where they have kLong tiles then.
 struct Cut {
     int pieces, each, rest;
     __device__ __forceinline__ Cut(const Params& p, int total)
-        : pieces(min((total + kLeast - 1) / kLeast, p.pieces)), each(pieces > 0 ? total / pieces : 0),
+        : pieces(min((total + kLeast - 1) / kLeast,
+                     total / p.waves >= kLong * p.pieces ? p.waves * p.pieces : p.pieces)),
+          each(pieces > 0 ? total / pieces : 0),
           rest(pieces > 0 ? total % pieces : 0)
     {
     }
@@ -222,16 +226,17 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
         fence_mbar_init();
     }
     __syncwarp();
-    grid_dependency_launch();
     // After a prefix's kernel this one need not wait for it, only for what came
     // before, which that kernel has waited for before it let this one start: the
     // SMs it leaves free, and those it is done with, work here meanwhile.  What
     // follows this kernel follows both, so its first CTA waits at its end.
     if (!p.after_prefix)
         grid_dependency_wait();
+    grid_dependency_launch();  // the join relies on what came before
 
     // this warp's piece; consecutive ones are on different SMs
-    const int piece = warp * gridDim.x + blockIdx.x;
+    const int ctas = p.pieces / kWarps, wave = static_cast<int>(blockIdx.x) >= ctas;
+    const int piece = wave * (p.pieces - ctas) + warp * ctas + blockIdx.x;
     int begin, end;
     Place r;
     if (!find_piece(p, piece, begin, end, r)) {
@@ -473,8 +478,9 @@ struct Join {
 
 __global__ void __launch_bounds__(256) attn_join_kernel(Params p, Join x)
 {
-    grid_dependency_launch();
-    grid_dependency_wait();
+    // Where the parts are follows from the lengths alone, which are complete:
+    // this kernel starts when the decode kernel's CTAs run, and those start, or
+    // go on, when what came before them is.
     const int lane = threadIdx.x & 31;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     const int64_t rows = static_cast<int64_t>(p.batch) * p.heads;
@@ -491,12 +497,16 @@ __global__ void __launch_bounds__(256) attn_join_kernel(Params p, Join x)
         const int t0 = sum_tiles(p, b) * units + (head * p.row_blocks + block) * tiles;
         const int c0 = cut.piece_of(t0), c1 = cut.piece_of(t0 + tiles - 1);
         whole = c0 == c1;
-        if (whole && x.splits == 0)
-            return;  // the output is there
+        if (whole && x.splits == 0) {  // the output is there
+            grid_dependency_wait();
+            return;
+        }
         own_parts = c1 - c0 + 1;
         first_slot = 2 * c0 + (cut.begin(c0) < t0 ? 1 : 0);  // that piece begins with another row
     }
     const int parts = x.splits + own_parts;
+    grid_dependency_launch();
+    grid_dependency_wait();
     // part i: its lse and where its sums are; slots first_slot, then 2 (c0 + 1), 2 (c0 + 2), ...
     auto find = [&](int i, const float*& o) {
         if (i < x.splits) {
@@ -575,12 +585,18 @@ comp_status_t launch_t(const CUtensorMap& mk, const CUtensorMap& mv, const Param
             done[dev.device] = true;
         }
     }
-    return launch_pdl(attn_decode_kernel<DP, NB>, p.pieces / kWarps, kThreads, C::kSmem, stream, mk, mv, p);
+    return launch_pdl(attn_decode_kernel<DP, NB>, p.waves * p.pieces / kWarps, kThreads, C::kSmem, stream, mk, mv, p);
 }
 
 // Pieces of the line of tiles: one for each warp of two CTAs an SM.  The
 // workspace's size must not depend on the device, so their number is bounded.
 constexpr int kMostPieces = 320 * kWarps;
+// Beside a prefix's kernel the CTAs start as SMs become free, and pieces half as
+// long fill its end better, where they are still long enough: 256 sequences
+// on a 32768-token prefix 237 -> 223 us (a third as long: 226), but 64 short ones
+// on 8192 tokens 40 -> 42 us.  Without a prefix all pieces start together, and
+// two waves of them cost 77 us where one takes 69 (48 ragged sequences).
+constexpr int kPrefixWaves = 2;  // the kernel tells the second by one comparison
 
 // Parts that the shared pages' keys are split into, so that about one wave of
 // the packed kernel's CTAs works on them; a part has at least four tiles of
@@ -604,7 +620,8 @@ struct Layout {
 Layout layout_of(const comp_kv_cache_t& c, int64_t batch, int heads, int splits)
 {
     const int group = heads / c.kv_heads;
-    const int64_t slots = 2 * kMostPieces * (group > 8 ? 16 : 8), rows = batch * heads;
+    const int64_t pieces = splits > 0 ? kPrefixWaves * kMostPieces : kMostPieces;
+    const int64_t slots = 2 * pieces * (group > 8 ? 16 : 8), rows = batch * heads;
     Layout l;
     l.part_o = 0;
     l.part_lse = l.part_o + slots * c.head_dim;
@@ -675,6 +692,7 @@ comp_status_t launch_attn_decode(const comp_kv_cache_t& cache, const float* q, i
     if ((width * cache.page_size / kTile + 1) * batch > INT32_MAX / (p.kv_heads * p.row_blocks))
         return COMP_ERR_INVALID_VALUE;
     p.pieces = 2 * dev.sm_count * kWarps < kMostPieces ? 2 * dev.sm_count * kWarps : kMostPieces;
+    p.waves = splits > 0 ? kPrefixWaves : 1;
     p.vec_q = (reinterpret_cast<uintptr_t>(q) & 7u) == 0 && q_token % 2 == 0 && q_head % 2 == 0;
     p.scale = scale;
     p.after_prefix = splits > 0;
