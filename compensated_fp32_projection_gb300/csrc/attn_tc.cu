@@ -960,7 +960,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // bytes) as they are: rows of `dpad` values, zeros past the head dimension,
 // head by head, so that a tile is one run of memory.
 // Each value is read once; the kernel above then reads every row once for
-// each 256 query rows.  blockIdx.y: k or v.
+// each 256 query rows.  Even CTAs: k, odd ones: v.
 struct Stage {
     const void* src[2];
     int64_t token[2], head[2];
@@ -973,10 +973,11 @@ struct Stage {
 __global__ void __launch_bounds__(256) attn_stage_kernel(Stage p)
 {
     grid_dependency_launch();
-    const int w = blockIdx.y, parts = p.dpad / 8;
+    grid_dependency_wait();
+    const int w = blockIdx.x & 1, parts = p.dpad / 8;
     const int64_t work = p.tokens * p.heads * parts;
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; u < work;
-         u += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    for (int64_t u = static_cast<int64_t>(blockIdx.x / 2) * blockDim.x + threadIdx.x; u < work;
+         u += static_cast<int64_t>(gridDim.x / 2) * blockDim.x) {
         const int part = static_cast<int>(u % parts);
         const int64_t row = u / parts, at = row / p.heads * p.token[w] + row % p.heads * p.head[w] + part * 8;
         const int64_t to = (row % p.heads * p.tokens + row / p.heads) * p.dpad + part * 8;
@@ -1135,9 +1136,10 @@ comp_status_t launch_attn(const comp_attn_t& a, const float* q, const void* k, c
                     a.v_head % 4 == 0;
             const int64_t work = a.total_k * a.kv_heads * (dpad / 8), most = dev.sm_count * 8;
             const int64_t blocks = (work + 255) / 256;
-            attn_stage_kernel<<<dim3(static_cast<unsigned>(blocks < most ? blocks : most), 2), 256, 0, stream>>>(s);
-            if (launch_status() != COMP_OK)
-                return COMP_ERR_LAUNCH;
+            const comp_status_t st = launch_pdl(attn_stage_kernel, static_cast<int>(2 * (blocks < most ? blocks : most)),
+                                                256, 0, stream, s);
+            if (st != COMP_OK)
+                return st;
             for (int i = 0; i < 2; ++i) {
                 planes[i] = s.hi[i];
                 planes[2 + i] = s.lo[i];
