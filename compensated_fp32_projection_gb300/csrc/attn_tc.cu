@@ -31,8 +31,8 @@
 // half.  S is overwritten in place by P (128 columns of 32 bits: hi and lo
 // pairs), which the second product reads from tensor memory.  Measured: 16384
 // causal tokens, 32 heads of 128 over 8 of FP16 keys, 2.26 ms, 1.94 PFLOP/s of
-// products; 4096 FP32 tokens, 32 heads, 357 us, 1.16 PFLOP/s; 24 prompts of 23
-// to 2011 tokens, 243 us, 1.02 PFLOP/s, where nearly half of a CTA's time passes
+// products; 4096 FP32 tokens, 32 heads, 343 us, 1.20 PFLOP/s; 24 prompts of 23
+// to 2011 tokens, 235 us, 1.05 PFLOP/s, where nearly half of a CTA's time passes
 // before its first product and after its last.
 //
 // Warps: 0 loads tiles of k and v (TMA, a ring of stages), 1 and 2 issue the
@@ -281,12 +281,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     // One load brings a half's rows of q, FP32, to where its planes will be
     // (tokens past the sequence's end too: rows that are not there).  Loads by
     // the threads would wait for each other in the small L1 that 227 KB of
-    // shared memory leave.
-    if (p.q_tokens > 0 && (warp == 4 || warp == 8) && lane == 0) {
-        mbar_arrive_expect_tx(&sm->qload[half], 128 * p.dim * 4);
-        tma_load_3d(smem + half * 2 * C::kQTile, &map_q, &sm->qload[half], 0, head * p.group,
-                    sm->q0 + rows128 * p.q_tokens);
-    }
+    // shared memory leave.  The second half's is issued with the first keys', so
+    // that the first half's lands, and is split, before.
+    auto load_q = [&] {
+        if (p.q_tokens > 0 && lane == 0) {
+            mbar_arrive_expect_tx(&sm->qload[half], 128 * p.dim * 4);
+            tma_load_3d(smem + half * 2 * C::kQTile, &map_q, &sm->qload[half], 0, head * p.group,
+                        sm->q0 + rows128 * p.q_tokens);
+        }
+    };
+    if (warp == 4)
+        load_q();
 
     // the part of its sequence's keys that this CTA goes through
     const int q0 = sm->q0, nq = sm->nq, k0 = sm->k0, nk = sm->nk;
@@ -345,6 +350,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     tc_fence_after();
+    if (warp == 8)
+        load_q();
     // All 512 columns are this CTA's, so they begin at 0: tensor-memory addresses
     // are constants to the issuing warp.
     const bool at_zero = sm->tmem_base == 0;
@@ -722,8 +729,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < DP / 2; ++i)
             o[i] = 0;
 
-        // o = o alpha + O' of tile j
-        auto take = [&](int j) {
+        // o = o alpha + O' of tile j, 32 values at a time; after each 32: done(c)
+        auto take_and = [&](int j, auto done) {
             const uint64_t a2 = f2_bits(alpha, alpha);
             const uint32_t from = lanes + 256 + half * 128 + (OB == 2 ? (j & 1) * 64 : 0);
             uint32_t r[2][32];
@@ -737,8 +744,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     o[c * 16 + i] = fma2(o[c * 16 + i], a2, u2_bits(x[2 * i], x[2 * i + 1]));
+                done(c);
             }
         };
+        auto take = [&](int j) { take_and(j, [](int) {}); };
 
         // Tile j's scores become P, and O' of the tile before is taken: first
         // where there is one buffer for it (P's arrival frees it), else last,
@@ -754,10 +763,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             tc_fence_after();
-            if (j > 0 && (OB == 1 || j == nh))
+            // A pair takes the last O' below, while its output's stores are under way
+            // (4096 FP32 tokens, 32 heads: 349 -> 343 us); alone the loop without
+            // that step came out slower (16384 causal tokens: 2.26 -> 2.36 ms).
+            if (!PAIR && j > 0 && (OB == 1 || j == nh))
                 take(j - 1);
             if (j == nh)
                 break;
+            if (PAIR && j > 0)
+                take(j - 1);
             {
                 if (__any_sync(0xffffffffu, row_lim < (j + 1) * BN)) {
                     // hidden scores to -inf, in place
@@ -848,23 +862,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr int kChunks = DP / 4;  // 16 bytes each
             uint8_t* const tile = smem + half * 2 * C::kQTile + w4 * (32 * DP * 4);
             const uint64_t norm2 = f2_bits(norm, norm);
+            const unsigned rows_there = __ballot_sync(0xffffffffu, valid);
+            const bool by_map = p.out_tokens > 0 && rows_there == 0xffffffffu;  // whole tokens, all there
+            const int token = part * p.out_part + q0 + (rows128 * 4 + w4) * p.out_tokens;
+            // a box is on its way while the next 32 values are taken
+            auto put = [&](int c) {
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c)
-                *reinterpret_cast<ulonglong2*>(tile + (c / 8) * 4096 + sw128(lane, c % 8)) =
-                    make_ulonglong2(mul2(o[2 * c], norm2), mul2(o[2 * c + 1], norm2));
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<ulonglong2*>(tile + c * 4096 + sw128(lane, i)) = make_ulonglong2(
+                        mul2(o[c * 16 + 2 * i], norm2), mul2(o[c * 16 + 2 * i + 1], norm2));
+                if (by_map && c * 32 < p.dim) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        tma_store_3d(&map_out, tile + c * 4096, c * 32, head * p.group, token);
+                }
+            };
+            if (PAIR && nh > 0) {
+                take_and(nh - 1, put);
+            } else {
+#pragma unroll
+                for (int c = 0; c < DP / 32; ++c)
+                    put(c);
+            }
             constexpr int kRows = 32 / kChunks;  // rows a warp writes at once
             const int chunk = lane % kChunks, d = chunk * 4;
-            const unsigned rows_there = __ballot_sync(0xffffffffu, valid);
-            if (p.out_tokens > 0 && rows_there == 0xffffffffu) {
-                // whole tokens, all there: by tensor map
-                fence_proxy_async_smem();
-                __syncwarp();
+            if (by_map) {
                 if (lane == 0) {
-                    const int token = part * p.out_part + q0 + (rows128 * 4 + w4) * p.out_tokens;
-#pragma unroll
-                    for (int x = 0; x < DP / 32; ++x)
-                        if (x * 32 < p.dim)
-                            tma_store_3d(&map_out, tile + x * 4096, x * 32, head * p.group, token);
                     bulk_commit_group();
                     if (sm->hurt) {  // written before values are added below
                         bulk_wait_group0();
