@@ -31,7 +31,7 @@
 // half.  S is overwritten in place by P (128 columns of 32 bits: hi and lo
 // pairs), which the second product reads from tensor memory.  Measured: 16384
 // causal tokens, 32 heads of 128 over 8 of FP16 keys, 2.26 ms, 1.94 PFLOP/s of
-// products; 4096 FP32 tokens, 32 heads, 343 us, 1.20 PFLOP/s; 24 prompts of 23
+// products; 4096 FP32 tokens, 32 heads, 335 us, 1.23 PFLOP/s; 24 prompts of 23
 // to 2011 tokens, 235 us, 1.05 PFLOP/s, where nearly half of a CTA's time passes
 // before its first product and after its last.
 //
@@ -96,6 +96,7 @@ struct Cfg {
     static constexpr uint32_t kStage = PL * kPlane;
     static constexpr uint32_t kKBox = BN / R * 128;             // bytes of 64 values of a stage's keys
     static constexpr int NS = DP == 128 ? 3 : (PL == 2 ? 4 : 6);
+    static_assert(!PAIR_ || NS % 2 == 1, "a stage's turn among the values");
     // Buffers of O' a half: what tensor memory has left beside S (2 x 128 of
     // 512 columns).
     static constexpr int OB = DP == 128 ? 1 : 2;
@@ -375,19 +376,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int s = i % NS;
                 if (i >= NS && !attn_warp_wait(&sm->empty[s], ((i / NS) - 1) & 1, &sm->abort, kFaultAttnLoad))
                     break;
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&sm->full[s], C::kStage);
+                // A pair's loads count on the first CTA's barrier, where the products are
+                // issued; only values that are looked through, on their own CTA's.
+                const bool looked = (i & 1) && (i >> 1) >= edge;
+                if (lane == 0) {
+                    if (PAIR && !looked && rank == 1)
+                        mbar_arrive(&sm->full[s]);
+                    else
+                        mbar_arrive_expect_tx(&sm->full[s], PAIR && !looked ? 2 * C::kStage : C::kStage);
+                }
                 __syncwarp();
                 if (PAIR) {
                     // this CTA's half: keys of k in boxes along the head dimension, 64
                     // values of v in boxes of 64 keys
                     if (lane < 2 * PL) {
+                        const uint32_t bar = mapa_shared(&sm->full[s], looked ? rank : 0);
                         const int plane = lane / 2, sub = lane % 2, is_v = i & 1;
                         const CUtensorMap* const map =
                             plane ? (is_v ? &map_v_lo : &map_k_lo) : (is_v ? &map_v : &map_k);
                         const int key = k0 + first + (i >> 1) * BN;
-                        tma_load_3d(stages + s * C::kStage + plane * C::kPlane + sub * 8192, map, &sm->full[s],
-                                    (is_v ? rank : sub) * 64, key + (is_v ? sub : rank) * 64, head);
+                        tma_load_3d_pair(stages + s * C::kStage + plane * C::kPlane + sub * 8192, map, bar,
+                                         (is_v ? rank : sub) * 64, key + (is_v ? sub : rank) * 64, head);
                     }
                     __syncwarp();
                     continue;
@@ -414,6 +423,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i < 2 * n) {  // abort: what was issued lands before the CTA leaves
                 for (int j = max(0, i - NS); j < i; ++j)
                     attn_drain_wait(&sm->full[j % NS], (j / NS) & 1);
+                if (PAIR) {  // those that count on the other CTA's barrier: time to land
+                    const long long start = clock64();
+                    while (clock64() - start < (1ll << 22)) {
+                    }
+                }
             }
         } else if (warp < 3 && rank == 0) {
             // ---------------- products: warp 1 issues those of the first half, warp 2 of the second
@@ -438,12 +452,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto wait_cluster = [&](uint64_t* bar, int phase) {
                 ok = ok && attn_wait_cluster(bar, phase & 1, &sm->abort, kFaultAttnMma);
             };
-            // a stage's tile, in a pair both CTAs' halves of it (which pass their warps 3)
+            // a stage's tile, in a pair both CTAs' halves of it (values that are looked
+            // through: when both warps 3 are done; every NS-th of them has this stage)
             auto wait_tile = [&](int s, int load, bool looked_through) {
                 if (PAIR && looked_through) {
-                    wait_cluster(&sm->checked[s], load / NS);
-                } else if (PAIR) {
-                    wait(&sm->checked[s], load / NS);
+                    wait_cluster(&sm->checked[s], (load / 2 - edge) / NS);
                 } else {
                     wait(&sm->full[s], load / NS);
                     if (looked_through)
@@ -619,14 +632,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 if (lane == 0) {
-                    // a pair's other CTA learns here that the load has landed; only what
-                    // this warp wrote itself needs a release over the cluster
                     if (!PAIR)
                         mbar_arrive(&sm->checked[s]);
                     else if ((i & 1) && j >= edge)
                         mbar_arrive_release_cluster(mapa_shared(&sm->checked[s], 0));
-                    else
-                        mbar_arrive_cluster(mapa_shared(&sm->checked[s], 0));
                     mbar_arrive(&sm->empty[s]);
                 }
             }
