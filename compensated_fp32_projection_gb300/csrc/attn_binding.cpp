@@ -8,11 +8,13 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
+#include <optional>
 #include <string>
 
 #include "compfp32.h"
@@ -174,19 +176,33 @@ int32_t* ints_out(const at::Tensor& t)
     return static_cast<int32_t*>(t.data_ptr());
 }
 
-comp_stream_t stream_of(PyObject* o, int device)
-{
-    if (o == Py_None)
-        return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream();
-    PyObject* const number = PyLong_Check(o) ? Py_NewRef(o) : PyObject_GetAttrString(o, "cuda_stream");
-    if (!number)
-        throw PythonError{};
-    void* const s = PyLong_AsVoidPtr(number);
-    Py_DECREF(number);
-    if (PyErr_Occurred())
-        throw PythonError{};
-    return s;
-}
+// The stream of a call.  While this lives it is the current one, so that what
+// the call allocates belongs to it: a workspace of another stream could be
+// given away before this one has used it, and an output could still be in use
+// there.
+struct Stream {
+    comp_stream_t at;
+    std::optional<c10::cuda::CUDAStreamGuard> guard;
+
+    Stream(PyObject* o, int device)
+    {
+        const auto on = static_cast<c10::DeviceIndex>(device);
+        at = c10::cuda::getCurrentCUDAStream(on).stream();
+        if (o == Py_None)
+            return;
+        PyObject* const number = PyLong_Check(o) ? Py_NewRef(o) : PyObject_GetAttrString(o, "cuda_stream");
+        if (!number)
+            throw PythonError{};
+        void* const given = PyLong_AsVoidPtr(number);
+        Py_DECREF(number);
+        if (PyErr_Occurred())
+            throw PythonError{};
+        if (given != at) {
+            at = given;
+            guard.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(given), on));
+        }
+    }
+};
 
 int64_t integer(PyObject* o)
 {
@@ -277,6 +293,7 @@ PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n)
             cu_q = ints(c);
             cu_k = ints(dense(a[5], at::kInt, "cu_k", device, c.sizes()));
         }
+        const Stream on(a[11], device);
         at::Tensor out;
         if (a[8] == Py_None) {
             out = fresh(q.sizes(), at::kFloat, device);
@@ -307,14 +324,13 @@ PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n)
         const Workspace ws(a[10], comp_attn_workspace_bytes(&d, f32 ? 4 : 2, kp, vp), device);
         const float* const qp = static_cast<const float*>(q.data_ptr());
         float* const op = static_cast<float*>(out.data_ptr());
-        const comp_stream_t s = stream_of(a[11], device);
         if (f32)
             check(comp_attn_f32(&d, qp, static_cast<const float*>(kp), static_cast<const float*>(vp), cu_q, cu_k, op,
-                                lse, ws.at, ws.bytes, s),
+                                lse, ws.at, ws.bytes, on.at),
                   "comp_attn_f32");
         else
             check(comp_attn_f32x16(&d, qp, static_cast<const uint16_t*>(kp), static_cast<const uint16_t*>(vp), cu_q,
-                                   cu_k, op, lse, ws.at, ws.bytes, s),
+                                   cu_k, op, lse, ws.at, ws.bytes, on.at),
                   "comp_attn_f32x16");
         return a[8] == Py_None ? THPVariable_Wrap(std::move(out)) : Py_NewRef(a[8]);
     });
@@ -339,7 +355,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n)
         check(comp_kv_append_f32(&c.c, static_cast<const float*>(k.data_ptr()),
                                  static_cast<const float*>(v.data_ptr()), k.stride(0), k.stride(1), v.stride(0),
                                  v.stride(1), tokens, ints(table), rows, table.size(1), cu, ints(start),
-                                 stream_of(a[7], c.device)),
+                                 Stream(a[7], c.device).at),
               "comp_kv_append_f32");
         return Py_NewRef(Py_None);
     });
@@ -358,6 +374,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n)
             refuse("q must be [rows of table, a multiple of kv_heads, head_dim]");
         const at::Tensor& lengths = dense(a[4], at::kInt, "lengths", c.device, {batch});
         const int64_t shared = integer(a[5]);
+        const Stream on(a[10], c.device);
         at::Tensor out = output(a[7], at::kFloat, "out", c.device, q.sizes());
         float* const lse = optional<float>(a[8], at::kFloat, "lse", c.device, {batch, h});
         const Workspace ws(a[9],
@@ -366,7 +383,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n)
         check(comp_attn_decode_f32x16(&c.c, static_cast<const float*>(q.data_ptr()), q.stride(0), q.stride(1),
                                       static_cast<int32_t>(h), scale_of(a[6], dim), ints(table), batch, width,
                                       ints(lengths), shared, static_cast<float*>(out.data_ptr()), lse, ws.at,
-                                      ws.bytes, stream_of(a[10], c.device)),
+                                      ws.bytes, on.at),
               "comp_attn_decode_f32x16");
         return a[7] == Py_None ? THPVariable_Wrap(std::move(out)) : Py_NewRef(a[7]);
     });
@@ -394,13 +411,14 @@ PyObject* reserve(PyObject*, PyObject* const* a, Py_ssize_t n)
         const int64_t rows = table.size(0);
         const at::Tensor& want = dense(a[1], at::kInt, "want", device, {rows});
         const at::Tensor& refs = list(a[2], "refs", device);
+        const Stream on(a[7], device);
         PyObject* const given[] = {a[4], a[5], a[6]};
         at::Tensor out[] = {output(a[4], at::kInt, "table_out", device, table.sizes()),
                             output(a[5], at::kInt, "refs_out", device, refs.sizes()),
                             output(a[6], at::kInt, "left", device, {1})};
         check(comp_kv_reserve(refs.size(0), static_cast<int32_t>(integer(a[3])), ints(table), ints(refs), rows,
                               table.size(1), ints(want), ints_out(out[0]), ints_out(out[1]), ints_out(out[2]),
-                              stream_of(a[7], device)),
+                              on.at),
               "comp_kv_reserve");
         return results(given, out);
     });
@@ -418,6 +436,7 @@ PyObject* fork(PyObject*, PyObject* const* a, Py_ssize_t n)
         const at::Tensor& refs = dense(a[4], at::kInt, "refs", c.device, {c.c.pages});
         const at::Tensor& parents = list(a[5], "parents", c.device);
         const at::Tensor& children = dense(a[6], at::kInt, "children", c.device, parents.sizes());
+        const Stream on(a[11], c.device);
         PyObject* const given[] = {a[7], a[8], a[9], a[10]};
         at::Tensor out[] = {output(a[7], at::kInt, "table_out", c.device, table.sizes()),
                             output(a[8], at::kInt, "lengths_out", c.device, lengths.sizes()),
@@ -425,7 +444,7 @@ PyObject* fork(PyObject*, PyObject* const* a, Py_ssize_t n)
                             output(a[10], at::kInt, "left", c.device, {1})};
         check(comp_kv_fork(&c.c, ints(table), ints(lengths), ints(refs), rows, table.size(1), ints(parents),
                            ints(children), parents.size(0), ints_out(out[0]), ints_out(out[1]), ints_out(out[2]),
-                           ints_out(out[3]), stream_of(a[11], c.device)),
+                           ints_out(out[3]), on.at),
               "comp_kv_fork");
         return results(given, out);
     });
@@ -442,13 +461,14 @@ PyObject* free_(PyObject*, PyObject* const* a, Py_ssize_t n)
         const at::Tensor& lengths = dense(a[1], at::kInt, "lengths", device, {rows});
         const at::Tensor& refs = list(a[2], "refs", device);
         const at::Tensor& seqs = list(a[3], "seqs", device);
+        const Stream on(a[7], device);
         PyObject* const given[] = {a[4], a[5], a[6]};
         at::Tensor out[] = {output(a[4], at::kInt, "table_out", device, table.sizes()),
                             output(a[5], at::kInt, "lengths_out", device, lengths.sizes()),
                             output(a[6], at::kInt, "refs_out", device, refs.sizes())};
         check(comp_kv_free(refs.size(0), ints(table), ints(lengths), ints(refs), rows, table.size(1), ints(seqs),
                            seqs.size(0), ints_out(out[0]), ints_out(out[1]), ints_out(out[2]),
-                           stream_of(a[7], device)),
+                           on.at),
               "comp_kv_free");
         return results(given, out);
     });
@@ -462,13 +482,14 @@ PyObject* compact(PyObject*, PyObject* const* a, Py_ssize_t n)
         Cache c(a[0], a[1]);
         const at::Tensor& table = table_of(a[2], c.device);
         const at::Tensor& refs = dense(a[3], at::kInt, "refs", c.device, {c.c.pages});
+        const Stream on(a[8], c.device);
         PyObject* const given[] = {a[4], a[5], a[6], a[7]};
         at::Tensor out[] = {output(a[4], at::kInt, "table_out", c.device, table.sizes()),
                             output(a[5], at::kInt, "refs_out", c.device, refs.sizes()),
                             output(a[6], at::kInt, "remap", c.device, refs.sizes()),
                             output(a[7], at::kInt, "live", c.device, {1})};
         check(comp_kv_compact(&c.c, ints(table), ints(refs), table.size(0), table.size(1), ints_out(out[0]),
-                              ints_out(out[1]), ints_out(out[2]), ints_out(out[3]), stream_of(a[8], c.device)),
+                              ints_out(out[1]), ints_out(out[2]), ints_out(out[3]), on.at),
               "comp_kv_compact");
         return results(given, out);
     });
@@ -482,7 +503,7 @@ PyObject* copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n)
         Cache c(a[0], a[1]);
         const at::Tensor& src = list(a[2], "src", c.device);
         const at::Tensor& dst = dense(a[3], at::kInt, "dst", c.device, src.sizes());
-        check(comp_kv_copy_pages(&c.c, ints(src), ints(dst), src.size(0), stream_of(a[4], c.device)),
+        check(comp_kv_copy_pages(&c.c, ints(src), ints(dst), src.size(0), Stream(a[4], c.device).at),
               "comp_kv_copy_pages");
         return Py_NewRef(Py_None);
     });

@@ -252,6 +252,31 @@ def test_reruns_side_stream_and_no_lse(pkg):
     assert torch.equal(third, out)
 
 
+def test_what_a_call_allocates_belongs_to_its_stream(pkg):
+    """An output allocated for another stream must not be memory that work queued
+    on the current stream, but not done yet, still writes."""
+    q, k, v = case([64], [64], 4, 2, 64, torch.float32, seed=10)
+    want = pkg.comp_attn_f32(q, k, v)
+    kp, vp = (torch.zeros(8, 2, 16, 64, dtype=torch.float16, device="cuda") for _ in range(2))
+    table, lengths = ints([[0, 1]]), ints([20])
+    decoded = pkg.comp_attn_decode_f32x16(q[:1], kp, vp, table, lengths)
+    refs, seqs = torch.zeros(8, dtype=torch.int32, device="cuda"), ints([5])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for call_it, right in ((lambda: pkg.comp_attn_f32(q, k, v, stream=side), want),
+                           (lambda: pkg.comp_attn_decode_f32x16(q[:1], kp, vp, table, lengths, stream=side), decoded),
+                           (lambda: pkg.comp_kv_free(table, lengths, refs, seqs, stream=side)[0], table)):
+        for queued in (right.numel() * right.element_size(), 4096, 1 << 16):
+            old = torch.empty(queued, dtype=torch.uint8, device="cuda")
+            torch.cuda._sleep(20_000_000)  # about 10 ms
+            old.fill_(0x7f)
+            del old  # the current stream may use this memory again: its work is in order
+            got = call_it()
+            side.synchronize()
+            torch.cuda.synchronize()
+            assert torch.equal(got, right)
+
+
 def test_one_sequence_without_offsets(pkg):
     q, k, v = case([50], [80], 4, 2, 64, torch.float32, seed=9)
     out = pkg.comp_attn_f32(q, k, v)
