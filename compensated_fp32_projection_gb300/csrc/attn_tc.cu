@@ -497,7 +497,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int j = -1; j < n; ++j) {
                 const int iv = 2 * j + 1, ik = 2 * j + 2;  // their loads
-                const bool has_v = j >= 0 && j < nh, has_k = j + 1 < nh;
+                if (j >= nh) {
+                    // Stages that only the other half uses are given back too, but not
+                    // before their load has landed: what the stage held before may still
+                    // be read, and this arrival would count for that.
+                    if (h == 1 || j >= 0)
+                        asm volatile("bar.sync %0, 64;" ::"r"(3 - h) : "memory");
+                    if (h == 0 || j + 1 < n)
+                        asm volatile("bar.arrive %0, 64;" ::"r"(2 + h) : "memory");
+                    if (elect_one()) {
+                        if (j >= 0) {
+                            wait(&sm->full[sv], iv / NS);
+                            commit(&sm->empty[sv]);
+                        }
+                        if (j + 1 < n) {
+                            wait(&sm->full[sk], ik / NS);
+                            commit(&sm->empty[sk]);
+                        }
+                    }
+                    __syncwarp();
+                    sk = sk + 2 >= NS ? sk + 2 - NS : sk + 2;
+                    sv = sv + 2 >= NS ? sv + 2 - NS : sv + 2;
+                    continue;
+                }
+                const bool has_v = j >= 0, has_k = j + 1 < nh;
                 if (elect_one()) {
                     if (has_v)
                         wait_tile(sv, iv, j >= edge);
@@ -554,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     }
-                    if (j >= 0)
+                    if (has_v)
                         commit(&sm->empty[sv]);
                     if (has_k)
                         wait_tile(sk, ik, false);
@@ -572,8 +595,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (h == 0 || j + 1 < n)
                     asm volatile("bar.arrive %0, 64;" ::"r"(2 + h) : "memory");
-                if (elect_one() && j + 1 < n)
+                if (elect_one() && j + 1 < n) {
+                    if (!has_k)
+                        wait(&sm->full[sk], ik / NS);
                     commit(&sm->empty[sk]);
+                }
                 __syncwarp();
                 sk = sk + 2 >= NS ? sk + 2 - NS : sk + 2;
                 sv = sv + 2 >= NS ? sv + 2 - NS : sv + 2;

@@ -348,6 +348,17 @@ def test_decode_sequences_shorter_than_the_prefix(pkg):
     check_decode(out, lse, q, k, v, table, n, 64 ** -0.5)
 
 
+@pytest.mark.parametrize("dim,swap", [(64, False), (128, False), (128, True)])
+def test_decode_shared_prefix_halves_see_differently_much(pkg, dim, swap):
+    """128 rows that see little of a long prefix beside 128 that see all of it: tiles
+    pass that only one half of a block uses."""
+    few, all_of_it = [i % 7 for i in range(128)], [1600 + i % 40 for i in range(128)]
+    lengths = all_of_it + few if swap else few + all_of_it
+    q, k, v, table, n = cache_case(lengths, 100, 16, 2, 2, dim, seed=dim + swap)
+    out, lse = decode(pkg, q, k, v, table, n, 100)
+    check_decode(out, lse, q, k, v, table, n, dim ** -0.5)
+
+
 @pytest.mark.parametrize("shared", [0, 4])
 def test_decode_pages_that_are_not_there(pkg, shared):
     """A page number outside the cache reads as zeros."""
