@@ -178,10 +178,11 @@ inline comp_status_t read_and_clear_word(const void* symbol, cudaStream_t stream
 }
 
 // The shared pages of a batch (the first entries of table row 0), in `splits`
-// parts: out [splits][batch * heads][head_dim], lse [splits][batch * heads].
+// parts, two a CTA if `fold` (an even number of them, up to 128 rows, heads of up
+// to 64): out [splits][batch * heads][head_dim], lse [splits][batch * heads].
 comp_status_t launch_attn_prefix(const comp_kv_cache_t& cache, const float* q, int64_t q_token, int64_t q_head,
                                  int heads, float scale, const int32_t* table, int64_t batch, const int32_t* lengths,
-                                 int64_t shared, int splits, float* out, float* lse, const DeviceInfo& dev,
+                                 int64_t shared, int splits, bool fold, float* out, float* lse, const DeviceInfo& dev,
                                  cudaStream_t stream);
 
 }  // namespace compfp32

@@ -76,8 +76,11 @@ constexpr uint32_t kFaultAttnTmem = 0x905;
 // or 2 (FP32, split).  PAIR: two CTAs of a cluster work on the same keys, 512
 // rows together: their products are issued as one (cta_group::2, M = 256), and
 // each holds half of every tile, half the keys of k and half the head
-// dimension of v.
-template <int DP_, int PL_, bool PAIR_>
+// dimension of v.  FOLD: the two halves have the same 128 rows and each a part of
+// the keys, for the few rows of a shared prefix: one half alone takes 3000 cycles
+// a tile, most of them waiting for the step before, two halves 4100 for a tile
+// of each.
+template <int DP_, int PL_, bool PAIR_, bool FOLD_ = false>
 struct Cfg {
     static constexpr int DP = DP_, PL = PL_;
     static constexpr int R = PAIR_ ? 2 : 1;                     // CTAs that share a tile
@@ -96,6 +99,8 @@ struct Cfg {
     static constexpr uint32_t kStage = PL * kPlane;
     static constexpr uint32_t kKBox = BN / R * 128;             // bytes of 64 values of a stage's keys
     static constexpr int NS = DP == 128 ? 3 : (PL == 2 ? 4 : 6);
+    static constexpr int kLoads = FOLD_ ? 4 : 2;                // of a tile: k and v, of each half
+    static_assert(!FOLD_ || (DP_ == 64 && PL_ == 1 && !PAIR_), "folded halves");
     static_assert(!PAIR_ || NS % 2 == 1, "a stage's turn among the values");
     // Buffers of O' a half: what tensor memory has left beside S (2 x 128 of
     // 512 columns).
@@ -107,7 +112,7 @@ struct Cfg {
 };
 
 struct Shared {
-    uint64_t full[6], empty[6];  // a stage has landed; both halves' products and warp 3 are done with it
+    uint64_t full[6], empty[6];  // a stage has landed; the products that read it and warp 3 are done with it
     uint64_t checked[6];         // warp 3 has looked through a stage (a barrier for each stage: it may be
                                  // several tiles ahead of the products)
     uint64_t qload[2];           // a half's q has landed, FP32
@@ -225,14 +230,14 @@ __device__ __forceinline__ void find_block(const Params& p, int block, Shared* s
         sm->block = -1;
 }
 
-template <int DP, int PL, bool PAIR>
+template <int DP, int PL, bool PAIR, bool FOLD>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                    const __grid_constant__ CUtensorMap map_k_lo, const __grid_constant__ CUtensorMap map_v_lo,
                    const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_out,
                    const Params p)
 {
-    using C = Cfg<DP, PL, PAIR>;
+    using C = Cfg<DP, PL, PAIR, FOLD>;
     constexpr int BN = C::BN, NS = C::NS, OB = C::OB, R = C::R;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -248,13 +253,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     grid_dependency_launch();
     const uint32_t rank = PAIR ? cluster_ctarank() : 0;
     const int item = blockIdx.x / R, head = item % p.kv_heads;
-    const int part = item / p.kv_heads % p.splits;
+    const int cta_part = item / p.kv_heads % p.splits;
     if (warp == 0)
         find_block<256 * R>(p, item / p.kv_heads / p.splits, sm);
     if (threadIdx.x == 64) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(&sm->full[i], 1);
-            mbar_init(&sm->empty[i], 3);
+            mbar_init(&sm->empty[i], FOLD ? 2 : 3);
             mbar_init(&sm->checked[i], R);
         }
         for (int h = 0; h < 2; ++h) {
@@ -278,7 +283,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;  // the grid is an upper bound
 
     // A half's rows in blocks of 128: this CTA's block of them.
-    const int half = (warp >> 2) - 1, rows128 = (2 * sm->block + half) * R + static_cast<int>(rank);
+    const int half = (warp >> 2) - 1;
+    const int rows128 = FOLD ? 0 : (2 * sm->block + half) * R + static_cast<int>(rank);
     // One load brings a half's rows of q, FP32, to where its planes will be
     // (tokens past the sequence's end too: rows that are not there).  Loads by
     // the threads would wait for each other in the small L1 that 227 KB of
@@ -294,10 +300,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 4)
         load_q();
 
-    // the part of its sequence's keys that this CTA goes through
+    // the part of its sequence's keys that this CTA, or this half, goes through
     const int q0 = sm->q0, nq = sm->nq, k0 = sm->k0, nk = sm->nk;
-    const int part_keys = ((nk + BN - 1) / BN + p.splits - 1) / p.splits * BN;
-    const int first = min(static_cast<int64_t>(nk), static_cast<int64_t>(part) * part_keys);
+    const int parts = FOLD ? 2 * p.splits : p.splits;
+    const int part_keys = ((nk + BN - 1) / BN + parts - 1) / parts * BN;
+    const int part = FOLD ? 2 * cta_part + max(half, 0) : cta_part;
+    auto begin_of = [&](int i) -> int { return min(static_cast<int64_t>(nk), static_cast<int64_t>(i) * part_keys); };
+    const int first = begin_of(part);
     const int keys = min(nk - first, part_keys);
 
     // rows: what each sees
@@ -368,17 +377,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtrlRegs));
         if (warp == 0) {
-            // ---------------- loads: K0, V0, K1, V1, ...
+            // ---------------- loads: K0, V0, K1, V1, ... (folded: each for one half, then the other)
+            // A lane has one box of every tile (16 at most), and the page of one of its
+            // pieces: looked up a tile ahead, or the ring would wait for it too (256 rows
+            // on 32768 shared keys: 223 us instead of 212).  A page that is not there: a
+            // place beyond the cache, which reads zeros.
             const int pieces = p.page_size ? BN / p.page_size : 1;
-            const int boxes = PL * C::kBoxes * pieces;
+            const int piece = lane % pieces, box = lane / pieces % C::kBoxes, plane = lane / pieces / C::kBoxes;
+            uint8_t* const to = stages + plane * C::kPlane + box * (BN * 128) + piece * p.page_size * 128;
+            auto begin = [&](int i) { return FOLD ? begin_of(2 * cta_part + (i & 1)) : first; };
+            auto look_up = [&](int i) {
+                const int at = begin(i) / p.page_size + i / C::kLoads * pieces + piece;
+                return at < p.table_pages ? p.table[at] : -1;
+            };
+            constexpr int kAhead = FOLD ? 2 : 1;  // tiles of a step
+            int pages[kAhead] = {}, coming[kAhead] = {};
+            if (p.page_size) {
+#pragma unroll
+                for (int h = 0; h < kAhead; ++h)
+                    coming[h] = look_up(h);
+            }
             int i = 0;
-            for (; i < 2 * n; ++i) {
-                const int s = i % NS;
+            for (; i < C::kLoads * n; ++i) {
+                const int s = i % NS, j = i / C::kLoads, is_v = FOLD ? i >> 1 & 1 : i & 1;
                 if (i >= NS && !attn_warp_wait(&sm->empty[s], ((i / NS) - 1) & 1, &sm->abort, kFaultAttnLoad))
                     break;
                 // A pair's loads count on the first CTA's barrier, where the products are
                 // issued; only values that are looked through, on their own CTA's.
-                const bool looked = (i & 1) && (i >> 1) >= edge;
+                const bool looked = is_v && j >= edge;
                 if (lane == 0) {
                     if (PAIR && !looked && rank == 1)
                         mbar_arrive(&sm->full[s]);
@@ -391,36 +417,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // values of v in boxes of 64 keys
                     if (lane < 2 * PL) {
                         const uint32_t bar = mapa_shared(&sm->full[s], looked ? rank : 0);
-                        const int plane = lane / 2, sub = lane % 2, is_v = i & 1;
+                        const int plane = lane / 2, sub = lane % 2;
                         const CUtensorMap* const map =
                             plane ? (is_v ? &map_v_lo : &map_k_lo) : (is_v ? &map_v : &map_k);
-                        const int key = k0 + first + (i >> 1) * BN;
+                        const int key = k0 + first + j * BN;
                         tma_load_3d_pair(stages + s * C::kStage + plane * C::kPlane + sub * 8192, map, bar,
                                          (is_v ? rank : sub) * 64, key + (is_v ? sub : rank) * 64, head);
                     }
                     __syncwarp();
                     continue;
                 }
-                for (int b = lane; b < boxes; b += 32) {
-                    const int piece = b % pieces, box = b / pieces % C::kBoxes, plane = b / pieces / C::kBoxes;
-                    uint8_t* const dst = stages + s * C::kStage + plane * C::kPlane + box * (BN * 128) +
-                                         piece * p.page_size * 128;
+                const int h = FOLD ? i & 1 : 0;
+                if (p.page_size && !is_v) {
+                    pages[h] = coming[h] >= 0 && coming[h] < p.pages ? coming[h] : p.pages;
+                    coming[h] = look_up(i + C::kLoads);
+                }
+                if (plane < PL) {
                     const CUtensorMap* const map =
-                        plane ? ((i & 1) ? &map_v_lo : &map_k_lo) : ((i & 1) ? &map_v : &map_k);
-                    const int key = first + (i >> 1) * BN;
-                    if (p.page_size) {
-                        // a page that is not there: a place beyond the cache, which reads zeros
-                        const int at = key / p.page_size + piece;
-                        const int page = at < p.table_pages ? p.table[at] : -1;
-                        tma_load_3d(dst, map, &sm->full[s], box * 64, 0,
-                                    (page >= 0 && page < p.pages ? page : p.pages) * p.kv_heads + head);
-                    } else {
-                        tma_load_3d(dst, map, &sm->full[s], box * 64, k0 + key, head);
-                    }
+                        plane ? (is_v ? &map_v_lo : &map_k_lo) : (is_v ? &map_v : &map_k);
+                    if (p.page_size)
+                        tma_load_3d(to + s * C::kStage, map, &sm->full[s], box * 64, 0, pages[h] * p.kv_heads + head);
+                    else
+                        tma_load_3d(to + s * C::kStage, map, &sm->full[s], box * 64, k0 + begin(i) + j * BN, head);
                 }
                 __syncwarp();
             }
-            if (i < 2 * n) {  // abort: what was issued lands before the CTA leaves
+            if (i < C::kLoads * n) {  // abort: what was issued lands before the CTA leaves
                 for (int j = max(0, i - NS); j < i; ++j)
                     attn_drain_wait(&sm->full[j % NS], (j / NS) & 1);
                 if (PAIR) {  // those that count on the other CTA's barrier: time to land
@@ -493,14 +515,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             };
-            int sk = 0, sv = NS - 1;  // stages of K of tile j + 1 and V of tile j
+            // stages of K of tile j + 1 and V of tile j, and their next ones
+            int sk = FOLD ? h : 0, sv = FOLD ? NS - 2 + h : NS - 1;
+            auto next = [](int x) {
+                x += C::kLoads % NS;
+                return x >= NS ? x - NS : x;
+            };
 #pragma unroll 1
             for (int j = -1; j < n; ++j) {
-                const int iv = 2 * j + 1, ik = 2 * j + 2;  // their loads
+                const int iv = FOLD ? 4 * j + 2 + h : 2 * j + 1, ik = FOLD ? 4 * j + 4 + h : 2 * j + 2;  // their loads
                 if (j >= nh) {
-                    // Stages that only the other half uses are given back too, but not
-                    // before their load has landed: what the stage held before may still
-                    // be read, and this arrival would count for that.
+                    // Stages that only the other half uses (folded: nobody) are given back
+                    // too, but not before their load has landed: what the stage held
+                    // before may still be read, and this arrival would count for that.
                     if (h == 1 || j >= 0)
                         asm volatile("bar.sync %0, 64;" ::"r"(3 - h) : "memory");
                     if (h == 0 || j + 1 < n)
@@ -516,8 +543,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     __syncwarp();
-                    sk = sk + 2 >= NS ? sk + 2 - NS : sk + 2;
-                    sv = sv + 2 >= NS ? sv + 2 - NS : sv + 2;
+                    sk = next(sk);
+                    sv = next(sv);
                     continue;
                 }
                 const bool has_v = j >= 0, has_k = j + 1 < nh;
@@ -601,8 +628,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     commit(&sm->empty[sk]);
                 }
                 __syncwarp();
-                sk = sk + 2 >= NS ? sk + 2 - NS : sk + 2;
-                sv = sv + 2 >= NS ? sv + 2 - NS : sv + 2;
+                sk = next(sk);
+                sv = next(sv);
             }
             if (elect_one() && *reinterpret_cast<volatile int*>(&sm->abort)) {
                 if (PAIR)
@@ -614,11 +641,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         } else if (warp == 3) {
             // ---------------- values that must not count
-            for (int i = 0; i < 2 * n; ++i) {
-                const int s = i % NS, j = i >> 1;
+            for (int i = 0; i < C::kLoads * n; ++i) {
+                const int s = i % NS, j = i / C::kLoads, is_v = FOLD ? i >> 1 & 1 : i & 1;
+                const int seen_to = FOLD ? sm->most[i & 1] : most;
                 if (!attn_warp_wait(&sm->full[s], (i / NS) & 1, &sm->abort, kFaultAttnValues))
                     break;
-                if ((i & 1) && j >= edge) {
+                if (is_v && j >= edge) {
                     uint8_t* const tile = stages + s * C::kStage;
                     bool seen = false;
                     constexpr int kBatch = 8;  // loads in flight a lane
@@ -644,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 }
                                 if (here) {
                                     *reinterpret_cast<uint4*>(tile + at + b * 512) = x[b];
-                                    seen |= j * BN + static_cast<int>((at + b * 512) / 128 % BN) < most;
+                                    seen |= j * BN + static_cast<int>((at + b * 512) / 128 % BN) < seen_to;
                                 }
                             }
                         }
@@ -660,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) {
                     if (!PAIR)
                         mbar_arrive(&sm->checked[s]);
-                    else if ((i & 1) && j >= edge)
+                    else if (is_v && j >= edge)
                         mbar_arrive_release_cluster(mapa_shared(&sm->checked[s], 0));
                     mbar_arrive(&sm->empty[s]);
                 }
@@ -1107,11 +1135,11 @@ int encode_tokens(CUtensorMap* map, const float* base, int dim, int heads, int g
     return done ? rows / group : 0;
 }
 
-template <int DP, int PL, bool PAIR = false>
+template <int DP, int PL, bool PAIR = false, bool FOLD = false>
 comp_status_t launch_t(const CUtensorMap (&maps)[6], const Params& p, int64_t grid, const DeviceInfo& dev,
                        cudaStream_t stream)
 {
-    using C = Cfg<DP, PL, PAIR>;
+    using C = Cfg<DP, PL, PAIR, FOLD>;
     static std::mutex mu;
     static bool done[64] = {};
     {
@@ -1119,7 +1147,7 @@ comp_status_t launch_t(const CUtensorMap (&maps)[6], const Params& p, int64_t gr
         if (dev.device < 0 || dev.device >= 64)
             return COMP_ERR_CUDA;
         if (!done[dev.device]) {
-            if (cudaFuncSetAttribute(attn_tc_kernel<DP, PL, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            if (cudaFuncSetAttribute(attn_tc_kernel<DP, PL, PAIR, FOLD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      static_cast<int>(C::kSmem)) != cudaSuccess) {
                 (void)cudaGetLastError();
                 return COMP_ERR_CUDA;
@@ -1127,7 +1155,7 @@ comp_status_t launch_t(const CUtensorMap (&maps)[6], const Params& p, int64_t gr
             done[dev.device] = true;
         }
     }
-    return launch_pdl_cluster(attn_tc_kernel<DP, PL, PAIR>, C::R, static_cast<int>(grid) * C::R, kThreads, C::kSmem,
+    return launch_pdl_cluster(attn_tc_kernel<DP, PL, PAIR, FOLD>, C::R, static_cast<int>(grid) * C::R, kThreads, C::kSmem,
                               stream, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], p);
 }
 
@@ -1195,8 +1223,8 @@ comp_status_t launch_attn(const comp_attn_t& a, const float* q, const void* k, c
                     a.v_head % 4 == 0;
             const int64_t work = a.total_k * a.kv_heads * (dpad / 8), most = dev.sm_count * 8;
             const int64_t blocks = (work + 255) / 256;
-            const comp_status_t st = launch_pdl(attn_stage_kernel, static_cast<int>(2 * (blocks < most ? blocks : most)),
-                                                256, 0, stream, s);
+            const int grid = static_cast<int>(2 * (blocks < most ? blocks : most));
+            const comp_status_t st = launch_pdl(attn_stage_kernel, grid, 256, 0, stream, s);
             if (st != COMP_OK)
                 return st;
             for (int i = 0; i < 2; ++i) {
@@ -1233,7 +1261,7 @@ comp_status_t launch_attn(const comp_attn_t& a, const float* q, const void* k, c
 
 comp_status_t launch_attn_prefix(const comp_kv_cache_t& cache, const float* q, int64_t q_token, int64_t q_head,
                                  int heads, float scale, const int32_t* table, int64_t batch, const int32_t* lengths,
-                                 int64_t shared, int splits, float* out, float* lse, const DeviceInfo& dev,
+                                 int64_t shared, int splits, bool fold, float* out, float* lse, const DeviceInfo& dev,
                                  cudaStream_t stream)
 {
     Params p{};
@@ -1255,7 +1283,7 @@ comp_status_t launch_attn_prefix(const comp_kv_cache_t& cache, const float* q, i
     p.kv_heads = cache.kv_heads;
     p.group = heads / cache.kv_heads;
     p.dim = cache.head_dim;
-    p.splits = splits;
+    p.splits = fold ? splits / 2 : splits;
     p.page_size = cache.page_size;
     p.table_pages = static_cast<int>(shared);
     p.pages = static_cast<int>(cache.pages);
@@ -1270,9 +1298,11 @@ comp_status_t launch_attn_prefix(const comp_kv_cache_t& cache, const float* q, i
     p.out_tokens = encode_tokens(&maps[5], out, p.dim, heads, p.group, batch * splits, p.out_token, p.out_head, 32,
                                  32, true);
     p.out_part = static_cast<int>(batch);
-    const int64_t grid = (batch * p.group + 255) / 256 * cache.kv_heads * splits;
+    const int64_t grid = (batch * p.group + 255) / 256 * cache.kv_heads * p.splits;
     if (grid > INT32_MAX)
         return COMP_ERR_INVALID_VALUE;
+    if (fold)
+        return launch_t<64, 1, false, true>(maps, p, grid, dev, stream);
     return cache.head_dim <= 64 ? launch_t<64, 1>(maps, p, grid, dev, stream)
                                 : launch_t<128, 1>(maps, p, grid, dev, stream);
 }

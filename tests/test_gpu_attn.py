@@ -359,6 +359,40 @@ def test_decode_shared_prefix_halves_see_differently_much(pkg, dim, swap):
     check_decode(out, lse, q, k, v, table, n, dim ** -0.5)
 
 
+@pytest.mark.parametrize("shared,page,batch,heads,kv_heads,dim", [
+    (300, 16, 5, 8, 2, 128), (64, 128, 33, 4, 2, 64), (129, 32, 16, 8, 1, 128), (129, 32, 17, 8, 1, 128),
+    (40, 128, 2, 3, 3, 96), (33, 32, 128, 1, 1, 64), (72, 16, 7, 5, 1, 8),
+])
+def test_decode_shared_prefix_of_few_rows(pkg, shared, page, batch, heads, kv_heads, dim):
+    """Long prefixes of up to 128 rows, and just above; some sequences end inside them."""
+    lengths = [shared * page + 31 * i % 170 for i in range(batch)]
+    lengths[1] = shared * page // 2 + 5
+    q, k, v, table, n = cache_case(lengths, shared, page, heads, kv_heads, dim, seed=shared + batch)
+    out, lse = decode(pkg, q, k, v, table, n, shared)
+    check_decode(out, lse, q, k, v, table, n, dim ** -0.5)
+    again, again_lse = decode(pkg, q, k, v, table, n, shared)
+    assert torch.equal(again, out) and torch.equal(again_lse, lse)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_decode_infinity_in_a_shared_value(pkg, dim):
+    """A value that is not finite reaches the rows that see it and no others."""
+    lengths = [3300, 1500, 900, 3200, 2999, 3000]
+    q, k, v, table, n = cache_case([3300] * 6, 100, 32, 4, 2, dim, seed=dim)
+    n = ints(lengths)
+    k.nan_to_num_(0.25), v.nan_to_num_(0.25)
+    plain, plain_lse = decode(pkg, q, k, v, table, n, 100)
+    check_decode(plain, plain_lse, q, k, v, table, n, dim ** -0.5)
+    token, head, column = 2999, 1, dim // 2 + 3
+    v[int(table[0, token // 32]), head, token % 32, column] = math.inf
+    out, lse = decode(pkg, q, k, v, table, n, 100)
+    assert torch.equal(lse, plain_lse)
+    sees = torch.tensor([x > token for x in lengths], device="cuda")
+    assert bool((out[sees][:, 2:, column] == math.inf).all())
+    out[sees.nonzero()[:, 0], 2:, column] = plain[sees.nonzero()[:, 0], 2:, column]
+    assert torch.equal(out, plain)
+
+
 @pytest.mark.parametrize("shared", [0, 4])
 def test_decode_pages_that_are_not_there(pkg, shared):
     """A page number outside the cache reads as zeros."""
