@@ -592,9 +592,10 @@ comp_status_t launch_t(const CUtensorMap& mk, const CUtensorMap& mv, const Param
 // workspace's size must not depend on the device, so their number is bounded.
 constexpr int kMostPieces = 320 * kWarps;
 // Beside a prefix's kernel the CTAs start as SMs become free, and pieces half as
-// long fill its end better, where they are still long enough: 256 sequences
-// on a 32768-token prefix 237 -> 223 us (a third as long: 226), but 64 short ones
-// on 8192 tokens 40 -> 42 us.  Without a prefix all pieces start together, and
+// long fill its end better, where they are still long enough: measured when the
+// prefix's kernel was slower, 256 sequences on a 32768-token prefix took 223 us
+// instead of 237 (a third as long: 226), but 64 short ones on 8192 tokens 42
+// instead of 40.  Without a prefix all pieces start together, and
 // two waves of them cost 77 us where one takes 69 (48 ragged sequences).
 constexpr int kPrefixWaves = 2;  // the kernel tells the second by one comparison
 
@@ -683,7 +684,8 @@ comp_status_t launch_attn_decode(const comp_kv_cache_t& cache, const float* q, i
     float* const ws = static_cast<float*>(workspace);
     if (splits > 0) {
         const comp_status_t st = launch_attn_prefix(cache, q, q_token, q_head, heads, scale, table, batch, lengths,
-                                                    shared, splits, split.fold, ws + at.pre_o, ws + at.pre_lse, dev, stream);
+                                                    shared, splits, split.fold, ws + at.pre_o, ws + at.pre_lse, dev,
+                                                    stream);
         if (st != COMP_OK)
             return st;
     }

@@ -31,7 +31,7 @@
 // half.  S is overwritten in place by P (128 columns of 32 bits: hi and lo
 // pairs), which the second product reads from tensor memory.  Measured: 16384
 // causal tokens, 32 heads of 128 over 8 of FP16 keys, 2.26 ms, 1.94 PFLOP/s of
-// products; 4096 FP32 tokens, 32 heads, 335 us, 1.23 PFLOP/s; 24 prompts of 23
+// products; 4096 FP32 tokens, 32 heads, 329 us, 1.25 PFLOP/s; 24 prompts of 23
 // to 2011 tokens, 235 us, 1.05 PFLOP/s, where nearly half of a CTA's time passes
 // before its first product and after its last.
 //
@@ -1155,8 +1155,8 @@ comp_status_t launch_t(const CUtensorMap (&maps)[6], const Params& p, int64_t gr
             done[dev.device] = true;
         }
     }
-    return launch_pdl_cluster(attn_tc_kernel<DP, PL, PAIR, FOLD>, C::R, static_cast<int>(grid) * C::R, kThreads, C::kSmem,
-                              stream, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], p);
+    return launch_pdl_cluster(attn_tc_kernel<DP, PL, PAIR, FOLD>, C::R, static_cast<int>(grid) * C::R, kThreads,
+                              C::kSmem, stream, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], p);
 }
 
 int64_t pad8(int64_t d)
