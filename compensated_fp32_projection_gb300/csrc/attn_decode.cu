@@ -468,7 +468,8 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
 
 // The parts of each row joined: the prefix's (splits of them), then those of
 // the sequence's own keys, in order.  One warp for each row, four values of
-// the head dimension a lane.
+// the head dimension a lane.  Four CTAs an SM: 36.2 -> 35.5 us for 64 sequences on
+// 8192 tokens, whose rows have 17 parts and more.
 struct Join {
     const float* pre_o;     // [splits][batch * heads][dim]
     const float* pre_lse;   // [splits][batch * heads]
@@ -476,7 +477,7 @@ struct Join {
     int splits, rows_a_unit;
 };
 
-__global__ void __launch_bounds__(256) attn_join_kernel(Params p, Join x)
+__global__ void __launch_bounds__(256, 4) attn_join_kernel(Params p, Join x)
 {
     // Where the parts are follows from the lengths alone, which are complete:
     // this kernel starts when the decode kernel's CTAs run, and those start, or

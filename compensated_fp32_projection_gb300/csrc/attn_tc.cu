@@ -88,9 +88,10 @@ struct Cfg {
     // 64 KB a stage beside the 128 KB of q: 64 keys leave three stages to one
     // CTA.  Products of 64 columns are bound by the shared memory that feeds
     // them (49 cycles instead of 32), so that a pair, which has room for 128,
-    // takes 304 us where one CTA takes 341 (4096 FP32 tokens, 16 heads of 128;
-    // causal, 32 heads: 349 against 366).  Its blocks of 512 rows want long
-    // sequences: it is used from 1024 rows on average on.
+    // takes 271 us where one CTA takes 322 (4096 FP32 tokens, 16 heads of 128;
+    // causal, 32 heads: 326 against 351, 1024 tokens of them 61 against 64, 512
+    // tokens 36.4 against 36.2).  Its blocks of 512 rows want long sequences: it
+    // is used from 1024 rows on average on.
     static constexpr int BN = DP == 128 && PL == 2 && !PAIR_ ? 64 : 128;
     static constexpr int kBoxes = DP / 64;                      // 64-wide boxes along D
     static constexpr uint32_t kQTile = 128 * DP * 2;            // one plane of one half

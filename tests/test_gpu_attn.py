@@ -463,3 +463,39 @@ def test_nothing_to_do(pkg):
     q, k, v = case([3], [0], 4, 2, 64, torch.float32)
     lse = torch.empty(3, 4, device="cuda")
     assert bool((pkg.comp_attn_f32(q, k, v, lse=lse) == 0).all()) and bool(lse.isneginf().all())
+
+
+# --------------------------------------------------------------------------
+# offsets beyond 32 bits
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("kv", [torch.float16, torch.float32])
+def test_packed_strides_beyond_2_31_elements(pkg, kv):
+    """Tokens 2^25 elements apart, 70 of them."""
+    n, apart = 70, 2 ** 25
+    q, k, v = case([n], [n], 4, 2, 128, kv, seed=11)
+    want = (pkg.comp_attn_f32 if kv == torch.float32 else pkg.comp_attn_f32x16)(q, k, v)
+
+    def spread(t):
+        wide = torch.empty(n, apart, dtype=t.dtype, device="cuda")
+        part = wide[:, -t.shape[1] * t.shape[2]:].unflatten(1, t.shape[1:])
+        part.copy_(t)
+        return part
+
+    q2, k2, v2 = spread(q), spread(k), spread(v)
+    out = spread(torch.zeros_like(q))
+    got = (pkg.comp_attn_f32 if kv == torch.float32 else pkg.comp_attn_f32x16)(q2, k2, v2, out=out)
+    assert torch.equal(got, want)
+
+
+def test_decode_pages_beyond_2_31_elements(pkg):
+    """The same tokens on pages far into a cache of 2^31 elements and more."""
+    lengths, shared = [700, 650, 1000, 513], 4
+    q, k, v, table, n = cache_case(lengths, shared, 128, 8, 2, 128, seed=12)
+    want, want_lse = decode(pkg, q, k, v, table, n, shared)
+    far = 2 ** 31 // (2 * 128 * 128) + 5  # the first page's number
+    big = [torch.empty(far + k.shape[0], 2, 128, 128, dtype=torch.float16, device="cuda") for _ in range(2)]
+    for b, t in zip(big, (k, v)):
+        b[far:] = t
+    moved = torch.where(table >= 0, table + far, table)
+    out, lse = decode(pkg, q, *big, moved, n, shared)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)

@@ -251,3 +251,32 @@ def test_refusals(pkg):
         pkg.comp_kv_append_f32(torch.zeros(3, 2, 64, device="cuda"), torch.zeros(3, 2, 64, device="cuda"), k, v, t, n)
     with pytest.raises(ValueError):
         pkg.comp_kv_copy_pages(k, v, one, ints([1, 2]))
+
+
+def test_pages_beyond_2_31_elements(pkg):
+    """New tokens, copies, a fork and a compaction at the far end of a large cache."""
+    far = 2 ** 31 // (2 * 128 * 128) + 3
+    k, v = (torch.zeros(far + 4, 2, 128, 128, dtype=torch.float16, device="cuda") for _ in range(2))
+    new = [torch.randn(130, 2, 128, device="cuda") for _ in range(2)]
+    table, start = ints([[far, far + 3, -1], [-1, -1, -1]]), ints([0, 0])
+    pkg.comp_kv_append_f32(*new, k, v, table, start, ints([0, 130, 130]))
+    for t, x in ((k, new[0]), (v, new[1])):
+        assert torch.equal(t[far].transpose(0, 1), x[:128].half())
+        assert torch.equal(t[far + 3, :, :2].transpose(0, 1), x[128:].half())
+    pkg.comp_kv_copy_pages(k, v, ints([far + 3]), ints([far + 1]))
+    assert torch.equal(k[far + 1], k[far + 3]) and torch.equal(v[far + 1], v[far + 3])
+    k[far + 1] = 0
+    # all pages before are taken, so that the fork's copy goes to the next free one
+    refs = torch.ones(far + 4, dtype=torch.int32, device="cuda")
+    refs[far + 1:far + 3] = 0
+    table, lengths, refs, left = pkg.comp_kv_fork(k, v, table, ints([130, 0]), refs, ints([0]), ints([1]))
+    assert left.item() == 1 and table.tolist() == [[far, far + 3, -1], [far, far + 1, -1]]
+    assert lengths.tolist() == [130, 130] and refs[far:].tolist() == [2, 1, 0, 1]
+    assert torch.equal(k[far + 1, :, :2], k[far + 3, :, :2]) and not k[far + 1, :, 2:].any()
+    # only those three are in use then: they move to the front
+    kept = [t[p].clone() for t in (k, v) for p in (far, far + 1, far + 3)]
+    refs[:far] = 0
+    table, refs, remap, live = pkg.comp_kv_compact(k, v, table, refs)
+    assert live.item() == 3 and table.tolist() == [[0, 2, -1], [0, 1, -1]] and refs[:4].tolist() == [2, 1, 1, 0]
+    assert remap[far:].tolist() == [0, 1, -1, 2] and int((remap >= 0).sum()) == 3
+    assert all(torch.equal(a, b) for a, b in zip(kept, [t[p] for t in (k, v) for p in (0, 1, 2)]))
