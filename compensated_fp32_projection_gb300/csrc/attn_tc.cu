@@ -183,8 +183,11 @@ __device__ __forceinline__ void rows_arrive(int id)
 }
 
 // This CTA's (or pair's) sequence and block of kRows rows: blocks are numbered
-// sequence by sequence, the last of one, which sees most keys, first.  One
-// warp; the offsets are read 32 sequences at a time.
+// sequence by sequence, the last of one, which sees most keys, first.  (All
+// sequences' blocks by their number, highest first, end with many short blocks at
+// once, which memory bounds: 245 us instead of 238 for the ragged prompts, 533
+// instead of 506 for 40 of 300 to 1500 tokens.)  One warp; the offsets are read
+// 32 sequences at a time.
 template <int kRows>
 __device__ __forceinline__ void find_block(const Params& p, int block, Shared* sm)
 {
