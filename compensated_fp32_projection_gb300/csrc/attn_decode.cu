@@ -62,7 +62,7 @@ struct Params {
     const int32_t* lengths;
     int64_t q_token, q_head, width;
     int batch, heads, kv_heads, group, row_blocks, dim;
-    int page_shift, pages, shared_keys, most_keys, pieces, waves, vec_q, after_prefix;
+    int page_shift, pages, shared_keys, most_keys, pieces, waves, vec_q, vec_out, after_prefix;
     float scale;
 };
 
@@ -439,11 +439,20 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
                 float* const dst = whole ? p.out + at_row * p.dim
                                          : p.part_o + (static_cast<int64_t>(part) * (NB * 8) + row) * p.dim;
                 const float norm = sum == 0.0f ? 0.0f : 1.0f / sum;
+                if (p.vec_out || !whole) {
 #pragma unroll
-                for (int t = 0; t < DP / 8; ++t)
-                    if (t * 8 < p.dim)
-                        *reinterpret_cast<float2*>(dst + t * 8 + quad * 2) =
-                            make_float2(lo_f(o[nb][t]) * norm, hi_f(o[nb][t]) * norm);
+                    for (int t = 0; t < DP / 8; ++t)
+                        if (t * 8 < p.dim)
+                            *reinterpret_cast<float2*>(dst + t * 8 + quad * 2) =
+                                make_float2(lo_f(o[nb][t]) * norm, hi_f(o[nb][t]) * norm);
+                } else {
+#pragma unroll
+                    for (int t = 0; t < DP / 8; ++t)
+                        if (t * 8 < p.dim) {
+                            dst[t * 8 + quad * 2] = lo_f(o[nb][t]) * norm;
+                            dst[t * 8 + quad * 2 + 1] = hi_f(o[nb][t]) * norm;
+                        }
+                }
                 if (quad == 0) {
                     const float lse =
                         sum == 0.0f ? -INFINITY : fmaf(m[nb], kAttnLn2, logf(sum * (1.0f / kAttnPScale)));
@@ -514,10 +523,8 @@ __global__ void __launch_bounds__(256, 4) attn_join_kernel(Params p, Join x)
             o = x.pre_o + (static_cast<int64_t>(i) * rows + row) * p.dim;
             return x.pre_lse[static_cast<int64_t>(i) * rows + row];
         }
-        if (whole) {
-            o = p.out + row * p.dim;
+        if (whole)  // its sums are read below
             return p.lse[row];
-        }
         const int64_t slot = i == x.splits ? first_slot : 2 * (first_slot / 2 + i - x.splits);
         o = p.part_o + (slot * x.rows_a_unit + in_block) * p.dim;
         return p.part_lse[slot * x.rows_a_unit + in_block];
@@ -542,7 +549,9 @@ __global__ void __launch_bounds__(256, 4) attn_join_kernel(Params p, Join x)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             acc[e] *= a;
-        const int n = min(32, parts - i0);
+        // the caller's out, the last part of a whole row, may lie at any address
+        const bool from_out = whole && i0 + 32 >= parts;
+        const int n = min(32, parts - i0) - from_out;
 #pragma unroll 16
         for (int i = 0; i < n; ++i) {
             const float wi = __shfl_sync(0xffffffffu, w, i);
@@ -557,11 +566,31 @@ __global__ void __launch_bounds__(256, 4) attn_join_kernel(Params p, Join x)
                 acc[3] = fmaf(v.w, wi, acc[3]);
             }
         }
+        if (from_out) {
+            const float wi = __shfl_sync(0xffffffffu, w, n);
+            const float* const o = p.out + row * p.dim + lane * 4;
+            if (lane * 4 < p.dim) {
+                const float4 v =
+                    p.vec_out ? *reinterpret_cast<const float4*>(o) : make_float4(o[0], o[1], o[2], o[3]);
+                acc[0] = fmaf(v.x, wi, acc[0]);
+                acc[1] = fmaf(v.y, wi, acc[1]);
+                acc[2] = fmaf(v.z, wi, acc[2]);
+                acc[3] = fmaf(v.w, wi, acc[3]);
+            }
+        }
     }
     const float norm = sum == 0.0f ? 0.0f : 1.0f / sum;
-    if (lane * 4 < p.dim)
-        *reinterpret_cast<float4*>(p.out + row * p.dim + lane * 4) =
-            make_float4(acc[0] * norm, acc[1] * norm, acc[2] * norm, acc[3] * norm);
+    if (lane * 4 < p.dim) {
+        float* const dst = p.out + row * p.dim + lane * 4;
+        if (p.vec_out) {
+            *reinterpret_cast<float4*>(dst) =
+                make_float4(acc[0] * norm, acc[1] * norm, acc[2] * norm, acc[3] * norm);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                dst[e] = acc[e] * norm;
+        }
+    }
     if (x.lse_out && lane == 0)
         x.lse_out[row] = sum == 0.0f ? -INFINITY : top + logf(sum);
 }
@@ -719,6 +748,7 @@ comp_status_t launch_attn_decode(const comp_kv_cache_t& cache, const float* q, i
     p.pieces = 2 * dev.sm_count * kWarps < kMostPieces ? 2 * dev.sm_count * kWarps : kMostPieces;
     p.waves = splits > 0 ? kPrefixWaves : 1;
     p.vec_q = (reinterpret_cast<uintptr_t>(q) & 7u) == 0 && q_token % 2 == 0 && q_head % 2 == 0;
+    p.vec_out = aligned16(out);  // rows are multiples of 32 bytes
     p.scale = scale;
     p.after_prefix = splits > 0;
     CUtensorMap mk{}, mv{};

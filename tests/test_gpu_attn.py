@@ -417,6 +417,23 @@ def test_decode_strided_queries_and_stream(pkg):
     check_decode(out, lse, q, k, v, table, n, 64 ** -0.5)
 
 
+@pytest.mark.parametrize("heads,kv_heads,dim", [(4, 2, 64), (8, 1, 128), (20, 2, 40)])
+@pytest.mark.parametrize("shared", [0, 5])
+def test_decode_out_at_any_address(pkg, shared, heads, kv_heads, dim):
+    """Rows written whole, rows joined from parts, and rows joined with a prefix's."""
+    lengths = [shared * 16 + n for n in (1, 0, 16, 5000, 33, 700)]
+    q, k, v, table, n = cache_case(lengths, shared, 16, heads, kv_heads, dim, seed=13)
+    want, want_lse = decode(pkg, q, k, v, table, n, shared)
+    check_decode(want, want_lse, q, k, v, table, n, dim ** -0.5)
+    for offset in (0, 1, 2, 3, 4, 6):
+        place = torch.full((want.numel() + 16,), 3.0, device="cuda")
+        out = place[offset:offset + want.numel()].view(want.shape)
+        got, lse = decode(pkg, q, k, v, table, n, shared, out=out)
+        assert got.data_ptr() == out.data_ptr()
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+        assert bool((place[:offset] == 3.0).all()) and bool((place[offset + want.numel():] == 3.0).all())
+
+
 def test_decode_long(pkg):
     q, k, v, table, n = cache_case([20000, 3, 9000], 0, 64, 2, 1, 128, seed=7)
     out, lse = decode(pkg, q, k, v, table, n)
