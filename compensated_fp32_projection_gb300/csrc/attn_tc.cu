@@ -789,7 +789,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t st = lanes + half * 128;
         const int row_lim = valid ? lim : INT32_MAX;  // rows that are not there are not stored
         float m = -INFINITY;        // the running maximum of s * c2
-        uint64_t l2 = 0;            // the running sum of 2^14 p, in two parts
+        // The running sum of 2^14 p, and what its additions have rounded away: one
+        // addition for each tile, of sums that begin at zero with the tile.  (Weights
+        // added one by one to the running sum all round the same way where they are
+        // equal: 4e-5 of it after 16384 keys, 2e-4 after 65536.)
+        float l = 0.0f, l_low = 0.0f;
         float alpha = 0.0f;         // what the sums so far are to be scaled by with the next O'
         uint64_t o[DP / 2];
 #pragma unroll
@@ -877,11 +881,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float shift = m_new == -INFINITY ? 0.0f : m_new;  // nothing seen yet: every p is 0
                 const float alpha_new = ex2(m - shift);
                 m = m_new;
-                l2 = mul2(l2, f2_bits(alpha_new, alpha_new));
                 // 2^14 p in one operation: the sum's rounding, at most 2^-21 of 14,
                 // is of the size of the scores' own
                 const uint64_t s2 = f2_bits(14.0f - shift, 14.0f - shift);
-                uint64_t l3 = 0;
+                uint64_t l2 = 0, l3 = 0;
 #pragma unroll 1
                 for (int c = 0; c < BN; c += 32) {
                     float w[32];
@@ -912,6 +915,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 l2 = add2(l2, l3);
+                {
+                    const float before = l * alpha_new;
+                    const float more = fmaf(l_low, alpha_new, lo_f(l2) + hi_f(l2));
+                    l = before + more;
+                    l_low = more - (l - before);
+                }
                 tmem_ld_wait32(x);
                 if (OB == 2 && j > 0)
                     take(j - 1);
@@ -920,7 +929,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // out, through shared memory (this warp's share of q's planes, which the
         // products of this half have read): a thread holds a row
-        const float l = (lo_f(l2) + hi_f(l2)) * (1.0f / kAttnPScale);
+        l *= 1.0f / kAttnPScale;
         // no key seen, or none that counts beside an infinite score (NaN stays NaN)
         const float norm = l == 0.0f ? 0.0f : (1.0f / kAttnPScale) / l;
         if (ok) {

@@ -175,6 +175,43 @@ def test_long(pkg, kv, heads, kv_heads, dim, n):
         compare(oc[rows, h], lc[rows, h], *exact_rows(qc[rows, h], kc[:, g], vc[:, g], seen, dim ** -0.5))
 
 
+def equal_keys(n, s1, dim, kv, queries, heads, kv_heads):
+    """Keys that all score 0 but the first, which scores s1; values about 1: the
+    additions of equal weights to a growing sum all round the same way."""
+    q = torch.ones(queries, heads, dim)
+    k = torch.zeros(n, kv_heads, dim)
+    k[0] = s1 * dim ** -0.5
+    v = torch.rand(n, kv_heads, dim, generator=torch.Generator().manual_seed(n)) + 0.5
+    return q, k.to(kv), v.to(kv)
+
+
+def compare_equal_keys(out, lse, q, k, v):
+    """All rows against one in 64 bits.  lse more closely than the tests' general
+    bound: sums of at most 64 equal terms (4e-6 with the exponentials' own error),
+    one compensated addition a tile, the logarithm and the last rounding."""
+    from attn_check import compare, exact_rows
+
+    heads, n = q.shape[1], k.shape[0]
+    for h in range(heads):
+        g = h // (heads // k.shape[1])
+        x_out, x_lse, tol, _ = exact_rows(q[:1, h], k[:, g], v[:, g], torch.ones(1, n, dtype=torch.bool),
+                                          q.shape[2] ** -0.5)
+        e = 4e-6 * q.shape[2] ** -0.5 * float((k[:, g].double().abs() @ q[0, h].double()).max())
+        ltol = e + 4e-6 + 2.0 ** -22 * x_lse.abs()
+        rows = out.shape[0]
+        compare(out[:, h].cpu(), lse[:, h].cpu(), x_out.expand(rows, -1), x_lse.expand(rows), tol.expand(rows, -1),
+                ltol.expand(rows))
+
+
+@pytest.mark.parametrize("kv", KV, ids=["f16", "f32"])
+@pytest.mark.parametrize("queries,dim", [(3, 64), (3, 128), (600, 128)])   # the last: pairs of CTAs for FP32
+@pytest.mark.parametrize("n,s1", [(16384, 0.3), (16384, 0.5), (65536, 0.7)])
+def test_many_equal_keys(pkg, n, s1, queries, dim, kv):
+    q, k, v = equal_keys(n, s1, dim, kv, queries, 2, 1)
+    out, lse = call(pkg, q.cuda(), k.cuda(), v.cuda(), [0, queries], [0, n], False)
+    compare_equal_keys(out, lse, q, k, v)
+
+
 def sampled(out, lse, q, k, v, cu, causal, every):
     """check_attn on some rows of each sequence (its first and last among them)."""
     from attn_check import compare, exact_rows
