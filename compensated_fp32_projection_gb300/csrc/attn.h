@@ -13,6 +13,7 @@ namespace compfp32 {
 constexpr float kAttnLog2E = 1.4426950408889634f;
 constexpr float kAttnLn2 = 0.6931471805599453f;
 constexpr float kAttnPScale = 16384.0f;             // 2^14: see split_p
+constexpr float kAttnLargeScore = 1048576.0f;       // 2^20: from here on s c - m is rounded step by step
 constexpr long long kAttnWaitLimit = 1ll << 31;     // cycles (about a second)
 
 // The fault word of the including file's kernels.

@@ -395,10 +395,16 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
                 const float alpha = ex2(m[nb] - shift);
                 m[nb] = m_new;
                 a2[nb] = f2_bits(alpha, alpha);
-                float w[4];  // 2^14 p
+                float w[4];  // 2^14 p; large scores: see the packed kernel
+                if (fabsf(shift) < kAttnLargeScore) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    w[e] = ex2(fmaf(x[e], c2, 14.0f - shift));
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = ex2(fmaf(x[e], c2, 14.0f - shift));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = ex2(__fsub_rn(__fmul_rn(x[e], c2), shift) + 14.0f);
+                }
                 split_p(w[0], w[1], pa[nb][0], pa[nb][1]);
                 split_p(w[2], w[3], pa[nb][2], pa[nb][3]);
                 l2[nb] = fma2(l2[nb], a2[nb], add2(f2_bits(w[0], w[1]), f2_bits(w[2], w[3])));

@@ -882,8 +882,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float alpha_new = ex2(m - shift);
                 m = m_new;
                 // 2^14 p in one operation: the sum's rounding, at most 2^-21 of 14,
-                // is of the size of the scores' own
-                const uint64_t s2 = f2_bits(14.0f - shift, 14.0f - shift);
+                // is of the size of the scores' own.  Beyond kAttnLargeScore the two
+                // roundings that s and 14 - m have apart would soon be whole units,
+                // and 2^14 p no FP16 value (from 2^27 on): there s becomes s c - m in
+                // place, the product rounded as the maximum is, so that it ends at 0.
+                uint64_t by = c22, s2 = f2_bits(14.0f - shift, 14.0f - shift);
+                const bool large = fabsf(shift) >= kAttnLargeScore;
+                if (__any_sync(0xffffffffu, large)) {
+                    tmem_ld_wait32(x);
+#pragma unroll 1
+                    for (int c = 0; c < BN; c += 16) {
+                        uint32_t r[16];
+                        tmem_ld16(st + c, r);
+                        tmem_ld_wait16(r);
+                        if (large) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                r[i] = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(r[i]), c2), shift));
+                        }
+                        __syncwarp();
+                        tmem_st16(st + c, r);
+                    }
+                    tmem_st_wait();
+                    tmem_ld32(st, x);
+                    if (large) {
+                        by = f2_bits(1.0f, 1.0f);
+                        s2 = f2_bits(14.0f, 14.0f);
+                    }
+                    __syncwarp();
+                }
                 uint64_t l2 = 0, l3 = 0;
 #pragma unroll 1
                 for (int c = 0; c < BN; c += 32) {
@@ -891,7 +918,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld_wait32(x);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const uint64_t y = fma2(u2_bits(x[2 * i], x[2 * i + 1]), c22, s2);
+                        const uint64_t y = fma2(u2_bits(x[2 * i], x[2 * i + 1]), by, s2);
                         w[2 * i] = ex2(lo_f(y));
                         w[2 * i + 1] = ex2(hi_f(y));
                     }

@@ -160,6 +160,38 @@ def test_sizes_of_scores(pkg, kv):
         check_attn(out, lse, q, k, v, [0, 260], [0, 260], True, scale)
 
 
+def large_scores(n, dim, unit, seed):
+    """Keys c_j (1, 1, ...) of shuffled multiples c_j of `unit`: a query a (1, 1, ...)
+    with a > 15 gives scores that are 100 and more apart, and far beside their
+    rounding, so the largest one's value is the output."""
+    c = torch.randperm(n, generator=torch.Generator().manual_seed(seed)) + 400
+    k = (unit * c).float()[:, None, None].expand(n, 1, dim).contiguous()
+    v = torch.randn(n, 1, dim, generator=torch.Generator().manual_seed(seed + 1))
+    return k, v
+
+
+def check_largest(out, lse, q, k, v, seen):
+    """out: what the two products round away (4e-6 of a value); lse: the score's own 4e-6."""
+    s = torch.where(seen, (q[:, 0].double() @ k[:, 0].double().T) * q.shape[2] ** -0.5, -math.inf)
+    top, at = s.max(1)
+    assert bool(((out[:, 0] - v[at, 0]).abs() <= 4e-6 * v[at, 0].abs()).all())
+    assert bool(((lse[:, 0].double() - top).abs() <= 4e-6 * top.abs()).all())
+
+
+@pytest.mark.parametrize("kv", KV, ids=["f16", "f32"])
+@pytest.mark.parametrize("n,dim", [(300, 64), (300, 128), (1100, 128)])
+@pytest.mark.parametrize("unit", [1, -1, 32, -32])
+def test_scores_of_any_size(pkg, kv, n, dim, unit):
+    """Scores from 5 10^4 to 3 10^10, in one warp's rows side by side."""
+    k, v = large_scores(n, dim, unit, seed=n)
+    k, v = k.to(kv), v.to(kv)
+    a = 2.0 ** (4 + torch.arange(n) % 12) * 1.96875
+    q = a[:, None, None].expand(n, 1, dim).contiguous()
+    q[1::2] *= 0.5078125  # bits below FP16's too
+    out, lse = call(pkg, q.cuda(), k.cuda(), v.cuda(), [0, n], [0, n], True)
+    check_largest(out.cpu(), lse.cpu(), q, k, v.float(), torch.ones(n, n, dtype=torch.bool).tril())
+
+
 @pytest.mark.parametrize("kv", KV, ids=["f16", "f32"])
 @pytest.mark.parametrize("heads,kv_heads,dim,n", [(2, 1, 128, 2500), (2, 2, 64, 4100)])
 def test_long(pkg, kv, heads, kv_heads, dim, n):
@@ -452,6 +484,21 @@ def test_decode_strided_queries_and_stream(pkg):
         out, lse = decode(pkg, wide[:, 2:6], k, v, table, n)
     side.synchronize()
     check_decode(out, lse, q, k, v, table, n, 64 ** -0.5)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("shared", [0, 16])
+@pytest.mark.parametrize("unit", [1, -1, 32, -32])
+def test_decode_scores_of_any_size(pkg, dim, shared, unit):
+    batch, n, page = 32, 704, 32
+    k, v = large_scores(n, dim, unit, seed=dim)
+    kp, vp = (x.half().view(n // page, page, 1, dim).transpose(1, 2).contiguous().cuda() for x in (k, v))
+    q = (2.0 ** (4 + torch.arange(batch) % 12) * 1.96875)[:, None, None].expand(batch, 1, dim).contiguous()
+    lengths = [max(1, n - 21 * i) for i in range(batch)]
+    table = ints([list(range(n // page))] * batch)
+    out, lse = decode(pkg, q.cuda(), kp, vp, table, ints(lengths), shared)
+    seen = torch.arange(n)[None] < torch.tensor(lengths)[:, None]
+    check_largest(out.cpu(), lse.cpu(), q, k, v.half().float(), seen)
 
 
 @pytest.mark.parametrize("heads,kv_heads,dim", [(4, 2, 64), (8, 1, 128), (20, 2, 40)])
