@@ -40,6 +40,14 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kLeast = 4;
 constexpr int kLong = 8;
+// Tiles that are added up before they are added to the sums so far: equal terms
+// (identical, zero or padding keys) all round the same way, so that a running sum
+// of every tile is off by 5e-5 after 65536 keys; with runs of 64 tiles, by 1e-6.
+// The sums of the runs before lie in the warp's slot of the workspace, which it
+// writes only later: 24 sequences of 8000 tokens, 64 heads over 4 of 128, take 77 us,
+// 74 without runs, 113 with those sums in registers and 123 with them in shared
+// memory, which leaves an SM one CTA.
+constexpr int kRun = 64;
 constexpr uint32_t kFaultDecode = 0xA01;
 
 // DP: head dimension padded to 64 or 128; NB: blocks of eight query heads.
@@ -214,6 +222,8 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full_of[kWarps][NS];
     __shared__ int abort_flag[kWarps];
+    __shared__ float2 l_far_of[kWarps][NB][32];
+    __shared__ float m_far_of[kWarps][NB][32];
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     uint8_t* const stages =
         reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023)) +
@@ -331,8 +341,11 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
             if (NB == 1)  // with two blocks the registers do not suffice
                 load_q(after);
         }
+        // the running maximum and the sums of a run; slot, l_far_of, m_far_of: of the runs before
         float m[NB];
         uint64_t l2[NB], o[NB][DP / 8];
+        const int part = 2 * piece + (fragment > 0 ? 1 : 0);
+        float* const slot = p.part_o + (static_cast<int64_t>(part) * (NB * 8) + g) * p.dim + quad * 2;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
             m[nb] = -INFINITY;
@@ -341,98 +354,128 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
             for (int t = 0; t < DP / 8; ++t)
                 o[nb][t] = 0;
         }
-        for (int t = 0; t < n; ++t, ++i) {
-            const int s = i % NS;
-            if (!attn_warp_wait(&full[s], (i / NS) & 1, &abort_flag[warp], kFaultDecode)) {
-                ok = false;
-                break;
-            }
-            uint8_t* const kt = stages + s * C::kStage;
-            uint8_t* const vt = kt + C::kPlane;
-            const int left = r.own - (r.tile + t) * kTile;  // keys of the tile that count
-            if (left < kTile) {
-                // beyond the sequence's end v may hold anything: 0 times that must be 0
+        for (int t0 = 0; ok && t0 < n; t0 += kRun) {
+            const int t1 = min(n, t0 + kRun);
+            for (int t = t0; t < t1; ++t, ++i) {
+                const int s = i % NS;
+                if (!attn_warp_wait(&full[s], (i / NS) & 1, &abort_flag[warp], kFaultDecode)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t* const kt = stages + s * C::kStage;
+                uint8_t* const vt = kt + C::kPlane;
+                const int left = r.own - (r.tile + t) * kTile;  // keys of the tile that count
+                if (left < kTile) {
+                    // beyond the sequence's end v may hold anything: 0 times that must be 0
 #pragma unroll
-                for (int x = 0; x < C::kBoxes; ++x)
-                    for (int u = lane; u < kTile * 8; u += 32)
-                        if (u / 8 >= left)
-                            *reinterpret_cast<uint4*>(vt + x * (kTile * 128) + u * 16) = make_uint4(0, 0, 0, 0);
-                fence_proxy_async_smem();  // before the next load into this stage
-                __syncwarp();
-            }
-            // two chains for each eight keys, the even and the odd steps of the head dimension
-            float c[NB][2][2][4] = {};
+                    for (int x = 0; x < C::kBoxes; ++x)
+                        for (int u = lane; u < kTile * 8; u += 32)
+                            if (u / 8 >= left)
+                                *reinterpret_cast<uint4*>(vt + x * (kTile * 128) + u * 16) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();  // before the next load into this stage
+                    __syncwarp();
+                }
+                // two chains for each eight keys, the even and the odd steps of the head dimension
+                float c[NB][2][2][4] = {};
 #pragma unroll
-            for (int k = 0; k < DP / 16; k += 2)
+                for (int k = 0; k < DP / 16; k += 2)
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
+                    for (int nt = 0; nt < 2; ++nt) {
+                        uint32_t b[4];
+                        ldmatrix4(smem_u32(kt) + (k / 4) * (kTile * 128) +
+                                      sw128(nt * 8 + (lane & 7), (k % 4) * 2 + (lane >> 3)),
+                                  b);
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) {
+                            mma16816(c[nb][nt][0], q[nb][k], b[0], b[1]);
+                            mma16816(c[nb][nt][1], q[nb][k + 1], b[2], b[3]);
+                        }
+                    }
+                uint32_t pa[NB][4];
+                uint64_t a2[NB];
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    float x[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int nt = e >> 1, col = e & 1, key = nt * 8 + quad * 2 + col;
+                        x[e] = fmaf(c[nb][nt][0][2 + col] + c[nb][nt][1][2 + col], 0x1p-10f,
+                                    c[nb][nt][0][col] + c[nb][nt][1][col]);
+                        x[e] = key < left ? x[e] : -INFINITY;
+                    }
+                    float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * c2;
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    const float m_new = fmaxf(m[nb], top), shift = m_new == -INFINITY ? 0.0f : m_new;
+                    const float alpha = ex2(m[nb] - shift);
+                    m[nb] = m_new;
+                    a2[nb] = f2_bits(alpha, alpha);
+                    float w[4];  // 2^14 p; large scores: see the packed kernel
+                    if (fabsf(shift) < kAttnLargeScore) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = ex2(fmaf(x[e], c2, 14.0f - shift));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = ex2(__fsub_rn(__fmul_rn(x[e], c2), shift) + 14.0f);
+                    }
+                    split_p(w[0], w[1], pa[nb][0], pa[nb][1]);
+                    split_p(w[2], w[3], pa[nb][2], pa[nb][3]);
+                    l2[nb] = fma2(l2[nb], a2[nb], add2(f2_bits(w[0], w[1]), f2_bits(w[2], w[3])));
+                }
+#pragma unroll
+                for (int d = 0; d < DP / 16; ++d) {
                     uint32_t b[4];
-                    ldmatrix4(smem_u32(kt) + (k / 4) * (kTile * 128) +
-                                  sw128(nt * 8 + (lane & 7), (k % 4) * 2 + (lane >> 3)),
-                              b);
+                    ldmatrix4_trans(
+                        smem_u32(vt) + (d / 4) * (kTile * 128) + sw128(lane & 15, (d % 4) * 2 + (lane >> 4)), b);
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) {
-                        mma16816(c[nb][nt][0], q[nb][k], b[0], b[1]);
-                        mma16816(c[nb][nt][1], q[nb][k + 1], b[2], b[3]);
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float y[4] = {};
+                            mma16816(y, pa[nb], b[2 * e], b[2 * e + 1]);
+                            const uint64_t both = add2(f2_bits(y[0], y[1]), f2_bits(y[2], y[3]));
+                            o[nb][2 * d + e] = fma2(o[nb][2 * d + e], a2[nb], both);
+                        }
+                }
+                __syncwarp();  // all lanes have read the stage
+                if (begin + loads < end)
+                    load();
+            }
+            if (t0 > 0) {
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    const float a = ex2(m_far_of[warp][nb][lane] - (m[nb] == -INFINITY ? 0.0f : m[nb]));
+                    const uint64_t a2 = f2_bits(a, a);
+                    const float2 l = l_far_of[warp][nb][lane];
+                    l2[nb] = fma2(f2_bits(l.x, l.y), a2, l2[nb]);
+#pragma unroll
+                    for (int x = 0; x < DP / 8; ++x)
+                        if (x * 8 < p.dim)
+                            o[nb][x] = fma2(*reinterpret_cast<const uint64_t*>(slot + nb * 8 * p.dim + x * 8), a2,
+                                            o[nb][x]);
+                }
+            }
+            if (t1 < n) {
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    m_far_of[warp][nb][lane] = m[nb];
+                    l_far_of[warp][nb][lane] = make_float2(lo_f(l2[nb]), hi_f(l2[nb]));
+                    l2[nb] = 0;
+#pragma unroll
+                    for (int x = 0; x < DP / 8; ++x) {
+                        if (x * 8 < p.dim)
+                            *reinterpret_cast<uint64_t*>(slot + nb * 8 * p.dim + x * 8) = o[nb][x];
+                        o[nb][x] = 0;
                     }
                 }
-            uint32_t pa[NB][4];
-            uint64_t a2[NB];
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                float x[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int nt = e >> 1, col = e & 1, key = nt * 8 + quad * 2 + col;
-                    x[e] = fmaf(c[nb][nt][0][2 + col] + c[nb][nt][1][2 + col], 0x1p-10f,
-                                c[nb][nt][0][col] + c[nb][nt][1][col]);
-                    x[e] = key < left ? x[e] : -INFINITY;
-                }
-                float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * c2;
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const float m_new = fmaxf(m[nb], top), shift = m_new == -INFINITY ? 0.0f : m_new;
-                const float alpha = ex2(m[nb] - shift);
-                m[nb] = m_new;
-                a2[nb] = f2_bits(alpha, alpha);
-                float w[4];  // 2^14 p; large scores: see the packed kernel
-                if (fabsf(shift) < kAttnLargeScore) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        w[e] = ex2(fmaf(x[e], c2, 14.0f - shift));
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        w[e] = ex2(__fsub_rn(__fmul_rn(x[e], c2), shift) + 14.0f);
-                }
-                split_p(w[0], w[1], pa[nb][0], pa[nb][1]);
-                split_p(w[2], w[3], pa[nb][2], pa[nb][3]);
-                l2[nb] = fma2(l2[nb], a2[nb], add2(f2_bits(w[0], w[1]), f2_bits(w[2], w[3])));
             }
-#pragma unroll
-            for (int d = 0; d < DP / 16; ++d) {
-                uint32_t b[4];
-                ldmatrix4_trans(
-                    smem_u32(vt) + (d / 4) * (kTile * 128) + sw128(lane & 15, (d % 4) * 2 + (lane >> 4)), b);
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float y[4] = {};
-                        mma16816(y, pa[nb], b[2 * e], b[2 * e + 1]);
-                        const uint64_t both = add2(f2_bits(y[0], y[1]), f2_bits(y[2], y[3]));
-                        o[nb][2 * d + e] = fma2(o[nb][2 * d + e], a2[nb], both);
-                    }
-            }
-            __syncwarp();  // all lanes have read the stage
-            if (begin + loads < end)
-                load();
         }
 
         // the row, or this warp's part of it
         if (ok) {
             const bool whole = n == r.tiles;
-            const int part = 2 * piece + (fragment > 0 ? 1 : 0);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
                 float sum = lo_f(l2[nb]) + hi_f(l2[nb]);
@@ -552,9 +595,7 @@ __global__ void __launch_bounds__(256, 4) attn_join_kernel(Params p, Join x)
         for (int o = 16; o; o >>= 1)
             s += __shfl_xor_sync(0xffffffffu, s, o);
         sum = fmaf(sum, a, s);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            acc[e] *= a;
+        float run[4] = {};  // of these 32: see kRun
         // the caller's out, the last part of a whole row, may lie at any address
         const bool from_out = whole && i0 + 32 >= parts;
         const int n = min(32, parts - i0) - from_out;
@@ -566,10 +607,10 @@ __global__ void __launch_bounds__(256, 4) attn_join_kernel(Params p, Join x)
             if (lane * 4 < p.dim) {
                 const float4 v = *reinterpret_cast<const float4*>(o + lane * 4);
                 // where nothing was seen the sums are 0
-                acc[0] = fmaf(v.x, wi, acc[0]);
-                acc[1] = fmaf(v.y, wi, acc[1]);
-                acc[2] = fmaf(v.z, wi, acc[2]);
-                acc[3] = fmaf(v.w, wi, acc[3]);
+                run[0] = fmaf(v.x, wi, run[0]);
+                run[1] = fmaf(v.y, wi, run[1]);
+                run[2] = fmaf(v.z, wi, run[2]);
+                run[3] = fmaf(v.w, wi, run[3]);
             }
         }
         if (from_out) {
@@ -578,12 +619,15 @@ __global__ void __launch_bounds__(256, 4) attn_join_kernel(Params p, Join x)
             if (lane * 4 < p.dim) {
                 const float4 v =
                     p.vec_out ? *reinterpret_cast<const float4*>(o) : make_float4(o[0], o[1], o[2], o[3]);
-                acc[0] = fmaf(v.x, wi, acc[0]);
-                acc[1] = fmaf(v.y, wi, acc[1]);
-                acc[2] = fmaf(v.z, wi, acc[2]);
-                acc[3] = fmaf(v.w, wi, acc[3]);
+                run[0] = fmaf(v.x, wi, run[0]);
+                run[1] = fmaf(v.y, wi, run[1]);
+                run[2] = fmaf(v.z, wi, run[2]);
+                run[3] = fmaf(v.w, wi, run[3]);
             }
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            acc[e] = fmaf(acc[e], a, run[e]);
     }
     const float norm = sum == 0.0f ? 0.0f : 1.0f / sum;
     if (lane * 4 < p.dim) {

@@ -224,15 +224,16 @@ def compare_equal_keys(out, lse, q, k, v):
     from attn_check import compare, exact_rows
 
     heads, n = q.shape[1], k.shape[0]
-    for h in range(heads):
-        g = h // (heads // k.shape[1])
-        x_out, x_lse, tol, _ = exact_rows(q[:1, h], k[:, g], v[:, g], torch.ones(1, n, dtype=torch.bool),
+    group = heads // k.shape[1]
+    for g in range(k.shape[1]):  # all queries are the same
+        x_out, x_lse, tol, _ = exact_rows(q[:1, 0].cpu(), k[:, g], v[:, g], torch.ones(1, n, dtype=torch.bool),
                                           q.shape[2] ** -0.5)
-        e = 4e-6 * q.shape[2] ** -0.5 * float((k[:, g].double().abs() @ q[0, h].double()).max())
+        e = 4e-6 * q.shape[2] ** -0.5 * float((k[:, g].double().abs() @ q[0, 0].double().cpu()).max())
         ltol = e + 4e-6 + 2.0 ** -22 * x_lse.abs()
-        rows = out.shape[0]
-        compare(out[:, h].cpu(), lse[:, h].cpu(), x_out.expand(rows, -1), x_lse.expand(rows), tol.expand(rows, -1),
-                ltol.expand(rows))
+        mine = out[:, g * group:(g + 1) * group].flatten(0, 1).cpu()
+        mine_lse = lse[:, g * group:(g + 1) * group].flatten().cpu()
+        rows = mine.shape[0]
+        compare(mine, mine_lse, x_out.expand(rows, -1), x_lse.expand(rows), tol.expand(rows, -1), ltol.expand(rows))
 
 
 @pytest.mark.parametrize("kv", KV, ids=["f16", "f32"])
@@ -484,6 +485,22 @@ def test_decode_strided_queries_and_stream(pkg):
         out, lse = decode(pkg, wide[:, 2:6], k, v, table, n)
     side.synchronize()
     check_decode(out, lse, q, k, v, table, n, 64 ** -0.5)
+
+
+@pytest.mark.parametrize("batch,heads,kv_heads,dim,n,s1", [
+    (160, 8, 8, 64, 65536, 0.3), (160, 8, 8, 128, 65536, 0.7), (160, 96, 8, 128, 65536, 0.3),  # long pieces of the line
+    (1, 2, 2, 64, 150000, 0.0), (1, 1, 1, 128, 100000, 0.0),                                   # rows in many parts
+])
+def test_decode_many_equal_keys(pkg, batch, heads, kv_heads, dim, n, s1):
+    """Every page but each row's first is the same one; all values of a column are equal."""
+    q, k, v = equal_keys(n, s1, dim, torch.float16, 1, heads, kv_heads)
+    v = v[:1].expand(n, kv_heads, dim)
+    kp, vp = (torch.stack([x[128:256], x[:128]]).transpose(1, 2).contiguous().cuda() for x in (k, v))
+    table = torch.zeros(batch, -(-n // 128), dtype=torch.int32, device="cuda")
+    table[:, 0] = 1
+    q = q.expand(batch, heads, dim).contiguous()
+    out, lse = decode(pkg, q.cuda(), kp, vp, table, ints([n] * batch))
+    compare_equal_keys(out, lse, q, k.float(), v.float())
 
 
 @pytest.mark.parametrize("dim", [64, 128])
