@@ -176,15 +176,17 @@ int32_t* ints_out(const at::Tensor& t)
     return static_cast<int32_t*>(t.data_ptr());
 }
 
-// The stream of a call.  While this lives it is the current one, so that what
+// The stream of a call.  While this lives the tensors' device is the current one,
+// which the library launches on, and the stream its current one, so that what
 // the call allocates belongs to it: a workspace of another stream could be
 // given away before this one has used it, and an output could still be in use
 // there.
 struct Stream {
     comp_stream_t at;
+    c10::cuda::CUDAGuard on_device;
     std::optional<c10::cuda::CUDAStreamGuard> guard;
 
-    Stream(PyObject* o, int device)
+    Stream(PyObject* o, int device) : on_device(static_cast<c10::DeviceIndex>(device))
     {
         const auto on = static_cast<c10::DeviceIndex>(device);
         at = c10::cuda::getCurrentCUDAStream(on).stream();
@@ -352,10 +354,11 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n)
         const int32_t* const cu = optional<const int32_t>(a[6], at::kInt, "cu", c.device, {rows + 1});
         if (!cu && tokens != rows)
             refuse("without cu there must be one token for each row of table");
+        const Stream on(a[7], c.device);
         check(comp_kv_append_f32(&c.c, static_cast<const float*>(k.data_ptr()),
                                  static_cast<const float*>(v.data_ptr()), k.stride(0), k.stride(1), v.stride(0),
                                  v.stride(1), tokens, ints(table), rows, table.size(1), cu, ints(start),
-                                 Stream(a[7], c.device).at),
+                                 on.at),
               "comp_kv_append_f32");
         return Py_NewRef(Py_None);
     });
@@ -503,8 +506,8 @@ PyObject* copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n)
         Cache c(a[0], a[1]);
         const at::Tensor& src = list(a[2], "src", c.device);
         const at::Tensor& dst = dense(a[3], at::kInt, "dst", c.device, src.sizes());
-        check(comp_kv_copy_pages(&c.c, ints(src), ints(dst), src.size(0), Stream(a[4], c.device).at),
-              "comp_kv_copy_pages");
+        const Stream on(a[4], c.device);
+        check(comp_kv_copy_pages(&c.c, ints(src), ints(dst), src.size(0), on.at), "comp_kv_copy_pages");
         return Py_NewRef(Py_None);
     });
 }

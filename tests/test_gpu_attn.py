@@ -347,6 +347,21 @@ def test_what_a_call_allocates_belongs_to_its_stream(pkg):
             assert torch.equal(got, right)
 
 
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs a device that is not the current one")
+def test_tensors_that_are_not_on_the_current_device(pkg):
+    q, k, v = case([64], [64], 4, 2, 64, torch.float16, seed=10)
+    want = pkg.comp_attn_f32x16(q, k, v)
+    kp, vp = (torch.zeros(8, 2, 16, 64, dtype=torch.float16, device="cuda:1") for _ in range(2))
+    got = pkg.comp_attn_f32x16(*(x.to("cuda:1") for x in (q, k, v)))
+    assert torch.cuda.current_device() == 0 and torch.equal(got.to("cuda:0"), want)
+    new = k[:1].float().to("cuda:1")
+    pkg.comp_kv_append_f32(new, new, kp, vp, ints([[3]]).to("cuda:1"), ints([5]).to("cuda:1"))
+    pkg.comp_kv_copy_pages(kp, vp, ints([3]).to("cuda:1"), ints([6]).to("cuda:1"))
+    torch.cuda.synchronize("cuda:1")
+    assert torch.cuda.current_device() == 0
+    assert torch.equal(kp[3, :, 5], k[0].to("cuda:1")) and torch.equal(kp[6], kp[3])
+
+
 def test_one_sequence_without_offsets(pkg):
     q, k, v = case([50], [80], 4, 2, 64, torch.float32, seed=9)
     out = pkg.comp_attn_f32(q, k, v)
