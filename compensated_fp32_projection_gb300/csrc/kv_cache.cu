@@ -11,6 +11,8 @@
 // against its range before it is used as an address.
 #include <cuda_fp16.h>
 
+#include <mutex>
+
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -575,17 +577,23 @@ unsigned grid_of(int64_t work, int64_t per, const DeviceInfo& dev, int per_sm)
     return static_cast<unsigned>(g < 1 ? 1 : (g > most ? most : g));
 }
 
-// The plan kernels' shared memory, raised above 48 KB once per device.
+// A plan kernel's shared memory, raised once per device to the most that it may be
+// asked for: another call may be about to launch with more than this one needs.
 template <typename Kernel>
-bool allow_smem(Kernel kernel, size_t bytes)
+bool allow_smem(Kernel kernel, int64_t most, std::mutex& mu, bool (&done)[64], const DeviceInfo& dev)
 {
-    if (bytes <= 48 * 1024 - 1024)
-        return true;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) ==
-        cudaSuccess)
-        return true;
-    (void)cudaGetLastError();
-    return false;
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev.device < 0 || dev.device >= 64)
+        return false;
+    if (!done[dev.device]) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most)) !=
+            cudaSuccess) {
+            (void)cudaGetLastError();
+            return false;
+        }
+        done[dev.device] = true;
+    }
+    return true;
 }
 
 comp_status_t copy_ints(const int32_t* src, int32_t* dst, int64_t n, const DeviceInfo& dev, cudaStream_t s)
@@ -677,7 +685,9 @@ comp_status_t comp_kv_reserve(int64_t pages, int32_t page_size, const int32_t* t
     if (st != COMP_OK)
         return st;
     const size_t smem = static_cast<size_t>(8 * rows);
-    if (!allow_smem(reserve_kernel, smem))
+    static std::mutex mu;
+    static bool done[64] = {};
+    if (!allow_smem(reserve_kernel, 8 * kMostRows, mu, done, dev))
         return COMP_ERR_CUDA;
     reserve_kernel<<<1, kPlanThreads, smem, s>>>(
         Tables{table, want, refs, table_out, nullptr, refs_out, rows, width, pages, page_size}, left);
@@ -708,7 +718,9 @@ comp_status_t comp_kv_fork(const comp_kv_cache_t* cache, const int32_t* table, c
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const Tables t{table, lengths, refs, table_out, lengths_out, refs_out, rows, width, pages, cache->page_size};
     const size_t smem = static_cast<size_t>(4 * n);
-    if (!allow_smem(fork_plan_kernel, smem))
+    static std::mutex mu;
+    static bool done[64] = {};
+    if (!allow_smem(fork_plan_kernel, 4 * kMostListed, mu, done, dev))
         return COMP_ERR_CUDA;
     fork_plan_kernel<<<1, kPlanThreads, smem, s>>>(t, parents, children, static_cast<int>(n), left);
     st = launch_status();

@@ -158,6 +158,41 @@ def test_compact(pkg, pages, share, in_place):
     assert torch.equal(bits(k), bits(kx)) and torch.equal(bits(v), bits(vx))
 
 
+def test_calls_of_different_size_from_two_threads(pkg):
+    """The plan kernels' shared memory grows with the call: a smaller call must not
+    take it from a larger one that is about to be launched (C calls: ctypes lets
+    the threads run)."""
+    import ctypes
+    import threading
+
+    lib = pkg._native.load()
+    k, v = pool(4, 1, 16, 64)
+    c = pkg._native.KvCache(k.data_ptr(), v.data_ptr(), 4, 16, 1, 64)
+    torch.cuda.synchronize()
+    states = []
+
+    def work(rows, n):
+        table, refs, want = (torch.full((m,), x, dtype=torch.int32, device="cuda")
+                             for m, x in ((rows, -1), (4, 0), (rows, 0)))
+        lens, parents, left = (torch.full((m,), x, dtype=torch.int32, device="cuda")
+                               for m, x in ((rows, 0), (n, -1), (1, 7)))
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        t, r, w, m, p, f = (x.data_ptr() for x in (table, refs, want, lens, parents, left))
+        for _ in range(400):
+            states.append(lib.comp_kv_reserve(4, 16, t, r, rows, 1, w, t, r, f, side.cuda_stream))
+            states.append(lib.comp_kv_fork(ctypes.byref(c), t, m, r, rows, 1, p, p, n, t, m, r, f, side.cuda_stream))
+        side.synchronize()
+        assert left.tolist() == [4]
+
+    threads = [threading.Thread(target=work, args=a) for a in ((16384, 32768), (6200, 12400), (7000, 14000))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(states) == 2400 and set(states) == {0}
+
+
 @pytest.mark.parametrize("in_place", [False, True])
 def test_reserve(pkg, in_place):
     pages, width, page = 3000, 40, 16
