@@ -47,7 +47,7 @@ def comp_attn_f32(q, k, v, cu_q=None, cu_k=None, *, scale=None, causal=True, out
     last query sees every key of its sequence, each earlier one a key less.
     scale defaults to head_dim ** -0.5.  lse, if given ([tokens, heads]),
     receives the log-sum-exp of each row.  A row that sees no key gives zeros
-    and -inf."""
+    and -inf, as do the tokens beyond the last sequence."""
     return _b.attn(True, q, k, v, cu_q, cu_k, scale, causal, out, lse, workspace, stream)
 
 

@@ -63,9 +63,12 @@ comp_status_t attn(const comp_attn_t* a, const float* q, const void* k, const vo
     if (!attn_ok(a, kv_bytes, &b) || (cu_q == nullptr) != (cu_k == nullptr) || (!cu_q && a->n_seq > 1) ||
         workspace_bytes < 0)
         return COMP_ERR_INVALID_VALUE;
-    if (a->total_q == 0 || a->n_seq == 0)
+    if (a->total_q == 0)
         return COMP_OK;
-    if (!q || !out || (b.k > 0 && (!k || !v)))
+    comp_attn_t seen = *a;
+    if (a->n_seq == 0)
+        seen.total_k = 0;  // no sequence has the keys
+    if (!q || !out || (seen.total_k > 0 && (!k || !v)))
         return COMP_ERR_INVALID_VALUE;
     const int64_t cu = cu_q ? 4 * (a->n_seq + 1) : 0;
     const Range in[] = {{q, b.q}, {k, b.k}, {v, b.v}, {cu_q, cu}, {cu_k, cu}};
@@ -79,7 +82,7 @@ comp_status_t attn(const comp_attn_t* a, const float* q, const void* k, const vo
     const comp_status_t st = current_device(&dev);
     if (st != COMP_OK)
         return st;
-    return launch_attn(*a, q, k, v, kv_bytes, cu_q, cu_k, out, lse, workspace, dev, static_cast<cudaStream_t>(stream));
+    return launch_attn(seen, q, k, v, kv_bytes, cu_q, cu_k, out, lse, workspace, dev, static_cast<cudaStream_t>(stream));
 }
 
 bool decode_ok(const comp_kv_cache_t* c, int64_t batch, int32_t heads, int64_t width, int64_t shared_pages,

@@ -187,7 +187,7 @@ __device__ __forceinline__ void rows_arrive(int id)
 // sequences' blocks by their number, highest first, end with many short blocks at
 // once, which memory bounds: 245 us instead of 238 for the ragged prompts, 533
 // instead of 506 for 40 of 300 to 1500 tokens.)  One warp; the offsets are read
-// 32 sequences at a time.
+// 32 sequences at a time.  Tokens beyond the last sequence are one more, without keys.
 template <int kRows>
 __device__ __forceinline__ void find_block(const Params& p, int block, Shared* sm)
 {
@@ -201,12 +201,15 @@ __device__ __forceinline__ void find_block(const Params& p, int block, Shared* s
         }
         return;
     }
-    for (int s0 = 0; s0 < p.n_seq; s0 += 32) {
+    for (int s0 = 0; s0 <= p.n_seq; s0 += 32) {
         const int s = s0 + lane;
         int n = 0, a = 0, b = 0, c = 0, d = 0;
-        if (s < p.n_seq) {
-            a = clampi(p.cu_q[s], 0, p.total_q), b = clampi(p.cu_q[s + 1], a, p.total_q);
-            c = clampi(p.cu_k[s], 0, p.total_k), d = clampi(p.cu_k[s + 1], c, p.total_k);
+        if (s <= p.n_seq) {
+            a = clampi(p.cu_q[s], 0, p.total_q), b = p.total_q;
+            if (s < p.n_seq) {
+                b = clampi(p.cu_q[s + 1], a, p.total_q);
+                c = clampi(p.cu_k[s], 0, p.total_k), d = clampi(p.cu_k[s + 1], c, p.total_k);
+            }
             const unsigned rows = static_cast<unsigned>(b - a) * static_cast<unsigned>(p.group);
             n = static_cast<int>((rows + (kRows - 1u)) / kRows);
         }
@@ -1210,7 +1213,7 @@ int64_t pad8(int64_t d)
 // caller's own FP16 rows can be loaded.
 int64_t attn_stage_bytes(const comp_attn_t& a, int kv_bytes, const void* k, const void* v)
 {
-    if (a.total_k == 0)
+    if (a.total_k == 0 || a.n_seq == 0)
         return 0;
     if (kv_bytes == 2 && aligned16(k) && aligned16(v) && map_legal(a.total_k, a.kv_heads, a.k_token, a.k_head) &&
         map_legal(a.total_k, a.kv_heads, a.v_token, a.v_head))
@@ -1285,9 +1288,10 @@ comp_status_t launch_attn(const comp_attn_t& a, const float* q, const void* k, c
                                  p.vec_out);
     const int64_t rows = a.total_q * p.group;
     // pairs of CTAs where the sequences fill their 512 rows on average (Cfg)
-    const bool pair = a.head_dim > 64 && kv_bytes == 4 && rows / a.n_seq >= 1024;
+    const bool pair = a.head_dim > 64 && kv_bytes == 4 && rows >= 1024 * a.n_seq;
     const int64_t block = pair ? 512 : 256;
-    const int64_t grid = (cu_q ? rows / block + a.n_seq : (rows + block - 1) / block) * a.kv_heads;
+    // n rows have at most (n + block - 1) / block blocks; the tokens beyond the last sequence are one more
+    const int64_t grid = (rows + (cu_q ? a.n_seq + 1 : 1) * (block - 1)) / block * a.kv_heads;
     if (grid > INT32_MAX / 2)
         return COMP_ERR_INVALID_VALUE;
     if (pair)

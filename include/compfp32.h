@@ -340,7 +340,9 @@ comp_status_t comp_gemm_f32x16_noalloc(const float* x, const uint16_t* W, float*
  *   query tokens attend to keys cu_k[i] .. cu_k[i+1]-1 of the total_k packed
  *   key tokens.  cu_q and cu_k are device arrays of n_seq + 1 ascending
  *   int32 starting at 0 (values outside 0..total are clamped); NULL for both
- *   means one sequence.  Lengths of zero are valid.
+ *   means one sequence.  Lengths of zero are valid.  Query tokens beyond
+ *   cu_q[n_seq] belong to no sequence and see no key, nor does any if n_seq
+ *   is 0.
  *   causal != 0: query t of n sees the keys j <= t + (m - n) of its m, so the
  *   last query sees all of them; causal == 0: every query sees all keys.
  *   heads is a multiple of kv_heads; head_dim 1 .. 128; scale finite and > 0.

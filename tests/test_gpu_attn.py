@@ -362,6 +362,36 @@ def test_tensors_that_are_not_on_the_current_device(pkg):
     assert torch.equal(kp[3, :, 5], k[0].to("cuda:1")) and torch.equal(kp[6], kp[3])
 
 
+@pytest.mark.parametrize("kv", KV, ids=["f16", "f32"])
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+@pytest.mark.parametrize("cu,tokens,dim", [([0], 5, 64), ([0], 700, 128), ([0, 4, 9], 10, 64), ([0, 256], 777, 64),
+                                           ([0, 600, 600, 1050], 2000, 128), (list(range(70)), 400, 80)], ids=str)
+def test_tokens_beyond_the_last_sequence(pkg, cu, tokens, dim, causal, kv):
+    """They see no key: zeros and -inf, and nothing stays unwritten."""
+    q, k, v = case([tokens], [tokens], 4, 2, dim, kv, seed=14)
+    out = torch.full_like(q, 7.0)
+    _, lse = call(pkg, q, k, v, cu, cu, causal, out=out)
+    n = cu[-1]
+    assert bool((out[n:] == 0).all()) and bool(lse[n:].isneginf().all())
+    check_attn(out[:n], lse[:n], q, k, v, cu, cu, causal, dim ** -0.5)
+
+
+def test_no_sequence(pkg):
+    """The C call with n_seq 0, with and without offsets."""
+    import ctypes
+
+    q, k, v = case([300], [300], 4, 2, 64, torch.float32, seed=14)
+    lib, cu = pkg._native.load(), ints([0])
+    a = pkg._native.Attn(0, 300, 300, 4, 2, 64, 1, 0.125, 256, 64, 128, 64, 128, 64, 256, 64)
+    stream = torch.cuda.current_stream().cuda_stream
+    for offsets in (None, cu.data_ptr()):
+        out, lse = torch.full_like(q, 7.0), torch.full((300, 4), 7.0, device="cuda")
+        assert lib.comp_attn_workspace_bytes(ctypes.byref(a), 4, k.data_ptr(), v.data_ptr()) == 0
+        assert lib.comp_attn_f32(ctypes.byref(a), q.data_ptr(), k.data_ptr(), v.data_ptr(), offsets, offsets,
+                                 out.data_ptr(), lse.data_ptr(), None, 0, stream) == 0
+        assert bool((out == 0).all()) and bool(lse.isneginf().all())
+
+
 def test_one_sequence_without_offsets(pkg):
     q, k, v = case([50], [80], 4, 2, 64, torch.float32, seed=9)
     out = pkg.comp_attn_f32(q, k, v)
