@@ -34,6 +34,8 @@ bool apart(const Range (&in)[N], const Range (&outs)[M])
     return true;
 }
 
+constexpr int64_t kMostAttnUnits = 1 << 29;  // sequences times key/value heads: blocks are counted in ints
+
 struct AttnBytes {
     int64_t q, k, v, out, lse;
 };
@@ -43,7 +45,7 @@ bool attn_ok(const comp_attn_t* a, int kv_bytes, AttnBytes* b)
     if (!a || a->n_seq < 0 || a->n_seq > INT32_MAX || a->total_q < 0 || a->total_q > INT32_MAX || a->total_k < 0 ||
         a->total_k > INT32_MAX || a->heads <= 0 || a->kv_heads <= 0 || a->heads > 65535 ||
         a->heads % a->kv_heads != 0 || a->head_dim < 1 || a->head_dim > 128 || !std::isfinite(a->scale) ||
-        !(a->scale > 0.0f) || a->total_q * a->heads > INT32_MAX)
+        !(a->scale > 0.0f) || a->total_q * a->heads > INT32_MAX || a->n_seq * a->kv_heads > kMostAttnUnits)
         return false;
     if (!strided_bytes(a->total_q, a->heads, a->head_dim, a->q_token, a->q_head, 4, &b->q) ||
         !strided_bytes(a->total_k, a->kv_heads, a->head_dim, a->k_token, a->k_head, kv_bytes, &b->k) ||
@@ -90,7 +92,8 @@ bool decode_ok(const comp_kv_cache_t* c, int64_t batch, int32_t heads, int64_t w
 {
     return kv_cache_ok(c, bytes) && batch >= 0 && heads > 0 && heads <= 65535 && heads % c->kv_heads == 0 &&
            width >= 0 && width <= INT32_MAX / (2 * c->page_size) && mul_ok(batch, width, entries) &&
-           batch <= INT32_MAX / heads && *entries <= INT64_MAX / 8 && shared_pages >= 0 && shared_pages <= width;
+           batch <= INT32_MAX / heads && *entries <= INT64_MAX / 8 && shared_pages >= 0 && shared_pages <= width &&
+           attn_decode_countable(*c, batch, heads, width);
 }
 
 }  // namespace

@@ -711,6 +711,18 @@ Split prefix_split(const comp_kv_cache_t& c, int64_t shared, int64_t batch, int 
     return {static_cast<int>(n), fold};
 }
 
+// Blocks of eight query heads that a warp takes at once, and how often a
+// key/value head's keys are gone through.
+int blocks_at_once(int group)
+{
+    return group > 8 ? 2 : 1;
+}
+
+int row_blocks(int group)
+{
+    return (group + 8 * blocks_at_once(group) - 1) / (8 * blocks_at_once(group));
+}
+
 // Floats of the workspace: parts of rows, the prefix's parts, the rows' lse.
 struct Layout {
     int64_t part_o, part_lse, pre_o, pre_lse, lse, total;
@@ -720,7 +732,7 @@ Layout layout_of(const comp_kv_cache_t& c, int64_t batch, int heads, int splits)
 {
     const int group = heads / c.kv_heads;
     const int64_t pieces = splits > 0 ? kPrefixWaves * kMostPieces : kMostPieces;
-    const int64_t slots = 2 * pieces * (group > 8 ? 16 : 8), rows = batch * heads;
+    const int64_t slots = 2 * pieces * 8 * blocks_at_once(group), rows = batch * heads;
     Layout l;
     l.part_o = 0;
     l.part_lse = l.part_o + slots * c.head_dim;
@@ -738,6 +750,12 @@ int64_t effective_shared(int64_t batch, int64_t shared_pages)
 }
 
 }  // namespace
+
+bool attn_decode_countable(const comp_kv_cache_t& cache, int64_t batch, int heads, int64_t width)
+{
+    const int64_t units = static_cast<int64_t>(cache.kv_heads) * row_blocks(heads / cache.kv_heads);
+    return (width * cache.page_size / kTile + 1) * batch <= INT32_MAX / units;
+}
 
 int64_t attn_decode_bytes(const comp_kv_cache_t& cache, int64_t batch, int heads, int64_t shared_pages)
 {
@@ -766,7 +784,7 @@ comp_status_t launch_attn_decode(const comp_kv_cache_t& cache, const float* q, i
         if (st != COMP_OK)
             return st;
     }
-    const int nb = group > 8 ? 2 : 1;
+    const int nb = blocks_at_once(group);
     Params p{};
     p.q = q;
     p.out = out;
@@ -783,15 +801,12 @@ comp_status_t launch_attn_decode(const comp_kv_cache_t& cache, const float* q, i
     p.heads = heads;
     p.kv_heads = cache.kv_heads;
     p.group = group;
-    p.row_blocks = (group + 8 * nb - 1) / (8 * nb);
+    p.row_blocks = row_blocks(group);
     p.dim = cache.head_dim;
     while ((1 << p.page_shift) < cache.page_size)
         ++p.page_shift;
     p.shared_keys = static_cast<int>(shared * cache.page_size);
     p.most_keys = static_cast<int>(width * cache.page_size);
-    // the line of tiles is counted in ints
-    if ((width * cache.page_size / kTile + 1) * batch > INT32_MAX / (p.kv_heads * p.row_blocks))
-        return COMP_ERR_INVALID_VALUE;
     p.pieces = 2 * dev.sm_count * kWarps < kMostPieces ? 2 * dev.sm_count * kWarps : kMostPieces;
     p.waves = splits > 0 ? kPrefixWaves : 1;
     p.vec_q = (reinterpret_cast<uintptr_t>(q) & 7u) == 0 && q_token % 2 == 0 && q_head % 2 == 0;

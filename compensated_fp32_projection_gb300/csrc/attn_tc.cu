@@ -1292,8 +1292,6 @@ comp_status_t launch_attn(const comp_attn_t& a, const float* q, const void* k, c
     const int64_t block = pair ? 512 : 256;
     // n rows have at most (n + block - 1) / block blocks; the tokens beyond the last sequence are one more
     const int64_t grid = (rows + (cu_q ? a.n_seq + 1 : 1) * (block - 1)) / block * a.kv_heads;
-    if (grid > INT32_MAX / 2)
-        return COMP_ERR_INVALID_VALUE;
     if (pair)
         return launch_t<128, 2, true>(maps, p, grid, dev, stream);
     if (a.head_dim <= 64)
@@ -1343,8 +1341,6 @@ comp_status_t launch_attn_prefix(const comp_kv_cache_t& cache, const float* q, i
                                  32, true);
     p.out_part = static_cast<int>(batch);
     const int64_t grid = (batch * p.group + 255) / 256 * cache.kv_heads * p.splits;
-    if (grid > INT32_MAX)
-        return COMP_ERR_INVALID_VALUE;
     if (fold)
         return launch_t<64, 1, false, true>(maps, p, grid, dev, stream);
     return cache.head_dim <= 64 ? launch_t<64, 1>(maps, p, grid, dev, stream)

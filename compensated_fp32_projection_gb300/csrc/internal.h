@@ -110,7 +110,9 @@ comp_status_t launch_gemm_f16x2(const uint16_t* hi, const uint16_t* lo, const ui
 // k (and of its v).
 bool kv_cache_ok(const comp_kv_cache_t* cache, int64_t* bytes);
 
-// Attention of single tokens over a cache (arguments validated; batch > 0).
+// Attention of single tokens over a cache (arguments validated; batch > 0), and
+// whether its line of tiles can be counted in ints (batch * heads can).
+bool attn_decode_countable(const comp_kv_cache_t& cache, int64_t batch, int heads, int64_t width);
 int64_t attn_decode_bytes(const comp_kv_cache_t& cache, int64_t batch, int heads, int64_t shared_pages);
 comp_status_t launch_attn_decode(const comp_kv_cache_t& cache, const float* q, int64_t q_token, int64_t q_head,
                                  int heads, float scale, const int32_t* table, int64_t batch, int64_t width,

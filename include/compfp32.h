@@ -346,6 +346,8 @@ comp_status_t comp_gemm_f32x16_noalloc(const float* x, const uint16_t* W, float*
  *   causal != 0: query t of n sees the keys j <= t + (m - n) of its m, so the
  *   last query sees all of them; causal == 0: every query sees all keys.
  *   heads is a multiple of kv_heads; head_dim 1 .. 128; scale finite and > 0.
+ *   heads is at most 65535, total_q * heads below 2^31, n_seq * kv_heads at
+ *   most 2^29.
  *   Strides count elements: q[t,h,d] = q[t*q_token + h*q_head + d], and so on
  *   (so q, k and v may be parts of one projection's output); not negative.
  *   The rows of out must not overlap each other.  lse is [total_q, heads], or
@@ -427,7 +429,10 @@ comp_status_t comp_kv_append_f32(const comp_kv_cache_t* cache, const float* k, c
  * The first shared_pages entries of all rows are the same pages, a prefix that
  * the batch shares: row 0's are read, once for the whole batch.
  * 0 shares nothing.  Workspace: comp_attn_decode_workspace_bytes, 16-byte
- * aligned.  A cache without pages takes only a table of width 0.
+ * aligned.  A cache without pages takes only a table of width 0.  heads is at
+ * most 65535, batch * heads below 2^31, and so is
+ * (width * page_size / 16 + 1) * batch * kv_heads * ceil(group / 16), where
+ * group = heads / kv_heads.
  */
 int64_t comp_attn_decode_workspace_bytes(const comp_kv_cache_t* cache, int64_t batch, int32_t heads, int64_t width,
                                          int64_t shared_pages);

@@ -103,6 +103,21 @@ def test_decode_arguments(lib):
     assert go(batch=0) == 0
 
 
+def test_sizes_that_cannot_be_counted(lib):
+    """Refused as arguments, before a device is asked for or anything is enqueued."""
+    far = [i << 44 for i in range(1, 9)]
+    for shared in (0, 2):
+        for pages_of, heads, want in ((cache(), 4, INVALID), (cache(kv_heads=1), 40, INVALID)):
+            assert lib.comp_attn_decode_workspace_bytes(pages_of, 1 << 20, heads, 1 << 12, shared) == 0
+            assert lib.comp_attn_decode_f32x16(pages_of, P(far[0]), 64 * heads, 64, heads, 0.1, P(far[1]), 1 << 20,
+                                               1 << 12, P(far[2]), shared, P(far[3]), None, P(far[4]), 1 << 40,
+                                               None) == want
+    assert lib.comp_attn_decode_workspace_bytes(cache(), 1 << 10, 4, 1 << 12, 2) > 0
+    for f32 in (False, True):
+        assert call(lib, attn(n_seq=(1 << 28) + 1), q=far[0], k=far[1], v=far[2], cu_q=far[3], cu_k=far[4],
+                    out=far[5], ws=far[6], f32=f32) == INVALID
+
+
 def test_page_arguments(lib):
     fork = lambda n=1, rows=2, width=4, out=6 * MB, lengths_out=7 * MB, refs_out=8 * MB, left=9 * MB, par=4 * MB: \
         lib.comp_kv_fork(cache(), P(MB), P(2 * MB), P(3 * MB), rows, width, P(par), P(5 * MB), n, P(out),
