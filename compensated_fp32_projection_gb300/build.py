@@ -3,7 +3,9 @@
 Each ``csrc/*.cu`` is compiled in parallel to an object under ``_build/`` and
 the objects are linked into one shared library next to this file.
 ``csrc/attn_binding.cpp`` is compiled with the host compiler at the same time
-and becomes ``_attn_binding.so``, the torch binding of the attention calls.  The CUDA
+and becomes ``_attn_binding.so``, the torch binding of the attention calls, for
+the torch that is there; without one, or with one without CUDA, the C library is
+all that is built.  The CUDA
 runtime is linked statically, so the library needs only the NVIDIA driver at
 run time (and loads, without running anything, on a machine with no GPU).
 
@@ -14,6 +16,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -64,10 +67,40 @@ def _deps():
     ] + [os.path.abspath(__file__)]
 
 
+def _torch_dir() -> str | None:
+    """The folder of a torch with CUDA, found without importing it."""
+    spec = importlib.util.find_spec("torch")
+    for d in (spec.submodule_search_locations or []) if spec else []:
+        if os.path.exists(os.path.join(d, "lib", "libc10_cuda.so")):
+            return d
+    return None
+
+
+def _torch_stamp(torch: str) -> str:
+    """What the binding's ABI depends on: this torch's place and version."""
+    with open(os.path.join(torch, "version.py")) as f:
+        version = re.search(r"__version__\s*=\s*['\"]([^'\"]+)", f.read())
+    return f"{torch} {version.group(1) if version else ''}\n"
+
+
+def _stamp_path() -> str:
+    return os.path.join(BUILD, "attn_binding.torch")
+
+
+def _built_for() -> str:
+    try:
+        with open(_stamp_path()) as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+    torch = _torch_dir()
+    made = [LIB] if torch is None else [LIB, BINDING]
+    if not all(os.path.exists(m) for m in made) or (torch is not None and _built_for() != _torch_stamp(torch)):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    t = min(os.path.getmtime(m) for m in made)
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -84,9 +117,8 @@ def _cuda_include() -> str:
     return os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
 
 
-def _compile_binding() -> str:
-    """The torch binding's object; torch's headers are found without importing it."""
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+def _compile_binding(torch: str) -> str:
+    """The binding's object, with the headers of the torch in this folder."""
     obj = os.path.join(BUILD, "attn_binding.o")
     inc = [INCLUDE, os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], _cuda_include()]
@@ -98,8 +130,8 @@ def _compile_binding() -> str:
     return obj
 
 
-def _link_binding(obj: str) -> None:
-    lib = os.path.join(importlib.util.find_spec("torch").submodule_search_locations[0], "lib")
+def _link_binding(obj: str, torch: str) -> None:
+    lib = os.path.join(torch, "lib")
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-shared", obj, "-o", tmp, "-L", PKG, "-l:libcompfp32.so", "-L", lib,
            "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
@@ -107,6 +139,8 @@ def _link_binding(obj: str) -> None:
     if p.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{p.stdout}\n{p.stderr}")
     os.replace(tmp, BINDING)
+    with open(_stamp_path(), "w") as f:
+        f.write(_torch_stamp(torch))
 
 
 # Kernels that move registers between warpgroups with setmaxnreg assume this
@@ -130,15 +164,16 @@ def _check_register_budget(ptxas_log: str) -> None:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link the library if any source changed; returns its path."""
+    """Compile and link the library if any source, or the torch of its binding,
+    changed; returns its path.  A binding that cannot be built is an error, raised
+    once the library is in place."""
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    srcs = _sources()
+    srcs, torch = _sources(), _torch_dir()
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
-        binding = ex.submit(_compile_binding)
+        binding = ex.submit(_compile_binding, torch) if torch is not None else None
         results = list(ex.map(_compile, srcs))
-        binding_obj = binding.result()
     with open(os.path.join(BUILD, "ptxas.txt"), "w") as f:
         for (obj, log), src in zip(results, srcs):
             f.write(f"== {os.path.basename(src)}\n{log}\n")
@@ -149,7 +184,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if p.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{p.stdout}\n{p.stderr}")
     os.replace(tmp, LIB)
-    _link_binding(binding_obj)
+    if binding is not None:
+        _link_binding(binding.result(), torch)
     if verbose:
         print(open(os.path.join(BUILD, "ptxas.txt")).read())
     return LIB
