@@ -214,6 +214,14 @@ int64_t integer(PyObject* o)
     return n;
 }
 
+bool truth(PyObject* o)
+{
+    const int t = PyObject_IsTrue(o);
+    if (t < 0)
+        throw PythonError{};
+    return t != 0;
+}
+
 float scale_of(PyObject* o, int64_t dim)
 {
     if (o == Py_None)
@@ -312,7 +320,7 @@ PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n)
         d.heads = static_cast<int32_t>(h);
         d.kv_heads = static_cast<int32_t>(k.size(1));
         d.head_dim = static_cast<int32_t>(dim);
-        d.causal = PyObject_IsTrue(a[7]) ? 1 : 0;
+        d.causal = truth(a[7]) ? 1 : 0;
         d.scale = scale_of(a[6], dim);
         d.q_token = q.stride(0);
         d.q_head = q.stride(1);

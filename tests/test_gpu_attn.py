@@ -620,6 +620,14 @@ def test_refusals(pkg):
             pkg.comp_attn_decode_f32x16(**{**dict(q=q, k_pages=k, v_pages=v, table=table, lengths=n), **bad})
 
 
+def test_arguments_that_cannot_be_taken_as_they_are(pkg):
+    """A truth value that raises."""
+    q, k, v = case([10], [10], 4, 2, 64, torch.float16)
+    with pytest.raises(RuntimeError):
+        pkg.comp_attn_f32x16(q, k, v, causal=torch.ones(2))
+    assert torch.equal(pkg.comp_attn_f32x16(q, k, v, causal=torch.ones(1)), pkg.comp_attn_f32x16(q, k, v))
+
+
 def test_nothing_to_do(pkg):
     q, k, v = case([0], [0], 4, 2, 64, torch.float16)
     assert pkg.comp_attn_f32x16(q, k, v).shape == (0, 4, 64)
