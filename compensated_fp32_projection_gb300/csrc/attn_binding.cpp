@@ -422,12 +422,15 @@ PyObject* reserve(PyObject*, PyObject* const* a, Py_ssize_t n)
         const int64_t rows = table.size(0);
         const at::Tensor& want = dense(a[1], at::kInt, "want", device, {rows});
         const at::Tensor& refs = list(a[2], "refs", device);
+        const int64_t page_size = integer(a[3]);
+        if (page_size < 0 || page_size > INT32_MAX)
+            refuse("page_size must be 16, 32, 64 or 128");
         const Stream on(a[7], device);
         PyObject* const given[] = {a[4], a[5], a[6]};
         at::Tensor out[] = {output(a[4], at::kInt, "table_out", device, table.sizes()),
                             output(a[5], at::kInt, "refs_out", device, refs.sizes()),
                             output(a[6], at::kInt, "left", device, {1})};
-        check(comp_kv_reserve(refs.size(0), static_cast<int32_t>(integer(a[3])), ints(table), ints(refs), rows,
+        check(comp_kv_reserve(refs.size(0), static_cast<int32_t>(page_size), ints(table), ints(refs), rows,
                               table.size(1), ints(want), ints_out(out[0]), ints_out(out[1]), ints_out(out[2]),
                               on.at),
               "comp_kv_reserve");

@@ -621,11 +621,15 @@ def test_refusals(pkg):
 
 
 def test_arguments_that_cannot_be_taken_as_they_are(pkg):
-    """A truth value that raises."""
+    """A truth value that raises, a number beyond 32 bits."""
     q, k, v = case([10], [10], 4, 2, 64, torch.float16)
     with pytest.raises(RuntimeError):
         pkg.comp_attn_f32x16(q, k, v, causal=torch.ones(2))
     assert torch.equal(pkg.comp_attn_f32x16(q, k, v, causal=torch.ones(1)), pkg.comp_attn_f32x16(q, k, v))
+    table, refs = ints([[-1, -1]]), ints([0, 0, 0])
+    for size in (2 ** 32 + 16, -2 ** 32 + 16, 2 ** 40):
+        with pytest.raises(ValueError):
+            pkg.comp_kv_reserve(table, ints([20]), refs, size)
 
 
 def test_nothing_to_do(pkg):
