@@ -94,6 +94,8 @@ const at::Tensor& typed(PyObject* o, at::ScalarType type, const char* name, int&
         refuse(std::string(name) + " must be " + type_name(type));
     if (!t.is_cuda())
         refuse(std::string(name) + " must be a CUDA tensor (there is no CPU path)");
+    if (t.is_neg())  // its memory holds the values before the negation
+        refuse(std::string(name) + " must not be a lazily negated view (see Tensor.resolve_neg)");
     if (device < 0)
         device = t.get_device();
     else if (t.get_device() != device)

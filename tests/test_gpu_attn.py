@@ -621,7 +621,7 @@ def test_refusals(pkg):
 
 
 def test_arguments_that_cannot_be_taken_as_they_are(pkg):
-    """A truth value that raises, a number beyond 32 bits."""
+    """A truth value that raises, a number beyond 32 bits, a negation not carried out."""
     q, k, v = case([10], [10], 4, 2, 64, torch.float16)
     with pytest.raises(RuntimeError):
         pkg.comp_attn_f32x16(q, k, v, causal=torch.ones(2))
@@ -630,6 +630,10 @@ def test_arguments_that_cannot_be_taken_as_they_are(pkg):
     for size in (2 ** 32 + 16, -2 ** 32 + 16, 2 ** 40):
         with pytest.raises(ValueError):
             pkg.comp_kv_reserve(table, ints([20]), refs, size)
+    with pytest.raises(ValueError):
+        pkg.comp_attn_f32x16(torch._neg_view(q), k, v)
+    want = pkg.comp_attn_f32x16(-q, k, v)
+    assert torch.equal(pkg.comp_attn_f32x16(torch._neg_view(q).resolve_neg(), k, v), want)
 
 
 def test_nothing_to_do(pkg):
