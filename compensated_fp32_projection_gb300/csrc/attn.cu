@@ -34,6 +34,7 @@ bool apart(const Range (&in)[N], const Range (&outs)[M])
     return true;
 }
 
+constexpr int64_t kMostAttnKeys = INT32_MAX - 255;  // a tile's end is an int too
 constexpr int64_t kMostAttnUnits = 1 << 29;  // sequences times key/value heads: blocks are counted in ints
 
 struct AttnBytes {
@@ -43,7 +44,7 @@ struct AttnBytes {
 bool attn_ok(const comp_attn_t* a, int kv_bytes, AttnBytes* b)
 {
     if (!a || a->n_seq < 0 || a->n_seq > INT32_MAX || a->total_q < 0 || a->total_q > INT32_MAX || a->total_k < 0 ||
-        a->total_k > INT32_MAX || a->heads <= 0 || a->kv_heads <= 0 || a->heads > 65535 ||
+        a->total_k > kMostAttnKeys || a->heads <= 0 || a->kv_heads <= 0 || a->heads > 65535 ||
         a->heads % a->kv_heads != 0 || a->head_dim < 1 || a->head_dim > 128 || !std::isfinite(a->scale) ||
         !(a->scale > 0.0f) || a->total_q * a->heads > INT32_MAX || a->n_seq * a->kv_heads > kMostAttnUnits)
         return false;

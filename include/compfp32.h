@@ -346,8 +346,8 @@ comp_status_t comp_gemm_f32x16_noalloc(const float* x, const uint16_t* W, float*
  *   causal != 0: query t of n sees the keys j <= t + (m - n) of its m, so the
  *   last query sees all of them; causal == 0: every query sees all keys.
  *   heads is a multiple of kv_heads; head_dim 1 .. 128; scale finite and > 0.
- *   heads is at most 65535, total_q * heads below 2^31, n_seq * kv_heads at
- *   most 2^29.
+ *   heads is at most 65535, total_q * heads below 2^31, total_k below
+ *   2^31 - 255, n_seq * kv_heads at most 2^29.
  *   Strides count elements: q[t,h,d] = q[t*q_token + h*q_head + d], and so on
  *   (so q, k and v may be parts of one projection's output); not negative.
  *   The rows of out must not overlap each other.  lse is [total_q, heads], or

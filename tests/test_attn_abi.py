@@ -116,6 +116,11 @@ def test_sizes_that_cannot_be_counted(lib):
     for f32 in (False, True):
         assert call(lib, attn(n_seq=(1 << 28) + 1), q=far[0], k=far[1], v=far[2], cu_q=far[3], cu_k=far[4],
                     out=far[5], ws=far[6], f32=f32) == INVALID
+        # a tile's last key must be an int
+        for keys in (2 ** 31 - 255, 2 ** 31 - 1, 2 ** 31):
+            assert call(lib, attn(total_k=keys), q=far[0], k=far[1], v=far[2], out=far[5], ws=far[6],
+                        ws_bytes=1 << 42, f32=f32) == INVALID
+    assert lib.comp_attn_workspace_bytes(attn(total_k=2 ** 31 - 256), 4, P(far[0]), P(far[1])) > 0
 
 
 def test_page_arguments(lib):
