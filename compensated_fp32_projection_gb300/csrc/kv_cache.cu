@@ -233,15 +233,20 @@ __global__ void __launch_bounds__(kCopyThreads) fork_copy_kernel(Tables t, comp_
     if (!enough || f.parent < 0 || f.rest == 0)
         return;
     const int32_t src = t.table[f.parent * t.width + f.full], dst = t.table_out[children[i] * t.width + f.full];
-    if (src < 0 || src >= t.pages || dst < 0 || dst >= t.pages)
+    if (dst < 0 || dst >= t.pages)
         return;
+    const bool there = src >= 0 && src < t.pages;  // if not it reads as zeros, and so must its copy
     const int64_t head = static_cast<int64_t>(t.page_size) * cache.head_dim / 8;  // uint4s
     for (int u = cta; u < 2 * cache.kv_heads; u += ctas) {
         uint4* const base = reinterpret_cast<uint4*>(u < cache.kv_heads ? cache.k : cache.v);
         const int64_t h = u < cache.kv_heads ? u : u - cache.kv_heads;
-        copy16(base + (src * static_cast<int64_t>(cache.kv_heads) + h) * head,
-               base + (dst * static_cast<int64_t>(cache.kv_heads) + h) * head,
-               static_cast<int64_t>(f.rest) * cache.head_dim / 8, 0, 1);
+        uint4* const to = base + (dst * static_cast<int64_t>(cache.kv_heads) + h) * head;
+        const int64_t n = static_cast<int64_t>(f.rest) * cache.head_dim / 8;
+        if (there)
+            copy16(base + (src * static_cast<int64_t>(cache.kv_heads) + h) * head, to, n, 0, 1);
+        else
+            for (int64_t i = threadIdx.x; i < n; i += blockDim.x)
+                to[i] = make_uint4(0, 0, 0, 0);
     }
 }
 

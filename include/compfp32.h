@@ -451,8 +451,9 @@ comp_status_t comp_attn_decode_f32x16(const comp_kv_cache_t* cache, const float*
  * of those it has (a row's pages are its leading entries that are not -1).
  * comp_kv_fork — make row children[i] a copy of row parents[i], i < n: full
  * pages are shared (refs + 1); a last page that is partly filled is copied to
- * a free page, its filled tokens only.  The children's rows must be distinct,
- * empty before, and no parents.  n is at most 32768.
+ * a free page, its filled tokens only (zeros if it is not there).  The
+ * children's rows must be distinct, empty before, and no parents.  n is at
+ * most 32768.
  * Both write left[0] = free pages left; where there are not enough, left[0]
  * is minus the number missing and nothing else changes (the *_out arrays get
  * what was there before).

@@ -8,6 +8,8 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
+from attn_check import check_decode  # noqa: E402
+
 
 @pytest.fixture(scope="module")
 def pkg():
@@ -129,6 +131,25 @@ def test_numbers_out_of_range_are_not_followed(pkg):
     assert torch.equal(bits(k), bits(kx))
     t4, _, _, live = pkg.comp_kv_compact(k, v, t, r)
     assert t4.tolist() == [[-1] * 3] * 3 and live.tolist() == [0]
+
+
+@pytest.mark.parametrize("gone", [-1, 77])
+def test_fork_of_a_page_that_is_not_there(pkg, gone):
+    """Such a page reads as zeros; the child's own copy of it must too."""
+    page, rest = 32, 9
+    k, v = pool(6, 2, page, 64)
+    t, n, r = ints([[4, gone], [-1, -1]]), ints([page + rest, 0]), ints([0, 0, 0, 0, 1, 0])
+    kx, vx = k.clone(), v.clone()
+    kx[0, :, :rest] = 0
+    vx[0, :, :rest] = 0
+    q = torch.randn(2, 4, 64, device="cuda")
+    q[1] = q[0]
+    t2, n2, r2, left = pkg.comp_kv_fork(k, v, t, n, r, ints([0]), ints([1]))
+    assert t2.tolist() == [[4, gone], [4, 0]] and r2.tolist() == [1, 0, 0, 0, 2, 0] and left.tolist() == [4]
+    assert torch.equal(bits(k), bits(kx)) and torch.equal(bits(v), bits(vx))
+    lse = torch.empty(2, 4, device="cuda")
+    out = pkg.comp_attn_decode_f32x16(q, k, v, t2, n2, lse=lse)
+    check_decode(out, lse, q, kx, vx, t2, n2, 64 ** -0.5)
 
 
 @pytest.mark.parametrize("pages", [1, 7, 300, 2048, 5000, 20011])
