@@ -178,6 +178,22 @@ def check_largest(out, lse, q, k, v, seen):
     assert bool(((lse[:, 0].double() - top).abs() <= 4e-6 * top.abs()).all())
 
 
+@pytest.mark.parametrize("n,dim", [(300, 64), (300, 128), (1100, 128)])
+@pytest.mark.parametrize("size", [1e-5, 1e-7, 1e-9])
+def test_small_values(pkg, n, dim, size):
+    """A split value is off by at most 2^-22 of it or 2^-35, whichever is more: in v the
+    2^-35 reach the output as they are, in q and k scores that are next to nothing."""
+    from attn_check import compare, exact_rows
+
+    q, k, v = case([n], [n], 1, 1, dim, torch.float32, seed=19)
+    for q2, k2, v2 in ((q, k, v * size), (q * size, k, v), (q, k * size, v)):
+        out, lse = (x.cpu()[:, 0] for x in call(pkg, q2, k2, v2, [0, n], [0, n], False))
+        qc, kc, vc = (x.cpu()[:, 0] for x in (q2, k2, v2))
+        x_out, x_lse, tol, ltol = exact_rows(qc, kc, vc, torch.ones(n, n, dtype=torch.bool), dim ** -0.5)
+        e = 2.0 ** -35 * dim ** -0.5 * float(torch.maximum(qc.abs().sum(1).max(), kc.abs().sum(1).max()))
+        compare(out, lse, x_out, x_lse, tol + 2.0 ** -35 + 2 * math.expm1(e) * float(vc.abs().max()), ltol + e)
+
+
 @pytest.mark.parametrize("kv", KV, ids=["f16", "f32"])
 @pytest.mark.parametrize("n,dim", [(300, 64), (300, 128), (1100, 128)])
 @pytest.mark.parametrize("unit", [1, -1, 32, -32])
@@ -642,6 +658,88 @@ def test_nothing_to_do(pkg):
     q, k, v = case([3], [0], 4, 2, 64, torch.float32)
     lse = torch.empty(3, 4, device="cuda")
     assert bool((pkg.comp_attn_f32(q, k, v, lse=lse) == 0).all()) and bool(lse.isneginf().all())
+
+
+# --------------------------------------------------------------------------
+# a workspace of the caller's, and the error's norm
+# --------------------------------------------------------------------------
+def with_workspace(need, call_it):
+    """Exactly `need` bytes between guards, at a 16-byte boundary; nothing beyond them
+    changes, fewer or misaligned ones are refused."""
+    import compensated_fp32_projection_gb300 as p
+
+    assert need > 0
+    place = torch.full((need + 512,), 0x5a, dtype=torch.uint8, device="cuda")
+    got = call_it(place[240:240 + need])
+    assert bool((place[:240] == 0x5a).all()) and bool((place[240 + need:] == 0x5a).all())
+    for bad in (place[240:240 + need - 1], place[244:244 + need]):
+        with pytest.raises(p.CompError):
+            call_it(bad)
+    return got
+
+
+@pytest.mark.parametrize("lens,heads,kv_heads,dim", [([1], 1, 1, 1), ([150, 37], 6, 2, 72), ([1100, 1200], 2, 1, 128),
+                                                     ([513], 4, 4, 64)], ids=str)
+@pytest.mark.parametrize("kv", KV, ids=["f16", "f32"])
+def test_packed_workspace(pkg, lens, heads, kv_heads, dim, kv):
+    import ctypes
+
+    q, k, v = case(lens, lens, heads, kv_heads, dim, kv, seed=15)
+    if kv == torch.float16:  # rows that the kernel cannot load where they are
+        k, v = (torch.nn.functional.pad(x, (1, 0))[..., 1:] for x in (k, v))
+    cu = cu_of(lens)
+    want, want_lse = call(pkg, q, k, v, cu, cu, True)
+    a = pkg._native.Attn(len(lens), q.shape[0], k.shape[0], heads, kv_heads, dim, 1, 0.5, *q.stride()[:2],
+                         *k.stride()[:2], *v.stride()[:2], *want.stride()[:2])
+    need = pkg._native.load().comp_attn_workspace_bytes(ctypes.byref(a), k.element_size(), k.data_ptr(), v.data_ptr())
+    out, lse = with_workspace(need, lambda ws: call(pkg, q, k, v, cu, cu, True, workspace=ws))
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("shared,page,batch,heads,kv_heads,dim", [
+    (0, 16, 3, 4, 2, 64), (0, 64, 9, 32, 2, 128), (5, 16, 40, 4, 2, 64), (64, 128, 33, 4, 2, 64),
+    (100, 32, 3, 8, 2, 128), (9, 64, 70, 40, 1, 72), (300, 16, 128, 2, 2, 8)])
+def test_decode_workspace(pkg, shared, page, batch, heads, kv_heads, dim):
+    import ctypes
+
+    lengths = [shared * page + (97 * i) % 3000 for i in range(batch)]
+    q, k, v, table, n = cache_case(lengths, shared, page, heads, kv_heads, dim, seed=16)
+    want, want_lse = decode(pkg, q, k, v, table, n, shared)
+    c = pkg._native.KvCache(k.data_ptr(), v.data_ptr(), k.shape[0], page, kv_heads, dim)
+    need = pkg._native.load().comp_attn_decode_workspace_bytes(ctypes.byref(c), batch, heads, table.shape[1], shared)
+    out, lse = with_workspace(need, lambda ws: decode(pkg, q, k, v, table, n, shared, workspace=ws))
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+# The error's norm: a score loses at most 2^-22 of each product by the split of q (and of
+# k) and a weight 2^-22, each with a sign of its own, and FP32 sums of up to 128 terms
+# and the exponential 2^-22 each: some 1e-6 of the output's norm.  An operand without its
+# lo half loses 2^-11, 3e-4 on average; 4e-6, what the projections hold, lies between.
+NORM = 4e-6
+
+
+@pytest.mark.parametrize("kv", KV, ids=["f16", "f32"])
+@pytest.mark.parametrize("n,heads,kv_heads,dim", [(900, 4, 2, 64), (900, 4, 2, 128), (2300, 2, 1, 128)])
+def test_norm_of_the_error(pkg, kv, n, heads, kv_heads, dim):
+    q, k, v = case([n], [n], heads, kv_heads, dim, kv, seed=17, q_scale=1.0)
+    out, _ = call(pkg, q, k, v, [0, n], [0, n], False)
+    kd, vd = (x.double().repeat_interleave(heads // kv_heads, 1) for x in (k, v))
+    want = torch.einsum("hnm,mhd->nhd", (torch.einsum("nhd,mhd->hnm", q.double(), kd) * dim ** -0.5).softmax(-1), vd)
+    assert float((out - want).norm() / want.norm()) < NORM
+
+
+@pytest.mark.parametrize("shared", [0, 20])
+@pytest.mark.parametrize("heads,kv_heads,dim", [(8, 2, 64), (16, 1, 128)])
+def test_norm_of_the_error_decode(pkg, shared, heads, kv_heads, dim):
+    q, k, v, table, n = cache_case([2000] * 8, shared, 64, heads, kv_heads, dim, seed=18)
+    out, _ = decode(pkg, q / 2, k, v, table, n, shared)
+    want = torch.empty_like(out, dtype=torch.float64)
+    for b in range(8):
+        kd, vd = (x[table[b, :32].long()].transpose(1, 2).flatten(0, 1)[:2000].double().repeat_interleave(
+            heads // kv_heads, 1) for x in (k, v))
+        p = (torch.einsum("hd,mhd->hm", q[b].double() / 2, kd) * dim ** -0.5).softmax(-1)
+        want[b] = torch.einsum("hm,mhd->hd", p, vd)
+    assert float((out - want).norm() / want.norm()) < NORM
 
 
 # --------------------------------------------------------------------------
