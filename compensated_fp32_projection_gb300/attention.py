@@ -45,6 +45,8 @@ def comp_attn_f32(q, k, v, cu_q=None, cu_k=None, *, scale=None, causal=True, out
     head strides.  Sequence i has the queries cu_q[i]:cu_q[i+1] and the keys
     cu_k[i]:cu_k[i+1] (int32; without them there is one sequence).  causal: the
     last query sees every key of its sequence, each earlier one a key less.
+    Magnitudes stay below 65520; float32 values below 1e-4 enter with an absolute
+    error of 2^-35 (float16 keys and values are exact).
     scale defaults to head_dim ** -0.5.  lse, if given ([tokens, heads]),
     receives the log-sum-exp of each row.  A row that sees no key gives zeros
     and -inf, as do the tokens beyond the last sequence."""
@@ -59,7 +61,7 @@ def comp_attn_f32x16(q, k, v, cu_q=None, cu_k=None, *, scale=None, causal=True, 
 
 def comp_kv_append_f32(k, v, k_pages, v_pages, table, start, cu=None, stream=None):
     """Write new tokens' float32 k, v [tokens, kv_heads, head_dim] into the cache
-    (rounded to float16).  Row r's tokens cu[r]:cu[r+1] (without cu: one for each
+    (rounded to float16, beyond its range to infinities).  Row r's tokens cu[r]:cu[r+1] (without cu: one for each
     row) go to positions start[r], start[r] + 1, ... of its pages."""
     _b.append(k, v, k_pages, v_pages, table, start, cu, stream)
 
@@ -76,8 +78,8 @@ def comp_attn_decode_f32x16(q, k_pages, v_pages, table, lengths, *, shared=0, sc
 
 
 def comp_kv_reserve(table, want, refs, page_size, table_out=None, refs_out=None, left=None, stream=None):
-    """Give row r of table the pages that want[r] tokens need, lowest free page
-    first.  Returns (table, refs, left), new tensors unless given (the inputs
+    """Give row r of table the pages that want[r] tokens need (at most as many as
+    the table is wide), lowest free page first.  Returns (table, refs, left), new tensors unless given (the inputs
     themselves may be given: updated in place).  left[0] is the number of free
     pages that remain; where it is negative that many are missing and nothing
     was changed."""

@@ -46,7 +46,8 @@ bool attn_ok(const comp_attn_t* a, int kv_bytes, AttnBytes* b)
     if (!a || a->n_seq < 0 || a->n_seq > INT32_MAX || a->total_q < 0 || a->total_q > INT32_MAX || a->total_k < 0 ||
         a->total_k > kMostAttnKeys || a->heads <= 0 || a->kv_heads <= 0 || a->heads > 65535 ||
         a->heads % a->kv_heads != 0 || a->head_dim < 1 || a->head_dim > 128 || !std::isfinite(a->scale) ||
-        !(a->scale > 0.0f) || a->total_q * a->heads > INT32_MAX || a->n_seq * a->kv_heads > kMostAttnUnits)
+        !(a->scale > 0.0f) || a->total_q * a->heads > INT32_MAX ||
+        a->n_seq * a->kv_heads > kMostAttnUnits)
         return false;
     if (!strided_bytes(a->total_q, a->heads, a->head_dim, a->q_token, a->q_head, 4, &b->q) ||
         !strided_bytes(a->total_k, a->kv_heads, a->head_dim, a->k_token, a->k_head, kv_bytes, &b->k) ||
@@ -85,7 +86,8 @@ comp_status_t attn(const comp_attn_t* a, const float* q, const void* k, const vo
     const comp_status_t st = current_device(&dev);
     if (st != COMP_OK)
         return st;
-    return launch_attn(seen, q, k, v, kv_bytes, cu_q, cu_k, out, lse, workspace, dev, static_cast<cudaStream_t>(stream));
+    return launch_attn(seen, q, k, v, kv_bytes, cu_q, cu_k, out, lse, workspace, dev,
+                       static_cast<cudaStream_t>(stream));
 }
 
 bool decode_ok(const comp_kv_cache_t* c, int64_t batch, int32_t heads, int64_t width, int64_t shared_pages,

@@ -1,6 +1,6 @@
 // Attention of single tokens over a paged FP16 cache: each key and value of a
-// sequence is read once for the query heads that share it, 4 D bytes for 4 D
-// operations a head, so the bound is HBM.
+// sequence is read once for up to 16 query heads that share it (once more for each
+// further 16), 4 D bytes for 4 D operations a head, so the bound is HBM.
 //
 // Tensor cores.  The m16n8k16 product has room for 16 rows; up to eight query
 // heads of a key/value head come in twice, rows 0..7 hi = fp16(x) and rows
@@ -669,10 +669,9 @@ comp_status_t launch_t(const CUtensorMap& mk, const CUtensorMap& mv, const Param
 // workspace's size must not depend on the device, so their number is bounded.
 constexpr int kMostPieces = 320 * kWarps;
 // Beside a prefix's kernel the CTAs start as SMs become free, and pieces half as
-// long fill its end better, where they are still long enough: measured when the
-// prefix's kernel was slower, 256 sequences on a 32768-token prefix took 223 us
-// instead of 237 (a third as long: 226), but 64 short ones on 8192 tokens 42
-// instead of 40.  Without a prefix all pieces start together, and
+// long fill its end better, where they are still long enough: 256 sequences on a
+// 32768-token prefix take 211 us instead of 230, 64 short ones on 8192 tokens 34.0
+// instead of 34.3.  Without a prefix all pieces start together, and
 // two waves of them cost 77 us where one takes 69 (48 ragged sequences).
 constexpr int kPrefixWaves = 2;  // the kernel tells the second by one comparison
 
@@ -681,7 +680,7 @@ constexpr int kPrefixWaves = 2;  // the kernel tells the second by one compariso
 // least four tiles: 24.9 us instead of 21.1 for 8 sequences on 512 tokens).
 // Where tiles are left then for twice as many parts, and a CTA has rows for one
 // half only, each half takes a part of its own (64 sequences on 8192 tokens, 16
-// heads of 64: 39.9 -> 36.1 us).  Heads wider than 64 gain nothing: their ring
+// heads of 64: 37.8 -> 34.0 us).  Heads wider than 64 gain nothing: their ring
 // holds three tiles, too few for two halves apart (45.8 us against 44.7 with
 // 16 rows on 16384 tokens).
 constexpr int kLeastTiles = 2;

@@ -23,7 +23,9 @@
 //   O' = P v          of this tile alone, into a fresh accumulator; added in
 //                     FP32 registers, o = o 2^(m_old - m_new) + O'.  The tensor
 //                     cores' own sums so never run over more than BN keys, and
-//                     rescaling costs the multiply of that addition.
+//                     rescaling costs the multiply of that addition.  One rounding
+//                     a tile: 2^-24 at most for each BN keys, and that only where
+//                     all of them go one way.
 //
 // Two products for FP16 keys and values, three for FP32 ones: the floor is
 // 4 D operations for each visible pair and product, at the tensor cores' FP16
@@ -31,8 +33,8 @@
 // half.  S is overwritten in place by P (128 columns of 32 bits: hi and lo
 // pairs), which the second product reads from tensor memory.  Measured: 16384
 // causal tokens, 32 heads of 128 over 8 of FP16 keys, 2.26 ms, 1.94 PFLOP/s of
-// products; 4096 FP32 tokens, 32 heads, 329 us, 1.25 PFLOP/s; 24 prompts of 23
-// to 2011 tokens, 235 us, 1.05 PFLOP/s, where nearly half of a CTA's time passes
+// products; 4096 FP32 tokens, 32 heads, 333 us, 1.24 PFLOP/s; 24 prompts of 23
+// to 2011 tokens, 238 us, 1.04 PFLOP/s, where nearly half of a CTA's time passes
 // before its first product and after its last.
 //
 // Warps: 0 loads tiles of k and v (TMA, a ring of stages), 1 and 2 issue the
@@ -88,10 +90,11 @@ struct Cfg {
     // 64 KB a stage beside the 128 KB of q: 64 keys leave three stages to one
     // CTA.  Products of 64 columns are bound by the shared memory that feeds
     // them (49 cycles instead of 32), so that a pair, which has room for 128,
-    // takes 271 us where one CTA takes 322 (4096 FP32 tokens, 16 heads of 128;
-    // causal, 32 heads: 326 against 351, 1024 tokens of them 61 against 64, 512
-    // tokens 36.4 against 36.2).  Its blocks of 512 rows want long sequences: it
-    // is used from 1024 rows on average on.
+    // takes 265 us where one CTA takes 321 (4096 FP32 tokens, 16 heads of 128, one
+    // sequence without offsets; causal, 32 heads: 323 against 349, 1024 tokens of
+    // them 58 against 62; in blocks of 512 rows 512 tokens took 36.4 against 36.2).
+    // Its blocks of 512 rows want long sequences: it is used from 1024 rows on
+    // average on.
     static constexpr int BN = DP == 128 && PL == 2 && !PAIR_ ? 64 : 128;
     static constexpr int kBoxes = DP / 64;                      // 64-wide boxes along D
     static constexpr uint32_t kQTile = 128 * DP * 2;            // one plane of one half

@@ -331,9 +331,18 @@ comp_status_t comp_gemm_f32x16_noalloc(const float* x, const uint16_t* W, float*
  * and outputs are binary32.  The products follow the method of the
  * projections: a binary32 operand enters the FP16 tensor cores as two binary16
  * values, and accumulators are FP32.  q and k must therefore stay below 65520
- * in magnitude, and v too (larger values give NaN).  A key that a row may not see
- * has no influence on it, whatever k and v hold there (infinities and NaN
- * included).
+ * in magnitude, and v too (larger values give NaN).  At the lower end a binary32
+ * value enters with an error of up to 2^-22 of it or 2^-35, whichever is more:
+ * values below 2^-13 (1e-4) lose bits, v of size 1e-6 keeps some 2e-5 of itself
+ * (binary16 values are exact).  A key that a row may not see has no influence on
+ * it, whatever k and v hold there (infinities and NaN included).  Where a row
+ * does see an infinity or a NaN in v, that component of its output is infinite
+ * or NaN, which of the two is not defined; in k, the whole row may be NaN.
+ * Sums over keys are rounded once for each 128 keys (packed prompts and shared
+ * prefixes), or once for each 16 in runs of 1024 and once for each run (a
+ * sequence's own pages).  Where all roundings go one way, as they can over
+ * identical keys and values, out may so be off by 2^-24 for each 128 keys, or by
+ * 2^-18 and 2^-24 for each 1024, beside what the products lose.
  *
  * comp_attn_t describes whole prompts packed one after the other:
  *   n_seq sequences; queries cu_q[i] .. cu_q[i+1]-1 of the total_q packed
@@ -377,7 +386,8 @@ int64_t comp_attn_workspace_bytes(const comp_attn_t* a, int kv_bytes, const void
  * scale outside the above, a needed pointer that is NULL, only one of cu_q and
  * cu_k, n_seq > 1 without them, a workspace that is smaller than
  * comp_attn_workspace_bytes or not 16-byte aligned where one is needed, or
- * out, lse or the workspace overlapping an input or each other.
+ * out, lse or the workspace overlapping an input or each other (from the first
+ * to the last element of each, whatever lies between their rows).
  */
 comp_status_t comp_attn_f32x16(const comp_attn_t* a, const float* q, const uint16_t* k, const uint16_t* v,
                                const int32_t* cu_q, const int32_t* cu_k, float* out, float* lse, void* workspace,
@@ -409,10 +419,10 @@ typedef struct comp_kv_cache {
 /*
  * comp_kv_append_f32 — write new tokens: k and v are binary32 [total, kv_heads,
  * head_dim] with token and head strides, rounded to binary16 (to nearest, ties
- * to even).  Row r's tokens are cu[r] .. cu[r+1]-1 (cu NULL: total == rows, one
- * token each) and go to positions start[r], start[r]+1, ... of its sequence,
- * whose pages the table must already list (see comp_kv_reserve).  lengths are
- * the caller's to advance.
+ * to even; magnitudes of 65520 and more become infinities).  Row r's tokens are
+ * cu[r] .. cu[r+1]-1 (cu NULL: total == rows, one token each) and go to
+ * positions start[r], start[r]+1, ... of its sequence, whose pages the table
+ * must already list (see comp_kv_reserve).  lengths are the caller's to advance.
  */
 comp_status_t comp_kv_append_f32(const comp_kv_cache_t* cache, const float* k, const float* v, int64_t k_token,
                                  int64_t k_head, int64_t v_token, int64_t v_head, int64_t total,
@@ -448,7 +458,9 @@ comp_status_t comp_attn_decode_f32x16(const comp_kv_cache_t* cache, const float*
  * order of the requests, so results never depend on timing.
  *
  * comp_kv_reserve — give row r the pages that want[r] tokens need, at the end
- * of those it has (a row's pages are its leading entries that are not -1).
+ * of those it has (a row's pages are its leading entries that are not -1; only
+ * -1 may follow them).  More tokens than width pages hold are taken as that
+ * many.  rows is at most 16384, rows * width below 2^31.
  * comp_kv_fork — make row children[i] a copy of row parents[i], i < n: full
  * pages are shared (refs + 1); a last page that is partly filled is copied to
  * a free page, its filled tokens only (zeros if it is not there).  The
