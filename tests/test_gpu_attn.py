@@ -536,6 +536,22 @@ def test_decode_pages_that_are_not_there(pkg, shared):
     check_decode(out, lse, q, k, v, table, n, 64 ** -0.5)
 
 
+@pytest.mark.parametrize("heads,kv_heads,dim", [(8, 8, 64), (8, 8, 128), (96, 8, 64), (72, 8, 128), (8, 8, 72)])
+def test_decode_many_long_rows_in_a_piece(pkg, heads, kv_heads, dim):
+    """A warp's piece of the line has several rows of more than a run of tiles."""
+    batch, pool, page = 1200, 48, 64
+    g = torch.Generator().manual_seed(dim)
+    k, v = (torch.randn(pool, kv_heads, page, dim, generator=g).half() for _ in range(2))
+    table = torch.randint(0, pool, (batch, 80), generator=g, dtype=torch.int32)
+    lengths = torch.randint(0, 80 * page + 1, (batch,), generator=g, dtype=torch.int32)
+    q = torch.randn(batch, heads, dim, generator=g) * 2
+    out, lse = decode(pkg, q.cuda(), k.cuda(), v.cuda(), table.cuda(), lengths.cuda())
+    some = torch.arange(7, batch, 199)
+    check_decode(out[some.cuda()], lse[some.cuda()], q[some], k, v, table[some], lengths[some], dim ** -0.5)
+    again, again_lse = decode(pkg, q.cuda(), k.cuda(), v.cuda(), table.cuda(), lengths.cuda())
+    assert torch.equal(again, out) and torch.equal(again_lse, lse)
+
+
 def test_decode_strided_queries_and_stream(pkg):
     q, k, v, table, n = cache_case([77, 300, 5], 0, 16, 4, 2, 64, seed=6)
     wide = torch.randn(3, 9, 64, device="cuda")
