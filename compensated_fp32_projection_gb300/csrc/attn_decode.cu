@@ -412,11 +412,11 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1)
                     a2[nb] = f2_bits(alpha, alpha);
                     // 2^14 p; the product rounded as the maximum is, or large scores would not
                     // end at 0 (see the packed kernel; a branch for them instead took 72 us
-                    // where this takes 69: 16 sequences of 16000 tokens, 40 heads over 1 of 128)
+                    // where this takes 68: 16 sequences of 16000 tokens, 40 heads over 1 of 128)
                     float w[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        w[e] = ex2(__fsub_rn(__fmul_rn(x[e], c2), shift)) * kAttnPScale;
+                        w[e] = ex2(__fadd_rn(__fsub_rn(__fmul_rn(x[e], c2), shift), 14.0f));
                     split_p(w[0], w[1], pa[nb][0], pa[nb][1]);
                     split_p(w[2], w[3], pa[nb][2], pa[nb][3]);
                     l2[nb] = fma2(l2[nb], a2[nb], add2(f2_bits(w[0], w[1]), f2_bits(w[2], w[3])));
