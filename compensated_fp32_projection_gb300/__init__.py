@@ -40,11 +40,20 @@ __all__ = [
     "comp_kv_free",
     "comp_kv_compact",
     "comp_kv_copy_pages",
+    "comp_rope_table",
+    "comp_rope_f32",
+    "comp_kv8_append_f32",
+    "comp_kv8_read_f32",
+    "comp_kv8_read_f16",
+    "comp_attn_decode_f32x8",
+    "comp_kv8_fork",
+    "comp_kv8_compact",
+    "comp_kv8_copy_pages",
     "device_status",
     "status_string",
 ]
 
-_ATTENTION = ("comp_attn_", "comp_kv_")
+_ATTENTION = ("comp_attn_", "comp_kv_", "comp_kv8_", "comp_rope_")
 
 
 def __getattr__(name):

@@ -24,7 +24,7 @@ COMP_ERR_CUDA = 6
 
 # Every symbol the header declares, with its ctypes signature.
 _i64, _int, _u32, _vp = ctypes.c_int64, ctypes.c_int, ctypes.c_uint32, ctypes.c_void_p
-_i32, _f32 = ctypes.c_int32, ctypes.c_float
+_i32, _f32, _f64 = ctypes.c_int32, ctypes.c_float, ctypes.c_double
 
 
 class Attn(ctypes.Structure):
@@ -39,6 +39,25 @@ class KvCache(ctypes.Structure):
     """comp_kv_cache_t"""
 
     _fields_ = [("k", _vp), ("v", _vp), ("pages", _i64), ("page_size", _i32), ("kv_heads", _i32), ("head_dim", _i32)]
+
+
+class Rope(ctypes.Structure):
+    """comp_rope_t"""
+
+    _fields_ = [("table", _vp), ("positions", _i64), ("rot", _i32), ("interleaved", _i32)]
+
+
+class RopeAngles(ctypes.Structure):
+    """comp_rope_angles_t"""
+
+    _fields_ = [(n, _f64) for n in ("base", "factor", "context", "low", "high", "magnitude")]
+
+
+class Kv8Cache(ctypes.Structure):
+    """comp_kv8_cache_t"""
+
+    _fields_ = [(n, _vp) for n in ("k", "v", "k_scale", "v_scale")] + [("pages", _i64)] + [
+        (n, _i32) for n in ("page_size", "kv_heads", "head_dim")]
 
 
 SIGNATURES = {
@@ -68,6 +87,17 @@ SIGNATURES = {
     "comp_kv_free": (_int, [_i64, _vp, _vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp]),
     "comp_kv_compact": (_int, [_vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
     "comp_kv_copy_pages": (_int, [_vp, _vp, _vp, _i64, _vp]),
+    "comp_rope_table": (_int, [_vp, _i32, _i64, _i64, _vp, _vp]),
+    "comp_rope_f32": (_int, [_vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp, _int, _vp, _i64, _i64, _vp]),
+    "comp_kv8_append_f32": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp]),
+    "comp_kv8_read_f32": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp]),
+    "comp_kv8_read_f16": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp]),
+    "comp_attn_decode_f32x8_workspace_bytes": (_i64, [_vp, _i64, _i32, _i64]),
+    "comp_attn_decode_f32x8": (_int, [_vp, _vp, _i64, _i64, _i32, _f32, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp,
+                                      _i64, _vp]),
+    "comp_kv8_fork": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "comp_kv8_compact": (_int, [_vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "comp_kv8_copy_pages": (_int, [_vp, _vp, _vp, _i64, _vp]),
     "comp_device_status": (_int, [_vp, ctypes.POINTER(_u32)]),
     "comp_check_wait_timeout": (_int, [_vp]),
     "comp_check_stalled_pipeline": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp]),

@@ -8,7 +8,11 @@ and nothing waits for the host.  Outputs that are not given are allocated.
 
 Caches are pairs of float16 tensors ``k_pages``, ``v_pages``
 [pages, kv_heads, page_size, head_dim]; a page table is an int32 tensor
-[rows, width] whose unused entries are -1.
+[rows, width] whose unused entries are -1.  8-bit caches (``comp_kv8_...``) are
+pairs of int8 tensors of that shape with a float32 scale for each 16 tokens of a
+head, ``k_scales``, ``v_scales`` [pages, kv_heads, page_size / 16].
+Rotary positions come from a float32 table [positions, rot / 2, 2] of cosines and
+sines, as comp_rope_table makes it.
 """
 from __future__ import annotations
 
@@ -34,6 +38,15 @@ __all__ = [
     "comp_kv_free",
     "comp_kv_compact",
     "comp_kv_copy_pages",
+    "comp_rope_table",
+    "comp_rope_f32",
+    "comp_kv8_append_f32",
+    "comp_kv8_read_f32",
+    "comp_kv8_read_f16",
+    "comp_attn_decode_f32x8",
+    "comp_kv8_fork",
+    "comp_kv8_compact",
+    "comp_kv8_copy_pages",
 ]
 
 
@@ -113,3 +126,74 @@ def comp_kv_compact(k_pages, v_pages, table, refs, table_out=None, refs_out=None
 def comp_kv_copy_pages(k_pages, v_pages, src, dst, stream=None):
     """Copy page src[i] of the cache to page dst[i]; the dst are distinct and no src."""
     _b.copy_pages(k_pages, v_pages, src, dst, stream)
+
+
+def comp_rope_table(positions, rot, *, base=10000.0, factor=1.0, context=0.0, low=1.0, high=32.0, magnitude=1.0,
+                    first=0, table=None, device="cuda", stream=None):
+    """The rotary table [positions, rot / 2, 2] of positions first, first + 1, ...:
+    magnitude times the cosine and sine of p a_i, in 64 bits, rounded once.
+
+    a_i = base^(-2 i / rot) / factor; with a context (the positions that a model was
+    trained on) only pairs of fewer than `low` turns over it are divided by factor,
+    those of more than `high` are not, and what lies between is blended."""
+    return _b.rope_table(positions, rot, base, factor, context, low, high, magnitude, first, table, device, stream)
+
+
+def comp_rope_f32(x, table, positions=None, *, interleaved=False, inverse=False, out=None, stream=None):
+    """Rotate x [tokens, heads, head_dim] float32 (any token and head strides): the
+    pairs (i, i + rot / 2) of each head's first rot dimensions, or (2 i, 2 i + 1)
+    with interleaved; the other dimensions stay.  Token t is at positions[t] (int32;
+    without them at t); one that the table does not have gives NaN.  inverse turns
+    back, which is also the call's gradient.  out may be x itself."""
+    return _b.rope(x, table, positions, interleaved, inverse, out, stream)
+
+
+def comp_kv8_append_f32(k, v, k_pages, v_pages, k_scales, v_scales, table, start, cu=None, *, rope=None,
+                        interleaved=False, stream=None):
+    """comp_kv_append_f32 into an 8-bit cache: each value becomes the nearest of 255
+    steps of its block's scale, the largest magnitude / 127; the tokens that are in
+    the block already are rounded again where that grows.  An infinity or a NaN
+    reads back as NaN and costs its neighbours nothing.  rope, a rotary table,
+    rotates the keys on the way, each at its position in its sequence (interleaved
+    as in comp_rope_f32)."""
+    _b.append8(k, v, k_pages, v_pages, k_scales, v_scales, table, start, cu, rope, interleaved, stream)
+
+
+def comp_kv8_read_f32(k_pages, v_pages, k_scales, v_scales, table, start, cu, total, *, k=None, v=None, stream=None):
+    """Read tokens back: (k, v) [total, kv_heads, head_dim] float32 (new unless
+    given; any token and head strides), tokens cu[r]:cu[r+1] from positions start[r],
+    start[r] + 1, ... of row r (cu None: one token for each row), so that packed
+    attention can see a sequence's past.  Zeros where there is no page, and behind
+    the last sequence."""
+    return _b.read8(True, k_pages, v_pages, k_scales, v_scales, table, start, cu, total, k, v, stream)
+
+
+def comp_kv8_read_f16(k_pages, v_pages, k_scales, v_scales, table, start, cu, total, *, k=None, v=None, stream=None):
+    """comp_kv8_read_f32 into float16 keys and values."""
+    return _b.read8(False, k_pages, v_pages, k_scales, v_scales, table, start, cu, total, k, v, stream)
+
+
+def comp_attn_decode_f32x8(q, k_pages, v_pages, k_scales, v_scales, table, lengths, *, rope=None, interleaved=False,
+                           scale=None, out=None, lse=None, workspace=None, stream=None):
+    """comp_attn_decode_f32x16 over an 8-bit cache (no shared prefix).  rope, a
+    rotary table, rotates each query at its sequence's last position."""
+    return _b.decode8(q, k_pages, v_pages, k_scales, v_scales, table, lengths, rope, interleaved, scale, out, lse,
+                      workspace, stream)
+
+
+def comp_kv8_fork(k_pages, v_pages, k_scales, v_scales, table, lengths, refs, parents, children, table_out=None,
+                  lengths_out=None, refs_out=None, left=None, stream=None):
+    """comp_kv_fork of an 8-bit cache."""
+    return _b.fork8(k_pages, v_pages, k_scales, v_scales, table, lengths, refs, parents, children, table_out,
+                    lengths_out, refs_out, left, stream)
+
+
+def comp_kv8_compact(k_pages, v_pages, k_scales, v_scales, table, refs, table_out=None, refs_out=None, remap=None,
+                     live=None, stream=None):
+    """comp_kv_compact of an 8-bit cache."""
+    return _b.compact8(k_pages, v_pages, k_scales, v_scales, table, refs, table_out, refs_out, remap, live, stream)
+
+
+def comp_kv8_copy_pages(k_pages, v_pages, k_scales, v_scales, src, dst, stream=None):
+    """comp_kv_copy_pages of an 8-bit cache."""
+    _b.copy_pages8(k_pages, v_pages, k_scales, v_scales, src, dst, stream)

@@ -2,17 +2,10 @@
 #include <cmath>
 
 #include "internal.h"
+#include "rope.cuh"
 
 namespace compfp32 {
 namespace {
-
-// Whether the rows of a [tokens, heads, dim] output do not overlap each other.
-bool rows_apart(int64_t tokens, int64_t heads, int64_t dim, int64_t token, int64_t head)
-{
-    return (tokens <= 1 && (heads <= 1 || head >= dim)) || (heads <= 1 && token >= dim) ||
-           (head >= dim && token >= (heads - 1) * head + dim) ||
-           (token >= dim && head >= (tokens - 1) * token + dim);
-}
 
 struct Range {
     const void* p;
@@ -90,13 +83,21 @@ comp_status_t attn(const comp_attn_t* a, const float* q, const void* k, const vo
                        static_cast<cudaStream_t>(stream));
 }
 
+// The sizes of a decode call over a cache of either type, which is checked already.
+template <typename Cache>
+bool decode_sizes_ok(const Cache* c, int64_t batch, int32_t heads, int64_t width, int64_t* entries)
+{
+    return batch >= 0 && heads > 0 && heads <= 65535 && heads % c->kv_heads == 0 &&
+           width >= 0 && width <= INT32_MAX / (2 * c->page_size) && mul_ok(batch, width, entries) &&
+           batch <= INT32_MAX / heads && *entries <= INT64_MAX / 8 &&
+           attn_decode_countable(c->kv_heads, c->page_size, batch, heads, width);
+}
+
 bool decode_ok(const comp_kv_cache_t* c, int64_t batch, int32_t heads, int64_t width, int64_t shared_pages,
                int64_t* bytes, int64_t* entries)
 {
-    return kv_cache_ok(c, bytes) && batch >= 0 && heads > 0 && heads <= 65535 && heads % c->kv_heads == 0 &&
-           width >= 0 && width <= INT32_MAX / (2 * c->page_size) && mul_ok(batch, width, entries) &&
-           batch <= INT32_MAX / heads && *entries <= INT64_MAX / 8 && shared_pages >= 0 && shared_pages <= width &&
-           attn_decode_countable(*c, batch, heads, width);
+    return kv_cache_ok(c, bytes) && decode_sizes_ok(c, batch, heads, width, entries) && shared_pages >= 0 &&
+           shared_pages <= width;
 }
 
 }  // namespace
@@ -165,6 +166,48 @@ comp_status_t comp_attn_decode_f32x16(const comp_kv_cache_t* cache, const float*
         return st;
     return launch_attn_decode(*cache, q, q_token, q_head, heads, scale, table, batch, width, lengths, shared_pages,
                               out, lse, workspace, dev, static_cast<cudaStream_t>(stream));
+}
+
+int64_t comp_attn_decode_f32x8_workspace_bytes(const comp_kv8_cache_t* cache, int64_t batch, int32_t heads,
+                                               int64_t width)
+{
+    int64_t bytes, scales, entries;
+    if (!kv8_cache_ok(cache, &bytes, &scales) || !decode_sizes_ok(cache, batch, heads, width, &entries) || batch == 0)
+        return 0;
+    return attn_decode8_bytes(*cache, heads);
+}
+
+comp_status_t comp_attn_decode_f32x8(const comp_kv8_cache_t* cache, const float* q, int64_t q_token, int64_t q_head,
+                                     int32_t heads, float scale, const int32_t* table, int64_t batch, int64_t width,
+                                     const int32_t* lengths, const comp_rope_t* rope, float* out, float* lse,
+                                     void* workspace, int64_t workspace_bytes, comp_stream_t stream)
+{
+    int64_t bytes, scales, entries, qb, rb;
+    if (!kv8_cache_ok(cache, &bytes, &scales) || !decode_sizes_ok(cache, batch, heads, width, &entries) ||
+        !std::isfinite(scale) || !(scale > 0.0f) || workspace_bytes < 0 ||
+        !strided_bytes(batch, heads, cache->head_dim, q_token, q_head, 4, &qb) ||
+        !rope_ok(rope, cache->head_dim, &rb))
+        return COMP_ERR_INVALID_VALUE;
+    if (batch == 0)
+        return COMP_OK;
+    if (!q || !lengths || !out || (entries > 0 && (!table || cache->pages == 0)))
+        return COMP_ERR_INVALID_VALUE;
+    const Range in[] = {{q, qb}, {cache->k, bytes}, {cache->v, bytes}, {cache->k_scale, scales},
+                        {cache->v_scale, scales}, {table, 4 * entries}, {lengths, 4 * batch},
+                        {rope ? rope->table : nullptr, rb}};
+    const Range outs[] = {{out, 4 * batch * heads * cache->head_dim}, {lse, lse ? 4 * batch * heads : 0},
+                {workspace, workspace_bytes}};
+    if (!apart(in, outs))
+        return COMP_ERR_INVALID_VALUE;
+    const int64_t need = attn_decode8_bytes(*cache, heads);
+    if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0)
+        return COMP_ERR_INVALID_VALUE;
+    DeviceInfo dev;
+    const comp_status_t st = current_device(&dev);
+    if (st != COMP_OK)
+        return st;
+    return launch_attn_decode8(*cache, q, q_token, q_head, heads, scale, table, batch, width, lengths, rope, out, lse,
+                               workspace, dev, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -43,6 +43,14 @@ inline bool strided_bytes(int64_t tokens, int64_t heads, int64_t dim, int64_t to
     return true;
 }
 
+// Whether the rows of a [tokens, heads, dim] output do not overlap each other.
+inline bool rows_apart(int64_t tokens, int64_t heads, int64_t dim, int64_t token, int64_t head)
+{
+    return (tokens <= 1 && (heads <= 1 || head >= dim)) || (heads <= 1 && token >= dim) ||
+           (head >= dim && token >= (heads - 1) * head + dim) ||
+           (token >= dim && head >= (tokens - 1) * token + dim);
+}
+
 // Properties of the current device, checked once per device.
 struct DeviceInfo {
     int device;
@@ -109,15 +117,26 @@ comp_status_t launch_gemm_f16x2(const uint16_t* hi, const uint16_t* lo, const ui
 // Whether a cache descriptor is one that the kernels take; the bytes of its
 // k (and of its v).
 bool kv_cache_ok(const comp_kv_cache_t* cache, int64_t* bytes);
+// The same of an 8-bit cache; the bytes of its k_scale (and of its v_scale).
+bool kv8_cache_ok(const comp_kv8_cache_t* cache, int64_t* bytes, int64_t* scales);
+// Whether a page table is one that the kernels take, and its entries.
+bool kv_table_ok(int64_t pages, int page_size, int64_t rows, int64_t width, int64_t* entries);
 
 // Attention of single tokens over a cache (arguments validated; batch > 0), and
 // whether its line of tiles can be counted in ints (batch * heads can).
-bool attn_decode_countable(const comp_kv_cache_t& cache, int64_t batch, int heads, int64_t width);
+bool attn_decode_countable(int kv_heads, int page_size, int64_t batch, int heads, int64_t width);
 int64_t attn_decode_bytes(const comp_kv_cache_t& cache, int64_t batch, int heads, int64_t shared_pages);
 comp_status_t launch_attn_decode(const comp_kv_cache_t& cache, const float* q, int64_t q_token, int64_t q_head,
                                  int heads, float scale, const int32_t* table, int64_t batch, int64_t width,
                                  const int32_t* lengths, int64_t shared_pages, float* out, float* lse,
                                  void* workspace, const DeviceInfo& dev, cudaStream_t stream);
+
+// The same over an 8-bit cache; rope: nullptr for none.
+int64_t attn_decode8_bytes(const comp_kv8_cache_t& cache, int heads);
+comp_status_t launch_attn_decode8(const comp_kv8_cache_t& cache, const float* q, int64_t q_token, int64_t q_head,
+                                  int heads, float scale, const int32_t* table, int64_t batch, int64_t width,
+                                  const int32_t* lengths, const comp_rope_t* rope, float* out, float* lse,
+                                  void* workspace, const DeviceInfo& dev, cudaStream_t stream);
 
 // One thread runs a bounded wait that cannot succeed (comp_check_wait_timeout).
 comp_status_t launch_check_wait_timeout(cudaStream_t stream);

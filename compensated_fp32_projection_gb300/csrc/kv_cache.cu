@@ -1,5 +1,7 @@
 // Maintenance of a paged cache of FP16 keys and values: writing new tokens,
-// and reserving, forking, freeing, compacting and copying pages.
+// and reserving, forking, freeing, compacting and copying pages.  The last four
+// serve the 8-bit cache too, whose pages have scales beside them (its tokens are
+// written in kv8_cache.cu).
 //
 // The bookkeeping (page tables, lengths, reference counts) lives in device
 // memory and is changed by kernels, so that a serving loop never waits for the
@@ -192,9 +194,31 @@ __device__ __forceinline__ void copy16(const uint4* src, uint4* dst, int64_t n, 
         dst[i] = __ldcs(src + i);
 }
 
+// Keys and values of either type as the copies see them.
+struct Store {
+    uint4* part[2];         // k, v
+    float* scale[2];        // one for each kScaled tokens of a head on a page (nullptr: none)
+    int64_t pages;
+    int kv_heads, page_size, row_vecs;  // uint4s of a token's head
+};
+
+constexpr int kScaled = COMP_KV8_BLOCK;
+
+Store store_of(const comp_kv_cache_t& c)
+{
+    return {{reinterpret_cast<uint4*>(c.k), reinterpret_cast<uint4*>(c.v)}, {nullptr, nullptr}, c.pages, c.kv_heads,
+            c.page_size, c.head_dim / 8};
+}
+
+Store store_of(const comp_kv8_cache_t& c)
+{
+    return {{reinterpret_cast<uint4*>(c.k), reinterpret_cast<uint4*>(c.v)}, {c.k_scale, c.v_scale}, c.pages,
+            c.kv_heads, c.page_size, c.head_dim / 16};
+}
+
 // Second launch: one CTA for each row (tables, lengths, counts of the shared
 // pages), then `ctas` for each child (the filled tokens of its last page).
-__global__ void __launch_bounds__(kCopyThreads) fork_copy_kernel(Tables t, comp_kv_cache_t cache,
+__global__ void __launch_bounds__(kCopyThreads) fork_copy_kernel(Tables t, Store cache,
                                                                  const int32_t* parents, const int32_t* children,
                                                                  int n, int ctas, const int32_t* left)
 {
@@ -236,17 +260,24 @@ __global__ void __launch_bounds__(kCopyThreads) fork_copy_kernel(Tables t, comp_
     if (dst < 0 || dst >= t.pages)
         return;
     const bool there = src >= 0 && src < t.pages;  // if not it reads as zeros, and so must its copy
-    const int64_t head = static_cast<int64_t>(t.page_size) * cache.head_dim / 8;  // uint4s
+    const int64_t head = static_cast<int64_t>(t.page_size) * cache.row_vecs;
     for (int u = cta; u < 2 * cache.kv_heads; u += ctas) {
-        uint4* const base = reinterpret_cast<uint4*>(u < cache.kv_heads ? cache.k : cache.v);
-        const int64_t h = u < cache.kv_heads ? u : u - cache.kv_heads;
-        uint4* const to = base + (dst * static_cast<int64_t>(cache.kv_heads) + h) * head;
-        const int64_t n = static_cast<int64_t>(f.rest) * cache.head_dim / 8;
+        const int is_v = u >= cache.kv_heads;
+        uint4* const base = cache.part[is_v];
+        const int64_t h = is_v ? u - cache.kv_heads : u;
+        const int64_t from = src * static_cast<int64_t>(cache.kv_heads) + h;
+        const int64_t into = dst * static_cast<int64_t>(cache.kv_heads) + h;
+        uint4* const to = base + into * head;
+        const int64_t n = static_cast<int64_t>(f.rest) * cache.row_vecs;
         if (there)
-            copy16(base + (src * static_cast<int64_t>(cache.kv_heads) + h) * head, to, n, 0, 1);
+            copy16(base + from * head, to, n, 0, 1);
         else
             for (int64_t i = threadIdx.x; i < n; i += blockDim.x)
                 to[i] = make_uint4(0, 0, 0, 0);
+        float* const scale = cache.scale[is_v];
+        const int blocks = t.page_size / kScaled;
+        if (scale && threadIdx.x * kScaled < f.rest)
+            scale[into * blocks + threadIdx.x] = there ? scale[from * blocks + threadIdx.x] : 0.0f;
     }
 }
 
@@ -439,17 +470,26 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const int32_
 constexpr int64_t kPiece = 4 * kCopyThreads;
 
 template <typename PageOf>
-__device__ __forceinline__ void copy_pages(const comp_kv_cache_t& cache, int64_t n, PageOf page_of)
+__device__ __forceinline__ void copy_pages(const Store& cache, int64_t n, PageOf page_of)
 {
-    const int64_t vecs = static_cast<int64_t>(cache.kv_heads) * cache.page_size * cache.head_dim / 8;
-    const int64_t pieces = (vecs + kPiece - 1) / kPiece;
-    for (int64_t u = blockIdx.x; u < n * 2 * pieces; u += gridDim.x) {
-        const int64_t i = u / (2 * pieces);
-        const int64_t piece = u % (2 * pieces);
+    const int64_t vecs = static_cast<int64_t>(cache.kv_heads) * cache.page_size * cache.row_vecs;
+    const int64_t pieces = (vecs + kPiece - 1) / kPiece, all = 2 * pieces + (cache.scale[0] ? 1 : 0);
+    for (int64_t u = blockIdx.x; u < n * all; u += gridDim.x) {
+        const int64_t i = u / all;
+        const int64_t piece = u % all;
         int64_t src, dst;
         if (!page_of(i, src, dst))
             continue;
-        uint4* const base = reinterpret_cast<uint4*>(piece < pieces ? cache.k : cache.v);
+        if (piece == 2 * pieces) {
+            const int64_t scales = static_cast<int64_t>(cache.kv_heads) * (cache.page_size / kScaled);
+            for (int64_t j = threadIdx.x; j < 2 * scales; j += blockDim.x) {
+                float* const scale = cache.scale[j >= scales];
+                const int64_t at = j >= scales ? j - scales : j;
+                scale[dst * scales + at] = scale[src * scales + at];
+            }
+            continue;
+        }
+        uint4* const base = cache.part[piece >= pieces];
         const int64_t first = (piece % pieces) * kPiece;
         copy16(base + src * vecs + first, base + dst * vecs + first, vecs - first < kPiece ? vecs - first : kPiece, 0,
                1);
@@ -457,7 +497,7 @@ __device__ __forceinline__ void copy_pages(const comp_kv_cache_t& cache, int64_t
 }
 
 // Second launch: the pages that move, the table and the counts renumbered.
-__global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(Tables t, comp_kv_cache_t cache,
+__global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(Tables t, Store cache,
                                                                     const int32_t* remap, const int32_t* live_in)
 {
     const int64_t live = live_in[0];
@@ -484,7 +524,7 @@ __global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(Tables t, co
     });
 }
 
-__global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(comp_kv_cache_t cache, const int32_t* from,
+__global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(Store cache, const int32_t* from,
                                                                   const int32_t* to, int64_t n)
 {
     copy_pages(cache, n, [&](int64_t i, int64_t& src, int64_t& dst) {
@@ -609,14 +649,14 @@ comp_status_t copy_ints(const int32_t* src, int32_t* dst, int64_t n, const Devic
     return launch_status();
 }
 
-bool table_ok(int64_t pages, int page_size, int64_t rows, int64_t width, int64_t* entries)
+}  // namespace
+
+bool kv_table_ok(int64_t pages, int page_size, int64_t rows, int64_t width, int64_t* entries)
 {
     return pages >= 0 && pages <= kMostPages && (page_size == 16 || page_size == 32 || page_size == 64 ||
            page_size == 128) && rows >= 0 && rows <= INT32_MAX / 2 && width >= 0 &&
            width <= INT32_MAX / (2 * page_size) && mul_ok(rows, width, entries) && *entries <= INT64_MAX / 8;
 }
-
-}  // namespace
 
 bool kv_cache_ok(const comp_kv_cache_t* c, int64_t* bytes)
 {
@@ -634,6 +674,137 @@ bool kv_cache_ok(const comp_kv_cache_t* c, int64_t* bytes)
     return true;
 }
 
+namespace {
+
+// What a call writes of a cache; the 16-bit one has no scales.
+struct Held {
+    const void* k;
+    const void* v;
+    const void* k_scale;
+    const void* v_scale;
+    int64_t bytes, scales;
+};
+
+bool held_of(const comp_kv_cache_t* c, Held* h)
+{
+    if (!kv_cache_ok(c, &h->bytes))
+        return false;
+    h->k = c->k;
+    h->v = c->v;
+    h->k_scale = h->v_scale = nullptr;
+    h->scales = 0;
+    return true;
+}
+
+bool held_of(const comp_kv8_cache_t* c, Held* h)
+{
+    if (!kv8_cache_ok(c, &h->bytes, &h->scales))
+        return false;
+    h->k = c->k;
+    h->v = c->v;
+    h->k_scale = c->k_scale;
+    h->v_scale = c->v_scale;
+    return true;
+}
+
+template <typename Cache>
+comp_status_t fork(const Cache* cache, const int32_t* table, const int32_t* lengths,
+                           const int32_t* refs, int64_t rows, int64_t width, const int32_t* parents,
+                           const int32_t* children, int64_t n, int32_t* table_out, int32_t* lengths_out,
+                           int32_t* refs_out, int32_t* left, comp_stream_t stream)
+{
+    Held h;
+    int64_t entries;
+    if (!held_of(cache, &h) || !kv_table_ok(cache->pages, cache->page_size, rows, width, &entries) || n < 0 ||
+        n > kMostListed)
+        return COMP_ERR_INVALID_VALUE;
+    const int64_t pages = cache->pages;
+    const Range r[] = {{h.k, h.bytes, nullptr, true}, {h.v, h.bytes, nullptr, true},
+                       {h.k_scale, h.scales, nullptr, true}, {h.v_scale, h.scales, nullptr, true},
+                       {table, 4 * entries}, {lengths, 4 * rows}, {refs, 4 * pages}, {parents, 4 * n},
+                       {children, 4 * n}, {table_out, 4 * entries, table, true},
+                       {lengths_out, 4 * rows, lengths, true}, {refs_out, 4 * pages, refs, true},
+                       {left, 4, nullptr, true}};
+    if (!ranges_ok(r))
+        return COMP_ERR_INVALID_VALUE;
+    DeviceInfo dev;
+    comp_status_t st = current_device(&dev);
+    if (st != COMP_OK)
+        return st;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const Tables t{table, lengths, refs, table_out, lengths_out, refs_out, rows, width, pages, cache->page_size};
+    const size_t smem = static_cast<size_t>(4 * n);
+    static std::mutex mu;
+    static bool done[64] = {};
+    if (!allow_smem(fork_plan_kernel, 4 * kMostListed, mu, done, dev))
+        return COMP_ERR_CUDA;
+    fork_plan_kernel<<<1, kPlanThreads, smem, s>>>(t, parents, children, static_cast<int>(n), left);
+    st = launch_status();
+    if (st != COMP_OK || rows == 0)
+        return st;
+    const int ctas = 2 * cache->kv_heads < 16 ? 2 * cache->kv_heads : 16;
+    fork_copy_kernel<<<static_cast<unsigned>(rows + n * ctas), kCopyThreads, 0, s>>>(
+        t, store_of(*cache), parents, children, static_cast<int>(n), ctas, left);
+    return launch_status();
+}
+
+template <typename Cache>
+comp_status_t compact(const Cache* cache, const int32_t* table, const int32_t* refs, int64_t rows,
+                              int64_t width, int32_t* table_out, int32_t* refs_out, int32_t* remap, int32_t* live,
+                              comp_stream_t stream)
+{
+    Held h;
+    int64_t entries;
+    if (!held_of(cache, &h) || !kv_table_ok(cache->pages, cache->page_size, rows, width, &entries))
+        return COMP_ERR_INVALID_VALUE;
+    const int64_t pages = cache->pages;
+    const Range r[] = {{h.k, h.bytes, nullptr, true}, {h.v, h.bytes, nullptr, true},
+                       {h.k_scale, h.scales, nullptr, true}, {h.v_scale, h.scales, nullptr, true}, {table, 4 * entries},
+                       {refs, 4 * pages}, {table_out, 4 * entries, table, true}, {refs_out, 4 * pages, refs, true},
+                       {remap, 4 * pages, nullptr, true}, {live, 4, nullptr, true}};
+    if (!ranges_ok(r))
+        return COMP_ERR_INVALID_VALUE;
+    DeviceInfo dev;
+    comp_status_t st = current_device(&dev);
+    if (st != COMP_OK)
+        return st;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    compact_plan_kernel<<<1, kPlanThreads, 0, s>>>(refs, pages, remap, live);
+    st = launch_status();
+    if (st != COMP_OK)
+        return st;
+    const Tables t{table, nullptr, refs, table_out, nullptr, refs_out, rows, width, pages, cache->page_size};
+    compact_move_kernel<<<static_cast<unsigned>(dev.sm_count * 8), kCopyThreads, 0, s>>>(t, store_of(*cache), remap,
+                                                                                           live);
+    return launch_status();
+}
+
+template <typename Cache>
+comp_status_t copy_listed(const Cache* cache, const int32_t* src, const int32_t* dst, int64_t n,
+                                 comp_stream_t stream)
+{
+    Held h;
+    if (!held_of(cache, &h) || n < 0 || n > kMostPages)
+        return COMP_ERR_INVALID_VALUE;
+    const Range r[] = {{h.k, h.bytes, nullptr, true}, {h.v, h.bytes, nullptr, true},
+                       {h.k_scale, h.scales, nullptr, true}, {h.v_scale, h.scales, nullptr, true}, {src, 4 * n}, {dst, 4 * n}};
+    if (!ranges_ok(r))
+        return COMP_ERR_INVALID_VALUE;
+    if (n == 0 || h.bytes == 0)
+        return COMP_OK;
+    DeviceInfo dev;
+    const comp_status_t st = current_device(&dev);
+    if (st != COMP_OK)
+        return st;
+    const int64_t vecs = static_cast<int64_t>(cache->kv_heads) * cache->page_size * store_of(*cache).row_vecs;
+    const int64_t units = n * 2 * ((vecs + kPiece - 1) / kPiece);
+    copy_pages_kernel<<<grid_of(units, 1, dev, 8), kCopyThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+        store_of(*cache), src, dst, n);
+    return launch_status();
+}
+
+}  // namespace
+
 }  // namespace compfp32
 
 using namespace compfp32;
@@ -646,7 +817,7 @@ comp_status_t comp_kv_append_f32(const comp_kv_cache_t* cache, const float* k, c
                                  const int32_t* start, comp_stream_t stream)
 {
     int64_t bytes, entries;
-    if (!kv_cache_ok(cache, &bytes) || !table_ok(cache->pages, cache->page_size, rows, width, &entries) ||
+    if (!kv_cache_ok(cache, &bytes) || !kv_table_ok(cache->pages, cache->page_size, rows, width, &entries) ||
         total < 0 || total > INT32_MAX || (!cu && total != rows))
         return COMP_ERR_INVALID_VALUE;
     int64_t kb, vb;
@@ -674,7 +845,7 @@ comp_status_t comp_kv_reserve(int64_t pages, int32_t page_size, const int32_t* t
                               int32_t* refs_out, int32_t* left, comp_stream_t stream)
 {
     int64_t entries;
-    if (!table_ok(pages, page_size, rows, width, &entries) || rows > kMostRows || entries > INT32_MAX)
+    if (!kv_table_ok(pages, page_size, rows, width, &entries) || rows > kMostRows || entries > INT32_MAX)
         return COMP_ERR_INVALID_VALUE;
     const Range r[] = {{table, 4 * entries}, {refs, 4 * pages}, {want, 4 * rows},
                        {table_out, 4 * entries, table, true}, {refs_out, 4 * pages, refs, true},
@@ -704,37 +875,8 @@ comp_status_t comp_kv_fork(const comp_kv_cache_t* cache, const int32_t* table, c
                            const int32_t* children, int64_t n, int32_t* table_out, int32_t* lengths_out,
                            int32_t* refs_out, int32_t* left, comp_stream_t stream)
 {
-    int64_t bytes, entries;
-    if (!kv_cache_ok(cache, &bytes) || !table_ok(cache->pages, cache->page_size, rows, width, &entries) || n < 0 ||
-        n > kMostListed)
-        return COMP_ERR_INVALID_VALUE;
-    const int64_t pages = cache->pages;
-    const Range r[] = {{cache->k, bytes, nullptr, true}, {cache->v, bytes, nullptr, true},
-                       {table, 4 * entries}, {lengths, 4 * rows}, {refs, 4 * pages}, {parents, 4 * n},
-                       {children, 4 * n}, {table_out, 4 * entries, table, true},
-                       {lengths_out, 4 * rows, lengths, true}, {refs_out, 4 * pages, refs, true},
-                       {left, 4, nullptr, true}};
-    if (!ranges_ok(r))
-        return COMP_ERR_INVALID_VALUE;
-    DeviceInfo dev;
-    comp_status_t st = current_device(&dev);
-    if (st != COMP_OK)
-        return st;
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const Tables t{table, lengths, refs, table_out, lengths_out, refs_out, rows, width, pages, cache->page_size};
-    const size_t smem = static_cast<size_t>(4 * n);
-    static std::mutex mu;
-    static bool done[64] = {};
-    if (!allow_smem(fork_plan_kernel, 4 * kMostListed, mu, done, dev))
-        return COMP_ERR_CUDA;
-    fork_plan_kernel<<<1, kPlanThreads, smem, s>>>(t, parents, children, static_cast<int>(n), left);
-    st = launch_status();
-    if (st != COMP_OK || rows == 0)
-        return st;
-    const int ctas = 2 * cache->kv_heads < 16 ? 2 * cache->kv_heads : 16;
-    fork_copy_kernel<<<static_cast<unsigned>(rows + n * ctas), kCopyThreads, 0, s>>>(
-        t, *cache, parents, children, static_cast<int>(n), ctas, left);
-    return launch_status();
+    return fork(cache, table, lengths, refs, rows, width, parents, children, n, table_out, lengths_out, refs_out, left,
+                stream);
 }
 
 comp_status_t comp_kv_free(int64_t pages, const int32_t* table, const int32_t* lengths, const int32_t* refs,
@@ -742,7 +884,7 @@ comp_status_t comp_kv_free(int64_t pages, const int32_t* table, const int32_t* l
                            int32_t* lengths_out, int32_t* refs_out, comp_stream_t stream)
 {
     int64_t entries;
-    if (!table_ok(pages, 16, rows, width, &entries) || n < 0 || n > INT32_MAX / 2)
+    if (!kv_table_ok(pages, 16, rows, width, &entries) || n < 0 || n > INT32_MAX / 2)
         return COMP_ERR_INVALID_VALUE;
     const Range r[] = {{table, 4 * entries}, {lengths, 4 * rows}, {refs, 4 * pages}, {seqs, 4 * n},
                        {table_out, 4 * entries, table, true}, {lengths_out, 4 * rows, lengths, true},
@@ -766,53 +908,39 @@ comp_status_t comp_kv_free(int64_t pages, const int32_t* table, const int32_t* l
     return launch_status();
 }
 
-comp_status_t comp_kv_compact(const comp_kv_cache_t* cache, const int32_t* table, const int32_t* refs, int64_t rows,
-                              int64_t width, int32_t* table_out, int32_t* refs_out, int32_t* remap, int32_t* live,
-                              comp_stream_t stream)
+comp_status_t comp_kv_compact(const comp_kv_cache_t* cache, const int32_t* table, const int32_t* refs,
+                              int64_t rows, int64_t width, int32_t* table_out, int32_t* refs_out, int32_t* remap,
+                              int32_t* live, comp_stream_t stream)
 {
-    int64_t bytes, entries;
-    if (!kv_cache_ok(cache, &bytes) || !table_ok(cache->pages, cache->page_size, rows, width, &entries))
-        return COMP_ERR_INVALID_VALUE;
-    const int64_t pages = cache->pages;
-    const Range r[] = {{cache->k, bytes, nullptr, true}, {cache->v, bytes, nullptr, true}, {table, 4 * entries},
-                       {refs, 4 * pages}, {table_out, 4 * entries, table, true}, {refs_out, 4 * pages, refs, true},
-                       {remap, 4 * pages, nullptr, true}, {live, 4, nullptr, true}};
-    if (!ranges_ok(r))
-        return COMP_ERR_INVALID_VALUE;
-    DeviceInfo dev;
-    comp_status_t st = current_device(&dev);
-    if (st != COMP_OK)
-        return st;
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    compact_plan_kernel<<<1, kPlanThreads, 0, s>>>(refs, pages, remap, live);
-    st = launch_status();
-    if (st != COMP_OK)
-        return st;
-    const Tables t{table, nullptr, refs, table_out, nullptr, refs_out, rows, width, pages, cache->page_size};
-    compact_move_kernel<<<static_cast<unsigned>(dev.sm_count * 8), kCopyThreads, 0, s>>>(t, *cache, remap, live);
-    return launch_status();
+    return compact(cache, table, refs, rows, width, table_out, refs_out, remap, live, stream);
 }
 
 comp_status_t comp_kv_copy_pages(const comp_kv_cache_t* cache, const int32_t* src, const int32_t* dst, int64_t n,
                                  comp_stream_t stream)
 {
-    int64_t bytes;
-    if (!kv_cache_ok(cache, &bytes) || n < 0 || n > kMostPages)
-        return COMP_ERR_INVALID_VALUE;
-    const Range r[] = {{cache->k, bytes, nullptr, true}, {cache->v, bytes, nullptr, true}, {src, 4 * n}, {dst, 4 * n}};
-    if (!ranges_ok(r))
-        return COMP_ERR_INVALID_VALUE;
-    if (n == 0 || bytes == 0)
-        return COMP_OK;
-    DeviceInfo dev;
-    const comp_status_t st = current_device(&dev);
-    if (st != COMP_OK)
-        return st;
-    const int64_t vecs = static_cast<int64_t>(cache->kv_heads) * cache->page_size * cache->head_dim / 8;
-    const int64_t units = n * 2 * ((vecs + kPiece - 1) / kPiece);
-    copy_pages_kernel<<<grid_of(units, 1, dev, 8), kCopyThreads, 0, static_cast<cudaStream_t>(stream)>>>(*cache, src,
-                                                                                                         dst, n);
-    return launch_status();
+    return copy_listed(cache, src, dst, n, stream);
+}
+
+comp_status_t comp_kv8_fork(const comp_kv8_cache_t* cache, const int32_t* table, const int32_t* lengths,
+                            const int32_t* refs, int64_t rows, int64_t width, const int32_t* parents,
+                            const int32_t* children, int64_t n, int32_t* table_out, int32_t* lengths_out,
+                            int32_t* refs_out, int32_t* left, comp_stream_t stream)
+{
+    return fork(cache, table, lengths, refs, rows, width, parents, children, n, table_out, lengths_out, refs_out, left,
+                stream);
+}
+
+comp_status_t comp_kv8_compact(const comp_kv8_cache_t* cache, const int32_t* table, const int32_t* refs,
+                               int64_t rows, int64_t width, int32_t* table_out, int32_t* refs_out, int32_t* remap,
+                               int32_t* live, comp_stream_t stream)
+{
+    return compact(cache, table, refs, rows, width, table_out, refs_out, remap, live, stream);
+}
+
+comp_status_t comp_kv8_copy_pages(const comp_kv8_cache_t* cache, const int32_t* src, const int32_t* dst, int64_t n,
+                                  comp_stream_t stream)
+{
+    return copy_listed(cache, src, dst, n, stream);
 }
 
 }  // extern "C"

@@ -499,6 +499,142 @@ comp_status_t comp_kv_copy_pages(const comp_kv_cache_t* cache, const int32_t* sr
                                  comp_stream_t stream);
 
 /*
+ * Rotary positions.
+ *
+ * A head's first `rot` dimensions are rot / 2 pairs, (i, i + rot / 2) or, where
+ * interleaved is not 0, (2 i, 2 i + 1); the others stay as they are.  At position
+ * p the pair (a, b) becomes (a c - b s, b c + a s), each a binary32 operation
+ * rounded to nearest even and never fused, with (c, s) = table[p][i]:
+ *   f_i = base^(-2 i / rot)
+ *   u_i = context f_i / (2 pi), the turns that it makes over `context` positions
+ *   g_i = min(max((u_i - low) / (high - low), 0), 1), or 0 if context is 0
+ *   a_i = f_i (g_i + (1 - g_i) / factor)
+ *   table[p][i] = magnitude (cos(p a_i), sin(p a_i))
+ * So factor 1 changes nothing; a larger one, with context 0, makes all positions
+ * that much denser (long contexts by interpolation); with the context that a model
+ * was trained on, pairs of more than `high` turns keep their frequency, those of
+ * fewer than `low` are interpolated, and what lies between is blended.
+ */
+typedef struct comp_rope {
+    const float* table;      /* [positions, rot / 2, 2], 8-byte aligned */
+    int64_t positions;
+    int32_t rot, interleaved;
+} comp_rope_t;
+
+typedef struct comp_rope_angles {
+    double base, factor, context, low, high, magnitude;
+} comp_rope_angles_t;
+
+/*
+ * comp_rope_table — the table of positions first .. first + positions - 1: angles
+ * and functions in binary64, rounded once.  rot is even, 2 .. 65536; first and
+ * positions at most 2^31 - 1; base and factor are positive, context is not
+ * negative, and high > low where it is positive; all finite.
+ */
+comp_status_t comp_rope_table(const comp_rope_angles_t* angles, int32_t rot, int64_t first, int64_t positions,
+                              float* table, comp_stream_t stream);
+
+/*
+ * comp_rope_f32 — rotate x [tokens, heads, head_dim] (token and head strides; not
+ * negative) into out, which may be x itself with x's strides, and shares memory
+ * with no input otherwise; its rows do not overlap each other.  Token t is at
+ * positions[t], or at position t if positions is NULL; where the table does not
+ * have the position, the values to be rotated become NaN.  inverse != 0 turns the
+ * other way (s becomes -s): the gradient of the call, and its inverse where the
+ * magnitude is 1.  head_dim is rot .. 65536, heads at most 65535, tokens at most
+ * 2^31 - 1.
+ */
+comp_status_t comp_rope_f32(const comp_rope_t* rope, const float* x, int64_t x_token, int64_t x_head, int64_t tokens,
+                            int32_t heads, int32_t head_dim, const int32_t* positions, int inverse, float* out,
+                            int64_t out_token, int64_t out_head, comp_stream_t stream);
+
+/*
+ * A paged cache of keys and values in 8 bits.  k and v are [pages, kv_heads,
+ * page_size, head_dim], dense, 16-byte aligned; 16 tokens of a head that stand
+ * together on a page (COMP_KV8_BLOCK) are a block with a scale of their own:
+ * k_scale and v_scale are [pages, kv_heads, page_size / 16] binary32.
+ * page_size is 16, 32, 64 or 128; head_dim a multiple of 16 up to 128.  A value is
+ *   code * |scale|   (binary32), NaN for the code -128,
+ * and the sign of a scale says that its block may have codes of -128.  A scale is
+ * zero or at least 2^-126.  Page tables, lengths and reference counts are those of
+ * comp_kv_cache_t; comp_kv_reserve and comp_kv_free serve this cache as well.
+ */
+#define COMP_KV8_BLOCK 16
+
+typedef struct comp_kv8_cache {
+    int8_t* k;
+    int8_t* v;
+    float* k_scale;
+    float* v_scale;
+    int64_t pages;
+    int32_t page_size, kv_heads, head_dim;
+} comp_kv8_cache_t;
+
+/*
+ * comp_kv8_append_f32 — write new tokens, addressed as in comp_kv_append_f32; the
+ * keys are rotated on the way, each at its position in its sequence (rope NULL:
+ * they are not).  For each block that new tokens join, with x their values:
+ *   kept  = |its scale| if tokens of the sequence before the first new one are
+ *           in the block, else 0
+ *   scale = max(kept, rn(max |x| * rn(1/127))), or 0 where that is below 2^-126
+ *   code  = rint(rn(x * rn(1/scale))), clamped to -127 .. 127
+ * and the codes of the tokens before become rint(rn(code * rn(kept/scale))).  An
+ * infinity or a NaN takes the code -128 and no part in the scale.  A value written
+ * at once is off by half a step, scale / 2; each later call that raises the block's
+ * scale rounds it again, by half of the larger step.  What stood behind the new
+ * tokens in their last block is no longer valid.  No other block changes.
+ * Errors: as comp_kv_append_f32; COMP_ERR_INVALID_VALUE also for a table of angles
+ * that is NULL, not 8-byte aligned or of an odd rot, or of one beyond head_dim.
+ */
+comp_status_t comp_kv8_append_f32(const comp_kv8_cache_t* cache, const float* k, const float* v, int64_t k_token,
+                                  int64_t k_head, int64_t v_token, int64_t v_head, int64_t total,
+                                  const int32_t* table, int64_t rows, int64_t width, const int32_t* cu,
+                                  const int32_t* start, const comp_rope_t* rope, comp_stream_t stream);
+
+/*
+ * comp_kv8_read_f32, comp_kv8_read_f16 — read tokens back: tokens cu[r] ..
+ * cu[r+1]-1 of k and v [total, kv_heads, head_dim] (token and head strides) are
+ * those at positions start[r], start[r]+1, ... of row r (cu NULL: one token each),
+ * so that packed attention can see a sequence's past.  Where the table has no page,
+ * and for the tokens behind cu[rows], zeros are written.  Neither k nor v shares
+ * memory with an input or with the other, from the first to the last element of
+ * each, and their rows do not overlap.  The binary16 form rounds
+ * the binary32 values (to nearest, ties to even; 65520 and more become infinities).
+ */
+comp_status_t comp_kv8_read_f32(const comp_kv8_cache_t* cache, float* k, float* v, int64_t k_token, int64_t k_head,
+                                int64_t v_token, int64_t v_head, int64_t total, const int32_t* table, int64_t rows,
+                                int64_t width, const int32_t* cu, const int32_t* start, comp_stream_t stream);
+comp_status_t comp_kv8_read_f16(const comp_kv8_cache_t* cache, uint16_t* k, uint16_t* v, int64_t k_token,
+                                int64_t k_head, int64_t v_token, int64_t v_head, int64_t total, const int32_t* table,
+                                int64_t rows, int64_t width, const int32_t* cu, const int32_t* start,
+                                comp_stream_t stream);
+
+/*
+ * comp_attn_decode_f32x8 — comp_attn_decode_f32x16 over an 8-bit cache, without a
+ * shared prefix; rope (or NULL) rotates each query at its sequence's last position,
+ * lengths[b] - 1.  The codes enter the products exactly and a block's scale is
+ * applied in binary32 to what its keys gave, so keys and values may have any
+ * magnitude as long as the scores stay finite.  Same limits on sizes.
+ */
+int64_t comp_attn_decode_f32x8_workspace_bytes(const comp_kv8_cache_t* cache, int64_t batch, int32_t heads,
+                                               int64_t width);
+comp_status_t comp_attn_decode_f32x8(const comp_kv8_cache_t* cache, const float* q, int64_t q_token, int64_t q_head,
+                                     int32_t heads, float scale, const int32_t* table, int64_t batch, int64_t width,
+                                     const int32_t* lengths, const comp_rope_t* rope, float* out, float* lse,
+                                     void* workspace, int64_t workspace_bytes, comp_stream_t stream);
+
+/* comp_kv_fork, comp_kv_compact and comp_kv_copy_pages of an 8-bit cache: the scales go with the tokens. */
+comp_status_t comp_kv8_fork(const comp_kv8_cache_t* cache, const int32_t* table, const int32_t* lengths,
+                            const int32_t* refs, int64_t rows, int64_t width, const int32_t* parents,
+                            const int32_t* children, int64_t n, int32_t* table_out, int32_t* lengths_out,
+                            int32_t* refs_out, int32_t* left, comp_stream_t stream);
+comp_status_t comp_kv8_compact(const comp_kv8_cache_t* cache, const int32_t* table, const int32_t* refs, int64_t rows,
+                               int64_t width, int32_t* table_out, int32_t* refs_out, int32_t* remap, int32_t* live,
+                               comp_stream_t stream);
+comp_status_t comp_kv8_copy_pages(const comp_kv8_cache_t* cache, const int32_t* src, const int32_t* dst, int64_t n,
+                                  comp_stream_t stream);
+
+/*
  * comp_device_status — waits for `stream`, then reports and clears the fault
  * word that kernels of this library set when a bounded wait inside them gives
  * up (they then skip the rest of their work and exit cleanly, leaving the
