@@ -83,20 +83,21 @@ comp_status_t attn(const comp_attn_t* a, const float* q, const void* k, const vo
                        static_cast<cudaStream_t>(stream));
 }
 
-// The sizes of a decode call over a cache of either type, which is checked already.
+// The sizes of a decode call over a cache of either type, which is checked already;
+// per_row: what a row takes of the line of tiles beside its tiles of 16.
 template <typename Cache>
-bool decode_sizes_ok(const Cache* c, int64_t batch, int32_t heads, int64_t width, int64_t* entries)
+bool decode_sizes_ok(const Cache* c, int64_t batch, int32_t heads, int64_t width, int per_row, int64_t* entries)
 {
     return batch >= 0 && heads > 0 && heads <= 65535 && heads % c->kv_heads == 0 &&
            width >= 0 && width <= INT32_MAX / (2 * c->page_size) && mul_ok(batch, width, entries) &&
            batch <= INT32_MAX / heads && *entries <= INT64_MAX / 8 &&
-           attn_decode_countable(c->kv_heads, c->page_size, batch, heads, width);
+           attn_decode_countable(c->kv_heads, c->page_size, batch, heads, width, per_row);
 }
 
 bool decode_ok(const comp_kv_cache_t* c, int64_t batch, int32_t heads, int64_t width, int64_t shared_pages,
                int64_t* bytes, int64_t* entries)
 {
-    return kv_cache_ok(c, bytes) && decode_sizes_ok(c, batch, heads, width, entries) && shared_pages >= 0 &&
+    return kv_cache_ok(c, bytes) && decode_sizes_ok(c, batch, heads, width, 1, entries) && shared_pages >= 0 &&
            shared_pages <= width;
 }
 
@@ -172,7 +173,7 @@ int64_t comp_attn_decode_f32x8_workspace_bytes(const comp_kv8_cache_t* cache, in
                                                int64_t width)
 {
     int64_t bytes, scales, entries;
-    if (!kv8_cache_ok(cache, &bytes, &scales) || !decode_sizes_ok(cache, batch, heads, width, &entries) || batch == 0)
+    if (!kv8_cache_ok(cache, &bytes, &scales) || !decode_sizes_ok(cache, batch, heads, width, 4, &entries) || batch == 0)
         return 0;
     return attn_decode8_bytes(*cache, heads);
 }
@@ -183,7 +184,7 @@ comp_status_t comp_attn_decode_f32x8(const comp_kv8_cache_t* cache, const float*
                                      void* workspace, int64_t workspace_bytes, comp_stream_t stream)
 {
     int64_t bytes, scales, entries, qb, rb;
-    if (!kv8_cache_ok(cache, &bytes, &scales) || !decode_sizes_ok(cache, batch, heads, width, &entries) ||
+    if (!kv8_cache_ok(cache, &bytes, &scales) || !decode_sizes_ok(cache, batch, heads, width, 4, &entries) ||
         !std::isfinite(scale) || !(scale > 0.0f) || workspace_bytes < 0 ||
         !strided_bytes(batch, heads, cache->head_dim, q_token, q_head, 4, &qb) ||
         !rope_ok(rope, cache->head_dim, &rb))

@@ -28,6 +28,16 @@
 #include <cmath>
 
 #include "attn.h"
+
+namespace compfp32 {
+namespace {
+constexpr int kTileShift = 4;
+constexpr int kTile = 1 << kTileShift;  // keys of a tile, the k of a product
+constexpr int kRowCost = 0;
+constexpr bool kJoinEarly = true;
+}
+}  // namespace compfp32
+
 #include "attn_line.cuh"
 #include "internal.h"
 #include "ptx.cuh"
@@ -477,10 +487,10 @@ int64_t effective_shared(int64_t batch, int64_t shared_pages)
 
 }  // namespace
 
-bool attn_decode_countable(int kv_heads, int page_size, int64_t batch, int heads, int64_t width)
+bool attn_decode_countable(int kv_heads, int page_size, int64_t batch, int heads, int64_t width, int per_row)
 {
     const int64_t units = static_cast<int64_t>(kv_heads) * row_blocks(heads / kv_heads);
-    return (width * page_size / kTile + 1) * batch <= INT32_MAX / units;
+    return (width * page_size / kTile + per_row) * batch <= INT32_MAX / units;
 }
 
 int64_t attn_decode_bytes(const comp_kv_cache_t& cache, int64_t batch, int heads, int64_t shared_pages)

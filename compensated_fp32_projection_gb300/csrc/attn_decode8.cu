@@ -7,16 +7,26 @@
 // once to what its 16 keys gave:
 //   s = (S_hi + 2^-10 S_lo) (scale kscale)     q split into hi and lo;
 //   o = o 2^(m_old - m_new) + vscale (O'_hi + O'_lo)   2^14 p split into hi and lo.
-// A tile is a block, 16 keys, and its products are added up in FP32 registers.
+// A product over a block's 16 keys starts afresh and is added up in FP32 registers.
+//
+// Products.  With half the bytes of the FP16 cache, time is as short for the
+// arithmetic, so the keys are the 16 rows of an m16n8k16 product and the columns
+// are four query heads, hi and lo of each side by side (the FP16 kernel has the
+// heads in the rows, eight of them, half empty where four share a key head):
+//   S^T = K q^T      a lane has two keys of one head, hi and lo sums together;
+//   O^T = V^T p^T    a lane has DP/8 dimensions of one head, likewise.
+// The weights go from one layout to the other by one transposition of 8 x 8 FP16
+// values each (movmatrix).  With four heads a key head, 48 sequences of 129 to 6001
+// tokens take 44 us where rows of eight heads take 51.
 //
 // Layout.  The sum over the head dimension may go in any order, and so may the
-// columns of the output: a lane's operands are 16 codes that stand side by side in
-// a row, whole 16-byte words of memory.  So a lane copies with cp.async just the
-// words that it will use itself, to places of its own in a ring of stages: no
-// registers wait for memory, shared memory has no conflicts, and the only
-// synchronisation is each lane's wait for its own copies (and one of the warp for
-// the two scales).  Codes become FP16 two at a time, 1024 + 128 + code by a
-// bitwise operation and one subtraction.
+// rows of the output and the keys of a block: a lane's operands are 16 codes that
+// stand side by side in a row, one 16-byte load from shared memory, and which keys
+// it has is chosen so that no load has bank conflicts (see key_of).  Codes become
+// FP16 two at a time, 1024 + 128 + code by a bitwise operation and one subtraction.
+// A warp loads its own tiles (TMA, keys and values apart).  An earlier form, in which each lane
+// copied just its own words with cp.async, needed no barrier and no swizzle, but
+// moved 3.9 TB/s at most: eight rows of 64 bytes an instruction.
 //
 // Work is cut and joined as in the FP16 kernel (attn_line.cuh).
 #include <cuda_fp16.h>
@@ -24,6 +34,21 @@
 #include <cmath>
 
 #include "attn.h"
+
+namespace compfp32 {
+namespace {
+constexpr int kTileShift = 0;       // a tile's size goes by the heads: see Cfg
+// A row's beginning (its queries, rotated and split, and its end) takes the time of
+// some tiles: 96 sequences of 33 to 2500 tokens of 16 heads of 64 take 30 us, 45 if
+// rows count by their keys alone (31 with 3, 33 with 4).
+constexpr int kRowCost = 2;
+// With the next call's kernel on the SMs before the join has begun, its CTAs are
+// spread unevenly: 16 sequences of 20001 to 65536 tokens, eight heads a key head, took
+// 172 us a call in a long row of calls where they take 136.
+constexpr bool kJoinEarly = false;
+}
+}  // namespace compfp32
+
 #include "attn_line.cuh"
 #include "internal.h"
 #include "ptx.cuh"
@@ -33,61 +58,102 @@
 namespace compfp32 {
 namespace {
 
-static_assert(kTile == COMP_KV8_BLOCK, "a tile has one scale");
+constexpr int kRunKeys = 1024;  // keys that are added up before they are added to the sums so far, as in the FP16 kernel
+constexpr uint32_t kFaultDecode8 = 0xB01;
 
-constexpr int kRun8 = 64;  // tiles that are added up before they are added to the sums so far, as in the FP16 kernel
-
-// DP: head dimension padded to 64 or 128; NB: blocks of eight query heads.
-template <int DP, int NB>
+// DP: head dimension padded to 64 or 128; NT: products' columns, four query heads each.
+// A tile is some blocks of 16 keys.  What a tile costs whatever its size (waits, loads,
+// the maximum) is some 190 instructions, a block's products and conversions are 300 to
+// 400, so larger tiles are faster until the SM waits for their loads: with four heads of
+// 128 tiles of 32 keys take 41 us where 64 take 44 (48 ragged sequences); with one head
+// of 64, 132 where 64 take 117, with 16 of 128, 202 where 64 take 191 (16 long ones).
+// One stage each for keys and values is enough, each filled again as soon as it has been
+// read, as the other is: two stages take 42 us (ragged) and 133 where one takes 124
+// (eight heads, long).
+template <int DP, int NT>
 struct Cfg {
     static constexpr int kWords = DP / 64;                  // 16-byte words of a key that a lane has
-    static constexpr uint32_t kPlane = kTile * DP;
-    static constexpr uint32_t kStage = 2 * kPlane + 16;     // k, v, the two scales
-    static constexpr int NS = DP == 128 ? 4 : 7;
-    static constexpr int kCtas = NB == 1 ? 3 : 2;           // an SM
-    static constexpr size_t kSmem = kWarps * NS * kStage;
+    static constexpr int kTileShift = DP == 128 && NT < 4 ? 5 : 6;
+    static constexpr int kTile = 1 << kTileShift, kBlocks = kTile / COMP_KV8_BLOCK;
+    static constexpr uint32_t kPlane = kTile * DP;          // the keys or the values of a tile
+    static constexpr int kCtas = NT == 4 ? 2 : 3;           // an SM
+    static constexpr size_t kSmem = 1024 + kWarps * 2 * kPlane;
 };
 
 struct Cache8 {
-    const int8_t* k;
-    const int8_t* v;
     const float* k_scale;
     const float* v_scale;
     comp_rope_t rope;
+    int wide;               // its angles stand on 16 bytes
 };
 
-// Copies 16 or 8 bytes, or zeros where `there` is false (src is then any address).
-__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool there)
+// Rows of DP codes in shared memory, swizzled by the TMA: the 16-byte chunk
+// `chunk` of a row (128-byte rows), or the same of 64-byte rows.
+template <int DP>
+__device__ __forceinline__ uint32_t swizzled(uint32_t row, uint32_t chunk)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+    return DP == 128 ? sw128(row, chunk) : row * 64u + ((chunk ^ ((row >> 1) & 3u)) << 4);
 }
 
-__device__ __forceinline__ void copy8_async(uint32_t dst, const void* src, bool there)
+// The key that stands at place `at` of eight.  A quarter of a warp loads four chunks
+// of the keys at two places, 2 a and 2 a + 1: with 128-byte rows their numbers
+// differ in bit 2, with 64-byte rows in bit 0.  For the values it (with 64-byte rows
+// half a warp, 8 bytes a lane) loads two (four) columns of dimensions of the keys at
+// the four even or the four odd places: with 128-byte rows these differ above bit 0,
+// with 64-byte rows in bit 0 or in bit 2.  So all 32 banks are read once.
+template <int DP>
+__device__ __forceinline__ int key_of(int at)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(there ? 8 : 0) : "memory");
+    return ((DP == 128 ? 0x36147250u : 0x65217430u) >> (4 * at)) & 7u;
 }
 
-__device__ __forceinline__ void copy4_async(uint32_t dst, const void* src, bool there)
+// A 4-byte copy that the barrier waits for: it counts one arrival of this thread
+// when the copy has landed.
+__device__ __forceinline__ void copy4_async(uint32_t dst, const void* src, bool there, uint64_t* bar)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-__device__ __forceinline__ void copies_commit()
+// Loads from shared memory, in order after the wait for the stage.
+__device__ __forceinline__ void lds(uint32_t at, uint32_t (&v)[4])
 {
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(at)
+                 : "memory");
 }
 
-template <int N>
-__device__ __forceinline__ void copies_wait()
+__device__ __forceinline__ void lds(uint32_t at, uint32_t (&v)[2])
 {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(at) : "memory");
+}
+
+__device__ __forceinline__ uint32_t lds(uint32_t at)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+
+// c += a b: a 16 x 16, b 16 x 8, FP16 in, FP32 sums.  Not volatile: the compiler
+// may mix the products of one block with the conversions of the next.
+__device__ __forceinline__ void mma16816_free(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // Bytes 0 and 2 of w, two codes, as FP16: 0x6400 + u is 1024 + u, u = code + 128.
+// One bitwise operation by hand: the compiler makes two of it.
 __device__ __forceinline__ uint32_t even_codes(uint32_t w)
 {
-    const uint32_t x = (w & 0x00ff00ffu) ^ 0x64806480u;
-    return pack_h2(__hsub2(*reinterpret_cast<const __half2*>(&x), __floats2half2_rn(1152.0f, 1152.0f)));
+    const uint32_t mask = 0x00ff00ffu, bias = 0x64806480u;  // 1152 twice
+    uint32_t x;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(x) : "r"(w), "r"(mask), "r"(bias));  // (w & mask) ^ bias
+    return pack_h2(__hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&bias)));
 }
 
 __device__ __forceinline__ uint32_t odd_codes(uint32_t w)
@@ -95,30 +161,77 @@ __device__ __forceinline__ uint32_t odd_codes(uint32_t w)
     return even_codes(w >> 8);
 }
 
-// NaN in the place of a code of -128.
-__device__ __forceinline__ uint32_t odd_to_nan(uint32_t h2)
+// An 8 x 8 matrix of FP16 values, two a lane, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t v)
 {
-    const uint32_t odd = 0xd800d800u;  // -128
-    return h2 | __heq2_mask(*reinterpret_cast<const __half2*>(&h2), *reinterpret_cast<const __half2*>(&odd));
+    uint32_t t;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(t) : "r"(v));
+    return t;
 }
 
-__device__ __forceinline__ bool has_odd(uint32_t w)
+// The bytes of w that are -128, a code that is not a number: 0x80 each.
+__device__ __forceinline__ uint32_t odd_bytes(uint32_t w)
 {
-    return __vcmpeq4(w, 0x80808080u) != 0;
+    return __vcmpeq4(w, 0x80808080u) & 0x80808080u;
 }
 
-template <int DP, int NB>
-__global__ void __launch_bounds__(kThreads, Cfg<DP, NB>::kCtas)
-    attn_decode8_kernel(const Params p, const Cache8 c)
+__device__ __forceinline__ void prefetch_l1(const void* p)
 {
-    using C = Cfg<DP, NB>;
-    constexpr int NS = C::NS, W = C::kWords;
-    extern __shared__ __align__(16) uint8_t stages_of[];
-    __shared__ float2 l_far_of[kWarps][NB][32];
-    __shared__ float m_far_of[kWarps][NB][32];
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p)
+{
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
+// Whether a block has such codes: the sign of its scale.
+__device__ __forceinline__ bool has_odd(float scale)
+{
+    return __float_as_int(scale) < 0;
+}
+
+template <int DP, int NT>
+__global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
+    attn_decode8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                        const Params p, const Cache8 c)
+{
+    using C = Cfg<DP, NT>;
+    constexpr int W = C::kWords, kDims = DP / 8;  // kDims: of a lane's output
+    constexpr int kTileShift = C::kTileShift, kTile = C::kTile, kBlocks = C::kBlocks, kRun = kRunKeys / kTile;
+    const int dim = p.dim;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t full_of[kWarps][2];             // keys, values
+    __shared__ float scale_of[kWarps][2][kBlocks];
+    __shared__ int abort_flag[kWarps];
+    __shared__ float2 far_of[kWarps][NT][32];           // maximum and sum
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    uint8_t* const stages = stages_of + warp * (NS * C::kStage);
-    const uint32_t stages32 = smem_u32(stages);
+    uint8_t* const stages =
+        reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023)) +
+        warp * (2 * C::kPlane);
+    const uint32_t k_stage = smem_u32(stages), v_stage = k_stage + C::kPlane;
+    uint64_t* const full = full_of[warp];
+    if (lane == 0) {
+        for (int i = 0; i < 2; ++i)
+            mbar_init(&full[i], 1 + kBlocks);  // the TMA's bytes and the scales
+        abort_flag[warp] = 0;
+        fence_mbar_init();
+    }
+    __syncwarp();
+    // What the first steps read one after the other comes into L2 meanwhile, a line a
+    // thread: lengths, page tables, queries.
+    {
+        const int64_t thread = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+        const int64_t lines = (static_cast<int64_t>(p.batch) * p.width + 31) / 32;
+        const int64_t q_lines = static_cast<int64_t>(p.heads) * dim / 32, row = (thread - lines) / q_lines;
+        if (thread < lines)
+            prefetch_l2(p.table + thread * 32);
+        else if (row < p.batch)
+            prefetch_l2(p.q + row * p.q_token + (thread - lines) % q_lines * 32 / dim * p.q_head +
+                        (thread - lines) % q_lines * 32 % dim);
+        if (threadIdx.x == 0 && blockIdx.x * 32 < p.batch)
+            prefetch_l2(p.lengths + blockIdx.x * 32);
+    }
     grid_dependency_wait();
     grid_dependency_launch();  // the join relies on what came before
 
@@ -130,258 +243,351 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NB>::kCtas)
     if (!find_piece(p, piece, begin, end, r))
         return;
 
-    // A lane has the codes of key g (and 8 + g) in the words quad + 4 j, and for the
-    // values those of the keys 2 quad, 2 quad + 1 and 8 more, dimensions g DP/8 on.
+    // A lane has the codes of the key at place g (and 8 more) in the words quad + 4 j,
+    // and for the values those of the keys at 2 quad and 2 quad + 1 (and 8 more),
+    // dimensions g kDims on.
     const int g = lane >> 2, quad = lane & 3;
     const float c2 = p.scale * kAttnLog2E;
-    const int v_dim = g * (DP / 8);
+    const int my_key = key_of<DP>(g);
+    const uint32_t k_at = swizzled<DP>(my_key, quad);
+    uint32_t v_at[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        v_at[e] = swizzled<DP>(key_of<DP>(quad * 2 + e), g * kDims / 16) + g * kDims % 16;
 
-    // Loads run NS - 1 tiles ahead.  The lanes hold the page numbers of 32 tiles of
-    // a row, fetched when the row is new; one that is not there reads as zeros.
+    // Loads.  The lanes hold the page numbers of a row's next tiles, fetched when it is
+    // new, 32 of them; one that is not there: a place beyond the cache, which reads
+    // zeros.  The first lanes have a block's scale each, and those whose block begins a
+    // page (or the tile) a box.  A tile's keys are loaded when those of the tile before
+    // have been read, and its values, from the place that `at_v` keeps, likewise.
     Place next = r;
-    int pages = 0, page_tile = 0, loads = 0;
+    int pages = 0, page_tile = 0, loads_k = 0, loads_v = 0, ahead = begin;  // ahead: the next place of the line
     const int blocks_shift = p.page_shift - 4;
+    const int box_shift = min(p.page_shift, kTileShift), split = kTileShift - box_shift;  // a tile is on 1 << split pages
+    const int my_box = lane * 16 >> box_shift, my_block = (lane * 16 & ((1 << box_shift) - 1)) >> 4;
+    struct {
+        int unit, slot;
+        bool there;
+    } at_v;
     auto look_up = [&] {
         page_tile = next.tile;
-        const int col = ((next.tile + lane) * kTile) >> p.page_shift;
-        pages = next.tile + lane < next.tiles && col < p.width ? p.table[next.b * p.width + col] : -1;
+        const int tile = next.tile + (lane >> split);
+        const int col = (next.tile * kTile + lane * (kTile >> split)) >> p.page_shift;
+        pages = tile < next.tiles && col < p.width ? p.table[next.b * p.width + col] : -1;
     };
-    auto load = [&] {
-        if (begin + loads < end) {
-            const int at = __shfl_sync(0xffffffffu, pages, next.tile - page_tile);
-            const bool there = at >= 0 && at < p.pages;
-            const int slot = (next.tile * kTile) & ((1 << p.page_shift) - 1);
-            const int64_t unit = (there ? at : 0) * static_cast<int64_t>(p.kv_heads) + next.unit / p.row_blocks;
-            const int64_t from = ((unit << p.page_shift) + slot) * p.dim;
-            const uint32_t to = stages32 + loads % NS * C::kStage;
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    const int d = (quad + 4 * j) * 16;
-                    const bool in = there && d < p.dim;
-                    copy16_async(to + ((nt * W + j) * 32 + lane) * 16, c.k + from + (in ? (nt * 8 + g) * p.dim + d : 0),
-                                 in);
-                }
-            const bool in = there && v_dim < p.dim;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int key = quad * 2 + (i & 1) + 8 * (i >> 1);
-                const int8_t* const src = c.v + from + (in ? key * p.dim + v_dim : 0);
-                if (DP == 128)
-                    copy16_async(to + C::kPlane + (i * 32 + lane) * 16, src, in);
-                else
-                    copy8_async(to + C::kPlane + (i * 32 + lane) * 8, src, in);
-            }
-            if (lane < 2)
-                copy4_async(to + 2 * C::kPlane + lane * 4,
-                            (lane ? c.v_scale : c.k_scale) + (unit << blocks_shift) + (slot >> 4), there);
-            if (begin + ++loads < end) {
-                if (++next.tile == next.tiles) {
-                    next_row(p, next);
-                    look_up();
-                } else if (next.tile == page_tile + 32) {
-                    look_up();
-                }
-            }
-        } else {
-            ++loads;
+    // A row's queries and angles, some tiles before they are needed: lines of 32 values.
+    auto prefetch_row = [&](const Place& at) {
+        const int head = at.unit / p.row_blocks, first_head = at.unit % p.row_blocks * (NT * 4);
+        const int heads = min(NT * 4, p.group - first_head), lines = (dim + 31) / 32;
+        for (int l = lane; l < heads * lines; l += 32)
+            prefetch_l1(p.q + at.b * p.q_token + (head * p.group + first_head + l / lines) * p.q_head + l % lines * 32);
+        const float* const angles = c.rope.rot > 0 ? angles_of(c.rope, at.own - 1) : nullptr;
+        if (angles && lane * 32 < c.rope.rot)
+            prefetch_l1(angles + lane * 32);
+    };
+    auto issue = [&](int is_v) {
+        if (lane == 0)
+            mbar_arrive_expect_tx(&full[is_v], C::kPlane);
+        __syncwarp();
+        if (lane < kBlocks) {
+            if (my_block == 0)
+                tma_load_3d(stages + is_v * C::kPlane + lane * (C::kPlane / kBlocks), is_v ? &map_v : &map_k,
+                            &full[is_v], 0, at_v.slot, at_v.there ? at_v.unit : p.pages * p.kv_heads);
+            const int64_t scale = (static_cast<int64_t>(at_v.unit) << blocks_shift) + (at_v.slot >> 4) + my_block;
+            copy4_async(smem_u32(&scale_of[warp][is_v][lane]), (is_v ? c.v_scale : c.k_scale) + scale, at_v.there,
+                        &full[is_v]);
         }
-        copies_commit();
+    };
+    auto load_k = [&] {
+        const int at = __shfl_sync(0xffffffffu, pages, ((next.tile - page_tile) << split) + (my_box & ((1 << split) - 1)));
+        at_v.there = at >= 0 && at < p.pages;
+        at_v.slot = (next.tile * kTile) & ((1 << p.page_shift) - 1);
+        at_v.unit = (at_v.there ? at : 0) * p.kv_heads + next.unit / p.row_blocks;
+        issue(0);
+        ++loads_k;
+        ++ahead;
+        if (++next.tile == next.tiles)
+            ahead += kRowCost;
+        if (ahead < end) {
+            if (next.tile == next.tiles) {
+                next_row(p, next);
+                look_up();
+                prefetch_row(next);
+            } else if (next.tile == page_tile + (32 >> split)) {
+                look_up();
+            }
+        }
+    };
+    auto load_v = [&] {
+        issue(1);
+        ++loads_v;
     };
     look_up();
-    for (int i = 0; i < NS - 1; ++i)
-        load();
+    if (ahead < end) {
+        load_k();
+        load_v();
+    }
 
+    bool ok = true;
     int i = 0, fragment = 0;
-    for (int at = begin; at < end; ++fragment) {
+    for (int at = begin; ok && at < end; ++fragment) {
         const int n = min(r.tiles - r.tile, end - at);
-        const int head = r.unit / p.row_blocks, first_head = r.unit % p.row_blocks * (NB * 8);
-        // The query heads, rotated and split: rows 0..7 of a block hi, 8..15 lo.  Step
-        // 4 j + w of the head dimension takes word w of the lane's codes, whose four
-        // stand in the order 0, 2, 1, 3.
-        uint32_t q[NB][DP / 16][4];
-        const float* const angles = c.rope.rot > 0 ? angles_of(c.rope, min(p.lengths[r.b], p.most_keys) - 1) : nullptr;
+        const int head = r.unit / p.row_blocks, first_head = r.unit % p.row_blocks * (NT * 4);
+        // The query heads, rotated and split: column 2 h of a product has hi of head h,
+        // 2 h + 1 lo.  Step 4 j + w of the head dimension takes word w of the lane's
+        // codes, whose four stand in the order 0, 2, 1, 3.
+        uint32_t q[NT][DP / 16][2];
+        const float* const angles = c.rope.rot > 0 ? angles_of(c.rope, r.own - 1) : nullptr;
+        // Halves of a head of DP that is all rotated: the partner of dimension d stands in
+        // the lane's word 4 steps on (heads of 128), or in the lane 2 quads on (64).
+        const bool paired = c.rope.rot == DP && !c.rope.interleaved && p.vec_q && c.wide && angles;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            const int hg = first_head + nb * 8 + g;
+        for (int nt = 0; nt < NT; ++nt) {
+            const int hg = first_head + nt * 4 + (g >> 1);
             const float* const src = p.q + r.b * p.q_token + (head * p.group + hg) * p.q_head;
+            float4 x[DP / 16];
 #pragma unroll
             for (int k = 0; k < DP / 16; ++k) {
                 const int d = (quad + 4 * (k / 4)) * 16 + k % 4 * 4;
-                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (hg < p.group && d < p.dim)
-                    x = load_rotated(src, d, c.rope, angles, p.vec_q != 0);
-                split2(x.x, x.z, q[nb][k][0], q[nb][k][1]);
-                split2(x.y, x.w, q[nb][k][2], q[nb][k][3]);
+                x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (hg < p.group && d < dim)
+                    x[k] = paired ? __ldg(reinterpret_cast<const float4*>(src + d))
+                                  : load_rotated(src, d, c.rope, angles, p.vec_q != 0, c.wide != 0);
+            }
+            if (paired) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const int i = (DP == 128 ? quad : quad & 1) * 16 + w * 4;
+                    const float4 a = load_angles(angles + 2 * i, true), b = load_angles(angles + 2 * i + 4, true);
+                    if constexpr (DP == 128) {
+                        const float4 y = x[w], z = x[w + 4];
+                        x[w] = make_float4(turn(y.x, a.x, z.x, a.y, false), turn(y.y, a.z, z.y, a.w, false),
+                                           turn(y.z, b.x, z.z, b.y, false), turn(y.w, b.z, z.w, b.w, false));
+                        x[w + 4] = make_float4(turn(z.x, a.x, y.x, a.y, true), turn(z.y, a.z, y.y, a.w, true),
+                                               turn(z.z, b.x, y.z, b.y, true), turn(z.w, b.z, y.w, b.w, true));
+                    } else {
+                        const float4 y = x[w];
+                        const float4 z = make_float4(__shfl_xor_sync(0xffffffffu, y.x, 2),
+                                                     __shfl_xor_sync(0xffffffffu, y.y, 2),
+                                                     __shfl_xor_sync(0xffffffffu, y.z, 2),
+                                                     __shfl_xor_sync(0xffffffffu, y.w, 2));
+                        const bool second = quad >= 2;
+                        x[w] = make_float4(turn(y.x, a.x, z.x, a.y, second), turn(y.y, a.z, z.y, a.w, second),
+                                           turn(y.z, b.x, z.z, b.y, second), turn(y.w, b.z, z.w, b.w, second));
+                    }
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k) {
+                uint32_t hi[2], lo[2];
+                split2(x[k].x, x[k].z, hi[0], lo[0]);
+                split2(x[k].y, x[k].w, hi[1], lo[1]);
+                q[nt][k][0] = g & 1 ? lo[0] : hi[0];
+                q[nt][k][1] = g & 1 ? lo[1] : hi[1];
             }
         }
-        // the running maximum and the sums of a run; slot, l_far_of, m_far_of: of the runs before
-        float m[NB];
-        uint64_t l2[NB], o[NB][DP / 8];
+        // Head `quad` of each four: the running maximum, the lane's part of the sum of the
+        // weights and its dimensions of the sums of a run; slot, far_of: of the runs before.
+        float m[NT], l[NT];
+        uint64_t o[NT][DP / 16];
         const int part = 2 * piece + (fragment > 0 ? 1 : 0);
-        // a lane's output: DP/8 dimensions from 2 quad DP/8 on, and the DP/8 after them
-        const int o_dim = quad * (DP / 4);
-        float* const slot = p.part_o + (static_cast<int64_t>(part) * (NB * 8) + g) * p.dim + o_dim;
+        const int o_dim = g * kDims;
+        float* const slot = p.part_o + (static_cast<int64_t>(part) * (NT * 4) + quad) * dim + o_dim;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            m[nb] = -INFINITY;
-            l2[nb] = 0;
+        for (int nt = 0; nt < NT; ++nt) {
+            m[nt] = -INFINITY;
+            l[nt] = 0.0f;
 #pragma unroll
-            for (int t = 0; t < DP / 8; ++t)
-                o[nb][t] = 0;
+            for (int t = 0; t < DP / 16; ++t)
+                o[nt][t] = 0;
         }
-        for (int t0 = 0; t0 < n; t0 += kRun8) {
-            const int t1 = min(n, t0 + kRun8);
+        auto ready = [&](int is_v) {
+            ok = __all_sync(0xffffffffu, mbar_try_wait(&full[is_v], i & 1)) ||
+                 attn_warp_wait(&full[is_v], i & 1, &abort_flag[warp], kFaultDecode8);
+            return ok;
+        };
+        for (int t0 = 0; ok && t0 < n; t0 += kRun) {
+            const int t1 = min(n, t0 + kRun);
             for (int t = t0; t < t1; ++t, ++i) {
-                copies_wait<NS - 2>();
-                __syncwarp();  // the scales; and all lanes have read the stage before
-                load();
-                const uint8_t* const stage = stages + i % NS * C::kStage;
-                const float2 scales = *reinterpret_cast<const float2*>(stage + 2 * C::kPlane);
+                if (!ready(0))
+                    break;
                 const int left = r.own - (r.tile + t) * kTile;  // keys of the tile that count
-                const float kc = fabsf(scales.x) * c2;
-                // two chains for each eight keys, the even and the odd steps of the head dimension
-                float s[NB][2][2][4] = {};
-                unsigned odd_keys[2] = {0, 0};  // four bits a key
+                float x[NT][kBlocks][2];  // of my_key and 8 more
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    bool odd = false;
+                for (int b = 0; b < kBlocks; ++b) {
+                    if (b > 0 && b * 16 >= left) {  // a block behind the end; its scale may be anything
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            x[nt][b][0] = x[nt][b][1] = -INFINITY;
+                        continue;
+                    }
+                    // two chains, the even and the odd steps of the head dimension
+                    float s[NT][2][4] = {};
 #pragma unroll
                     for (int j = 0; j < W; ++j) {
-                        const uint4 x = *reinterpret_cast<const uint4*>(stage + ((nt * W + j) * 32 + lane) * 16);
-                        const uint32_t word[4] = {x.x, x.y, x.z, x.w};
-                        if (scales.x < 0.0f || __float_as_uint(scales.x) == 0x80000000u)
-                            odd |= has_odd(x.x) || has_odd(x.y) || has_odd(x.z) || has_odd(x.w);
+                        uint32_t word[2][4];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)  // the swizzle leaves bit 2 of a chunk in its place
+                            lds(k_stage + (k_at ^ (j * 64)) + (b * 16 + e * 8) * DP, word[e]);
 #pragma unroll
                         for (int w = 0; w < 4; ++w) {
-                            const uint32_t b0 = even_codes(word[w]), b1 = odd_codes(word[w]);
+                            const uint32_t a[4] = {even_codes(word[0][w]), even_codes(word[1][w]),
+                                                   odd_codes(word[0][w]), odd_codes(word[1][w])};
 #pragma unroll
-                            for (int nb = 0; nb < NB; ++nb)
-                                mma16816(s[nb][nt][w & 1], q[nb][j * 4 + w], b0, b1);
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma16816_free(s[nt][w & 1], a, q[nt][j * 4 + w][0], q[nt][j * 4 + w][1]);
                         }
                     }
-                    if (__float_as_int(scales.x) < 0)
-                        odd_keys[nt] = __ballot_sync(0xffffffffu, odd);
-                }
-                uint32_t pa[NB][4];
+                    const float ks = scale_of[warp][0][b], kc = fabsf(ks) * c2;
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    float x[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int nt = e >> 1, col = e & 1, key = quad * 2 + col;
-                        x[e] = fmaf(s[nb][nt][0][2 + col] + s[nb][nt][1][2 + col], 0x1p-10f,
-                                    s[nb][nt][0][col] + s[nb][nt][1][col]);
-                        x[e] = __fmul_rn(x[e], kc);
-                        if ((odd_keys[nt] >> (4 * key)) & 0xfu)
-                            x[e] = __int_as_float(0x7fffffff);
-                        x[e] = nt * 8 + key < left ? x[e] : -INFINITY;
-                    }
-                    float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    const float m_new = fmaxf(m[nb], top), shift = m_new == -INFINITY ? 0.0f : m_new;
-                    if (__any_sync(0xffffffffu, m_new > m[nb])) {  // rare after some tiles
-                        const float alpha = ex2(m[nb] - shift);
-                        const uint64_t a2 = f2_bits(alpha, alpha);
-                        l2[nb] = mul2(l2[nb], a2);
-#pragma unroll
-                        for (int d = 0; d < DP / 8; ++d)
-                            o[nb][d] = mul2(o[nb][d], a2);
-                    }
-                    m[nb] = m_new;
-                    // 2^14 p; each step rounded as the maximum was, or large scores would not end at 0
-                    float w[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        w[e] = ex2(__fadd_rn(__fsub_rn(x[e], shift), 14.0f));
-                    split_p(w[0], w[1], pa[nb][0], pa[nb][1]);
-                    split_p(w[2], w[3], pa[nb][2], pa[nb][3]);
-                    l2[nb] = add2(l2[nb], add2(f2_bits(w[0], w[1]), f2_bits(w[2], w[3])));
-                }
-                // the values: four keys' codes of DP/8 dimensions
-                constexpr int VW = DP / 32;
-                uint32_t v[4][VW];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (DP == 128) {
-                        const uint4 x =
-                            *reinterpret_cast<const uint4*>(stage + C::kPlane + (k * 32 + lane) * 16);
-                        v[k][0] = x.x;
-                        v[k][1] = x.y;
-                        v[k][VW - 2] = x.z;
-                        v[k][VW - 1] = x.w;
-                    } else {
-                        const uint2 x = *reinterpret_cast<const uint2*>(stage + C::kPlane + (k * 32 + lane) * 8);
-                        v[k][0] = x.x;
-                        v[k][1] = x.y;
-                    }
-                }
-                const bool odd_v = __float_as_int(scales.y) < 0;
-                if (odd_v) {  // beyond the sequence's end 0 times a NaN must be 0
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (quad * 2 + (k & 1) + 8 * (k >> 1) >= left)
-#pragma unroll
-                            for (int w = 0; w < VW; ++w)
-                                v[k][w] = 0;
-                }
-                const float vs = fabsf(scales.y);
-                const uint64_t vs2 = f2_bits(vs, vs);
-#pragma unroll
-                for (int w = 0; w < VW; ++w)
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        // dimensions 4 w + 2 half and the next of two keys: bytes a0 a1 b0 b1
-                        const uint32_t p01 = __byte_perm(v[0][w], v[1][w], half ? 0x7632 : 0x5410);
-                        const uint32_t p23 = __byte_perm(v[2][w], v[3][w], half ? 0x7632 : 0x5410);
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const int d = 4 * w + 2 * half + e;
-                            uint32_t b0 = e ? odd_codes(p01) : even_codes(p01);
-                            uint32_t b1 = e ? odd_codes(p23) : even_codes(p23);
-                            if (odd_v) {
-                                b0 = odd_to_nan(b0);
-                                b1 = odd_to_nan(b1);
+                            const float(&y)[2][4] = s[nt];
+                            const uint64_t both = add2(f2_bits(y[0][2 * e], y[0][2 * e + 1]),
+                                                       f2_bits(y[1][2 * e], y[1][2 * e + 1]));
+                            x[nt][b][e] = __fmul_rn(fmaf(hi_f(both), 0x1p-10f, lo_f(both)), kc);
+                        }
+                    const int end_of = left - b * 16;  // keys of the block that count
+                    if (end_of < 16 || has_odd(ks)) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            unsigned odd = 0;  // four bits a place
+                            if (has_odd(ks)) {
+                                uint32_t any = 0;
+#pragma unroll
+                                for (int j = 0; j < W; ++j) {
+                                    uint32_t word[4];
+                                    lds(k_stage + (k_at ^ (j * 64)) + (b * 16 + e * 8) * DP, word);
+                                    any |= odd_bytes(word[0]) | odd_bytes(word[1]) | odd_bytes(word[2]) |
+                                           odd_bytes(word[3]);
+                                }
+                                odd = __ballot_sync(0xffffffffu, any != 0) >> (4 * g) & 0xfu;
                             }
 #pragma unroll
-                            for (int nb = 0; nb < NB; ++nb) {
-                                float y[4] = {};
-                                mma16816(y, pa[nb], b0, b1);
-                                o[nb][d] = fma2(f2_bits(y[0], y[1]), vs2,
-                                                fma2(f2_bits(y[2], y[3]), vs2, o[nb][d]));
-                            }
+                            for (int nt = 0; nt < NT; ++nt)
+                                x[nt][b][e] = e * 8 + my_key >= end_of ? -INFINITY
+                                              : odd ? __int_as_float(0x7fffffff) : x[nt][b][e];
                         }
                     }
+                }
+                __syncwarp();  // all lanes have read the keys
+                if (ahead < end)
+                    load_k();
+                uint32_t pb[NT][kBlocks][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float top = fmaxf(x[nt][0][0], x[nt][0][1]);
+#pragma unroll
+                    for (int b = 1; b < kBlocks; ++b)
+                        top = fmaxf(top, fmaxf(x[nt][b][0], x[nt][b][1]));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                    const float m_new = fmaxf(m[nt], top), shift = m_new == -INFINITY ? 0.0f : m_new;
+                    if (__any_sync(0xffffffffu, m_new > m[nt])) {  // rare after some tiles
+                        const float alpha = ex2(m[nt] - shift);
+                        const uint64_t a2 = f2_bits(alpha, alpha);
+                        l[nt] *= alpha;
+#pragma unroll
+                        for (int d = 0; d < DP / 16; ++d)
+                            o[nt][d] = mul2(o[nt][d], a2);
+                    }
+                    m[nt] = m_new;
+                    // 2^14 p; each step rounded as the maximum was, or large scores would not end at 0
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int b = 0; b < kBlocks; ++b) {
+                        const uint64_t e = add2(add2(f2_bits(x[nt][b][0], x[nt][b][1]), f2_bits(-shift, -shift)),
+                                                f2_bits(14.0f, 14.0f));
+                        const float w0 = ex2(lo_f(e)), w1 = ex2(hi_f(e));
+                        uint32_t hi, lo;
+                        split_p(w0, w1, hi, lo);
+                        pb[nt][b][0] = transposed(__byte_perm(hi, lo, 0x5410));
+                        pb[nt][b][1] = transposed(__byte_perm(hi, lo, 0x7632));
+                        sum += w0 + w1;
+                    }
+                    l[nt] += sum;
+                }
+                if (!ready(1))
+                    break;
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b) {
+                    if (b > 0 && b * 16 >= left)
+                        continue;
+                    // the values: four keys' codes of kDims dimensions
+                    constexpr int VW = DP / 32;
+                    uint32_t v[4][VW];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        lds(v_stage + v_at[k & 1] + (b * 16 + (k >> 1) * 8) * DP, v[k]);
+                    const float vs = scale_of[warp][1][b];
+                    const uint64_t vs2 = f2_bits(fabsf(vs), fabsf(vs));
+#pragma unroll
+                    for (int d = 0; d < DP / 16; ++d) {
+                        // dimensions 2 d and 2 d + 1 of two keys: bytes a0 a1 b0 b1
+                        const uint32_t p01 = __byte_perm(v[0][d / 2], v[1][d / 2], d & 1 ? 0x7632 : 0x5410);
+                        const uint32_t p23 = __byte_perm(v[2][d / 2], v[3][d / 2], d & 1 ? 0x7632 : 0x5410);
+                        const uint32_t a[4] = {even_codes(p01), odd_codes(p01), even_codes(p23), odd_codes(p23)};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float y[4] = {};
+                            mma16816_free(y, a, pb[nt][b][0], pb[nt][b][1]);
+                            o[nt][d] = fma2(f2_bits(y[0] + y[1], y[2] + y[3]), vs2, o[nt][d]);
+                        }
+                    }
+                    if (has_odd(vs)) {
+                        // the components in which a key that counts is not a number: a bit for
+                        // each of the lane's dimensions, of its four keys, then of all 16
+                        uint32_t odd = 0;
+                        for (int k = 0; k < 4; ++k)
+                            if (key_of<DP>(quad * 2 + (k & 1)) + b * 16 + 8 * (k >> 1) < left)
+                                for (int w = 0; w < VW; ++w) {
+                                    const uint32_t word =
+                                        lds(v_stage + v_at[k & 1] + (b * 16 + (k >> 1) * 8) * DP + w * 4);
+                                    odd |= ((odd_bytes(word) >> 7) * 0x00204081u >> 21 & 0xfu) << (4 * w);
+                                }
+                        odd |= __shfl_xor_sync(0xffffffffu, odd, 1);
+                        odd |= __shfl_xor_sync(0xffffffffu, odd, 2);
+                        const float nan = __int_as_float(0x7fffffff);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int d = 0; d < DP / 16; ++d)
+                                o[nt][d] = f2_bits((odd >> (2 * d)) & 1 ? nan : lo_f(o[nt][d]),
+                                                   (odd >> (2 * d + 1)) & 1 ? nan : hi_f(o[nt][d]));
+                    }
+                }
+                __syncwarp();  // all lanes have read the values
+                if (loads_v < loads_k)
+                    load_v();
             }
             if (t0 > 0) {
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    const float a = ex2(m_far_of[warp][nb][lane] - (m[nb] == -INFINITY ? 0.0f : m[nb]));
-                    const uint64_t a2 = f2_bits(a, a);
-                    const float2 l = l_far_of[warp][nb][lane];
-                    l2[nb] = fma2(f2_bits(l.x, l.y), a2, l2[nb]);
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float2 far = far_of[warp][nt][lane];
+                    const float a = ex2(far.x - (m[nt] == -INFINITY ? 0.0f : m[nt]));
+                    l[nt] = fmaf(far.y, a, l[nt]);
+                    if (o_dim < dim)
 #pragma unroll
-                    for (int x = 0; x < DP / 8; ++x)
-                        o[nb][x] = fma2(f2_bits(o_dim + x < p.dim ? slot[nb * 8 * p.dim + x] : 0.0f,
-                                                o_dim + DP / 8 + x < p.dim ? slot[nb * 8 * p.dim + DP / 8 + x] : 0.0f),
-                                        a2, o[nb][x]);
+                        for (int d = 0; d < DP / 16; d += 2) {
+                            const float4 y = *reinterpret_cast<const float4*>(slot + nt * 4 * dim + 2 * d);
+                            o[nt][d] = fma2(f2_bits(y.x, y.y), f2_bits(a, a), o[nt][d]);
+                            o[nt][d + 1] = fma2(f2_bits(y.z, y.w), f2_bits(a, a), o[nt][d + 1]);
+                        }
                 }
             }
             if (t1 < n) {
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    m_far_of[warp][nb][lane] = m[nb];
-                    l_far_of[warp][nb][lane] = make_float2(lo_f(l2[nb]), hi_f(l2[nb]));
-                    l2[nb] = 0;
+                for (int nt = 0; nt < NT; ++nt) {
+                    far_of[warp][nt][lane] = make_float2(m[nt], l[nt]);
+                    l[nt] = 0.0f;
 #pragma unroll
-                    for (int x = 0; x < DP / 8; ++x) {
-                        if (o_dim + x < p.dim)
-                            slot[nb * 8 * p.dim + x] = lo_f(o[nb][x]);
-                        if (o_dim + DP / 8 + x < p.dim)
-                            slot[nb * 8 * p.dim + DP / 8 + x] = hi_f(o[nb][x]);
-                        o[nb][x] = 0;
+                    for (int d = 0; d < DP / 16; d += 2) {
+                        if (o_dim < dim)
+                            *reinterpret_cast<float4*>(slot + nt * 4 * dim + 2 * d) = make_float4(
+                                lo_f(o[nt][d]), hi_f(o[nt][d]), lo_f(o[nt][d + 1]), hi_f(o[nt][d + 1]));
+                        o[nt][d] = o[nt][d + 1] = 0;
                     }
                 }
             }
@@ -390,57 +596,76 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NB>::kCtas)
         // the row, or this warp's part of it
         const bool whole = n == r.tiles;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            float sum = lo_f(l2[nb]) + hi_f(l2[nb]);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            const int row = nb * 8 + g, hg = first_head + row;
-            if (hg >= p.group)
+        for (int nt = 0; nt < NT; ++nt) {
+            float sum = l[nt];
+            sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+            const int row = nt * 4 + quad, hg = first_head + row;
+            if (!ok || hg >= p.group)
                 continue;
             const int64_t at_row = static_cast<int64_t>(r.b) * p.heads + head * p.group + hg;
-            float* const dst = (whole ? p.out + at_row * p.dim
-                                      : p.part_o + (static_cast<int64_t>(part) * (NB * 8) + row) * p.dim) +
+            float* const dst = (whole ? p.out + at_row * dim
+                                      : p.part_o + (static_cast<int64_t>(part) * (NT * 4) + row) * dim) +
                                o_dim;
             const float norm = sum == 0.0f ? 0.0f : 1.0f / sum;
             const bool vec = p.vec_out || !whole;
+            if (o_dim < dim)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-                for (int d = 0; d < DP / 8; d += 4) {
-                    if (o_dim + e * (DP / 8) + d >= p.dim)
-                        continue;
-                    float y[4];
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        y[x] = (e ? hi_f(o[nb][d + x]) : lo_f(o[nb][d + x])) * norm;
-                    float* const to = dst + e * (DP / 8) + d;
+                for (int d = 0; d < DP / 16; d += 2) {
+                    const float y[4] = {lo_f(o[nt][d]) * norm, hi_f(o[nt][d]) * norm, lo_f(o[nt][d + 1]) * norm,
+                                        hi_f(o[nt][d + 1]) * norm};
                     if (vec) {
-                        *reinterpret_cast<float4*>(to) = make_float4(y[0], y[1], y[2], y[3]);
+                        *reinterpret_cast<float4*>(dst + 2 * d) = make_float4(y[0], y[1], y[2], y[3]);
                     } else {
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            to[x] = y[x];
+                        for (int e = 0; e < 4; ++e)
+                            dst[2 * d + e] = y[e];
                     }
                 }
-            if (quad == 0) {
-                const float lse = sum == 0.0f ? -INFINITY : fmaf(m[nb], kAttnLn2, logf(sum * (1.0f / kAttnPScale)));
+            if (g == 0) {
+                const float lse = sum == 0.0f ? -INFINITY : fmaf(m[nt], kAttnLn2, logf(sum * (1.0f / kAttnPScale)));
                 if (!whole)
-                    p.part_lse[part * (NB * 8) + row] = lse;
+                    p.part_lse[part * (NT * 4) + row] = lse;
                 else if (p.lse)
                     p.lse[at_row] = lse;
             }
         }
-        at += n;
+        at += n + kRowCost;
         if (at < end)
             next_row(p, r);
     }
-    copies_wait<0>();
+    if (!ok) {  // what was issued lands before the warp leaves
+        if (loads_k > 0)
+            attn_drain_wait(&full[0], (loads_k - 1) & 1);
+        if (loads_v > 0)
+            attn_drain_wait(&full[1], (loads_v - 1) & 1);
+    }
 }
 
-template <int DP, int NB>
-comp_status_t launch_t(Params p, const Cache8& c, const DeviceInfo& dev, cudaStream_t stream)
+// A cache's codes: rows are the tokens of one head on one page.
+bool encode_codes(CUtensorMap* map, const int8_t* base, const comp_kv8_cache_t& c, int tile_shift)
 {
-    using C = Cfg<DP, NB>;
+    EncodeTiledFn fn = encode_fn();
+    if (!fn)
+        return false;
+    const bool wide = c.head_dim > 64;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(c.page_size),
+                                static_cast<cuuint64_t>(c.pages * c.kv_heads)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(c.head_dim),
+                                   static_cast<cuuint64_t>(c.page_size) * static_cast<cuuint64_t>(c.head_dim)};
+    const cuuint32_t rows = c.page_size < 1 << tile_shift ? c.page_size : 1 << tile_shift;
+    const cuuint32_t box[3] = {wide ? 128u : 64u, rows, 1}, estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<int8_t*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DP, int NT>
+comp_status_t launch_t(const CUtensorMap& mk, const CUtensorMap& mv, const Params& p, const Cache8& c,
+                       const DeviceInfo& dev, cudaStream_t stream)
+{
+    using C = Cfg<DP, NT>;
     static std::mutex mu;
     static bool done[64] = {};
     {
@@ -448,7 +673,7 @@ comp_status_t launch_t(Params p, const Cache8& c, const DeviceInfo& dev, cudaStr
         if (dev.device < 0 || dev.device >= 64)
             return COMP_ERR_CUDA;
         if (!done[dev.device]) {
-            if (cudaFuncSetAttribute(attn_decode8_kernel<DP, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            if (cudaFuncSetAttribute(attn_decode8_kernel<DP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      static_cast<int>(C::kSmem)) != cudaSuccess) {
                 (void)cudaGetLastError();
                 return COMP_ERR_CUDA;
@@ -456,29 +681,40 @@ comp_status_t launch_t(Params p, const Cache8& c, const DeviceInfo& dev, cudaStr
             done[dev.device] = true;
         }
     }
-    return launch_pdl(attn_decode8_kernel<DP, NB>, p.pieces / kWarps, kThreads, C::kSmem, stream, p, c);
+    return launch_pdl(attn_decode8_kernel<DP, NT>, p.pieces / kWarps, kThreads, C::kSmem, stream, mk, mv, p, c);
 }
 
 // Pieces of the line of tiles: one for each warp that the SMs hold.  The
 // workspace's size must not depend on the device, so their number is bounded.
 constexpr int kMostSms = 160;
 
-int ctas_an_sm(int nb)
+// Columns of four query heads that a warp takes at once.
+int columns_at_once(int group)
 {
-    return nb == 1 ? Cfg<128, 1>::kCtas : Cfg<128, 2>::kCtas;
+    return group > 8 ? 4 : (group > 4 ? 2 : 1);
+}
+
+int ctas_an_sm(int nt)
+{
+    return nt == 4 ? Cfg<128, 4>::kCtas : Cfg<128, 1>::kCtas;
+}
+
+int tile_shift_for(int head_dim, int nt)
+{
+    return head_dim <= 64 ? Cfg<64, 1>::kTileShift : (nt == 4 ? Cfg<128, 4>::kTileShift : Cfg<128, 1>::kTileShift);
 }
 
 // Floats of the workspace: parts of rows, and their lse.
-int64_t slots_of(int nb)
+int64_t slots_of(int nt)
 {
-    return 2 * static_cast<int64_t>(ctas_an_sm(nb)) * kMostSms * kWarps * 8 * nb;
+    return 2 * static_cast<int64_t>(ctas_an_sm(nt)) * kMostSms * kWarps * 4 * nt;
 }
 
 }  // namespace
 
 int64_t attn_decode8_bytes(const comp_kv8_cache_t& cache, int heads)
 {
-    return 4 * slots_of(blocks_at_once(heads / cache.kv_heads)) * (cache.head_dim + 1);
+    return 4 * slots_of(columns_at_once(heads / cache.kv_heads)) * (cache.head_dim + 1);
 }
 
 comp_status_t launch_attn_decode8(const comp_kv8_cache_t& cache, const float* q, int64_t q_token, int64_t q_head,
@@ -486,14 +722,14 @@ comp_status_t launch_attn_decode8(const comp_kv8_cache_t& cache, const float* q,
                                   const int32_t* lengths, const comp_rope_t* rope, float* out, float* lse,
                                   void* workspace, const DeviceInfo& dev, cudaStream_t stream)
 {
-    const int group = heads / cache.kv_heads, nb = blocks_at_once(group);
+    const int group = heads / cache.kv_heads, nt = columns_at_once(group);
     float* const ws = static_cast<float*>(workspace);
     Params p{};
     p.q = q;
     p.out = out;
     p.lse = lse;
     p.part_o = ws;
-    p.part_lse = ws + slots_of(nb) * cache.head_dim;
+    p.part_lse = ws + slots_of(nt) * cache.head_dim;
     p.table = table;
     p.lengths = lengths;
     p.q_token = q_token;
@@ -509,21 +745,37 @@ comp_status_t launch_attn_decode8(const comp_kv8_cache_t& cache, const float* q,
     while ((1 << p.page_shift) < cache.page_size)
         ++p.page_shift;
     p.most_keys = static_cast<int>(width * cache.page_size);
-    p.pieces = (dev.sm_count < kMostSms ? dev.sm_count : kMostSms) * ctas_an_sm(nb) * kWarps;
+    p.pieces = (dev.sm_count < kMostSms ? dev.sm_count : kMostSms) * ctas_an_sm(nt) * kWarps;
     p.waves = 1;
     p.vec_q = aligned16(q) && q_token % 4 == 0 && q_head % 4 == 0;
     p.vec_out = aligned16(out);  // rows are multiples of 64 bytes
     p.scale = scale;
-    const Cache8 c{cache.k, cache.v, cache.k_scale, cache.v_scale, rope ? *rope : comp_rope_t{}};
+    p.tile_shift = tile_shift_for(cache.head_dim, nt);
+    const Cache8 c{cache.k_scale, cache.v_scale, rope ? *rope : comp_rope_t{},
+                   rope && angles_wide(*rope)};
+    CUtensorMap mk{}, mv{};
+    if (width > 0) {  // otherwise there are no tiles
+        if (!encode_codes(&mk, cache.k, cache, p.tile_shift) || !encode_codes(&mv, cache.v, cache, p.tile_shift))
+            return COMP_ERR_CUDA;
+    }
     comp_status_t st;
     if (cache.head_dim <= 64)
-        st = nb == 1 ? launch_t<64, 1>(p, c, dev, stream) : launch_t<64, 2>(p, c, dev, stream);
+        st = nt == 1   ? launch_t<64, 1>(mk, mv, p, c, dev, stream)
+             : nt == 2 ? launch_t<64, 2>(mk, mv, p, c, dev, stream)
+                       : launch_t<64, 4>(mk, mv, p, c, dev, stream);
     else
-        st = nb == 1 ? launch_t<128, 1>(p, c, dev, stream) : launch_t<128, 2>(p, c, dev, stream);
+        st = nt == 1   ? launch_t<128, 1>(mk, mv, p, c, dev, stream)
+             : nt == 2 ? launch_t<128, 2>(mk, mv, p, c, dev, stream)
+                       : launch_t<128, 4>(mk, mv, p, c, dev, stream);
     if (st != COMP_OK)
         return st;
-    const Join x{nullptr, nullptr, lse, 0, 8 * nb};
+    const Join x{nullptr, nullptr, lse, 0, 4 * nt};
     return launch_pdl(attn_join_kernel, static_cast<int>((batch * heads + 7) / 8), 256, 0, stream, p, x);
+}
+
+comp_status_t read_and_clear_decode8_fault(cudaStream_t stream, uint32_t* where)
+{
+    return read_and_clear_word(&g_attn_fault_word, stream, where);
 }
 
 }  // namespace compfp32

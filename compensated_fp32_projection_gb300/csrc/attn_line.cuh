@@ -1,6 +1,9 @@
 // Attention of single tokens over pages, whatever the cache's type: the line of
 // tiles, its pieces, and the join of the parts of rows that were cut.  Included
-// by the decode kernels, each of which has its own copies.
+// by the decode kernels, each of which has its own copies and defines before:
+//   kTileShift log2 of the keys of a tile, or 0 where Params says;
+//   kRowCost   tiles that the beginning of a row costs as much time as;
+//   kJoinEarly whether the join lets the next kernel start before it has begun.
 #pragma once
 
 #include "attn.h"
@@ -11,11 +14,10 @@
 namespace compfp32 {
 namespace {
 
-constexpr int kTile = 16;       // keys of a tile, the k of a product
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kLeast = 4;
-constexpr int kLong = 8;
+constexpr int kLeastKeys = 64;
+constexpr int kLongKeys = 128;
 
 struct Params {
     const float* q;
@@ -29,7 +31,13 @@ struct Params {
     int batch, heads, kv_heads, group, row_blocks, dim;
     int page_shift, pages, shared_keys, most_keys, pieces, waves, vec_q, vec_out, after_prefix;
     float scale;
+    int tile_shift;         // where kTileShift is 0
 };
+
+__device__ __forceinline__ int tile_shift_of(const Params& p)
+{
+    return kTileShift > 0 ? kTileShift : p.tile_shift;
+}
 
 // Keys of a sequence beyond the shared pages, and their tiles.
 __device__ __forceinline__ int own_keys(const Params& p, int b)
@@ -38,35 +46,43 @@ __device__ __forceinline__ int own_keys(const Params& p, int b)
     return max(0, min(n, p.most_keys) - p.shared_keys);
 }
 
-__device__ __forceinline__ int tiles_of(int own)
+__device__ __forceinline__ int tiles_of(const Params& p, int own)
 {
-    return (own + kTile - 1) / kTile;
+    return (own + (1 << tile_shift_of(p)) - 1) >> tile_shift_of(p);
 }
 
-// Sum of the tiles of the sequences before `end` by one warp.
+// What a row of this many tiles takes of the line.
+__device__ __forceinline__ int line_of(int tiles)
+{
+    return tiles > 0 ? tiles + kRowCost : 0;
+}
+
+// What the sequences before `end` take of the line for each unit, by one warp.
 __device__ __forceinline__ int sum_tiles(const Params& p, int end)
 {
     int n = 0;
 #pragma unroll 4
     for (int b = threadIdx.x & 31; b < end; b += 32)
-        n += tiles_of(own_keys(p, b));
+        n += line_of(tiles_of(p, own_keys(p, b)));
     return __reduce_add_sync(0xffffffffu, n);
 }
 
 // The line of tiles: sequence by sequence, within one head unit by head unit
-// (a key/value head and a block of its query heads), cut into pieces that
+// (a key/value head and a block of its query heads), kRowCost empty places before
+// each row, cut into pieces that
 // differ by at most one tile: the first `rest` have one more.  A piece has about
-// kLeast tiles at least: a part of a row costs its join more than a tile costs.
-// There are `waves` times as many pieces where they have kLong tiles then.
+// kLeastKeys at least: a part of a row costs its join more than a tile costs.
+// There are `waves` times as many pieces where they have kLongKeys then.
 struct Cut {
     int pieces, each, rest;
     __device__ __forceinline__ Cut(const Params& p, int total)
-        : pieces(min((total + kLeast - 1) / kLeast,
-                     total / p.waves >= kLong * p.pieces ? p.waves * p.pieces : p.pieces)),
+        : pieces(min((total + least(p, kLeastKeys) - 1) / least(p, kLeastKeys),
+                     total / p.waves >= least(p, kLongKeys) * p.pieces ? p.waves * p.pieces : p.pieces)),
           each(pieces > 0 ? total / pieces : 0),
           rest(pieces > 0 ? total % pieces : 0)
     {
     }
+    static __device__ __forceinline__ int least(const Params& p, int keys) { return max(keys >> tile_shift_of(p), 1); }
     __device__ __forceinline__ int begin(int piece) const { return piece * each + min(piece, rest); }
     __device__ __forceinline__ int piece_of(int tile) const
     {
@@ -83,7 +99,7 @@ struct Place {
 __device__ __forceinline__ void set_row(const Params& p, Place& r)
 {
     r.own = r.b < p.batch ? own_keys(p, r.b) : 0;
-    r.tiles = tiles_of(r.own);
+    r.tiles = tiles_of(p, r.own);
 }
 
 // The next row that has tiles.
@@ -108,7 +124,7 @@ __device__ __forceinline__ bool find_piece(const Params& p, int piece, int& begi
     int mine = 0;
 #pragma unroll 8
     for (int b = first; b < last; ++b)
-        mine += tiles_of(own_keys(p, b));
+        mine += line_of(tiles_of(p, own_keys(p, b)));
     int x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -127,12 +143,12 @@ __device__ __forceinline__ bool find_piece(const Params& p, int piece, int& begi
     if (here) {
         for (r.b = first;; ++r.b) {
             set_row(p, r);
-            if (at < r.tiles * units)
+            if (at < line_of(r.tiles) * units)
                 break;
-            at -= r.tiles * units;
+            at -= line_of(r.tiles) * units;
         }
-        r.unit = at / r.tiles;
-        r.tile = at % r.tiles;
+        r.unit = at / line_of(r.tiles);
+        r.tile = at % line_of(r.tiles) - kRowCost;
     }
     const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
     r.b = __shfl_sync(0xffffffffu, r.b, src);
@@ -140,6 +156,10 @@ __device__ __forceinline__ bool find_piece(const Params& p, int piece, int& begi
     r.tile = __shfl_sync(0xffffffffu, r.tile, src);
     r.own = __shfl_sync(0xffffffffu, r.own, src);
     r.tiles = __shfl_sync(0xffffffffu, r.tiles, src);
+    if (kRowCost > 0) {  // a piece that begins with empty places begins behind them
+        begin += max(-r.tile, 0);
+        r.tile = max(r.tile, 0);
+    }
     return true;
 }
 
@@ -176,13 +196,13 @@ __global__ void __launch_bounds__(256, 4) attn_join_kernel(Params p, Join x)
         return;
     const int b = static_cast<int>(row / p.heads), h = static_cast<int>(row % p.heads);
     const int head = h / p.group, block = h % p.group / x.rows_a_unit, in_block = h % p.group % x.rows_a_unit;
-    const int units = p.kv_heads * p.row_blocks, tiles = tiles_of(own_keys(p, b));
+    const int units = p.kv_heads * p.row_blocks, tiles = tiles_of(p, own_keys(p, b));
     // the pieces that have this row's tiles
     int first_slot = 0, own_parts = 0;
     bool whole = false;
     if (tiles > 0) {
         const Cut cut(p, sum_tiles(p, p.batch) * units);
-        const int t0 = sum_tiles(p, b) * units + (head * p.row_blocks + block) * tiles;
+        const int t0 = sum_tiles(p, b) * units + (head * p.row_blocks + block) * line_of(tiles) + kRowCost;
         const int c0 = cut.piece_of(t0), c1 = cut.piece_of(t0 + tiles - 1);
         whole = c0 == c1;
         if (whole && x.splits == 0) {  // the output is there
@@ -190,10 +210,11 @@ __global__ void __launch_bounds__(256, 4) attn_join_kernel(Params p, Join x)
             return;
         }
         own_parts = c1 - c0 + 1;
-        first_slot = 2 * c0 + (cut.begin(c0) < t0 ? 1 : 0);  // that piece begins with another row
+        first_slot = 2 * c0 + (cut.begin(c0) < t0 - kRowCost ? 1 : 0);  // that piece begins with another row
     }
     const int parts = x.splits + own_parts;
-    grid_dependency_launch();
+    if (kJoinEarly)
+        grid_dependency_launch();
     grid_dependency_wait();
     // part i: its lse and where its sums are; slots first_slot, then 2 (c0 + 1), 2 (c0 + 2), ...
     auto find = [&](int i, const float*& o) {

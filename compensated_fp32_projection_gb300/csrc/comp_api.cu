@@ -366,7 +366,8 @@ comp_status_t comp_device_status(comp_stream_t stream, uint32_t* where)
     const comp_status_t tc = read_and_clear_fault(s, where);
     const comp_status_t attn = read_and_clear_attn_fault(s, where);
     const comp_status_t decode = read_and_clear_decode_fault(s, where);
-    return tc != COMP_OK ? tc : (attn != COMP_OK ? attn : decode);
+    const comp_status_t decode8 = read_and_clear_decode8_fault(s, where);
+    return tc != COMP_OK ? tc : (attn != COMP_OK ? attn : (decode != COMP_OK ? decode : decode8));
 }
 
 const char* comp_status_string(comp_status_t status)

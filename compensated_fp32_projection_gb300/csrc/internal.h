@@ -124,7 +124,7 @@ bool kv_table_ok(int64_t pages, int page_size, int64_t rows, int64_t width, int6
 
 // Attention of single tokens over a cache (arguments validated; batch > 0), and
 // whether its line of tiles can be counted in ints (batch * heads can).
-bool attn_decode_countable(int kv_heads, int page_size, int64_t batch, int heads, int64_t width);
+bool attn_decode_countable(int kv_heads, int page_size, int64_t batch, int heads, int64_t width, int per_row);
 int64_t attn_decode_bytes(const comp_kv_cache_t& cache, int64_t batch, int heads, int64_t shared_pages);
 comp_status_t launch_attn_decode(const comp_kv_cache_t& cache, const float* q, int64_t q_token, int64_t q_head,
                                  int heads, float scale, const int32_t* table, int64_t batch, int64_t width,
@@ -147,6 +147,7 @@ comp_status_t read_and_clear_fault(cudaStream_t stream, uint32_t* where);
 // The same of the attention kernels; `where` is written only if there is a fault.
 comp_status_t read_and_clear_attn_fault(cudaStream_t stream, uint32_t* where);
 comp_status_t read_and_clear_decode_fault(cudaStream_t stream, uint32_t* where);
+comp_status_t read_and_clear_decode8_fault(cudaStream_t stream, uint32_t* where);
 
 // Packed attention (arguments validated; sizes > 0 but total_k) and the
 // workspace it needs for k and v.

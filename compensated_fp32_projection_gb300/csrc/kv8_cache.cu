@@ -139,7 +139,7 @@ struct Source {
 // than 64 and 8 for others.
 template <int STEPS>
 __global__ void __launch_bounds__(kThreads) append8_kernel(const Params p, const Source k, const Source v,
-                                                           const comp_rope_t rope)
+                                                           const comp_rope_t rope, const int wide)
 {
     grid_dependency_launch();
     const comp_kv8_cache_t& c = p.cache;
@@ -170,7 +170,8 @@ __global__ void __launch_bounds__(kThreads) append8_kernel(const Params p, const
                 continue;
             const float* const row = x0 + t * src.token;
             if (turns)
-                x[i] = load_rotated(row, at.d, rope, angles_of(rope, w.position + t), src.vec != 0);
+                x[i] = load_rotated(row, at.d, rope, angles_of(rope, w.position + t), src.vec != 0,
+                                    wide != 0);
             else if (src.vec)
                 x[i] = __ldcs(reinterpret_cast<const float4*>(row + at.d));
             else
@@ -428,12 +429,13 @@ comp_status_t comp_kv8_append_f32(const comp_kv8_cache_t* cache, const float* k,
     const Source ks{k, k_token, k_head, rows_vec(k, k_token, k_head, 4)};
     const Source vs{v, v_token, v_head, rows_vec(v, v_token, v_head, 4)};
     const comp_rope_t r = rope ? *rope : comp_rope_t{};
+    const int wide = angles_wide(r);
     const unsigned grid = grid_of(p.slots * 2 * cache->kv_heads, dev);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (cache->head_dim > 64)
-        append8_kernel<16><<<grid, kThreads, 0, s>>>(p, ks, vs, r);
+        append8_kernel<16><<<grid, kThreads, 0, s>>>(p, ks, vs, r, wide);
     else
-        append8_kernel<8><<<grid, kThreads, 0, s>>>(p, ks, vs, r);
+        append8_kernel<8><<<grid, kThreads, 0, s>>>(p, ks, vs, r, wide);
     return launch_status();
 }
 

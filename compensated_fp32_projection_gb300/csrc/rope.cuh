@@ -22,9 +22,25 @@ __device__ __forceinline__ const float* angles_of(const comp_rope_t& r, int64_t 
     return position >= 0 && position < r.positions ? r.table + position * r.rot : nullptr;
 }
 
+// The angles of two pairs that stand together, (c, s) each.  wide: on 16 bytes.
+__device__ __forceinline__ float4 load_angles(const float* at, bool wide)
+{
+    if (wide)
+        return __ldg(reinterpret_cast<const float4*>(at));
+    const float2 a = __ldg(reinterpret_cast<const float2*>(at)), b = __ldg(reinterpret_cast<const float2*>(at + 2));
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// Whether a position's angles stand on 16 bytes.
+inline bool angles_wide(const comp_rope_t& r)
+{
+    return (reinterpret_cast<uintptr_t>(r.table) & 15u) == 0 && r.rot % 4 == 0;
+}
+
 // Four values of a head from dimension d on (a multiple of 4), rotated: x is the
-// head, `at` the position's angles.  vec: x is 16-byte aligned.
-__device__ __forceinline__ float4 load_rotated(const float* x, int d, const comp_rope_t& r, const float* at, bool vec)
+// head, `at` the position's angles.  vec: x is 16-byte aligned; wide: `at` is.
+__device__ __forceinline__ float4 load_rotated(const float* x, int d, const comp_rope_t& r, const float* at, bool vec,
+                                               bool wide)
 {
     float v[4];
     if (vec) {
@@ -45,14 +61,23 @@ __device__ __forceinline__ float4 load_rotated(const float* x, int d, const comp
                 v[e] = d + e < r.rot ? __int_as_float(0x7fffffff) : v[e];
         } else if (r.interleaved) {
             // rot is even: a pair is rotated or not
+            if (wide) {
+                const float4 cs = load_angles(at + d, true);
+                const float a = v[0], b = v[1], e = v[2], f = v[3];
+                v[0] = turn(a, cs.x, b, cs.y, false);
+                v[1] = turn(b, cs.x, a, cs.y, true);
+                v[2] = turn(e, cs.z, f, cs.w, false);
+                v[3] = turn(f, cs.z, e, cs.w, true);
+            } else {
 #pragma unroll
-            for (int e = 0; e < 4; e += 2)
-                if (d + e < r.rot) {
-                    const float2 cs = __ldg(reinterpret_cast<const float2*>(at + d + e));
-                    const float a = v[e], b = v[e + 1];
-                    v[e] = turn(a, cs.x, b, cs.y, false);
-                    v[e + 1] = turn(b, cs.x, a, cs.y, true);
-                }
+                for (int e = 0; e < 4; e += 2)
+                    if (d + e < r.rot) {
+                        const float2 cs = __ldg(reinterpret_cast<const float2*>(at + d + e));
+                        const float a = v[e], b = v[e + 1];
+                        v[e] = turn(a, cs.x, b, cs.y, false);
+                        v[e + 1] = turn(b, cs.x, a, cs.y, true);
+                    }
+            }
         } else {
             const int half = r.rot / 2;
             if (half % 4 == 0) {  // d and its partners lie in one half each
@@ -71,9 +96,10 @@ __device__ __forceinline__ float4 load_rotated(const float* x, int d, const comp
                         y[e] = __ldg(x + partner + e);
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 cs = __ldg(reinterpret_cast<const float2*>(at + 2 * (i + e)));
+                for (int e = 0; e < 4; e += 2) {
+                    const float4 cs = load_angles(at + 2 * (i + e), wide);
                     v[e] = turn(v[e], cs.x, y[e], cs.y, second);
+                    v[e + 1] = turn(v[e + 1], cs.z, y[e + 1], cs.w, second);
                 }
             } else {
 #pragma unroll

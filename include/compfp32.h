@@ -614,7 +614,8 @@ comp_status_t comp_kv8_read_f16(const comp_kv8_cache_t* cache, uint16_t* k, uint
  * shared prefix; rope (or NULL) rotates each query at its sequence's last position,
  * lengths[b] - 1.  The codes enter the products exactly and a block's scale is
  * applied in binary32 to what its keys gave, so keys and values may have any
- * magnitude as long as the scores stay finite.  Same limits on sizes.
+ * magnitude as long as the scores stay finite.  Same limits on sizes, but that
+ * (width * page_size / 16 + 4) * batch * kv_heads * ceil(group / 16) is below 2^31.
  */
 int64_t comp_attn_decode_f32x8_workspace_bytes(const comp_kv8_cache_t* cache, int64_t batch, int32_t heads,
                                                int64_t width);

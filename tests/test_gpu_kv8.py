@@ -310,6 +310,25 @@ def test_decode_scales_of_any_size(pkg):
     check(pkg, q, cache, table, ints(lens), scale=0.02)
 
 
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("heads", [4, 12])
+def test_decode_what_lies_behind_the_end(pkg, heads, page):
+    """Blocks that no token has been written to may hold anything, NaN for a scale too."""
+    dim = 64
+    cache = pool(30, 1, page, dim)
+    lens = [1, 16, 17, 32, 33, 48, 49, 64, 65]
+    table = rows_of(lens, page, 29, seed=1)
+    table = [r + [29, 29] for r in table]
+    want = pkg.comp_attn_decode_f32x8(torch.ones(9, heads, dim, device="cuda"), *cache, ints(table), ints(lens))
+    for r, n in zip(table, lens):
+        for block in range(-(-n // 16), len(r) * page // 16):
+            p = r[block * 16 // page]
+            for t in cache[2:]:
+                t[p, :, block % (page // 16)] = math.nan
+    got = pkg.comp_attn_decode_f32x8(torch.ones(9, heads, dim, device="cuda"), *cache, ints(table), ints(lens))
+    assert torch.equal(got, want) and not got.isnan().any()
+
+
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("heads", [4, 12])
 def test_decode_with_codes_that_are_not_numbers(pkg, dim, heads):
