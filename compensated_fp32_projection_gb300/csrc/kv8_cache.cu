@@ -13,10 +13,14 @@
 // scale; the sign of the block's scale says that it has such codes, so that the
 // kernels that read look for them in those blocks only.
 //
-// Both kernels stream, 5 bytes a value (6 and 3 with keys and values that are read
-// back as FP16), and HBM is the bound.  A warp takes a block of a head: its 16
-// rows are all loaded before the first is used (up to 64 values a lane, the block
-// passes through registers once), and the maximum is one reduction in the warp.
+// Both kernels stream, 5 bytes a value (3 where values are read back as FP16), and
+// HBM is the bound.  A warp takes a block of a head: its 16 rows are all loaded
+// before the first is used (up to 64 values a lane, the block passes through
+// registers once), and the maximum is one reduction in the warp.  Where a block's
+// tokens and its page are takes some dependent loads, and its positions' angles are
+// the same for all heads: a CTA finds them once for a few blocks (a warp each) and
+// then goes over their heads.  With a search by each warp for its block of a head,
+// 32768 tokens of 8 heads of 128 took 287 us to write and read back, now NNN.
 #include <cuda_fp16.h>
 
 #include <cmath>
@@ -31,7 +35,6 @@ namespace {
 
 constexpr int kBlock = COMP_KV8_BLOCK;
 constexpr int kThreads = 256;
-constexpr uint32_t kNan4 = 0x80808080u;  // four codes of -128
 
 struct Params {
     comp_kv8_cache_t cache;
@@ -100,33 +103,87 @@ __device__ __forceinline__ Work work_of(const Params& p, int64_t slot)
     return w;
 }
 
-// The page that has a position, or -1.
-__device__ __forceinline__ int64_t page_of(const Params& p, const Work& w)
+// The page that has a position, or a negative number.
+__device__ __forceinline__ int64_t page_of(const Params& p, int64_t row, int64_t position)
 {
-    const int64_t col = w.position < 0 || w.row >= p.rows ? p.width : w.position / p.cache.page_size;
-    const int64_t page = col < p.width ? p.table[w.row * p.width + col] : -1;
+    const int64_t col = position < 0 || row >= p.rows ? p.width : position / p.cache.page_size;
+    const int64_t page = col < p.width ? p.table[row * p.width + col] : -1;
     return page < p.cache.pages ? page : -1;
 }
 
-// How a warp goes over a block: lanes_a_row lanes have a row's codes, four each.
+// Blocks that a CTA finds at once.
+constexpr int kMostItems = 4;
+
+struct Item {
+    int64_t row, token0, position, unit;  // unit: of the page's first head; negative: no page
+    int from, to, slot;
+    bool begins;
+};
+
+// By all threads: the CTA's blocks, but for their pages; `count` of them are there.
+__device__ __forceinline__ int find_items(const Params& p, int items, Item* item)
+{
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * items;
+    const int warp = threadIdx.x >> 5;
+    const int count = static_cast<int>(min(static_cast<int64_t>(items), p.slots - first));
+    if (warp < count) {
+        const Work w = work_of(p, first + warp);
+        if ((threadIdx.x & 31) == 0)
+            item[warp] = Item{w.row, w.token0, w.position, -1, w.from, w.to, 0, w.begins};
+    }
+    __syncthreads();
+    return count;
+}
+
+// Then their pages, for the threads that a later __syncthreads orders behind this.
+__device__ __forceinline__ void find_pages(const Params& p, int count, Item* item)
+{
+    if (threadIdx.x < count) {
+        Item& w = item[threadIdx.x];
+        const int64_t page = w.to > w.from ? page_of(p, w.row, w.position) : -1;
+        w.unit = page < 0 ? -1 : page * p.cache.kv_heads;
+        w.slot = page < 0 ? 0 : static_cast<int>(w.position % p.cache.page_size);
+    }
+}
+
+// How a warp goes over a block: `a_row` lanes have a row, `values` each.
 struct Lanes {
     int rows_at_once, row, d;
     bool in;
-    __device__ __forceinline__ explicit Lanes(int dim)
+    __device__ __forceinline__ Lanes(int dim, int values)
     {
-        const int lane = threadIdx.x & 31, a_row = dim / 4;
+        const int lane = threadIdx.x & 31, a_row = dim / values;
         rows_at_once = 32 / a_row;
         row = lane / a_row;
-        d = lane % a_row * 4;
+        d = lane % a_row * values;
         in = row < rows_at_once;
     }
 };
 
-__device__ __forceinline__ int code_of(float x, float inverse)
+// rint(rn(x * inverse)) within +-127, as the low byte of the result: 1.5 2^23 added
+// rounds to a whole number, to nearest even.  (The conversion instructions run at a
+// quarter of that rate and bound the kernel.)
+__device__ __forceinline__ uint32_t code_of(float x, float inverse)
 {
-    if (!(fabsf(x) < INFINITY))
-        return -128;
-    return static_cast<int>(fminf(fmaxf(rintf(__fmul_rn(x, inverse)), -127.0f), 127.0f));
+    const float y = fminf(fmaxf(__fmul_rn(x, inverse), -127.0f), 127.0f);
+    return __float_as_uint(__fadd_rn(y, 12582912.0f));
+}
+
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
+// Byte e of w, a code, as a number: 2^23 + 128 + code by its bits.
+__device__ __forceinline__ float number_of(uint32_t w, int e)
+{
+    return __fadd_rn(__uint_as_float(__byte_perm(w ^ 0x80808080u, 0x4b000000u, 0x7650 + e)), -8388736.0f);
+}
+
+// All bits of the bytes of w that are -128, the code of what is no number.
+__device__ __forceinline__ uint32_t odd_bytes(uint32_t w)
+{
+    return __vcmpeq4(w, 0x80808080u);
 }
 
 struct Source {
@@ -135,33 +192,30 @@ struct Source {
     int vec;
 };
 
+// How keys turn: not at all; pairs side by side, or halves whose partner of four
+// values is four values of another lane; other halves, whose partners are loaded.
+enum Turn { kStill, kPairs, kHalves, kOddHalves };
+
 // STEPS: how often the warp moves on in a block's 16 rows, 16 for heads wider
 // than 64 and 8 for others.
-template <int STEPS>
-__global__ void __launch_bounds__(kThreads) append8_kernel(const Params p, const Source k, const Source v,
-                                                           const comp_rope_t rope, const int wide)
+template <int STEPS, int TURN>
+__global__ void __launch_bounds__(kThreads, 2) append8_kernel(const Params p, const Source k, const Source v,
+                                                              const comp_rope_t rope, const int items)
 {
     grid_dependency_launch();
+    __shared__ Item item[kMostItems];
+    extern __shared__ float2 angles[];  // [items][kBlock][rot / 2]
     const comp_kv8_cache_t& c = p.cache;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-    const int heads = 2 * c.kv_heads, blocks = c.page_size / kBlock;
-    const Lanes at(c.head_dim);
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); u < p.slots * heads;
-         u += warps) {
-        const Work w = work_of(p, u / heads);
-        const int64_t page = w.row < p.rows && w.to > w.from ? page_of(p, w) : -1;
-        if (page < 0)
-            continue;
-        const int head = static_cast<int>(u % heads) / 2, is_v = static_cast<int>(u % 2);
-        const Source& src = is_v ? v : k;
-        const bool turns = !is_v && rope.rot > 0;
-        const int slot = static_cast<int>(w.position % c.page_size);
-        const int64_t unit = page * c.kv_heads + head;
-        int8_t* const codes = (is_v ? c.v : c.k) + (unit * c.page_size + slot) * c.head_dim;
-        float* const scale_at = (is_v ? c.v_scale : c.k_scale) + unit * blocks + slot / kBlock;
-        const float* const x0 = src.x + w.token0 * src.token + head * src.head;
-        const float was = w.begins && w.from > 0 ? *scale_at : 0.0f;
-        float4 x[STEPS];
+    const int heads = 2 * c.kv_heads, blocks = c.page_size / kBlock, half = rope.rot / 2;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int count = find_items(p, items, item);
+    const Lanes at(c.head_dim, 4);
+    float4 x[STEPS];
+    const int units = count * heads;
+    auto load = [&](int u) {
+        const Item& w = item[u / heads];
+        const Source& src = u % 2 ? v : k;
+        const float* const x0 = src.x + w.token0 * src.token + (u % heads / 2) * src.head + at.d;
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
             const int t = i * at.rows_at_once + at.row;
@@ -169,60 +223,144 @@ __global__ void __launch_bounds__(kThreads) append8_kernel(const Params p, const
             if (!at.in || t < w.from || t >= w.to)
                 continue;
             const float* const row = x0 + t * src.token;
-            if (turns)
-                x[i] = load_rotated(row, at.d, rope, angles_of(rope, w.position + t), src.vec != 0,
-                                    wide != 0);
-            else if (src.vec)
-                x[i] = __ldcs(reinterpret_cast<const float4*>(row + at.d));
+            if (src.vec)
+                x[i] = __ldcs(reinterpret_cast<const float4*>(row));
             else
-                x[i] = make_float4(row[at.d], row[at.d + 1], row[at.d + 2], row[at.d + 3]);
+                x[i] = make_float4(row[0], row[1], row[2], row[3]);
         }
-        // the largest finite magnitude; as bits they have the same order
-        float top = 0.0f;
-        bool odd = false;
+    };
+    // the first values, the pages and the angles, none of which needs another
+    if (warp < units)
+        load(warp);
+    find_pages(p, count, item);
+    if constexpr (TURN != kStill) {
+        for (int r = warp; r < count * kBlock; r += kThreads / 32) {
+            const Item& w = item[r / kBlock];
+            const int t = r % kBlock;
+            if (t < w.from || t >= w.to)
+                continue;
+            const float* const row = angles_of(rope, w.position + t);
+            const float nan = __int_as_float(0x7fffffff);
+            for (int i = lane; i < half; i += 32)
+                angles[r * half + i] = row ? __ldg(reinterpret_cast<const float2*>(row) + i) : make_float2(nan, nan);
+        }
+    }
+    __syncthreads();
+    for (int u = warp; u < units; u += kThreads / 32) {
+        if (u != warp)
+            load(u);
+        const Item& w = item[u / heads];
+        if (w.unit < 0)
+            continue;
+        const int head = u % heads / 2, is_v = u % 2;
+        const Source& src = is_v ? v : k;
+        const int64_t unit = w.unit + head;
+        int8_t* const codes = (is_v ? c.v : c.k) + (unit * c.page_size + w.slot) * c.head_dim + at.d;
+        float* const scale_at = (is_v ? c.v_scale : c.k_scale) + unit * blocks + w.slot / kBlock;
+        const bool stays = w.begins && w.from > 0;
+        const float was = stays ? *scale_at : 0.0f;
+        if (TURN != kStill && !is_v) {
+            const float2* const turns = angles + u / heads * kBlock * half;
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-            const float m[4] = {fabsf(x[i].x), fabsf(x[i].y), fabsf(x[i].z), fabsf(x[i].w)};
+            for (int i = 0; i < STEPS; ++i) {
+                const int t = i * at.rows_at_once + at.row;
+                const bool here = at.in && t >= w.from && t < w.to && at.d < rope.rot;
+                float y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                if constexpr (TURN == kPairs) {
+                    if (here)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const bool finite = m[e] < INFINITY;
-                odd |= !finite;
-                top = finite ? fmaxf(top, m[e]) : top;
+                        for (int e = 0; e < 4; e += 2)
+                            if (at.d + e < rope.rot) {
+                                const float2 cs = turns[t * half + (at.d + e) / 2];
+                                const float a = y[e], b = y[e + 1];
+                                y[e] = turn(a, cs.x, b, cs.y, false);
+                                y[e + 1] = turn(b, cs.x, a, cs.y, true);
+                            }
+                } else if constexpr (TURN == kHalves) {
+                    const bool second = at.d >= half;
+                    const int partner = (lane + (second ? -half / 4 : half / 4)) & 31, j = second ? at.d - half : at.d;
+                    const float z[4] = {__shfl_sync(0xffffffffu, y[0], partner), __shfl_sync(0xffffffffu, y[1], partner),
+                                        __shfl_sync(0xffffffffu, y[2], partner), __shfl_sync(0xffffffffu, y[3], partner)};
+                    if (here)
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2) {
+                            const float4 cs = *reinterpret_cast<const float4*>(turns + t * half + j + e);
+                            y[e] = turn(y[e], cs.x, z[e], cs.y, second);
+                            y[e + 1] = turn(y[e + 1], cs.z, z[e + 1], cs.w, second);
+                        }
+                } else {
+                    const float* const row = src.x + (w.token0 + t) * src.token + head * src.head;
+                    if (here)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (at.d + e < rope.rot) {
+                                const bool second = at.d + e >= half;
+                                const int j = second ? at.d + e - half : at.d + e;
+                                const float2 cs = turns[t * half + j];
+                                y[e] = turn(y[e], cs.x, row[second ? j : j + half], cs.y, second);
+                            }
+                }
+                x[i] = make_float4(y[0], y[1], y[2], y[3]);
             }
         }
-        top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-        odd = __any_sync(0xffffffffu, odd) || (__float_as_uint(was) >> 31) != 0;
+        // the largest finite magnitude; as bits they have the same order, and what is no
+        // number is larger
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i)
+            top = max(max(max(top, __float_as_uint(x[i].x) & 0x7fffffffu), __float_as_uint(x[i].y) & 0x7fffffffu),
+                      max(__float_as_uint(x[i].z) & 0x7fffffffu, __float_as_uint(x[i].w) & 0x7fffffffu));
+        top = __reduce_max_sync(0xffffffffu, top);
+        const bool new_odd = top >= 0x7f800000u, odd = new_odd || (__float_as_uint(was) >> 31) != 0;
+        if (new_odd) {
+            top = 0;
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i) {
+                const float m[4] = {fabsf(x[i].x), fabsf(x[i].y), fabsf(x[i].z), fabsf(x[i].w)};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    top = m[e] < INFINITY ? max(top, __float_as_uint(m[e])) : top;
+            }
+            top = __reduce_max_sync(0xffffffffu, top);
+        }
         const float kept = fabsf(was);
-        float scale = __fmul_rn(top, 0x1.020408p-7f);  // 1/127
+        float scale = __fmul_rn(__uint_as_float(top), 0x1.020408p-7f);  // 1/127
         scale = scale < 0x1p-126f ? 0.0f : scale;
         scale = kept > scale ? kept : scale;
         const float inverse = scale > 0.0f ? __frcp_rn(scale) : 0.0f;
-        const bool again = kept != scale && w.begins && w.from > 0;
+        const bool again = stays && kept != scale;
         const float ratio = again && scale > 0.0f ? __fdiv_rn(kept, scale) : 0.0f;
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
             const int t = i * at.rows_at_once + at.row;
-            if (!at.in || t >= w.to || (t < w.from && !again))
+            if (!at.in || t < w.from || t >= w.to)
                 continue;
-            char4* const to = reinterpret_cast<char4*>(codes + static_cast<int64_t>(t) * c.head_dim + at.d);
-            int q[4];
-            if (t < w.from) {
-                const char4 old = *to;
-                const int o[4] = {old.x, old.y, old.z, old.w};
+            uint32_t q = low_bytes(code_of(x[i].x, inverse), code_of(x[i].y, inverse), code_of(x[i].z, inverse),
+                                   code_of(x[i].w, inverse));
+            if (new_odd) {
+                const float m[4] = {fabsf(x[i].x), fabsf(x[i].y), fabsf(x[i].z), fabsf(x[i].w)};
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    q[e] = o[e] == -128 ? -128 : static_cast<int>(rintf(__fmul_rn(static_cast<float>(o[e]), ratio)));
-            } else {
-                q[0] = code_of(x[i].x, inverse);
-                q[1] = code_of(x[i].y, inverse);
-                q[2] = code_of(x[i].z, inverse);
-                q[3] = code_of(x[i].w, inverse);
+                    if (!(m[e] < INFINITY))
+                        q = (q & ~(0xffu << (8 * e))) | (0x80u << (8 * e));
             }
-            *to = make_char4(static_cast<signed char>(q[0]), static_cast<signed char>(q[1]),
-                             static_cast<signed char>(q[2]), static_cast<signed char>(q[3]));
+            *reinterpret_cast<uint32_t*>(codes + t * c.head_dim) = q;
         }
-        if ((threadIdx.x & 31) == 0)
+        if (again) {
+#pragma unroll 4
+            for (int t = at.row; t < w.from; t += at.rows_at_once) {
+                uint32_t* const to = reinterpret_cast<uint32_t*>(codes + t * c.head_dim);
+                if (!at.in)
+                    continue;
+                const uint32_t old = *to, was_odd = odd_bytes(old);
+                const uint32_t q = low_bytes(code_of(number_of(old, 0), ratio), code_of(number_of(old, 1), ratio),
+                                             code_of(number_of(old, 2), ratio), code_of(number_of(old, 3), ratio));
+                *to = (q & ~was_odd) | (0x80808080u & was_odd);
+            }
+        }
+        if (lane == 0)
             *scale_at = odd ? -scale : scale;
+        __syncwarp();
     }
 }
 
@@ -232,47 +370,62 @@ struct Sink {
     int vec;
 };
 
-__device__ __forceinline__ float value_of(int code, float scale)
-{
-    return code == -128 ? __int_as_float(0x7fffffff) : __fmul_rn(static_cast<float>(code), scale);
-}
-
+// STEPS: how often the warp moves on in a block's 16 rows; a lane writes 16 bytes of
+// each, so that it has 4 codes (for binary32) or 8.
 template <typename T, int STEPS>
-__global__ void __launch_bounds__(kThreads) read8_kernel(const Params p, const Sink k, const Sink v)
+__global__ void __launch_bounds__(kThreads, 3) read8_kernel(const Params p, const Sink k, const Sink v, const int items)
 {
+    constexpr int V = 16 / sizeof(T), WORDS = V / 4;
     grid_dependency_launch();
+    __shared__ Item item[kMostItems];
     const comp_kv8_cache_t& c = p.cache;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
     const int heads = 2 * c.kv_heads, blocks = c.page_size / kBlock;
-    const Lanes at(c.head_dim);
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); u < p.slots * heads;
-         u += warps) {
-        const Work w = work_of(p, u / heads);
-        if (w.to <= w.from)
-            continue;
-        const int64_t page = page_of(p, w);  // -1 for tokens of no sequence too: zeros
-        const int head = static_cast<int>(u % heads) / 2, is_v = static_cast<int>(u % 2);
+    const int count = find_items(p, items, item);
+    find_pages(p, count, item);
+    __syncthreads();
+    const Lanes at(c.head_dim, V);
+    for (int u = threadIdx.x >> 5; u < count * heads; u += kThreads / 32) {
+        const Item& w = item[u / heads];
+        const int head = u % heads / 2, is_v = u % 2;
         const Sink& dst = is_v ? v : k;
-        const int slot = page < 0 ? 0 : static_cast<int>(w.position % c.page_size);
-        const int64_t unit = page < 0 ? 0 : page * c.kv_heads + head;
-        const int8_t* const codes = (is_v ? c.v : c.k) + (unit * c.page_size + slot) * c.head_dim;
-        const float scale = page < 0 ? 0.0f : fabsf((is_v ? c.v_scale : c.k_scale)[unit * blocks + slot / kBlock]);
-        char4 q[STEPS];
+        const bool there = w.unit >= 0;  // no page, and tokens of no sequence: zeros
+        const int64_t unit = there ? w.unit + head : 0;
+        const int8_t* const codes = (is_v ? c.v : c.k) + (unit * c.page_size + w.slot) * c.head_dim + at.d;
+        const float held = there ? (is_v ? c.v_scale : c.k_scale)[unit * blocks + w.slot / kBlock] : 0.0f;
+        T* const to0 = static_cast<T*>(dst.x) + w.token0 * dst.token + head * dst.head + at.d;
+        uint32_t q[STEPS][WORDS];
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
             const int t = i * at.rows_at_once + at.row;
-            q[i] = make_char4(0, 0, 0, 0);
-            if (at.in && t >= w.from && t < w.to && page >= 0)
-                q[i] = __ldcs(reinterpret_cast<const char4*>(codes + static_cast<int64_t>(t) * c.head_dim + at.d));
+            const bool in = at.in && t >= w.from && t < w.to && there;
+#pragma unroll
+            for (int j = 0; j < WORDS; ++j)
+                q[i][j] = 0;
+            if (in) {
+                if constexpr (WORDS == 1) {
+                    q[i][0] = __ldcs(reinterpret_cast<const uint32_t*>(codes + t * c.head_dim));
+                } else {
+                    const uint2 f = __ldcs(reinterpret_cast<const uint2*>(codes + t * c.head_dim));
+                    q[i][0] = f.x;
+                    q[i][1] = f.y;
+                }
+            }
         }
+        const float scale = fabsf(held);
+        const bool odd = __float_as_int(held) < 0;
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
             const int t = i * at.rows_at_once + at.row;
             if (!at.in || t < w.from || t >= w.to)
                 continue;
-            T* const to = static_cast<T*>(dst.x) + (w.token0 + t) * dst.token + head * dst.head + at.d;
-            const float x[4] = {value_of(q[i].x, scale), value_of(q[i].y, scale), value_of(q[i].z, scale),
-                                value_of(q[i].w, scale)};
+            T* const to = to0 + t * dst.token;
+            float x[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                x[e] = __fmul_rn(number_of(q[i][e / 4], e % 4), scale);
+                if (odd && ((q[i][e / 4] >> (8 * (e % 4))) & 0xffu) == 0x80u)
+                    x[e] = __int_as_float(0x7fffffff);
+            }
             if constexpr (sizeof(T) == 4) {
                 if (dst.vec) {
                     *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
@@ -280,13 +433,16 @@ __global__ void __launch_bounds__(kThreads) read8_kernel(const Params p, const S
                 }
             } else {
                 if (dst.vec) {
-                    *reinterpret_cast<uint2*>(to) = make_uint2(pack_h2(__floats2half2_rn(x[0], x[1])),
-                                                               pack_h2(__floats2half2_rn(x[2], x[3])));
+                    uint32_t h[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        h[e] = pack_h2(__floats2half2_rn(x[2 * e], x[2 * e + 1]));
+                    *reinterpret_cast<uint4*>(to) = make_uint4(h[0], h[1], h[2], h[3]);
                     continue;
                 }
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < V; ++e)
                 if constexpr (sizeof(T) == 4)
                     to[e] = x[e];
                 else
@@ -295,16 +451,32 @@ __global__ void __launch_bounds__(kThreads) read8_kernel(const Params p, const S
     }
 }
 
-unsigned grid_of(int64_t warps, const DeviceInfo& dev)
+// Blocks for each CTA: as many as give its warps a block of a head each.
+int items_for(int kv_heads)
 {
-    const int64_t most = static_cast<int64_t>(dev.sm_count) * 8, g = (warps + kThreads / 32 - 1) / (kThreads / 32);
-    return static_cast<unsigned>(g < 1 ? 1 : (g > most ? most : g));
+    return kv_heads >= 4 ? 1 : 4 / kv_heads;
 }
 
-// Rows of `elem`-byte values whose parts of four are aligned to their size.
+template <int STEPS>
+void launch_append(const Params& p, const Source& k, const Source& v, const comp_rope_t& r, cudaStream_t s)
+{
+    const int items = items_for(p.cache.kv_heads);  // their angles are 32 KB at most
+    const unsigned grid = static_cast<unsigned>((p.slots + items - 1) / items);
+    const size_t smem = static_cast<size_t>(items) * kBlock * r.rot * sizeof(float);
+    if (r.rot == 0)
+        append8_kernel<STEPS, kStill><<<grid, kThreads, smem, s>>>(p, k, v, r, items);
+    else if (r.interleaved)
+        append8_kernel<STEPS, kPairs><<<grid, kThreads, smem, s>>>(p, k, v, r, items);
+    else if (r.rot % 8 == 0)
+        append8_kernel<STEPS, kHalves><<<grid, kThreads, smem, s>>>(p, k, v, r, items);
+    else
+        append8_kernel<STEPS, kOddHalves><<<grid, kThreads, smem, s>>>(p, k, v, r, items);
+}
+
+// Rows of `elem`-byte values that begin on 16 bytes.
 int rows_vec(const void* x, int64_t token, int64_t head, int elem)
 {
-    return reinterpret_cast<uintptr_t>(x) % (4 * static_cast<uintptr_t>(elem)) == 0 && token % 4 == 0 && head % 4 == 0;
+    return aligned16(x) && token * elem % 16 == 0 && head * elem % 16 == 0;
 }
 
 // The slots of a call; see slot_of_row.  One more for the tokens behind the last sequence.
@@ -350,18 +522,19 @@ comp_status_t read8(const comp_kv8_cache_t* cache, void* k, void* v, int elem, i
     const Params p{*cache, table, cu, start, rows, width, total, slots_of(total, rows, cu)};
     const Sink ks{k, k_token, k_head, rows_vec(k, k_token, k_head, elem)};
     const Sink vs{v, v_token, v_head, rows_vec(v, v_token, v_head, elem)};
-    const unsigned grid = grid_of(p.slots * 2 * cache->kv_heads, dev);
+    const int items = items_for(cache->kv_heads);
+    const unsigned grid = static_cast<unsigned>((p.slots + items - 1) / items);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (elem == 4) {
         if (cache->head_dim > 64)
-            read8_kernel<float, 16><<<grid, kThreads, 0, s>>>(p, ks, vs);
+            read8_kernel<float, 16><<<grid, kThreads, 0, s>>>(p, ks, vs, items);
         else
-            read8_kernel<float, 8><<<grid, kThreads, 0, s>>>(p, ks, vs);
+            read8_kernel<float, 8><<<grid, kThreads, 0, s>>>(p, ks, vs, items);
     } else {
         if (cache->head_dim > 64)
-            read8_kernel<__half, 16><<<grid, kThreads, 0, s>>>(p, ks, vs);
+            read8_kernel<__half, 8><<<grid, kThreads, 0, s>>>(p, ks, vs, items);
         else
-            read8_kernel<__half, 8><<<grid, kThreads, 0, s>>>(p, ks, vs);
+            read8_kernel<__half, 4><<<grid, kThreads, 0, s>>>(p, ks, vs, items);
     }
     return launch_status();
 }
@@ -429,13 +602,11 @@ comp_status_t comp_kv8_append_f32(const comp_kv8_cache_t* cache, const float* k,
     const Source ks{k, k_token, k_head, rows_vec(k, k_token, k_head, 4)};
     const Source vs{v, v_token, v_head, rows_vec(v, v_token, v_head, 4)};
     const comp_rope_t r = rope ? *rope : comp_rope_t{};
-    const int wide = angles_wide(r);
-    const unsigned grid = grid_of(p.slots * 2 * cache->kv_heads, dev);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (cache->head_dim > 64)
-        append8_kernel<16><<<grid, kThreads, 0, s>>>(p, ks, vs, r, wide);
+        launch_append<16>(p, ks, vs, r, s);
     else
-        append8_kernel<8><<<grid, kThreads, 0, s>>>(p, ks, vs, r, wide);
+        launch_append<8>(p, ks, vs, r, s);
     return launch_status();
 }
 

@@ -67,7 +67,7 @@ __device__ __forceinline__ void load_n(const float* p, float (&v)[N])
         v[1] = f.y;
         v[2] = f.z;
         v[3] = f.w;
-    } else if constexpr (N == 2) {
+    } else if constexpr (N == 2) {  // of a half: on 8 bytes; of a pair: anywhere
         v[0] = p[0];
         v[1] = p[1];
     } else {
@@ -90,10 +90,10 @@ __device__ __forceinline__ void store_n(float* p, const float (&v)[N])
 // A unit of work: REST values of a head that do not turn; P pairs that do, N values
 // one after the other (interleaved, N = 2 P) or N = P from each half.  x and out
 // may be the same, so loads are plain ones, all of a unit's before its stores.
-template <int P, bool INTER>
+template <int P, bool INTER, int REST>
 __global__ void __launch_bounds__(kMostThreads) rope_kernel(const Params p)
 {
-    constexpr int N = INTER ? 2 * P : P, REST = N == 4 ? 4 : 1;
+    constexpr int N = INTER ? 2 * P : P;
     grid_dependency_launch();
     const int each = p.units * p.chunks;
     const int half = p.rope.rot / 2;
@@ -155,19 +155,18 @@ __global__ void __launch_bounds__(kMostThreads) rope_kernel(const Params p)
     }
 }
 
-template <int P, bool INTER>
+template <int P, bool INTER, int REST>
 comp_status_t launch_t(Params p, cudaStream_t stream)
 {
-    constexpr int kRest = P * (INTER ? 2 : 1) == 4 ? 4 : 1;
     p.turning = p.rope.rot / 2 / P;
-    p.units = p.turning + (p.dim - p.rope.rot) / kRest;
+    p.units = p.turning + (p.dim - p.rope.rot) / REST;
     p.chunks = (p.heads + kHeads - 1) / kHeads;
     const int64_t each = static_cast<int64_t>(p.units) * p.chunks;
     p.tokens_a_cta = each >= kThreads ? 1 : static_cast<int>(kThreads / each);
     const int64_t ctas = (p.tokens + p.tokens_a_cta - 1) / p.tokens_a_cta;
     const int64_t work = each * p.tokens_a_cta;
     const int threads = static_cast<int>(work < kMostThreads ? (work + 31) / 32 * 32 : kMostThreads);
-    rope_kernel<P, INTER><<<static_cast<unsigned>(ctas), threads, 0, stream>>>(p);
+    rope_kernel<P, INTER, REST><<<static_cast<unsigned>(ctas), threads, 0, stream>>>(p);
     return launch_status();
 }
 
@@ -244,15 +243,18 @@ comp_status_t comp_rope_f32(const comp_rope_t* rope, const float* x, int64_t x_t
     p.dim = head_dim;
     p.inverse = inverse != 0;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // four values at once where every row begins on 16 bytes and its parts are multiples of four
+    // four values at once where every row begins on 16 bytes and its parts are multiples
+    // of four (of two for each half)
     const auto rows16 = [](const float* at, int64_t token, int64_t head) {
         return aligned16(at) && token % 4 == 0 && head % 4 == 0;
     };
     const bool vec = rows16(x, x_token, x_head) && rows16(out, out_token, out_head) && head_dim % 4 == 0 &&
-                     rope->rot % (rope->interleaved ? 4 : 8) == 0;
+                     rope->rot % 4 == 0;
     if (rope->interleaved)
-        return vec ? launch_t<2, true>(p, s) : launch_t<1, true>(p, s);
-    return vec ? launch_t<4, false>(p, s) : launch_t<1, false>(p, s);
+        return vec ? launch_t<2, true, 4>(p, s) : launch_t<1, true, 1>(p, s);
+    if (!vec)
+        return launch_t<1, false, 1>(p, s);
+    return rope->rot % 8 == 0 ? launch_t<4, false, 4>(p, s) : launch_t<2, false, 4>(p, s);
 }
 
 }  // extern "C"
