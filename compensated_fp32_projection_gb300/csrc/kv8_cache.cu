@@ -25,6 +25,7 @@
 
 #include <cmath>
 
+#include "attn.h"
 #include "internal.h"
 #include "ptx.cuh"
 #include "rope.cuh"
@@ -160,24 +161,40 @@ struct Lanes {
     }
 };
 
-// rint(rn(x * inverse)) within +-127, as the low byte of the result: 1.5 2^23 added
-// rounds to a whole number, to nearest even.  (The conversion instructions run at a
-// quarter of that rate and bound the kernel.)
-__device__ __forceinline__ uint32_t code_of(float x, float inverse)
+// rint(rn(x * inverse)) as the low byte of the result, two values: 1.5 2^23 added rounds
+// to a whole number, to nearest even.  (The conversion instructions run at a quarter of
+// that rate and bounded the kernel.)  No value leaves +-127: inverse is within 2^-23 of
+// 127 over the block's largest, or of 1 over a larger scale.
+__device__ __forceinline__ uint64_t codes_of(float x, float y, float inverse)
 {
-    const float y = fminf(fmaxf(__fmul_rn(x, inverse), -127.0f), 127.0f);
-    return __float_as_uint(__fadd_rn(y, 12582912.0f));
+    // two products one by one: the compiler fuses a packed one with the addition
+    return add2(f2_bits(__fmul_rn(x, inverse), __fmul_rn(y, inverse)), f2_bits(12582912.0f, 12582912.0f));
 }
 
-__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+// Four values' codes.
+__device__ __forceinline__ uint32_t codes_of(const float4& x, float inverse)
 {
-    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+    const uint64_t a = codes_of(x.x, x.y, inverse), b = codes_of(x.z, x.w, inverse);
+    return __byte_perm(__byte_perm(static_cast<uint32_t>(a), static_cast<uint32_t>(a >> 32), 0x0040),
+                       __byte_perm(static_cast<uint32_t>(b), static_cast<uint32_t>(b >> 32), 0x0040), 0x5410);
 }
 
-// Byte e of w, a code, as a number: 2^23 + 128 + code by its bits.
-__device__ __forceinline__ float number_of(uint32_t w, int e)
+// The largest magnitude of three; NaN if one of them is.
+__device__ __forceinline__ float largest(float a, float b, float c)
 {
-    return __fadd_rn(__uint_as_float(__byte_perm(w ^ 0x80808080u, 0x4b000000u, 0x7650 + e)), -8388736.0f);
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Four codes as numbers: 2^23 + 128 + code by its bits.
+__device__ __forceinline__ float4 numbers_of(uint32_t w, float scale)
+{
+    const uint32_t u = w ^ 0x80808080u;
+    const uint64_t bias = f2_bits(-8388736.0f, -8388736.0f), s = f2_bits(scale, scale);
+    const uint64_t a = mul2(add2(u2_bits(__byte_perm(u, 0x4b000000u, 0x7650), __byte_perm(u, 0x4b000000u, 0x7651)), bias), s);
+    const uint64_t b = mul2(add2(u2_bits(__byte_perm(u, 0x4b000000u, 0x7652), __byte_perm(u, 0x4b000000u, 0x7653)), bias), s);
+    return make_float4(lo_f(a), hi_f(a), lo_f(b), hi_f(b));
 }
 
 // All bits of the bytes of w that are -128, the code of what is no number.
@@ -212,21 +229,31 @@ __global__ void __launch_bounds__(kThreads, 2) append8_kernel(const Params p, co
     const Lanes at(c.head_dim, 4);
     float4 x[STEPS];
     const int units = count * heads;
+    // All 16 rows are new, in places that vector loads take, and the steps fit them.
+    auto whole_of = [&](const Item& w, const Source& src) {
+        return w.from == 0 && w.to == kBlock && src.vec && STEPS * at.rows_at_once == kBlock;
+    };
     auto load = [&](int u) {
         const Item& w = item[u / heads];
         const Source& src = u % 2 ? v : k;
-        const float* const x0 = src.x + w.token0 * src.token + (u % heads / 2) * src.head + at.d;
+        const float* row = src.x + (w.token0 + at.row) * src.token + (u % heads / 2) * src.head + at.d;
+        const int64_t step = at.rows_at_once * src.token;
+        if (whole_of(w, src)) {
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-            const int t = i * at.rows_at_once + at.row;
-            x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (!at.in || t < w.from || t >= w.to)
-                continue;
-            const float* const row = x0 + t * src.token;
-            if (src.vec)
-                x[i] = __ldcs(reinterpret_cast<const float4*>(row));
-            else
-                x[i] = make_float4(row[0], row[1], row[2], row[3]);
+            for (int i = 0; i < STEPS; ++i, row += step)
+                x[i] = at.in ? __ldcs(reinterpret_cast<const float4*>(row)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i, row += step) {
+                const int t = i * at.rows_at_once + at.row;
+                x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (!at.in || t < w.from || t >= w.to)
+                    continue;
+                if (src.vec)
+                    x[i] = __ldcs(reinterpret_cast<const float4*>(row));
+                else
+                    x[i] = make_float4(row[0], row[1], row[2], row[3]);
+            }
         }
     };
     // the first values, the pages and the angles, none of which needs another
@@ -303,59 +330,64 @@ __global__ void __launch_bounds__(kThreads, 2) append8_kernel(const Params p, co
                 x[i] = make_float4(y[0], y[1], y[2], y[3]);
             }
         }
-        // the largest finite magnitude; as bits they have the same order, and what is no
-        // number is larger
-        uint32_t top = 0;
+        // the largest finite magnitude; not negative, it has the order of its bits
+        float top = 0.0f;
 #pragma unroll
         for (int i = 0; i < STEPS; ++i)
-            top = max(max(max(top, __float_as_uint(x[i].x) & 0x7fffffffu), __float_as_uint(x[i].y) & 0x7fffffffu),
-                      max(__float_as_uint(x[i].z) & 0x7fffffffu, __float_as_uint(x[i].w) & 0x7fffffffu));
-        top = __reduce_max_sync(0xffffffffu, top);
-        const bool new_odd = top >= 0x7f800000u, odd = new_odd || (__float_as_uint(was) >> 31) != 0;
+            top = largest(largest(top, x[i].x, x[i].y), x[i].z, x[i].w);
+        const bool new_odd = __any_sync(0xffffffffu, !(top < INFINITY));
+        const bool odd = new_odd || (__float_as_uint(was) >> 31) != 0;
         if (new_odd) {
-            top = 0;
+            top = 0.0f;
 #pragma unroll
             for (int i = 0; i < STEPS; ++i) {
                 const float m[4] = {fabsf(x[i].x), fabsf(x[i].y), fabsf(x[i].z), fabsf(x[i].w)};
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    top = m[e] < INFINITY ? max(top, __float_as_uint(m[e])) : top;
+                    top = m[e] < INFINITY ? fmaxf(top, m[e]) : top;
             }
-            top = __reduce_max_sync(0xffffffffu, top);
         }
+        top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
         const float kept = fabsf(was);
-        float scale = __fmul_rn(__uint_as_float(top), 0x1.020408p-7f);  // 1/127
+        float scale = __fmul_rn(top, 0x1.020408p-7f);  // 1/127
         scale = scale < 0x1p-126f ? 0.0f : scale;
         scale = kept > scale ? kept : scale;
         const float inverse = scale > 0.0f ? __frcp_rn(scale) : 0.0f;
         const bool again = stays && kept != scale;
         const float ratio = again && scale > 0.0f ? __fdiv_rn(kept, scale) : 0.0f;
+        int8_t* to = codes + at.row * c.head_dim;
+        const int step = at.rows_at_once * c.head_dim;
+        if (whole_of(w, src) && !new_odd) {
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-            const int t = i * at.rows_at_once + at.row;
-            if (!at.in || t < w.from || t >= w.to)
-                continue;
-            uint32_t q = low_bytes(code_of(x[i].x, inverse), code_of(x[i].y, inverse), code_of(x[i].z, inverse),
-                                   code_of(x[i].w, inverse));
-            if (new_odd) {
-                const float m[4] = {fabsf(x[i].x), fabsf(x[i].y), fabsf(x[i].z), fabsf(x[i].w)};
+            for (int i = 0; i < STEPS; ++i, to += step)
+                if (at.in)
+                    *reinterpret_cast<uint32_t*>(to) = codes_of(x[i], inverse);
+        } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (!(m[e] < INFINITY))
-                        q = (q & ~(0xffu << (8 * e))) | (0x80u << (8 * e));
+            for (int i = 0; i < STEPS; ++i, to += step) {
+                const int t = i * at.rows_at_once + at.row;
+                if (!at.in || t < w.from || t >= w.to)
+                    continue;
+                uint32_t q = codes_of(x[i], inverse);
+                if (new_odd) {
+                    const float m[4] = {fabsf(x[i].x), fabsf(x[i].y), fabsf(x[i].z), fabsf(x[i].w)};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (!(m[e] < INFINITY))
+                            q = (q & ~(0xffu << (8 * e))) | (0x80u << (8 * e));
+                }
+                *reinterpret_cast<uint32_t*>(to) = q;
             }
-            *reinterpret_cast<uint32_t*>(codes + t * c.head_dim) = q;
         }
         if (again) {
 #pragma unroll 4
             for (int t = at.row; t < w.from; t += at.rows_at_once) {
-                uint32_t* const to = reinterpret_cast<uint32_t*>(codes + t * c.head_dim);
+                uint32_t* const stays_at = reinterpret_cast<uint32_t*>(codes + t * c.head_dim);
                 if (!at.in)
                     continue;
-                const uint32_t old = *to, was_odd = odd_bytes(old);
-                const uint32_t q = low_bytes(code_of(number_of(old, 0), ratio), code_of(number_of(old, 1), ratio),
-                                             code_of(number_of(old, 2), ratio), code_of(number_of(old, 3), ratio));
-                *to = (q & ~was_odd) | (0x80808080u & was_odd);
+                const uint32_t old = *stays_at, was_odd = odd_bytes(old);
+                const uint32_t q = codes_of(numbers_of(old, 1.0f), ratio);
+                *stays_at = (q & ~was_odd) | (0x80808080u & was_odd);
             }
         }
         if (lane == 0)
@@ -394,59 +426,90 @@ __global__ void __launch_bounds__(kThreads, 3) read8_kernel(const Params p, cons
         const float held = there ? (is_v ? c.v_scale : c.k_scale)[unit * blocks + w.slot / kBlock] : 0.0f;
         T* const to0 = static_cast<T*>(dst.x) + w.token0 * dst.token + head * dst.head + at.d;
         uint32_t q[STEPS][WORDS];
+        auto fetch = [&](uint32_t(&f)[WORDS], const int8_t* from) {
+            if constexpr (WORDS == 1) {
+                f[0] = __ldcs(reinterpret_cast<const uint32_t*>(from));
+            } else {
+                const uint2 two = __ldcs(reinterpret_cast<const uint2*>(from));
+                f[0] = two.x;
+                f[1] = two.y;
+            }
+        };
+        auto write = [&](T* to, const float4(&x)[WORDS]) {
+            if constexpr (sizeof(T) == 4)
+                *reinterpret_cast<float4*>(to) = x[0];
+            else
+                *reinterpret_cast<uint4*>(to) =
+                    make_uint4(pack_h2(__floats2half2_rn(x[0].x, x[0].y)), pack_h2(__floats2half2_rn(x[0].z, x[0].w)),
+                               pack_h2(__floats2half2_rn(x[WORDS - 1].x, x[WORDS - 1].y)),
+                               pack_h2(__floats2half2_rn(x[WORDS - 1].z, x[WORDS - 1].w)));
+        };
+        const float scale = fabsf(held);
+        const int8_t* from = codes + at.row * c.head_dim;
+        T* to = to0 + at.row * dst.token;
+        const int step = at.rows_at_once * c.head_dim;
+        const int64_t to_step = at.rows_at_once * dst.token;
+        // all 16 rows, numbers all of them, to places that vector stores take
+        if (w.from == 0 && w.to == kBlock && there && dst.vec && STEPS * at.rows_at_once == kBlock) {
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-            const int t = i * at.rows_at_once + at.row;
-            const bool in = at.in && t >= w.from && t < w.to && there;
+            for (int i = 0; i < STEPS; ++i, from += step) {
 #pragma unroll
-            for (int j = 0; j < WORDS; ++j)
-                q[i][j] = 0;
-            if (in) {
-                if constexpr (WORDS == 1) {
-                    q[i][0] = __ldcs(reinterpret_cast<const uint32_t*>(codes + t * c.head_dim));
-                } else {
-                    const uint2 f = __ldcs(reinterpret_cast<const uint2*>(codes + t * c.head_dim));
-                    q[i][0] = f.x;
-                    q[i][1] = f.y;
+                for (int j = 0; j < WORDS; ++j)
+                    q[i][j] = 0;
+                if (at.in)
+                    fetch(q[i], from);
+            }
+            if (__float_as_int(held) >= 0) {
+#pragma unroll
+                for (int i = 0; i < STEPS; ++i, to += to_step) {
+                    float4 x[WORDS];
+#pragma unroll
+                    for (int j = 0; j < WORDS; ++j)
+                        x[j] = numbers_of(q[i][j], scale);
+                    if (at.in)
+                        write(to, x);
                 }
+                continue;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i, from += step) {
+                const int t = i * at.rows_at_once + at.row;
+#pragma unroll
+                for (int j = 0; j < WORDS; ++j)
+                    q[i][j] = 0;
+                if (at.in && t >= w.from && t < w.to && there)
+                    fetch(q[i], from);
             }
         }
-        const float scale = fabsf(held);
-        const bool odd = __float_as_int(held) < 0;
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
+        for (int i = 0; i < STEPS; ++i, to += to_step) {
             const int t = i * at.rows_at_once + at.row;
             if (!at.in || t < w.from || t >= w.to)
                 continue;
-            T* const to = to0 + t * dst.token;
-            float x[V];
+            float4 x[WORDS];
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                x[e] = __fmul_rn(number_of(q[i][e / 4], e % 4), scale);
-                if (odd && ((q[i][e / 4] >> (8 * (e % 4))) & 0xffu) == 0x80u)
-                    x[e] = __int_as_float(0x7fffffff);
+            for (int j = 0; j < WORDS; ++j) {
+                x[j] = numbers_of(q[i][j], scale);
+                const uint32_t odd = odd_bytes(q[i][j]);
+                const float nan = __int_as_float(0x7fffffff);
+                x[j] = make_float4(odd & 0xffu ? nan : x[j].x, odd & 0xff00u ? nan : x[j].y,
+                                   odd & 0xff0000u ? nan : x[j].z, odd >> 24 ? nan : x[j].w);
             }
-            if constexpr (sizeof(T) == 4) {
-                if (dst.vec) {
-                    *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
-                    continue;
-                }
-            } else {
-                if (dst.vec) {
-                    uint32_t h[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        h[e] = pack_h2(__floats2half2_rn(x[2 * e], x[2 * e + 1]));
-                    *reinterpret_cast<uint4*>(to) = make_uint4(h[0], h[1], h[2], h[3]);
-                    continue;
-                }
+            if (dst.vec) {
+                write(to, x);
+                continue;
             }
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                if constexpr (sizeof(T) == 4)
-                    to[e] = x[e];
-                else
-                    to[e] = __float2half_rn(x[e]);
+            for (int j = 0; j < WORDS; ++j) {
+                const float y[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if constexpr (sizeof(T) == 4)
+                        to[4 * j + e] = y[e];
+                    else
+                        to[4 * j + e] = __float2half_rn(y[e]);
+            }
         }
     }
 }
