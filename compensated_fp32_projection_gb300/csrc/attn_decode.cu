@@ -33,6 +33,7 @@ namespace compfp32 {
 namespace {
 constexpr int kTileShift = 4;
 constexpr int kTile = 1 << kTileShift;  // keys of a tile, the k of a product
+constexpr int kLeastKeys = 64;
 constexpr int kRowCost = 0;
 constexpr bool kJoinEarly = true;
 }

@@ -10,14 +10,17 @@
 // A product over a block's 16 keys starts afresh and is added up in FP32 registers.
 //
 // Products.  With half the bytes of the FP16 cache, time is as short for the
-// arithmetic, so the keys are the 16 rows of an m16n8k16 product and the columns
-// are four query heads, hi and lo of each side by side (the FP16 kernel has the
-// heads in the rows, eight of them, half empty where four share a key head):
-//   S^T = K q^T      a lane has two keys of one head, hi and lo sums together;
-//   O^T = V^T p^T    a lane has DP/8 dimensions of one head, likewise.
-// The weights go from one layout to the other by one transposition of 8 x 8 FP16
-// values each (movmatrix).  With four heads a key head, 48 sequences of 129 to 6001
-// tokens take 44 us where rows of eight heads take 51.
+// arithmetic, so the keys are the 16 rows of an m16n8k16 product and the eight
+// columns are query heads (the FP16 kernel has eight heads in the rows, hi and lo):
+//   S^T = K q^T      a lane has two keys of a head (or of two);
+//   O^T = V^T p^T    a lane has DP/8 dimensions of it.
+// The weights go from one layout to the other by a transposition of 8 x 8 FP16
+// values (movmatrix).  Where up to four heads share a key head, hi and lo of each
+// stand side by side (Four): half the products, weights and sums of rows of eight
+// heads, 48 sequences of 129 to 6001 tokens take 44 us instead of 51.  Otherwise the
+// columns are eight heads, hi in one product and lo in another, and a lane has two
+// heads side by side for packed arithmetic (Eight): 16 sequences of 20001 to 65536
+// tokens with 16 heads a key head take 175 us, as two Fours for each eight 199.
 //
 // Layout.  The sum over the head dimension may go in any order, and so may the
 // rows of the output and the keys of a block: a lane's operands are 16 codes that
@@ -38,6 +41,7 @@
 namespace compfp32 {
 namespace {
 constexpr int kTileShift = 0;       // a tile's size goes by the heads: see Cfg
+constexpr int kLeastKeys = 32;      // a sequence of 777 alone takes 12.3 us, with 64 12.7, with 128 13.4
 // A row's beginning (its queries, rotated and split, and its end) takes the time of
 // some tiles: 96 sequences of 33 to 2500 tokens of 16 heads of 64 take 30 us, 45 if
 // rows count by their keys alone (31 with 3, 33 with 4).
@@ -61,12 +65,13 @@ namespace {
 constexpr int kRunKeys = 1024;  // keys that are added up before they are added to the sums so far, as in the FP16 kernel
 constexpr uint32_t kFaultDecode8 = 0xB01;
 
-// DP: head dimension padded to 64 or 128; NT: products' columns, four query heads each.
+// DP: head dimension padded to 64 or 128; NT: query heads of a warp, in fours.
 // A tile is some blocks of 16 keys.  What a tile costs whatever its size (waits, loads,
 // the maximum) is some 190 instructions, a block's products and conversions are 300 to
 // 400, so larger tiles are faster until the SM waits for their loads: with four heads of
-// 128 tiles of 32 keys take 41 us where 64 take 44 (48 ragged sequences); with one head
-// of 64, 132 where 64 take 117, with 16 of 128, 202 where 64 take 191 (16 long ones).
+// 128 tiles of 32 keys take 41 us where 64 take 44 (48 ragged sequences), with eight 31
+// and 34; with one head of 64, 129 where 64 take 108, with 16 of 128, 179 where 64
+// take 175 (16 long ones).
 // One stage each for keys and values is enough, each filled again as soon as it has been
 // read, as the other is: two stages take 42 us (ragged) and 133 where one takes 124
 // (eight heads, long).
@@ -191,6 +196,238 @@ __device__ __forceinline__ bool has_odd(float scale)
     return __float_as_int(scale) < 0;
 }
 
+// A query head's values in a lane: step 4 j + w of the head dimension takes word w of the
+// lane's codes, whose four stand in the order 0, 2, 1, 3.
+__device__ __forceinline__ void split_step(const float4& x, uint32_t (&hi)[2], uint32_t (&lo)[2])
+{
+    split2(x.x, x.z, hi[0], lo[0]);
+    split2(x.y, x.w, hi[1], lo[1]);
+}
+
+__device__ __forceinline__ float warp_max_of_places(float x)
+{
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+
+__device__ __forceinline__ float warp_sum_of_places(float x)
+{
+    x += __shfl_xor_sync(0xffffffffu, x, 4);
+    x += __shfl_xor_sync(0xffffffffu, x, 8);
+    return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
+
+// Up to four query heads: hi and lo of each side by side in a product's eight columns.
+// A lane has head quad's scores of its two keys, its part of the sum, DP/8 dimensions.
+template <int DP, int BLOCKS>
+struct Four {
+    static constexpr int kHeads = 1;                    // of a lane
+    uint32_t q[DP / 16][2], pb[BLOCKS][2];
+    float s[2][4], x[BLOCKS][2], m, l;
+    uint64_t o[DP / 16];
+
+    static __device__ __forceinline__ int q_head(int lane) { return lane >> 3; }
+    static __device__ __forceinline__ int out_head(int quad, int) { return quad; }
+    __device__ __forceinline__ void put(int k, const float4& v, int g)
+    {
+        uint32_t hi[2], lo[2];
+        split_step(v, hi, lo);
+        q[k][0] = g & 1 ? lo[0] : hi[0];
+        q[k][1] = g & 1 ? lo[1] : hi[1];
+    }
+    __device__ __forceinline__ void reset()
+    {
+        m = -INFINITY;
+        l = 0.0f;
+#pragma unroll
+        for (int d = 0; d < DP / 16; ++d)
+            o[d] = 0;
+    }
+    __device__ __forceinline__ void begin_scores()
+    {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            s[0][e] = s[1][e] = 0.0f;
+    }
+    // two chains, the even and the odd steps
+    __device__ __forceinline__ void score(int k, const uint32_t (&a)[4]) { mma16816_free(s[k & 1], a, q[k][0], q[k][1]); }
+    __device__ __forceinline__ void end_scores(int b, float kc)
+    {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint64_t both = add2(f2_bits(s[0][2 * e], s[0][2 * e + 1]), f2_bits(s[1][2 * e], s[1][2 * e + 1]));
+            x[b][e] = __fmul_rn(fmaf(hi_f(both), 0x1p-10f, lo_f(both)), kc);
+        }
+    }
+    __device__ __forceinline__ void set_score(int b, int e, float v) { x[b][e] = v; }
+    // 2^14 p as the values' products take them; the sums so far follow the maximum
+    __device__ __forceinline__ void weights()
+    {
+        float top = fmaxf(x[0][0], x[0][1]);
+#pragma unroll
+        for (int b = 1; b < BLOCKS; ++b)
+            top = fmaxf(top, fmaxf(x[b][0], x[b][1]));
+        const float m_new = fmaxf(m, warp_max_of_places(top)), shift = m_new == -INFINITY ? 0.0f : m_new;
+        if (__any_sync(0xffffffffu, m_new > m)) {  // rare after some tiles
+            const float alpha = ex2(m - shift);
+            l *= alpha;
+#pragma unroll
+            for (int d = 0; d < DP / 16; ++d)
+                o[d] = mul2(o[d], f2_bits(alpha, alpha));
+        }
+        m = m_new;
+        float sum = 0.0f;
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b) {
+            // each step rounded as the maximum was, or large scores would not end at 0
+            const uint64_t e = add2(add2(f2_bits(x[b][0], x[b][1]), f2_bits(-shift, -shift)), f2_bits(14.0f, 14.0f));
+            const float w0 = ex2(lo_f(e)), w1 = ex2(hi_f(e));
+            uint32_t hi, lo;
+            split_p(w0, w1, hi, lo);
+            pb[b][0] = transposed(__byte_perm(hi, lo, 0x5410));
+            pb[b][1] = transposed(__byte_perm(hi, lo, 0x7632));
+            sum += w0 + w1;
+        }
+        l += sum;
+    }
+    // dimensions 2 d and 2 d + 1 of a block
+    __device__ __forceinline__ void value(int b, int d, const uint32_t (&a)[4], float vs)
+    {
+        float y[4] = {};
+        mma16816_free(y, a, pb[b][0], pb[b][1]);
+        o[d] = fma2(f2_bits(y[0] + y[1], y[2] + y[3]), f2_bits(vs, vs), o[d]);
+    }
+    // dimensions 4 j .. 4 j + 3 of the lane's head
+    __device__ __forceinline__ float4 four(int j, int) const
+    {
+        return make_float4(lo_f(o[2 * j]), hi_f(o[2 * j]), lo_f(o[2 * j + 1]), hi_f(o[2 * j + 1]));
+    }
+    __device__ __forceinline__ void set_four(int j, int, const float4& v)
+    {
+        o[2 * j] = f2_bits(v.x, v.y);
+        o[2 * j + 1] = f2_bits(v.z, v.w);
+    }
+    __device__ __forceinline__ float2 sums(int) const { return make_float2(m, l); }
+    __device__ __forceinline__ void set_sum(int, float v) { l = v; }
+};
+
+// Up to eight query heads: a product's eight columns are hi of all, another's lo.  A lane
+// has the heads 2 quad and 2 quad + 1 side by side, so that most operations do two.
+template <int DP, int BLOCKS>
+struct Eight {
+    static constexpr int kHeads = 2;
+    uint32_t q[DP / 16][2][2], pb[BLOCKS][2][2];        // hi, lo
+    float s[2][4];
+    uint64_t x[BLOCKS][2], m, l, o[DP / 16][2];
+
+    static __device__ __forceinline__ int q_head(int lane) { return lane >> 2; }
+    static __device__ __forceinline__ int out_head(int quad, int h) { return quad * 2 + h; }
+    __device__ __forceinline__ void put(int k, const float4& v, int) { split_step(v, q[k][0], q[k][1]); }
+    __device__ __forceinline__ void reset()
+    {
+        m = f2_bits(-INFINITY, -INFINITY);
+        l = 0;
+#pragma unroll
+        for (int d = 0; d < DP / 16; ++d)
+            o[d][0] = o[d][1] = 0;
+    }
+    __device__ __forceinline__ void begin_scores()
+    {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            s[0][e] = s[1][e] = 0.0f;
+    }
+    // two chains, hi and lo
+    __device__ __forceinline__ void score(int k, const uint32_t (&a)[4])
+    {
+        mma16816_free(s[0], a, q[k][0][0], q[k][0][1]);
+        mma16816_free(s[1], a, q[k][1][0], q[k][1][1]);
+    }
+    __device__ __forceinline__ void end_scores(int b, float kc)
+    {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            x[b][e] = mul2(fma2(f2_bits(s[1][2 * e], s[1][2 * e + 1]), f2_bits(0x1p-10f, 0x1p-10f),
+                                f2_bits(s[0][2 * e], s[0][2 * e + 1])),
+                           f2_bits(kc, kc));
+    }
+    __device__ __forceinline__ void set_score(int b, int e, float v) { x[b][e] = f2_bits(v, v); }
+    __device__ __forceinline__ void weights()
+    {
+        float top0 = fmaxf(lo_f(x[0][0]), lo_f(x[0][1])), top1 = fmaxf(hi_f(x[0][0]), hi_f(x[0][1]));
+#pragma unroll
+        for (int b = 1; b < BLOCKS; ++b) {
+            top0 = fmaxf(top0, fmaxf(lo_f(x[b][0]), lo_f(x[b][1])));
+            top1 = fmaxf(top1, fmaxf(hi_f(x[b][0]), hi_f(x[b][1])));
+        }
+        const float m0 = fmaxf(lo_f(m), warp_max_of_places(top0)), m1 = fmaxf(hi_f(m), warp_max_of_places(top1));
+        const float shift0 = m0 == -INFINITY ? 0.0f : m0, shift1 = m1 == -INFINITY ? 0.0f : m1;
+        if (__any_sync(0xffffffffu, m0 > lo_f(m) || m1 > hi_f(m))) {
+            const uint64_t alpha = f2_bits(ex2(lo_f(m) - shift0), ex2(hi_f(m) - shift1));
+            l = mul2(l, alpha);
+#pragma unroll
+            for (int d = 0; d < DP / 16; ++d) {
+                o[d][0] = mul2(o[d][0], alpha);
+                o[d][1] = mul2(o[d][1], alpha);
+            }
+        }
+        m = f2_bits(m0, m1);
+        const uint64_t shift = f2_bits(-shift0, -shift1);
+        uint64_t sum = 0;
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint64_t y = add2(add2(x[b][e], shift), f2_bits(14.0f, 14.0f));
+                const float w0 = ex2(lo_f(y)), w1 = ex2(hi_f(y));
+                uint32_t hi, lo;
+                split_p(w0, w1, hi, lo);
+                pb[b][0][e] = transposed(hi);
+                pb[b][1][e] = transposed(lo);
+                sum = add2(sum, f2_bits(w0, w1));
+            }
+        l = add2(l, sum);
+    }
+    // hi and lo have no scale between them and add up in one product's sums
+    __device__ __forceinline__ void value(int b, int d, const uint32_t (&a)[4], float vs)
+    {
+        float y[4] = {};
+        mma16816_free(y, a, pb[b][1][0], pb[b][1][1]);
+        mma16816_free(y, a, pb[b][0][0], pb[b][0][1]);
+        o[d][0] = fma2(f2_bits(y[0], y[1]), f2_bits(vs, vs), o[d][0]);
+        o[d][1] = fma2(f2_bits(y[2], y[3]), f2_bits(vs, vs), o[d][1]);
+    }
+    static __device__ __forceinline__ float part(uint64_t v, int h) { return h ? hi_f(v) : lo_f(v); }
+    __device__ __forceinline__ float4 four(int j, int h) const
+    {
+        return make_float4(part(o[2 * j][0], h), part(o[2 * j][1], h), part(o[2 * j + 1][0], h), part(o[2 * j + 1][1], h));
+    }
+    __device__ __forceinline__ void set_four(int j, int h, const float4& v)
+    {
+        const float y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            uint64_t& to = o[2 * j + e / 2][e % 2];
+            to = h ? f2_bits(lo_f(to), y[e]) : f2_bits(y[e], hi_f(to));
+        }
+    }
+    __device__ __forceinline__ float2 sums(int h) const { return make_float2(part(m, h), part(l, h)); }
+    __device__ __forceinline__ void set_sum(int h, float v) { l = h ? f2_bits(lo_f(l), v) : f2_bits(v, hi_f(l)); }
+};
+
+template <int DP, int NT, int BLOCKS>
+struct MathOf {
+    using T = Eight<DP, BLOCKS>;
+    static constexpr int kSets = NT / 2, kSetHeads = 8;
+};
+
+template <int DP, int BLOCKS>
+struct MathOf<DP, 1, BLOCKS> {
+    using T = Four<DP, BLOCKS>;
+    static constexpr int kSets = 1, kSetHeads = 4;
+};
+
 template <int DP, int NT>
 __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
     attn_decode8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
@@ -204,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
     __shared__ uint64_t full_of[kWarps][2];             // keys, values
     __shared__ float scale_of[kWarps][2][kBlocks];
     __shared__ int abort_flag[kWarps];
-    __shared__ float2 far_of[kWarps][NT][32];           // maximum and sum
+    __shared__ float2 far_of[kWarps][NT][32];           // maximum and sum of each head of a lane
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     uint8_t* const stages =
         reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023)) +
@@ -328,22 +565,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
         load_v();
     }
 
+    using Math = MathOf<DP, NT, kBlocks>;
+    using Rows = typename Math::T;
+    constexpr int kSets = Math::kSets;
+    Rows rows[kSets];
     bool ok = true;
     int i = 0, fragment = 0;
     for (int at = begin; ok && at < end; ++fragment) {
         const int n = min(r.tiles - r.tile, end - at);
         const int head = r.unit / p.row_blocks, first_head = r.unit % p.row_blocks * (NT * 4);
-        // The query heads, rotated and split: column 2 h of a product has hi of head h,
-        // 2 h + 1 lo.  Step 4 j + w of the head dimension takes word w of the lane's
-        // codes, whose four stand in the order 0, 2, 1, 3.
-        uint32_t q[NT][DP / 16][2];
+        // The query heads, rotated and split.
         const float* const angles = c.rope.rot > 0 ? angles_of(c.rope, r.own - 1) : nullptr;
         // Halves of a head of DP that is all rotated: the partner of dimension d stands in
         // the lane's word 4 steps on (heads of 128), or in the lane 2 quads on (64).
         const bool paired = c.rope.rot == DP && !c.rope.interleaved && p.vec_q && c.wide && angles;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int hg = first_head + nt * 4 + (g >> 1);
+        for (int set = 0; set < kSets; ++set) {
+            const int hg = first_head + set * Math::kSetHeads + Rows::q_head(lane);
             const float* const src = p.q + r.b * p.q_token + (head * p.group + hg) * p.q_head;
             float4 x[DP / 16];
 #pragma unroll
@@ -378,29 +616,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
                 }
             }
 #pragma unroll
-            for (int k = 0; k < DP / 16; ++k) {
-                uint32_t hi[2], lo[2];
-                split2(x[k].x, x[k].z, hi[0], lo[0]);
-                split2(x[k].y, x[k].w, hi[1], lo[1]);
-                q[nt][k][0] = g & 1 ? lo[0] : hi[0];
-                q[nt][k][1] = g & 1 ? lo[1] : hi[1];
-            }
+            for (int k = 0; k < DP / 16; ++k)
+                rows[set].put(k, x[k], g);
+            rows[set].reset();
         }
-        // Head `quad` of each four: the running maximum, the lane's part of the sum of the
-        // weights and its dimensions of the sums of a run; slot, far_of: of the runs before.
-        float m[NT], l[NT];
-        uint64_t o[NT][DP / 16];
         const int part = 2 * piece + (fragment > 0 ? 1 : 0);
         const int o_dim = g * kDims;
-        float* const slot = p.part_o + (static_cast<int64_t>(part) * (NT * 4) + quad) * dim + o_dim;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            m[nt] = -INFINITY;
-            l[nt] = 0.0f;
-#pragma unroll
-            for (int t = 0; t < DP / 16; ++t)
-                o[nt][t] = 0;
-        }
+        // where the sums of the runs before stand, and far_of has what belongs to them
+        float* const slot = p.part_o + static_cast<int64_t>(part) * (NT * 4) * dim + o_dim;
+        auto row_of = [&](int set, int h) { return set * Math::kSetHeads + Rows::out_head(quad, h); };
         auto ready = [&](int is_v) {
             ok = __all_sync(0xffffffffu, mbar_try_wait(&full[is_v], i & 1)) ||
                  attn_warp_wait(&full[is_v], i & 1, &abort_flag[warp], kFaultDecode8);
@@ -412,17 +636,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
                 if (!ready(0))
                     break;
                 const int left = r.own - (r.tile + t) * kTile;  // keys of the tile that count
-                float x[NT][kBlocks][2];  // of my_key and 8 more
 #pragma unroll
                 for (int b = 0; b < kBlocks; ++b) {
                     if (b > 0 && b * 16 >= left) {  // a block behind the end; its scale may be anything
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            x[nt][b][0] = x[nt][b][1] = -INFINITY;
+                        for (int set = 0; set < kSets; ++set) {
+                            rows[set].set_score(b, 0, -INFINITY);
+                            rows[set].set_score(b, 1, -INFINITY);
+                        }
                         continue;
                     }
-                    // two chains, the even and the odd steps of the head dimension
-                    float s[NT][2][4] = {};
+#pragma unroll
+                    for (int set = 0; set < kSets; ++set)
+                        rows[set].begin_scores();
 #pragma unroll
                     for (int j = 0; j < W; ++j) {
                         uint32_t word[2][4];
@@ -434,20 +660,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
                             const uint32_t a[4] = {even_codes(word[0][w]), even_codes(word[1][w]),
                                                    odd_codes(word[0][w]), odd_codes(word[1][w])};
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                mma16816_free(s[nt][w & 1], a, q[nt][j * 4 + w][0], q[nt][j * 4 + w][1]);
+                            for (int set = 0; set < kSets; ++set)
+                                rows[set].score(j * 4 + w, a);
                         }
                     }
-                    const float ks = scale_of[warp][0][b], kc = fabsf(ks) * c2;
+                    const float ks = scale_of[warp][0][b];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float(&y)[2][4] = s[nt];
-                            const uint64_t both = add2(f2_bits(y[0][2 * e], y[0][2 * e + 1]),
-                                                       f2_bits(y[1][2 * e], y[1][2 * e + 1]));
-                            x[nt][b][e] = __fmul_rn(fmaf(hi_f(both), 0x1p-10f, lo_f(both)), kc);
-                        }
+                    for (int set = 0; set < kSets; ++set)
+                        rows[set].end_scores(b, fabsf(ks) * c2);
                     const int end_of = left - b * 16;  // keys of the block that count
                     if (end_of < 16 || has_odd(ks)) {
 #pragma unroll
@@ -464,51 +684,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
                                 }
                                 odd = __ballot_sync(0xffffffffu, any != 0) >> (4 * g) & 0xfu;
                             }
+                            const bool out = e * 8 + my_key >= end_of;
+                            if (out || odd)
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                x[nt][b][e] = e * 8 + my_key >= end_of ? -INFINITY
-                                              : odd ? __int_as_float(0x7fffffff) : x[nt][b][e];
+                                for (int set = 0; set < kSets; ++set)
+                                    rows[set].set_score(b, e, out ? -INFINITY : __int_as_float(0x7fffffff));
                         }
+                        __syncwarp();
                     }
                 }
                 __syncwarp();  // all lanes have read the keys
                 if (ahead < end)
                     load_k();
-                uint32_t pb[NT][kBlocks][2];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float top = fmaxf(x[nt][0][0], x[nt][0][1]);
-#pragma unroll
-                    for (int b = 1; b < kBlocks; ++b)
-                        top = fmaxf(top, fmaxf(x[nt][b][0], x[nt][b][1]));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                    const float m_new = fmaxf(m[nt], top), shift = m_new == -INFINITY ? 0.0f : m_new;
-                    if (__any_sync(0xffffffffu, m_new > m[nt])) {  // rare after some tiles
-                        const float alpha = ex2(m[nt] - shift);
-                        const uint64_t a2 = f2_bits(alpha, alpha);
-                        l[nt] *= alpha;
-#pragma unroll
-                        for (int d = 0; d < DP / 16; ++d)
-                            o[nt][d] = mul2(o[nt][d], a2);
-                    }
-                    m[nt] = m_new;
-                    // 2^14 p; each step rounded as the maximum was, or large scores would not end at 0
-                    float sum = 0.0f;
-#pragma unroll
-                    for (int b = 0; b < kBlocks; ++b) {
-                        const uint64_t e = add2(add2(f2_bits(x[nt][b][0], x[nt][b][1]), f2_bits(-shift, -shift)),
-                                                f2_bits(14.0f, 14.0f));
-                        const float w0 = ex2(lo_f(e)), w1 = ex2(hi_f(e));
-                        uint32_t hi, lo;
-                        split_p(w0, w1, hi, lo);
-                        pb[nt][b][0] = transposed(__byte_perm(hi, lo, 0x5410));
-                        pb[nt][b][1] = transposed(__byte_perm(hi, lo, 0x7632));
-                        sum += w0 + w1;
-                    }
-                    l[nt] += sum;
-                }
+                for (int set = 0; set < kSets; ++set)
+                    rows[set].weights();
                 if (!ready(1))
                     break;
 #pragma unroll
@@ -522,7 +712,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
                     for (int k = 0; k < 4; ++k)
                         lds(v_stage + v_at[k & 1] + (b * 16 + (k >> 1) * 8) * DP, v[k]);
                     const float vs = scale_of[warp][1][b];
-                    const uint64_t vs2 = f2_bits(fabsf(vs), fabsf(vs));
 #pragma unroll
                     for (int d = 0; d < DP / 16; ++d) {
                         // dimensions 2 d and 2 d + 1 of two keys: bytes a0 a1 b0 b1
@@ -530,11 +719,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
                         const uint32_t p23 = __byte_perm(v[2][d / 2], v[3][d / 2], d & 1 ? 0x7632 : 0x5410);
                         const uint32_t a[4] = {even_codes(p01), odd_codes(p01), even_codes(p23), odd_codes(p23)};
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            float y[4] = {};
-                            mma16816_free(y, a, pb[nt][b][0], pb[nt][b][1]);
-                            o[nt][d] = fma2(f2_bits(y[0] + y[1], y[2] + y[3]), vs2, o[nt][d]);
-                        }
+                        for (int set = 0; set < kSets; ++set)
+                            rows[set].value(b, d, a, fabsf(vs));
                     }
                     if (has_odd(vs)) {
                         // the components in which a key that counts is not a number: a bit for
@@ -551,86 +737,93 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
                         odd |= __shfl_xor_sync(0xffffffffu, odd, 2);
                         const float nan = __int_as_float(0x7fffffff);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                        for (int set = 0; set < kSets; ++set)
 #pragma unroll
-                            for (int d = 0; d < DP / 16; ++d)
-                                o[nt][d] = f2_bits((odd >> (2 * d)) & 1 ? nan : lo_f(o[nt][d]),
-                                                   (odd >> (2 * d + 1)) & 1 ? nan : hi_f(o[nt][d]));
+                            for (int h = 0; h < Rows::kHeads; ++h)
+#pragma unroll
+                                for (int j = 0; j < kDims / 4; ++j) {
+                                    const float4 y = rows[set].four(j, h);
+                                    const uint32_t bad = odd >> (4 * j);
+                                    rows[set].set_four(j, h, make_float4(bad & 1 ? nan : y.x, bad & 2 ? nan : y.y,
+                                                                         bad & 4 ? nan : y.z, bad & 8 ? nan : y.w));
+                                }
                     }
                 }
                 __syncwarp();  // all lanes have read the values
                 if (loads_v < loads_k)
                     load_v();
             }
-            if (t0 > 0) {
+            if (t0 == 0 && t1 == n)
+                continue;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const float2 far = far_of[warp][nt][lane];
-                    const float a = ex2(far.x - (m[nt] == -INFINITY ? 0.0f : m[nt]));
-                    l[nt] = fmaf(far.y, a, l[nt]);
-                    if (o_dim < dim)
+            for (int set = 0; set < kSets; ++set)
 #pragma unroll
-                        for (int d = 0; d < DP / 16; d += 2) {
-                            const float4 y = *reinterpret_cast<const float4*>(slot + nt * 4 * dim + 2 * d);
-                            o[nt][d] = fma2(f2_bits(y.x, y.y), f2_bits(a, a), o[nt][d]);
-                            o[nt][d + 1] = fma2(f2_bits(y.z, y.w), f2_bits(a, a), o[nt][d + 1]);
-                        }
-                }
-            }
-            if (t1 < n) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    far_of[warp][nt][lane] = make_float2(m[nt], l[nt]);
-                    l[nt] = 0.0f;
-#pragma unroll
-                    for (int d = 0; d < DP / 16; d += 2) {
+                for (int h = 0; h < Rows::kHeads; ++h) {
+                    float2& far = far_of[warp][set * Rows::kHeads + h][lane];
+                    float* const sums = slot + row_of(set, h) * dim;
+                    if (t0 > 0) {  // added to those of the runs before
+                        const float2 now = rows[set].sums(h);
+                        const float a = ex2(far.x - (now.x == -INFINITY ? 0.0f : now.x));
+                        rows[set].set_sum(h, fmaf(far.y, a, now.y));
                         if (o_dim < dim)
-                            *reinterpret_cast<float4*>(slot + nt * 4 * dim + 2 * d) = make_float4(
-                                lo_f(o[nt][d]), hi_f(o[nt][d]), lo_f(o[nt][d + 1]), hi_f(o[nt][d + 1]));
-                        o[nt][d] = o[nt][d + 1] = 0;
+#pragma unroll
+                            for (int j = 0; j < kDims / 4; ++j) {
+                                const float4 y = *reinterpret_cast<const float4*>(sums + 4 * j), z = rows[set].four(j, h);
+                                rows[set].set_four(j, h, make_float4(fmaf(y.x, a, z.x), fmaf(y.y, a, z.y),
+                                                                     fmaf(y.z, a, z.z), fmaf(y.w, a, z.w)));
+                            }
+                    }
+                    if (t1 < n) {  // and put there, to begin anew
+                        far = rows[set].sums(h);
+                        rows[set].set_sum(h, 0.0f);
+#pragma unroll
+                        for (int j = 0; j < kDims / 4; ++j) {
+                            if (o_dim < dim)
+                                *reinterpret_cast<float4*>(sums + 4 * j) = rows[set].four(j, h);
+                            rows[set].set_four(j, h, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+                        }
                     }
                 }
-            }
         }
 
         // the row, or this warp's part of it
         const bool whole = n == r.tiles;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float sum = l[nt];
-            sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-            const int row = nt * 4 + quad, hg = first_head + row;
-            if (!ok || hg >= p.group)
-                continue;
-            const int64_t at_row = static_cast<int64_t>(r.b) * p.heads + head * p.group + hg;
-            float* const dst = (whole ? p.out + at_row * dim
-                                      : p.part_o + (static_cast<int64_t>(part) * (NT * 4) + row) * dim) +
-                               o_dim;
-            const float norm = sum == 0.0f ? 0.0f : 1.0f / sum;
-            const bool vec = p.vec_out || !whole;
-            if (o_dim < dim)
+        for (int set = 0; set < kSets; ++set)
 #pragma unroll
-                for (int d = 0; d < DP / 16; d += 2) {
-                    const float y[4] = {lo_f(o[nt][d]) * norm, hi_f(o[nt][d]) * norm, lo_f(o[nt][d + 1]) * norm,
-                                        hi_f(o[nt][d + 1]) * norm};
-                    if (vec) {
-                        *reinterpret_cast<float4*>(dst + 2 * d) = make_float4(y[0], y[1], y[2], y[3]);
-                    } else {
+            for (int h = 0; h < Rows::kHeads; ++h) {
+                const float2 last = rows[set].sums(h);
+                const float sum = warp_sum_of_places(last.y);
+                const int row = row_of(set, h), hg = first_head + row;
+                if (!ok || hg >= p.group)
+                    continue;
+                const int64_t at_row = static_cast<int64_t>(r.b) * p.heads + head * p.group + hg;
+                float* const dst = (whole ? p.out + at_row * dim
+                                          : p.part_o + (static_cast<int64_t>(part) * (NT * 4) + row) * dim) +
+                                   o_dim;
+                const float norm = sum == 0.0f ? 0.0f : 1.0f / sum;
+                if (o_dim < dim)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            dst[2 * d + e] = y[e];
+                    for (int j = 0; j < kDims / 4; ++j) {
+                        const float4 z = rows[set].four(j, h);
+                        const float y[4] = {z.x * norm, z.y * norm, z.z * norm, z.w * norm};
+                        if (p.vec_out || !whole) {
+                            *reinterpret_cast<float4*>(dst + 4 * j) = make_float4(y[0], y[1], y[2], y[3]);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                dst[4 * j + e] = y[e];
+                        }
                     }
+                if (g == 0) {
+                    const float lse =
+                        sum == 0.0f ? -INFINITY : fmaf(last.x, kAttnLn2, logf(sum * (1.0f / kAttnPScale)));
+                    if (!whole)
+                        p.part_lse[part * (NT * 4) + row] = lse;
+                    else if (p.lse)
+                        p.lse[at_row] = lse;
                 }
-            if (g == 0) {
-                const float lse = sum == 0.0f ? -INFINITY : fmaf(m[nt], kAttnLn2, logf(sum * (1.0f / kAttnPScale)));
-                if (!whole)
-                    p.part_lse[part * (NT * 4) + row] = lse;
-                else if (p.lse)
-                    p.lse[at_row] = lse;
             }
-        }
         at += n + kRowCost;
         if (at < end)
             next_row(p, r);
@@ -699,9 +892,15 @@ int ctas_an_sm(int nt)
     return nt == 4 ? Cfg<128, 4>::kCtas : Cfg<128, 1>::kCtas;
 }
 
+template <int DP>
+int tile_shift_of_columns(int nt)
+{
+    return nt == 4 ? Cfg<DP, 4>::kTileShift : (nt == 2 ? Cfg<DP, 2>::kTileShift : Cfg<DP, 1>::kTileShift);
+}
+
 int tile_shift_for(int head_dim, int nt)
 {
-    return head_dim <= 64 ? Cfg<64, 1>::kTileShift : (nt == 4 ? Cfg<128, 4>::kTileShift : Cfg<128, 1>::kTileShift);
+    return head_dim <= 64 ? tile_shift_of_columns<64>(nt) : tile_shift_of_columns<128>(nt);
 }
 
 // Floats of the workspace: parts of rows, and their lse.

@@ -2,6 +2,7 @@
 // tiles, its pieces, and the join of the parts of rows that were cut.  Included
 // by the decode kernels, each of which has its own copies and defines before:
 //   kTileShift log2 of the keys of a tile, or 0 where Params says;
+//   kLeastKeys keys of a piece at least, about;
 //   kRowCost   tiles that the beginning of a row costs as much time as;
 //   kJoinEarly whether the join lets the next kernel start before it has begun.
 #pragma once
@@ -16,7 +17,6 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kLeastKeys = 64;
 constexpr int kLongKeys = 128;
 
 struct Params {
