@@ -153,9 +153,10 @@ def comp_kv8_append_f32(k, v, k_pages, v_pages, k_scales, v_scales, table, start
     """comp_kv_append_f32 into an 8-bit cache: each value becomes the nearest of 255
     steps of its block's scale, the largest magnitude / 127; the tokens that are in
     the block already are rounded again where that grows.  An infinity or a NaN
-    reads back as NaN and costs its neighbours nothing.  rope, a rotary table,
-    rotates the keys on the way, each at its position in its sequence (interleaved
-    as in comp_rope_f32)."""
+    reads back as NaN and costs its neighbours nothing.  What stood behind the new
+    tokens in their last block of 16 is no longer valid, and tokens of two rows must
+    not join the same block in one call.  rope, a rotary table, rotates the keys on
+    the way, each at its position in its sequence (interleaved as in comp_rope_f32)."""
     _b.append8(k, v, k_pages, v_pages, k_scales, v_scales, table, start, cu, rope, interleaved, stream)
 
 
@@ -176,7 +177,8 @@ def comp_kv8_read_f16(k_pages, v_pages, k_scales, v_scales, table, start, cu, to
 def comp_attn_decode_f32x8(q, k_pages, v_pages, k_scales, v_scales, table, lengths, *, rope=None, interleaved=False,
                            scale=None, out=None, lse=None, workspace=None, stream=None):
     """comp_attn_decode_f32x16 over an 8-bit cache (no shared prefix).  rope, a
-    rotary table, rotates each query at its sequence's last position."""
+    rotary table, rotates each query at its sequence's last position, lengths[b] - 1
+    (NaN if the table does not have it)."""
     return _b.decode8(q, k_pages, v_pages, k_scales, v_scales, table, lengths, rope, interleaved, scale, out, lse,
                       workspace, stream)
 

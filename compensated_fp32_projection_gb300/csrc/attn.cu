@@ -173,7 +173,8 @@ int64_t comp_attn_decode_f32x8_workspace_bytes(const comp_kv8_cache_t* cache, in
                                                int64_t width)
 {
     int64_t bytes, scales, entries;
-    if (!kv8_cache_ok(cache, &bytes, &scales) || !decode_sizes_ok(cache, batch, heads, width, 4, &entries) || batch == 0)
+    if (!kv8_cache_ok(cache, &bytes, &scales) || !decode_sizes_ok(cache, batch, heads, width, 4, &entries) ||
+        batch == 0)
         return 0;
     return attn_decode8_bytes(*cache, heads);
 }

@@ -770,7 +770,8 @@ PyObject* read8(PyObject*, PyObject* const* a, Py_ssize_t n)
     });
 }
 
-// decode8(q, k_pages, v_pages, k_scales, v_scales, table, lengths, rope, interleaved, scale, out, lse, workspace, stream)
+// decode8(q, k_pages, v_pages, k_scales, v_scales, table, lengths, rope, interleaved, scale, out, lse, workspace,
+//         stream)
 PyObject* decode8(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     return guarded([&] {

@@ -62,7 +62,8 @@ constexpr bool kJoinEarly = false;
 namespace compfp32 {
 namespace {
 
-constexpr int kRunKeys = 1024;  // keys that are added up before they are added to the sums so far, as in the FP16 kernel
+// Keys that are added up before they are added to the sums so far, as in the FP16 kernel.
+constexpr int kRunKeys = 1024;
 constexpr uint32_t kFaultDecode8 = 0xB01;
 
 // DP: head dimension padded to 64 or 128; NT: query heads of a warp, in fours.
@@ -251,7 +252,10 @@ struct Four {
             s[0][e] = s[1][e] = 0.0f;
     }
     // two chains, the even and the odd steps
-    __device__ __forceinline__ void score(int k, const uint32_t (&a)[4]) { mma16816_free(s[k & 1], a, q[k][0], q[k][1]); }
+    __device__ __forceinline__ void score(int k, const uint32_t (&a)[4])
+    {
+        mma16816_free(s[k & 1], a, q[k][0], q[k][1]);
+    }
     __device__ __forceinline__ void end_scores(int b, float kc)
     {
 #pragma unroll
@@ -401,7 +405,8 @@ struct Eight {
     static __device__ __forceinline__ float part(uint64_t v, int h) { return h ? hi_f(v) : lo_f(v); }
     __device__ __forceinline__ float4 four(int j, int h) const
     {
-        return make_float4(part(o[2 * j][0], h), part(o[2 * j][1], h), part(o[2 * j + 1][0], h), part(o[2 * j + 1][1], h));
+        return make_float4(part(o[2 * j][0], h), part(o[2 * j][1], h), part(o[2 * j + 1][0], h),
+                           part(o[2 * j + 1][1], h));
     }
     __device__ __forceinline__ void set_four(int j, int h, const float4& v)
     {
@@ -460,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
     {
         const int64_t thread = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
         const int64_t lines = (static_cast<int64_t>(p.batch) * p.width + 31) / 32;
-        const int64_t q_lines = static_cast<int64_t>(p.heads) * dim / 32, row = (thread - lines) / q_lines;
+        const int64_t q_lines = (static_cast<int64_t>(p.heads) * dim + 31) / 32, row = (thread - lines) / q_lines;
         if (thread < lines)
             prefetch_l2(p.table + thread * 32);
         else if (row < p.batch)
@@ -500,7 +505,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
     Place next = r;
     int pages = 0, page_tile = 0, loads_k = 0, loads_v = 0, ahead = begin;  // ahead: the next place of the line
     const int blocks_shift = p.page_shift - 4;
-    const int box_shift = min(p.page_shift, kTileShift), split = kTileShift - box_shift;  // a tile is on 1 << split pages
+    const int box_shift = min(p.page_shift, kTileShift);
+    const int split = kTileShift - box_shift;       // a tile is on 1 << split pages
     const int my_box = lane * 16 >> box_shift, my_block = (lane * 16 & ((1 << box_shift) - 1)) >> 4;
     struct {
         int unit, slot;
@@ -536,7 +542,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
         }
     };
     auto load_k = [&] {
-        const int at = __shfl_sync(0xffffffffu, pages, ((next.tile - page_tile) << split) + (my_box & ((1 << split) - 1)));
+        const int box = ((next.tile - page_tile) << split) + (my_box & ((1 << split) - 1));
+        const int at = __shfl_sync(0xffffffffu, pages, box);
         at_v.there = at >= 0 && at < p.pages;
         at_v.slot = (next.tile * kTile) & ((1 << p.page_shift) - 1);
         at_v.unit = (at_v.there ? at : 0) * p.kv_heads + next.unit / p.row_blocks;
@@ -768,7 +775,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
                         if (o_dim < dim)
 #pragma unroll
                             for (int j = 0; j < kDims / 4; ++j) {
-                                const float4 y = *reinterpret_cast<const float4*>(sums + 4 * j), z = rows[set].four(j, h);
+                                const float4 y = *reinterpret_cast<const float4*>(sums + 4 * j);
+                                const float4 z = rows[set].four(j, h);
                                 rows[set].set_four(j, h, make_float4(fmaf(y.x, a, z.x), fmaf(y.y, a, z.y),
                                                                      fmaf(y.z, a, z.z), fmaf(y.w, a, z.w)));
                             }

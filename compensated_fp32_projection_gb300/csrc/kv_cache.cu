@@ -769,8 +769,8 @@ comp_status_t compact_pages(const Cache* cache, const int32_t* table, const int3
     const int64_t pages = cache->pages;
     const Range r[] = {{h.k, h.bytes, nullptr, true}, {h.v, h.bytes, nullptr, true},
                        {h.k_scale, h.scales, nullptr, true}, {h.v_scale, h.scales, nullptr, true},
-                       {table, 4 * entries}, {refs, 4 * pages}, {table_out, 4 * entries, table, true}, {refs_out, 4 * pages, refs, true},
-                       {remap, 4 * pages, nullptr, true}, {live, 4, nullptr, true}};
+                       {table, 4 * entries}, {refs, 4 * pages}, {table_out, 4 * entries, table, true},
+                       {refs_out, 4 * pages, refs, true}, {remap, 4 * pages, nullptr, true}, {live, 4, nullptr, true}};
     if (!ranges_ok(r))
         return COMP_ERR_INVALID_VALUE;
     DeviceInfo dev;

@@ -582,7 +582,9 @@ typedef struct comp_kv8_cache {
  * infinity or a NaN takes the code -128 and no part in the scale.  A value written
  * at once is off by half a step, scale / 2; each later call that raises the block's
  * scale rounds it again, by half of the larger step.  What stood behind the new
- * tokens in their last block is no longer valid.  No other block changes.
+ * tokens in their last block is no longer valid.  No other block changes.  Tokens of
+ * two rows must not join the same block in one call.  With cu, total / 16 + 2 * rows
+ * is below 2^31 - 1 (here and in the calls that read).
  * Errors: as comp_kv_append_f32; COMP_ERR_INVALID_VALUE also for a table of angles
  * that is NULL, not 8-byte aligned or of an odd rot, or of one beyond head_dim.
  */
@@ -598,8 +600,8 @@ comp_status_t comp_kv8_append_f32(const comp_kv8_cache_t* cache, const float* k,
  * so that packed attention can see a sequence's past.  Where the table has no page,
  * and for the tokens behind cu[rows], zeros are written.  Neither k nor v shares
  * memory with an input or with the other, from the first to the last element of
- * each, and their rows do not overlap.  The binary16 form rounds
- * the binary32 values (to nearest, ties to even; 65520 and more become infinities).
+ * each, and their rows do not overlap.  The binary16 form rounds the binary32 values
+ * (to nearest, ties to even; 65520 and more become infinities).
  */
 comp_status_t comp_kv8_read_f32(const comp_kv8_cache_t* cache, float* k, float* v, int64_t k_token, int64_t k_head,
                                 int64_t v_token, int64_t v_head, int64_t total, const int32_t* table, int64_t rows,
@@ -612,10 +614,11 @@ comp_status_t comp_kv8_read_f16(const comp_kv8_cache_t* cache, uint16_t* k, uint
 /*
  * comp_attn_decode_f32x8 — comp_attn_decode_f32x16 over an 8-bit cache, without a
  * shared prefix; rope (or NULL) rotates each query at its sequence's last position,
- * lengths[b] - 1.  The codes enter the products exactly and a block's scale is
- * applied in binary32 to what its keys gave, so keys and values may have any
- * magnitude as long as the scores stay finite.  Same limits on sizes, but that
- * (width * page_size / 16 + 4) * batch * kv_heads * ceil(group / 16) is below 2^31.
+ * lengths[b] - 1 (a row whose position the table does not have gets NaN).  The codes
+ * enter the products exactly and a block's scale is applied in binary32 to what its
+ * keys gave, so keys and values may have any magnitude as long as the scores stay
+ * finite.  Same limits on sizes, but that (width * page_size / 16 + 4) * batch *
+ * kv_heads * ceil(group / 16) is below 2^31.
  */
 int64_t comp_attn_decode_f32x8_workspace_bytes(const comp_kv8_cache_t* cache, int64_t batch, int32_t heads,
                                                int64_t width);

@@ -179,6 +179,22 @@ def test_values_of_any_kind(pkg):
         assert same(cache, k_plain, v_plain)
 
 
+def test_a_block_that_nothing_was_written_to(pkg):
+    """Tokens that begin inside a block whose scale was never set: it does not reach them."""
+    for junk in (math.nan, math.inf, -math.inf):
+        cache = pool(3, 2, 32, 64)
+        for t in cache[2:]:
+            t.fill_(junk)
+        x = torch.randn(20, 4, 64, generator=torch.Generator().manual_seed(0)).cuda()
+        table, start, cu = ints([[2, 1]]), ints([21]), ints([0, 20])
+        pkg.comp_kv8_append_f32(x[:, :2], x[:, 2:], *cache, table, start, cu)
+        k, v = pkg.comp_kv8_read_f32(*cache, table, start, cu, 20)
+        for got, want, scales in ((k, x[:, :2], cache[2]), (v, x[:, 2:], cache[3])):
+            step = torch.cat([scales[2, :, 1].expand(11, 2), scales[1, :, 0].expand(9, 2)]).abs()
+            # half a step, and 2^-21 of 127 steps for the operations
+            assert ((got - want).abs() <= step[..., None] * (0.5 + 127 * 2.0 ** -21)).all()
+
+
 def test_pages_that_are_not_there(pkg):
     heads, page, dim = 2, 32, 64
     cache = pool(6, heads, page, dim)

@@ -148,7 +148,8 @@ def test_refusals(pkg):
     for bad in (x.half(), x.cpu(), x[0], x.transpose(1, 2), x[..., :14], x[:, :0]):
         with pytest.raises((ValueError, pkg.CompError)):
             pkg.comp_rope_f32(bad, t)
-    for bad in (t.double(), t[0], t[..., :1], t.transpose(0, 1), t.cpu(), t[:, :0], torch.zeros(8, 9, 2, device="cuda")):
+    for bad in (t.double(), t[0], t[..., :1], t.transpose(0, 1), t.cpu(), t[:, :0],
+                torch.zeros(8, 9, 2, device="cuda")):
         with pytest.raises(ValueError):
             pkg.comp_rope_f32(x, bad)
     with pytest.raises(TypeError):

@@ -106,6 +106,15 @@ def test_append_and_read_arguments(lib):
     assert append(lib, c=cache(pages=0)) == 0   # nowhere to write to
 
 
+def test_sizes_that_a_grid_does_not_have(lib):
+    far = 1 << 44
+    for f in (append, read):
+        assert f(lib, total=1 << 20, rows=(1 << 30) - 1, width=0 if f is read else 1, cu=far, start=2 * far,
+                 table=3 * far) == INVALID
+    assert read(lib, f16=True, total=(1 << 31) - 1, rows=(1 << 30) - 100, width=1, cu=far, start=2 * far,
+                table=3 * far) == INVALID
+
+
 def rotate(lib, r=None, x=MB, x_token=256, x_head=64, tokens=10, heads=4, dim=64, positions=None, out=4 * MB,
            out_token=256, out_head=64):
     return lib.comp_rope_f32(r or rope(), P(x), x_token, x_head, tokens, heads, dim, P(positions), 0, P(out),
