@@ -25,6 +25,7 @@
 #include <cuda_fp16.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "attn.h"
 #include "internal.h"
@@ -235,19 +236,24 @@ __global__ void __launch_bounds__(kThreads, 2) append8_kernel(const Params p, co
     auto whole_of = [&](const Item& w, const Source& src) {
         return w.from == 0 && w.to == kBlock && src.vec && STEPS * at.rows_at_once == kBlock;
     };
-    auto load = [&](int u) {
+    // A few new rows, as where each sequence goes on by a token, take one step from the
+    // first of them on: a small part of the code, whose fetch is most of such a call.
+    auto few_of = [&](const Item& w) { return w.to - w.from <= at.rows_at_once; };
+    auto load = [&](int u, auto steps) {
+        constexpr int N = decltype(steps)::value;
         const Item& w = item[u / heads];
         const Source& src = u % 2 ? v : k;
-        const float* row = src.x + (w.token0 + at.row) * src.token + (u % heads / 2) * src.head + at.d;
+        const int t0 = (N == 1 ? w.from : 0) + at.row;
+        const float* row = src.x + (w.token0 + t0) * src.token + (u % heads / 2) * src.head + at.d;
         const int64_t step = at.rows_at_once * src.token;
-        if (whole_of(w, src)) {
+        if (N > 1 && whole_of(w, src)) {
 #pragma unroll
-            for (int i = 0; i < STEPS; ++i, row += step)
+            for (int i = 0; i < N; ++i, row += step)
                 x[i] = at.in ? __ldcs(reinterpret_cast<const float4*>(row)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         } else {
 #pragma unroll
-            for (int i = 0; i < STEPS; ++i, row += step) {
-                const int t = i * at.rows_at_once + at.row;
+            for (int i = 0; i < N; ++i, row += step) {
+                const int t = t0 + i * at.rows_at_once;
                 x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 if (!at.in || t < w.from || t >= w.to)
                     continue;
@@ -258,30 +264,10 @@ __global__ void __launch_bounds__(kThreads, 2) append8_kernel(const Params p, co
             }
         }
     };
-    // the first values, the pages and the angles, none of which needs another
-    if (warp < units)
-        load(warp);
-    find_pages(p, count, item);
-    if constexpr (TURN != kStill) {
-        for (int r = warp; r < count * kBlock; r += kThreads / 32) {
-            const Item& w = item[r / kBlock];
-            const int t = r % kBlock;
-            if (t < w.from || t >= w.to)
-                continue;
-            const float* const row = angles_of(rope, w.position + t);
-            const float nan = __int_as_float(0x7fffffff);
-            for (int i = lane; i < half; i += 32)
-                angles[r * half + i] = row ? __ldg(reinterpret_cast<const float2*>(row) + i) : make_float2(nan, nan);
-        }
-    }
-    __syncthreads();
-    for (int u = warp; u < units; u += kThreads / 32) {
-        if (u != warp)
-            load(u);
+    auto write = [&](int u, auto steps) {
+        constexpr int N = decltype(steps)::value;
         const Item& w = item[u / heads];
-        if (w.unit < 0)
-            continue;
-        const int head = u % heads / 2, is_v = u % 2;
+        const int head = u % heads / 2, is_v = u % 2, t0 = (N == 1 ? w.from : 0) + at.row;
         const Source& src = is_v ? v : k;
         const int64_t unit = w.unit + head;
         int8_t* const codes = (is_v ? c.v : c.k) + (unit * c.page_size + w.slot) * c.head_dim + at.d;
@@ -291,8 +277,8 @@ __global__ void __launch_bounds__(kThreads, 2) append8_kernel(const Params p, co
         if (TURN != kStill && !is_v) {
             const float2* const turns = angles + u / heads * kBlock * half;
 #pragma unroll
-            for (int i = 0; i < STEPS; ++i) {
-                const int t = i * at.rows_at_once + at.row;
+            for (int i = 0; i < N; ++i) {
+                const int t = t0 + i * at.rows_at_once;
                 const bool here = at.in && t >= w.from && t < w.to && at.d < rope.rot;
                 float y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
                 if constexpr (TURN == kPairs) {
@@ -337,14 +323,14 @@ __global__ void __launch_bounds__(kThreads, 2) append8_kernel(const Params p, co
         // the largest finite magnitude; not negative, it has the order of its bits
         float top = 0.0f;
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i)
+        for (int i = 0; i < N; ++i)
             top = largest(largest(top, x[i].x, x[i].y), x[i].z, x[i].w);
         const bool new_odd = __any_sync(0xffffffffu, !(top < INFINITY));
         const bool odd = new_odd || (__float_as_uint(was) >> 31) != 0;
         if (new_odd) {
             top = 0.0f;
 #pragma unroll
-            for (int i = 0; i < STEPS; ++i) {
+            for (int i = 0; i < N; ++i) {
                 const float m[4] = {fabsf(x[i].x), fabsf(x[i].y), fabsf(x[i].z), fabsf(x[i].w)};
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -359,17 +345,17 @@ __global__ void __launch_bounds__(kThreads, 2) append8_kernel(const Params p, co
         const float inverse = scale > 0.0f ? __frcp_rn(scale) : 0.0f;
         const bool again = stays && kept != scale;
         const float ratio = again && scale > 0.0f ? __fdiv_rn(kept, scale) : 0.0f;
-        int8_t* to = codes + at.row * c.head_dim;
+        int8_t* to = codes + t0 * c.head_dim;
         const int step = at.rows_at_once * c.head_dim;
-        if (whole_of(w, src) && !new_odd) {
+        if (N > 1 && whole_of(w, src) && !new_odd) {
 #pragma unroll
-            for (int i = 0; i < STEPS; ++i, to += step)
+            for (int i = 0; i < N; ++i, to += step)
                 if (at.in)
                     *reinterpret_cast<uint32_t*>(to) = codes_of(x[i], inverse);
         } else {
 #pragma unroll
-            for (int i = 0; i < STEPS; ++i, to += step) {
-                const int t = i * at.rows_at_once + at.row;
+            for (int i = 0; i < N; ++i, to += step) {
+                const int t = t0 + i * at.rows_at_once;
                 if (!at.in || t < w.from || t >= w.to)
                     continue;
                 uint32_t q = codes_of(x[i], inverse);
@@ -397,6 +383,43 @@ __global__ void __launch_bounds__(kThreads, 2) append8_kernel(const Params p, co
         if (lane == 0)
             *scale_at = odd ? -scale : scale;
         __syncwarp();
+    };
+    const std::integral_constant<int, STEPS> all{};
+    const std::integral_constant<int, 1> one{};
+    // the first values, the pages and the angles, none of which needs another
+    if (warp < units) {
+        if (few_of(item[warp / heads]))
+            load(warp, one);
+        else
+            load(warp, all);
+    }
+    find_pages(p, count, item);
+    if constexpr (TURN != kStill) {
+        for (int r = warp; r < count * kBlock; r += kThreads / 32) {
+            const Item& w = item[r / kBlock];
+            const int t = r % kBlock;
+            if (t < w.from || t >= w.to)
+                continue;
+            const float* const row = angles_of(rope, w.position + t);
+            const float nan = __int_as_float(0x7fffffff);
+            for (int i = lane; i < half; i += 32)
+                angles[r * half + i] = row ? __ldg(reinterpret_cast<const float2*>(row) + i) : make_float2(nan, nan);
+        }
+    }
+    __syncthreads();
+    for (int u = warp; u < units; u += kThreads / 32) {
+        const Item& w = item[u / heads];
+        if (few_of(w)) {
+            if (u != warp)
+                load(u, one);
+            if (w.unit >= 0)
+                write(u, one);
+        } else {
+            if (u != warp)
+                load(u, all);
+            if (w.unit >= 0)
+                write(u, all);
+        }
     }
 }
 
