@@ -396,6 +396,80 @@ def test_decode_long(pkg, seqs, n, heads, kv_heads, dim):
                              dim ** -0.5)
 
 
+@pytest.mark.parametrize("heads,kv_heads", [(4, 2), (6, 1)])
+def test_decode_many_short_sequences(pkg, heads, kv_heads):
+    """More sequences than lanes, most of them shorter than a tile, many empty; rows share pieces."""
+    rng, dim, page, batch = random.Random(7), 64, 16, 1500
+    lens = [rng.choice([0, 0, 1, 2, 15, 16, 17, 40, 64, 65, 130]) for _ in range(batch)]
+    need = sum(-(-n // page) for n in lens)
+    cache = pool(need, kv_heads, page, dim)
+    table = ints(rows_of(lens, page, need, seed=2))
+    g = torch.Generator().manual_seed(0)
+    q = torch.randn(batch, heads, dim, generator=g).cuda()
+    lse = torch.empty(batch, heads, device="cuda")
+    out = pkg.comp_attn_decode_f32x8(q, *cache, table, ints(lens), lse=lse)
+    k, v = ((c.double() * s.double().repeat_interleave(16, 2)[..., None])[table.long().clamp_min(0)]
+            .transpose(1, 2).flatten(2, 3).repeat_interleave(heads // kv_heads, 1)
+            for c, s in ((cache[0], cache[2]), (cache[1], cache[3])))
+    seen = (torch.arange(k.shape[2], device="cuda") < ints(lens)[:, None])[:, None]
+    x = (torch.einsum("bhd,bhjd->bhj", q.double(), k) / 8).masked_fill(~seen, -math.inf)
+    e = 4e-6 * torch.einsum("bhd,bhjd->bhj", q.double().abs(), k.abs()).masked_fill(~seen, 0).amax(-1) / 8
+    want = torch.logsumexp(x, -1)
+    some = ints(lens) > 0
+    assert torch.isneginf(lse[~some]).all() and not out[~some].any()
+    assert ((lse - want).abs() <= e + 4e-6 * (1 + want.abs()))[some].all()
+    p = torch.softmax(x, -1).nan_to_num(0.0)
+    # as in attn_check, and 2^-39 of each weight (kv8_check)
+    size = torch.einsum("bhj,bhjd->bhd", p, v.abs())
+    tol = (2 * torch.expm1(e) + 8e-6)[..., None] * size + 2.0 ** -39 * (v.abs() * seen[..., None]).sum(2) + 1e-30
+    assert ((out - torch.einsum("bhj,bhjd->bhd", p, v)).abs() <= tol)[some].all()
+
+
+def test_broadcast_inputs(pkg):
+    """One head's keys for all heads, one token for all rows: strides of zero are read as they are."""
+    cache, other = pool(8, 3, 16, 64), pool(8, 3, 16, 64)
+    x = torch.randn(1, 1, 64, device="cuda")
+    table, start, t = ints([[0, 1], [2, 3], [4, 5]]), ints([3, 0, 17]), pkg.comp_rope_table(40, 64)
+    k, v = x.expand(3, 3, 64), (2 * x).expand(3, 3, 64)
+    pkg.comp_kv8_append_f32(k, v, *cache, table, start, rope=t)
+    pkg.comp_kv8_append_f32(k.contiguous(), v.contiguous(), *other, table, start, rope=t)
+    assert all(torch.equal(a, b) for a, b in zip(cache, other))
+    q = x.expand(3, 6, 64)
+    assert torch.equal(pkg.comp_attn_decode_f32x8(q, *cache, table, start + 1, rope=t),
+                       pkg.comp_attn_decode_f32x8(q.contiguous(), *cache, table, start + 1, rope=t))
+    assert torch.equal(pkg.comp_rope_f32(q, t, start), pkg.comp_rope_f32(q.contiguous(), t, start))
+
+
+def test_two_streams_at_once(pkg):
+    """Calls on two streams, each with a cache of its own, do not disturb each other."""
+    lens = [700, 90, 1200]
+    runs = []
+    for seed in (1, 2):
+        cache = pool(80, 2, 32, 128, seed=seed)
+        table = ints(rows_of([n + 40 for n in lens], 32, 80, seed=seed))
+        x = torch.randn(3, 12, 128, generator=torch.Generator().manual_seed(seed)).cuda()
+        runs.append((cache, table, x, torch.cuda.Stream()))
+    angles = pkg.comp_rope_table(1300, 128)
+
+    def step(cache, table, x, n, stream=None):
+        pkg.comp_kv8_append_f32(x[:, 8:10], x[:, 10:], *cache, table, n, rope=angles, stream=stream)
+        return pkg.comp_attn_decode_f32x8(x[:, :8], *cache, table, n + 1, rope=angles, stream=stream)
+
+    at = [ints([n + i for n in lens]) for i in range(31)]
+    want = []
+    for cache, table, x, _ in runs:
+        own = [t.clone() for t in cache]
+        want.append([step(own, table, x, at[i]) for i in range(30)])
+    torch.cuda.synchronize()
+    got = [[], []]
+    for i in range(30):
+        for r, (cache, table, x, s) in enumerate(runs):
+            with torch.cuda.stream(s):
+                got[r].append(step(cache, table, x, at[i]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for r in (0, 1) for a, b in zip(got[r], want[r]))
+
+
 def test_decode_identical_keys(pkg):
     """Equal terms round the same way each time: sums of 65536 of them stay within the tolerance."""
     cache = pool(512, 1, 128, 64)
