@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 2) append8_kernel(const Params p, co
 {
     grid_dependency_launch();
     __shared__ Item item[kMostItems];
-    extern __shared__ float2 angles[];  // [items][kBlock][rot / 2]
+    extern __shared__ __align__(16) float2 angles[];  // [items][kBlock][rot / 2], read two at a time
     const comp_kv8_cache_t& c = p.cache;
     const int heads = 2 * c.kv_heads, blocks = c.page_size / kBlock, half = rope.rot / 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
