@@ -36,6 +36,7 @@ constexpr int kTile = 1 << kTileShift;  // keys of a tile, the k of a product
 constexpr int kLeastKeys = 64;
 constexpr int kRowCost = 0;
 constexpr bool kJoinEarly = true;
+constexpr float kJoinWeight = 1.0f;
 }
 }  // namespace compfp32
 

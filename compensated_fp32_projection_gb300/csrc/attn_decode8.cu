@@ -22,6 +22,13 @@
 // heads side by side for packed arithmetic (Eight): 16 sequences of 20001 to 65536
 // tokens with 16 heads a key head take 175 us, as two Fours for each eight 199.
 //
+// Large values.  The sums hold 2^14 p times the values, and leave binary32 with one
+// value of 2^114, or 2^16 of 2^98, where their mean is an ordinary number.  A warp whose
+// results are not all numbers goes through its keys once more with values of kDown
+// times their size, and replaces those that were not.  The second pass is a copy of the
+// first in the code, so that the first is what it would be alone: a flag in one copy, or a
+// look at each tile's scales before its products, took 1 to 3 % of every call.
+//
 // Layout.  The sum over the head dimension may go in any order, and so may the
 // rows of the output and the keys of a block: a lane's operands are 16 codes that
 // stand side by side in a row, one 16-byte load from shared memory, and which keys
@@ -50,6 +57,7 @@ constexpr int kRowCost = 2;
 // spread unevenly: 16 sequences of 20001 to 65536 tokens, eight heads a key head, took
 // 172 us a call in a long row of calls where they take 136.
 constexpr bool kJoinEarly = false;
+constexpr float kJoinWeight = 0x1p-12f;  // a row has fewer than 2^12 parts
 }
 }  // namespace compfp32
 
@@ -65,6 +73,10 @@ namespace {
 // Keys that are added up before they are added to the sums so far, as in the FP16 kernel.
 constexpr int kRunKeys = 1024;
 constexpr uint32_t kFaultDecode8 = 0xB01;
+
+// The sums over all keys that a table can name, fewer than 2^30, stay below 2^124 with
+// this for any values that are binary32 numbers.
+constexpr float kDown = 0x1p-48f;
 
 // DP: head dimension padded to 64 or 128; NT: query heads of a warp, in fours.
 // A tile is some blocks of 16 keys.  What a tile costs whatever its size (waits, loads,
@@ -112,6 +124,16 @@ __device__ __forceinline__ int key_of(int at)
 {
     return ((DP == 128 ? 0x36147250u : 0x65217430u) >> (4 * at)) & 7u;
 }
+
+// The largest magnitude of three; NaN if one of them is.
+__device__ __forceinline__ float largest(float a, float b, float c)
+{
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+__device__ __forceinline__ bool is_number(float x) { return fabsf(x) < INFINITY; }
 
 // A 4-byte copy that the barrier waits for: it counts one arrival of this thread
 // when the copy has landed.
@@ -433,57 +455,34 @@ struct MathOf<DP, 1, BLOCKS> {
     static constexpr int kSets = 1, kSetHeads = 4;
 };
 
+// What a CTA's warps keep beside their tiles, each its own.
 template <int DP, int NT>
-__global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
-    attn_decode8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                        const Params p, const Cache8 c)
+struct Shared {
+    uint64_t full[kWarps][2];                           // keys, values
+    float scale[kWarps][2][Cfg<DP, NT>::kBlocks];
+    int abort_flag[kWarps];
+    float2 far[kWarps][NT][32];                         // maximum and sum of each head of a lane
+};
+
+// A pass over a warp's piece of the line; whether there is a result that may be a number
+// and is not.  SMALL: the second one, with values of kDown times their size, which replaces
+// those.  i: the tiles that went through the stages so far.
+template <int DP, int NT, bool SMALL>
+__device__ __forceinline__ bool go_over(const CUtensorMap& map_k, const CUtensorMap& map_v, const Params& p,
+                                        const Cache8& c, Shared<DP, NT>& shared, uint8_t* const stages,
+                                        const int piece, int& i)
 {
     using C = Cfg<DP, NT>;
     constexpr int W = C::kWords, kDims = DP / 8;  // kDims: of a lane's output
     constexpr int kTileShift = C::kTileShift, kTile = C::kTile, kBlocks = C::kBlocks, kRun = kRunKeys / kTile;
     const int dim = p.dim;
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full_of[kWarps][2];             // keys, values
-    __shared__ float scale_of[kWarps][2][kBlocks];
-    __shared__ int abort_flag[kWarps];
-    __shared__ float2 far_of[kWarps][NT][32];           // maximum and sum of each head of a lane
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    uint8_t* const stages =
-        reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023)) +
-        warp * (2 * C::kPlane);
     const uint32_t k_stage = smem_u32(stages), v_stage = k_stage + C::kPlane;
-    uint64_t* const full = full_of[warp];
-    if (lane == 0) {
-        for (int i = 0; i < 2; ++i)
-            mbar_init(&full[i], 1 + kBlocks);  // the TMA's bytes and the scales
-        abort_flag[warp] = 0;
-        fence_mbar_init();
-    }
-    __syncwarp();
-    // What the first steps read one after the other comes into L2 meanwhile, a line a
-    // thread: lengths, page tables, queries.
-    {
-        const int64_t thread = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-        const int64_t lines = (static_cast<int64_t>(p.batch) * p.width + 31) / 32;
-        const int64_t q_lines = (static_cast<int64_t>(p.heads) * dim + 31) / 32, row = (thread - lines) / q_lines;
-        if (thread < lines)
-            prefetch_l2(p.table + thread * 32);
-        else if (row < p.batch)
-            prefetch_l2(p.q + row * p.q_token + (thread - lines) % q_lines * 32 / dim * p.q_head +
-                        (thread - lines) % q_lines * 32 % dim);
-        if (threadIdx.x == 0 && blockIdx.x * 32 < p.batch)
-            prefetch_l2(p.lengths + blockIdx.x * 32);
-    }
-    grid_dependency_wait();
-    grid_dependency_launch();  // the join relies on what came before
-
-    // this warp's piece; consecutive ones are on different SMs
-    const int ctas = p.pieces / kWarps;
-    const int piece = warp * ctas + blockIdx.x;
+    uint64_t* const full = shared.full[warp];
     int begin, end;
     Place r;
     if (!find_piece(p, piece, begin, end, r))
-        return;
+        return false;
 
     // A lane has the codes of the key at place g (and 8 more) in the words quad + 4 j,
     // and for the values those of the keys at 2 quad and 2 quad + 1 (and 8 more),
@@ -503,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
     // page (or the tile) a box.  A tile's keys are loaded when those of the tile before
     // have been read, and its values, from the place that `at_v` keeps, likewise.
     Place next = r;
-    int pages = 0, page_tile = 0, loads_k = 0, loads_v = 0, ahead = begin;  // ahead: the next place of the line
+    int pages = 0, page_tile = 0, loads_k = i, loads_v = i, ahead = begin;  // ahead: the next place of the line
     const int blocks_shift = p.page_shift - 4;
     const int box_shift = min(p.page_shift, kTileShift);
     const int split = kTileShift - box_shift;       // a tile is on 1 << split pages
@@ -523,7 +522,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
         const int head = at.unit / p.row_blocks, first_head = at.unit % p.row_blocks * (NT * 4);
         const int heads = min(NT * 4, p.group - first_head), lines = (dim + 31) / 32;
         for (int l = lane; l < heads * lines; l += 32)
-            prefetch_l1(p.q + at.b * p.q_token + (head * p.group + first_head + l / lines) * p.q_head + l % lines * 32);
+            prefetch_l1(p.q + at.b * p.q_token + (head * p.group + first_head + l / lines) * p.q_head +
+                        l % lines * 32);
         const float* const angles = c.rope.rot > 0 ? angles_of(c.rope, at.own - 1) : nullptr;
         if (angles && lane * 32 < c.rope.rot)
             prefetch_l1(angles + lane * 32);
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
                 tma_load_3d(stages + is_v * C::kPlane + lane * (C::kPlane / kBlocks), is_v ? &map_v : &map_k,
                             &full[is_v], 0, at_v.slot, at_v.there ? at_v.unit : p.pages * p.kv_heads);
             const int64_t scale = (static_cast<int64_t>(at_v.unit) << blocks_shift) + (at_v.slot >> 4) + my_block;
-            copy4_async(smem_u32(&scale_of[warp][is_v][lane]), (is_v ? c.v_scale : c.k_scale) + scale, at_v.there,
+            copy4_async(smem_u32(&shared.scale[warp][is_v][lane]), (is_v ? c.v_scale : c.k_scale) + scale, at_v.there,
                         &full[is_v]);
         }
     };
@@ -576,8 +576,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
     using Rows = typename Math::T;
     constexpr int kSets = Math::kSets;
     Rows rows[kSets];
-    bool ok = true;
-    int i = 0, fragment = 0;
+    bool ok = true, lost = false;
+    int fragment = 0;
     for (int at = begin; ok && at < end; ++fragment) {
         const int n = min(r.tiles - r.tile, end - at);
         const int head = r.unit / p.row_blocks, first_head = r.unit % p.row_blocks * (NT * 4);
@@ -629,12 +629,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
         }
         const int part = 2 * piece + (fragment > 0 ? 1 : 0);
         const int o_dim = g * kDims;
-        // where the sums of the runs before stand, and far_of has what belongs to them
-        float* const slot = p.part_o + static_cast<int64_t>(part) * (NT * 4) * dim + o_dim;
+        // where the sums of the runs before stand, and shared.far has what belongs to them
+        float* const slot =
+            p.part_o + static_cast<int64_t>(SMALL ? 2 * p.pieces + piece : part) * (NT * 4) * dim + o_dim;
         auto row_of = [&](int set, int h) { return set * Math::kSetHeads + Rows::out_head(quad, h); };
         auto ready = [&](int is_v) {
             ok = __all_sync(0xffffffffu, mbar_try_wait(&full[is_v], i & 1)) ||
-                 attn_warp_wait(&full[is_v], i & 1, &abort_flag[warp], kFaultDecode8);
+                 attn_warp_wait(&full[is_v], i & 1, &shared.abort_flag[warp], kFaultDecode8);
             return ok;
         };
         for (int t0 = 0; ok && t0 < n; t0 += kRun) {
@@ -671,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
                                 rows[set].score(j * 4 + w, a);
                         }
                     }
-                    const float ks = scale_of[warp][0][b];
+                    const float ks = shared.scale[warp][0][b];
 #pragma unroll
                     for (int set = 0; set < kSets; ++set)
                         rows[set].end_scores(b, fabsf(ks) * c2);
@@ -718,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         lds(v_stage + v_at[k & 1] + (b * 16 + (k >> 1) * 8) * DP, v[k]);
-                    const float vs = scale_of[warp][1][b];
+                    const float vs = shared.scale[warp][1][b], value_scale = SMALL ? fabsf(vs) * kDown : fabsf(vs);
 #pragma unroll
                     for (int d = 0; d < DP / 16; ++d) {
                         // dimensions 2 d and 2 d + 1 of two keys: bytes a0 a1 b0 b1
@@ -727,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
                         const uint32_t a[4] = {even_codes(p01), odd_codes(p01), even_codes(p23), odd_codes(p23)};
 #pragma unroll
                         for (int set = 0; set < kSets; ++set)
-                            rows[set].value(b, d, a, fabsf(vs));
+                            rows[set].value(b, d, a, value_scale);
                     }
                     if (has_odd(vs)) {
                         // the components in which a key that counts is not a number: a bit for
@@ -766,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
             for (int set = 0; set < kSets; ++set)
 #pragma unroll
                 for (int h = 0; h < Rows::kHeads; ++h) {
-                    float2& far = far_of[warp][set * Rows::kHeads + h][lane];
+                    float2& far = shared.far[warp][set * Rows::kHeads + h][lane];
                     float* const sums = slot + row_of(set, h) * dim;
                     if (t0 > 0) {  // added to those of the runs before
                         const float2 now = rows[set].sums(h);
@@ -809,12 +810,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
                 float* const dst = (whole ? p.out + at_row * dim
                                           : p.part_o + (static_cast<int64_t>(part) * (NT * 4) + row) * dim) +
                                    o_dim;
-                const float norm = sum == 0.0f ? 0.0f : 1.0f / sum;
+                const float norm = sum == 0.0f ? 0.0f : (SMALL ? 1.0f / kDown : 1.0f) / sum;
+                float top = 0.0f;
                 if (o_dim < dim)
 #pragma unroll
                     for (int j = 0; j < kDims / 4; ++j) {
                         const float4 z = rows[set].four(j, h);
-                        const float y[4] = {z.x * norm, z.y * norm, z.z * norm, z.w * norm};
+                        float y[4] = {z.x * norm, z.y * norm, z.z * norm, z.w * norm};
+                        if constexpr (SMALL) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (is_number(dst[4 * j + e]))
+                                    y[e] = dst[4 * j + e];
+                        } else {
+                            top = largest(largest(top, y[0], y[1]), y[2], y[3]);
+                        }
                         if (p.vec_out || !whole) {
                             *reinterpret_cast<float4*>(dst + 4 * j) = make_float4(y[0], y[1], y[2], y[3]);
                         } else {
@@ -823,7 +833,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
                                 dst[4 * j + e] = y[e];
                         }
                     }
-                if (g == 0) {
+                lost = lost || (!is_number(top) && is_number(sum));
+                if (!SMALL && g == 0) {
                     const float lse =
                         sum == 0.0f ? -INFINITY : fmaf(last.x, kAttnLn2, logf(sum * (1.0f / kAttnPScale)));
                     if (!whole)
@@ -842,6 +853,53 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
         if (loads_v > 0)
             attn_drain_wait(&full[1], (loads_v - 1) & 1);
     }
+    return ok && __any_sync(0xffffffffu, lost);
+}
+
+template <int DP, int NT>
+__global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtas)
+    attn_decode8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                        const __grid_constant__ Params p, const __grid_constant__ Cache8 c)
+{
+    using C = Cfg<DP, NT>;
+    const int dim = p.dim;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Shared<DP, NT> shared;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    uint8_t* const stages =
+        reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023)) +
+        warp * (2 * C::kPlane);
+    if (lane == 0) {
+        for (int i = 0; i < 2; ++i)
+            mbar_init(&shared.full[warp][i], 1 + C::kBlocks);  // the TMA's bytes and the scales
+        shared.abort_flag[warp] = 0;
+        fence_mbar_init();
+    }
+    __syncwarp();
+    // What the first steps read one after the other comes into L2 meanwhile, a line a
+    // thread: lengths, page tables, queries.
+    {
+        const int64_t thread = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+        const int64_t lines = (static_cast<int64_t>(p.batch) * p.width + 31) / 32;
+        const int64_t q_lines = (static_cast<int64_t>(p.heads) * dim + 31) / 32, row = (thread - lines) / q_lines;
+        if (thread < lines)
+            prefetch_l2(p.table + thread * 32);
+        else if (row < p.batch)
+            prefetch_l2(p.q + row * p.q_token + (thread - lines) % q_lines * 32 / dim * p.q_head +
+                        (thread - lines) % q_lines * 32 % dim);
+        if (threadIdx.x == 0 && blockIdx.x * 32 < p.batch)
+            prefetch_l2(p.lengths + blockIdx.x * 32);
+    }
+    grid_dependency_wait();
+    grid_dependency_launch();  // the join relies on what came before
+
+    // this warp's piece; consecutive ones are on different SMs
+    const int ctas = p.pieces / kWarps;
+    const int piece = warp * ctas + blockIdx.x;
+
+    int i = 0;
+    if (go_over<DP, NT, false>(map_k, map_v, p, c, shared, stages, piece, i))
+        go_over<DP, NT, true>(map_k, map_v, p, c, shared, stages, piece, i);
 }
 
 // A cache's codes: rows are the tokens of one head on one page.
@@ -911,10 +969,11 @@ int tile_shift_for(int head_dim, int nt)
     return head_dim <= 64 ? tile_shift_of_columns<64>(nt) : tile_shift_of_columns<128>(nt);
 }
 
-// Floats of the workspace: parts of rows, and their lse.
+// Floats of the workspace: for each piece two parts of rows and the sums of a second pass,
+// and their lse.
 int64_t slots_of(int nt)
 {
-    return 2 * static_cast<int64_t>(ctas_an_sm(nt)) * kMostSms * kWarps * 4 * nt;
+    return 3 * static_cast<int64_t>(ctas_an_sm(nt)) * kMostSms * kWarps * 4 * nt;
 }
 
 }  // namespace

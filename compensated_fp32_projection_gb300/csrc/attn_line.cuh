@@ -4,7 +4,9 @@
 //   kTileShift log2 of the keys of a tile, or 0 where Params says;
 //   kLeastKeys keys of a piece at least, about;
 //   kRowCost   tiles that the beginning of a row costs as much time as;
-//   kJoinEarly whether the join lets the next kernel start before it has begun.
+//   kJoinEarly whether the join lets the next kernel start before it has begun;
+//   kJoinWeight the largest weight in the join's sums, a power of two: 1, or less where the
+//              sums of some parts' values may leave binary32 and their mean does not.
 #pragma once
 
 #include "attn.h"
@@ -239,12 +241,13 @@ __global__ void __launch_bounds__(256, 4) attn_join_kernel(Params p, Join x)
         t = fmaxf(top, t);
         const float shift = t == -INFINITY ? 0.0f : t, a = expf(top - shift);
         top = t;
-        const float w = expf(y - shift);  // a part that sees nothing weighs nothing; NaN stays NaN
+        float w = expf(y - shift);  // a part that sees nothing weighs nothing; NaN stays NaN
         float s = w;
 #pragma unroll
         for (int o = 16; o; o >>= 1)
             s += __shfl_xor_sync(0xffffffffu, s, o);
         sum = fmaf(sum, a, s);
+        w *= kJoinWeight;
         float run[4] = {};  // of these 32: see kRun
         // the caller's out, the last part of a whole row, may lie at any address
         const bool from_out = whole && i0 + 32 >= parts;
@@ -279,7 +282,7 @@ __global__ void __launch_bounds__(256, 4) attn_join_kernel(Params p, Join x)
         for (int e = 0; e < 4; ++e)
             acc[e] = fmaf(acc[e], a, run[e]);
     }
-    const float norm = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const float norm = sum == 0.0f ? 0.0f : 1.0f / kJoinWeight / sum;
     if (lane * 4 < p.dim) {
         float* const dst = p.out + row * p.dim + lane * 4;
         if (p.vec_out) {

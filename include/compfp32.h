@@ -614,11 +614,15 @@ comp_status_t comp_kv8_read_f16(const comp_kv8_cache_t* cache, uint16_t* k, uint
 /*
  * comp_attn_decode_f32x8 — comp_attn_decode_f32x16 over an 8-bit cache, without a
  * shared prefix; rope (or NULL) rotates each query at its sequence's last position,
- * lengths[b] - 1 (a row whose position the table does not have gets NaN).  The codes
- * enter the products exactly and a block's scale is applied in binary32 to what its
- * keys gave, so keys and values may have any magnitude as long as the scores stay
- * finite.  Same limits on sizes, but that (width * page_size / 16 + 4) * batch *
- * kv_heads * ceil(group / 16) is below 2^31.
+ * lengths[b] - 1 with the length clamped (a row whose position the table does not have
+ * gets NaN).  The codes enter the products exactly and a block's scale is applied in
+ * binary32 to what its keys gave, so keys and values may have any magnitude as long as
+ * the scores, and `scale` times a block's scale, stay finite; rotated queries stay below
+ * 65520 in magnitude.  A key's weight enters with an error of up to 2^-22 of it or 2^-39
+ * of the largest weight, whichever is more: out is off by up to 2^-39 sum_j |v_j|
+ * where it consists of such small weights times far larger values, and by up to
+ * 2^-126 in any case.  Same limits on sizes, but that (width * page_size / 16 + 4) *
+ * batch * kv_heads * ceil(group / 16) is below 2^31.
  */
 int64_t comp_attn_decode_f32x8_workspace_bytes(const comp_kv8_cache_t* cache, int64_t batch, int32_t heads,
                                                int64_t width);

@@ -1,0 +1,161 @@
+"""The 8-bit cache over its ranges: values up to the largest numbers, every plan of the decode kernel with
+rotated queries, sequence starts that do not ascend."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+import kv8_check as plain  # noqa: E402
+from test_gpu_kv8 import check, ints, pkg, plain_of, pool, rows_of  # noqa: E402,F401
+
+# Query heads on a key head: up to four, up to eight, up to sixteen, and more.
+GROUPS = [(4, 1), (6, 2), (5, 1), (8, 1), (14, 2), (16, 1), (40, 2)]
+
+
+def largest(cache):
+    return max(float((c.abs().amax((2, 3)).float()[..., None] * s.abs()).max()) for c, s in
+               ((cache[0], cache[2]), (cache[1], cache[3])))
+
+
+@pytest.mark.parametrize("heads,kv_heads", GROUPS)
+@pytest.mark.parametrize("page,dim", [(16, 128), (64, 64), (32, 48)])
+def test_decode_large_values(pkg, heads, kv_heads, page, dim):  # noqa: F811
+    """Values up to the largest numbers: sums of many of them leave 32 bits, means do not."""
+    lens = [1, 16, 0, 17, 300, 2500]
+    pages = sum(-(-n // page) for n in lens)
+    table = ints(rows_of(lens, page, pages, seed=3))
+    q = torch.randn(len(lens), heads, dim, generator=torch.Generator().manual_seed(dim)).cuda()
+    for size in (2.0 ** 75, 2.0 ** 82, 2.0 ** 110, 2.0 ** 127):
+        cache = pool(pages, kv_heads, page, dim, seed=heads)
+        cache[3].mul_(size / (128 * cache[3].max()))
+        out, _ = check(pkg, q, cache, table, ints(lens))
+        assert out.isfinite().all()
+        # one key: its value; its weight is off by 2^-22 as it enters, and four operations round
+        value = plain_of(cache)[1].values(torch.float64)[int(table[0, 0]), :, 0].cuda().repeat_interleave(
+            heads // kv_heads, 0)
+        assert ((out[0].double() - value).abs() <= 2.0 ** -21 * value.abs()).all()
+
+
+@pytest.mark.parametrize("heads,kv_heads", GROUPS)
+def test_decode_equal_largest_values(pkg, heads, kv_heads):  # noqa: F811
+    """The worst of it: the largest number a code and a scale make, for every key and with either sign."""
+    dim, n = 64, 6000
+    cache = pool(-(-n // 64), kv_heads, 64, dim)
+    cache[1].fill_(127)
+    cache[3].fill_(2.0 ** 121 * (1 - 2.0 ** -7))
+    cache[1][..., 1::2].neg_()
+    lens = ints([n])
+    table = ints([list(range(len(cache[0])))])
+    q = torch.randn(1, heads, dim, generator=torch.Generator().manual_seed(0)).cuda()
+    out, _ = check(pkg, q, cache, table, lens)
+    assert out.isfinite().all() and (out[..., ::2] > 0).all() and (out[..., 1::2] < 0).all()
+    # signs that alternate over the keys
+    cache[1][:, :, ::2].neg_()
+    out, _ = check(pkg, q, cache, table, lens)
+    assert out.isfinite().all()
+
+
+@pytest.mark.parametrize("heads,kv_heads", GROUPS)
+@pytest.mark.parametrize("dim", [64, 128])
+def test_decode_large_beside_small_values(pkg, heads, kv_heads, dim):  # noqa: F811
+    """Blocks of all sizes from 1e-20 to 1e36, in one sequence and one after the other."""
+    page, lens = 32, [1500, 90, 33, 700]
+    pages = sum(-(-n // page) for n in lens)
+    table = ints(rows_of(lens, page, pages, seed=5))
+    q = torch.randn(4, heads, dim, generator=torch.Generator().manual_seed(dim)).cuda()
+    for seed in range(3):
+        cache = pool(pages, kv_heads, page, dim, seed=seed)
+        g = torch.Generator().manual_seed(seed)
+        power = torch.randint(-20, 36, cache[3].shape, generator=g).double()
+        if seed == 2:                        # every other sequence's values are small
+            power.fill_(-20)
+            for row in (0, 2):
+                at = [p for p in table[row].tolist() if p >= 0]
+                power[at] = torch.randint(20, 36, power[at].shape, generator=g).double()
+        cache[3].copy_((cache[3].double().cpu() * 10 ** power).float())
+        cache[3][0, :, 0] = 0.0
+        check(pkg, q, cache, table, ints(lens), scale=0.02)
+    # a dimension in which the large blocks have a code of 0 keeps its small values
+    cache = pool(pages, kv_heads, page, dim)
+    cache[3][::2] *= 1e30
+    cache[3][1::2] *= 1e-20
+    cache[1][::2, ..., 3] = 0
+    out, _ = check(pkg, q, cache, table, ints(lens))
+    assert (out[0, :, 3] != 0).all()
+
+
+@pytest.mark.parametrize("seqs,n,heads,kv_heads,dim", [(5, 70001, 16, 8, 64), (8, 70001, 32, 4, 128),
+                                                       (8, 70001, 36, 4, 128), (5, 70001, 8, 8, 128),
+                                                       (10, 70001, 32, 4, 64)])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** 80, 2.0 ** 121])
+def test_decode_long_at_any_size(pkg, seqs, n, heads, kv_heads, dim, size):  # noqa: F811
+    """Pieces of several runs of sums, against 64-bit sums; at 2^80 one block in seventy has a scale beyond 2^76."""
+    page = 128
+    lens = [n - 997 * i for i in range(seqs)]
+    need = [-(-m // page) for m in lens]
+    cache = pool(sum(need), kv_heads, page, dim, seed=1)
+    cache[3].mul_(size)
+    assert largest(cache) < 3.4e38
+    table = ints(rows_of(lens, page, sum(need), seed=4))
+    q = torch.randn(seqs, heads, dim, generator=torch.Generator().manual_seed(0)).cuda()
+    lse = torch.empty(seqs, heads, device="cuda")
+    out = pkg.comp_attn_decode_f32x8(q, *cache, table, ints(lens), lse=lse)
+    assert out.isfinite().all()
+    group = heads // kv_heads
+    for b, h in ((0, 0), (seqs // 2, group), (seqs - 1, heads - 1)):
+        at = table[b, :need[b]].long()
+        k, v = ((c[at, h // group].double() * s[at, h // group].double().repeat_interleave(16, 1)[..., None])
+                .flatten(0, 1)[:lens[b]] for c, s in ((cache[0], cache[2]), (cache[1], cache[3])))
+        plain.check_rows(out[b, h][None].cpu(), lse[b, h][None].cpu(), q[b, h][None].cpu(), k.cpu(), v.cpu(),
+                         dim ** -0.5)
+
+
+@pytest.mark.parametrize("heads,kv_heads", GROUPS)
+@pytest.mark.parametrize("dim", [64, 112])
+def test_decode_large_values_beside_nan(pkg, heads, kv_heads, dim):  # noqa: F811
+    """A code that is not a number costs its own dimension, whatever the others' size; outputs at any address."""
+    page, lens = 16, [1500, 40, 1100]
+    pages = sum(-(-n // page) for n in lens)
+    table = ints(rows_of(lens, page, pages, seed=5))
+    q = torch.randn(3, heads, dim, generator=torch.Generator().manual_seed(dim)).cuda()
+    cache = pool(pages, kv_heads, page, dim)
+    cache[3].mul_(1e36)
+    at = int(table[0, 70])
+    cache[1][at, :, 3, 7] = -128
+    cache[3][at, :, 0].neg_()
+    clean = [t.clone() for t in cache]
+    clean[1][at, :, 3, 7] = 0
+    flat = torch.full((3 * heads * dim + 2,), 5.0, device="cuda")
+    out = pkg.comp_attn_decode_f32x8(q, *cache, table, ints(lens), out=flat[1:-1].view(3, heads, dim))
+    want, _ = check(pkg, q, clean, table, ints(lens))
+    rest = [d for d in range(dim) if d != 7]
+    assert torch.equal(out[..., rest], want[..., rest]) and torch.equal(out[1:], want[1:])
+    assert out[0, :, 7].isnan().all() and out[0][:, rest].isfinite().all() and flat[0] == 5 and flat[-1] == 5
+
+
+def test_decode_large_values_in_a_graph(pkg):  # noqa: F811
+    """Large and ordinary values in turn, the same workspace, of exactly its size."""
+    import ctypes
+
+    from compensated_fp32_projection_gb300 import _native
+
+    lens = [2000, 3, 777]
+    cache = pool(200, 2, 16, 64)
+    table = ints(rows_of(lens, 16, 200, seed=3))
+    q = torch.randn(3, 16, 64, generator=torch.Generator().manual_seed(0)).cuda()
+    out = torch.zeros(3, 16, 64, device="cuda")
+    c = _native.Kv8Cache(*(t.data_ptr() for t in cache), 200, 16, 2, 64)
+    size = _native.load().comp_attn_decode_f32x8_workspace_bytes(ctypes.byref(c), 3, 16, table.shape[1])
+    workspace = torch.full((size + 64,), 255, dtype=torch.uint8, device="cuda")
+    graph, n = torch.cuda.CUDAGraph(), ints(lens)
+    want = pkg.comp_attn_decode_f32x8(q, *cache, table, n)
+    with torch.cuda.graph(graph):
+        pkg.comp_attn_decode_f32x8(q, *cache, table, n, out=out, workspace=workspace[:size])
+    scales = cache[3].clone()
+    for power in (0, 123, 0, 110, 123):
+        cache[3].copy_(scales * 2.0 ** power)
+        graph.replay()
+        # powers of two change no bits of the sums
+        assert torch.equal(out, want * 2.0 ** power)
+    assert (workspace[size:] == 255).all()
