@@ -159,3 +159,43 @@ def test_decode_large_values_in_a_graph(pkg):  # noqa: F811
         # powers of two change no bits of the sums
         assert torch.equal(out, want * 2.0 ** power)
     assert (workspace[size:] == 255).all()
+
+
+@pytest.mark.parametrize("heads,kv_heads", [(5, 1), (7, 1), (8, 1), (14, 2), (64, 8)])
+@pytest.mark.parametrize("page,dim", [(16, 128), (32, 64), (64, 112), (128, 80), (16, 16)])
+def test_decode_five_to_eight_heads(pkg, heads, kv_heads, page, dim):  # noqa: F811
+    lens = [1, 0, 15, 16, 17, 33, 130, 77, 1200]
+    pages = sum(-(-n // page) for n in lens)
+    cache = pool(pages, kv_heads, page, dim, seed=heads)
+    table = ints(rows_of(lens, page, pages, seed=3))
+    q = torch.randn(len(lens), heads, dim, generator=torch.Generator().manual_seed(dim)).cuda()
+    check(pkg, q, cache, table, ints(lens))
+    wide = torch.randn(len(lens), heads + 1, dim + 3, generator=torch.Generator().manual_seed(1)).cuda()
+    check(pkg, wide[:, 1:, 2:-1], cache, table, ints(lens), scale=0.3)
+
+
+@pytest.mark.parametrize("heads,kv_heads", GROUPS)
+@pytest.mark.parametrize("dim,rot,interleaved", [(128, 128, False), (128, 128, True), (64, 64, False), (64, 64, True),
+                                                 (128, 64, False), (128, 20, True), (96, 96, False), (80, 20, False),
+                                                 (48, 48, True), (112, 4, False)])
+def test_decode_rotates_queries_of_any_group(pkg, heads, kv_heads, dim, rot, interleaved):  # noqa: F811
+    """Queries and angles at any address, against a rotation and sums of their own."""
+    lens = [1, 40, 0, 133, 600]
+    cache = pool(60, kv_heads, 16, dim)
+    table = ints(rows_of(lens, 16, 60, seed=3))
+    angles = pkg.comp_rope_table(640, rot, magnitude=0.9)
+    q = torch.randn(5, heads, dim, generator=torch.Generator().manual_seed(dim)).cuda()
+    check(pkg, q, cache, table, ints(lens), angles, interleaved)
+    off = torch.empty(angles.numel() + 2, device="cuda")[2:].view(angles.shape).copy_(angles)  # on 8 bytes, not on 16
+    check(pkg, q, cache, table, ints(lens), off, interleaved)
+    wide = torch.randn(5, heads, dim + 3, generator=torch.Generator().manual_seed(1)).cuda()[..., 1:-2]
+    check(pkg, wide, cache, table, ints(lens), angles, interleaved)
+    # a length beyond the pages' table ends where that does, and so does the position
+    limit = table.shape[1] * 16
+    call = lambda n: pkg.comp_attn_decode_f32x8(q, *cache, table, ints(lens[:4] + [n]), rope=angles,  # noqa: E731
+                                                interleaved=interleaved)
+    assert torch.equal(call(10000), call(limit)) and call(limit).isfinite().all()
+    # a position that the table does not have
+    out = pkg.comp_attn_decode_f32x8(q, *cache, table, ints(lens), rope=angles[:599].contiguous(),
+                                     interleaved=interleaved)
+    assert out[4].isnan().all() and not out[:4].isnan().any()
