@@ -199,3 +199,28 @@ def test_decode_rotates_queries_of_any_group(pkg, heads, kv_heads, dim, rot, int
     out = pkg.comp_attn_decode_f32x8(q, *cache, table, ints(lens), rope=angles[:599].contiguous(),
                                      interleaved=interleaved)
     assert out[4].isnan().all() and not out[:4].isnan().any()
+
+
+def test_bad_sequence_starts_write_nothing_else(pkg):  # noqa: F811
+    """cu that does not ascend, or leaves the tokens: what stands around the cache and the outputs stays."""
+    around = [torch.full((8, 1, 16, 32), 77, dtype=torch.int8, device="cuda") for _ in range(2)]
+    around += [torch.full((8, 1, 1), 5.0, device="cuda") for _ in range(2)]
+    cache = [t[1:-1] for t in around]
+    x = torch.randn(20, 1, 32, generator=torch.Generator().manual_seed(0)).cuda()
+    table, start = ints([[0, 1], [2, 3], [4, 5]]), ints([0, 0, 0])
+    for cu in ([0, 50, 7, 20], [5, 3, 2, 1], [-7, 3, 30, 90], [20, 20, 20, 20], [0, -2 ** 31, 2 ** 31 - 1, 4]):
+        pkg.comp_kv8_append_f32(x, x, *cache, table, start, ints(cu))
+        out = torch.full((2, 24, 1, 32), 9.0, device="cuda")
+        pkg.comp_kv8_read_f32(*cache, table, start, ints(cu), 20, k=out[0, 2:22], v=out[1, 2:22])
+        for t, was in zip(around, (77, 77, 5.0, 5.0)):
+            assert (t[0] == was).all() and (t[-1] == was).all()
+        assert (out[:, :2] == 9).all() and (out[:, 22:] == 9).all() and out.isfinite().all()
+    # ascending, but not from 0: the tokens before belong to no sequence, and those behind read zeros
+    out = torch.full((2, 20, 1, 32), 9.0, device="cuda")
+    pkg.comp_kv8_append_f32(x, x, *cache, table, start, ints([3, 3, 9, 17]))
+    pkg.comp_kv8_read_f32(*cache, table, start, ints([3, 3, 9, 17]), 20, k=out[0], v=out[1])
+    k, v = plain_of(cache)
+    want = plain.read(k.values(), table.tolist(), [0, 0, 0], [3, 3, 9, 17], 20)
+    assert torch.equal(out[0, 3:].cpu(), want[3:]) and torch.equal(out[1, 3:], out[0, 3:])
+    # half a step of the largest possible scale, and 2^-21 of 127 steps for the operations
+    assert float((out[0, 3:17] - x[3:17]).abs().max()) <= float(x.abs().max()) / 127 * (0.5 + 127 * 2.0 ** -21)
