@@ -143,8 +143,10 @@ def comp_rope_f32(x, table, positions=None, *, interleaved=False, inverse=False,
     """Rotate x [tokens, heads, head_dim] float32 (any token and head strides): the
     pairs (i, i + rot / 2) of each head's first rot dimensions, or (2 i, 2 i + 1)
     with interleaved; the other dimensions stay.  Token t is at positions[t] (int32;
-    without them at t); one that the table does not have gives NaN.  inverse turns
-    back, which is also the call's gradient.  out may be x itself."""
+    without them at t); one that the table does not have gives NaN.  out may be x
+    itself.  inverse turns back, and turns a gradient of the result into one of x.
+    As with the other calls, autograd does not see it: the result does not require a
+    gradient, and a training step makes the inverse call itself."""
     return _b.rope(x, table, positions, interleaved, inverse, out, stream)
 
 
@@ -177,8 +179,10 @@ def comp_kv8_read_f16(k_pages, v_pages, k_scales, v_scales, table, start, cu, to
 def comp_attn_decode_f32x8(q, k_pages, v_pages, k_scales, v_scales, table, lengths, *, rope=None, interleaved=False,
                            scale=None, out=None, lse=None, workspace=None, stream=None):
     """comp_attn_decode_f32x16 over an 8-bit cache (no shared prefix).  rope, a
-    rotary table, rotates each query at its sequence's last position, lengths[b] - 1
-    (NaN if the table does not have it)."""
+    rotary table, rotates each query at its sequence's last position, lengths[b] - 1,
+    the length clamped to the pages that the table lists (NaN if the rotary table does
+    not have it).  Values may be of any size; keys too, as long as the scores stay
+    finite.  Rotated queries stay below 65520."""
     return _b.decode8(q, k_pages, v_pages, k_scales, v_scales, table, lengths, rope, interleaved, scale, out, lse,
                       workspace, stream)
 

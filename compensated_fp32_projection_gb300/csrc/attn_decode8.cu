@@ -17,17 +17,18 @@
 // The weights go from one layout to the other by a transposition of 8 x 8 FP16
 // values (movmatrix).  Where up to four heads share a key head, hi and lo of each
 // stand side by side (Four): half the products, weights and sums of rows of eight
-// heads, 48 sequences of 129 to 6001 tokens take 44 us instead of 51.  Otherwise the
+// heads, 48 sequences of 129 to 6001 tokens take 41 us instead of 45.  Otherwise the
 // columns are eight heads, hi in one product and lo in another, and a lane has two
 // heads side by side for packed arithmetic (Eight): 16 sequences of 20001 to 65536
-// tokens with 16 heads a key head take 175 us, as two Fours for each eight 199.
+// tokens with 16 heads a key head take 173 us, as two Fours for each eight 203.
 //
 // Large values.  The sums hold 2^14 p times the values, and leave binary32 with one
 // value of 2^114, or 2^16 of 2^98, where their mean is an ordinary number.  A warp whose
 // results are not all numbers goes through its keys once more with values of kDown
 // times their size, and replaces those that were not.  The second pass is a copy of the
 // first in the code, so that the first is what it would be alone: a flag in one copy, or a
-// look at each tile's scales before its products, took 1 to 3 % of every call.
+// look at each tile's scales before its products, took 1 to 3 % of every call.  The 48
+// sequences take 78 us where all of them go through it.
 //
 // Layout.  The sum over the head dimension may go in any order, and so may the
 // rows of the output and the keys of a block: a lane's operands are 16 codes that
@@ -48,14 +49,16 @@
 namespace compfp32 {
 namespace {
 constexpr int kTileShift = 0;       // a tile's size goes by the heads: see Cfg
-constexpr int kLeastKeys = 32;      // a sequence of 777 alone takes 12.3 us, with 64 12.7, with 128 13.4
+constexpr int kLeastKeys = 32;      // a sequence of 777 alone takes 12.3 us, with 64 12.8, with 128 13.2
 // A row's beginning (its queries, rotated and split, and its end) takes the time of
-// some tiles: 96 sequences of 33 to 2500 tokens of 16 heads of 64 take 30 us, 45 if
-// rows count by their keys alone (31 with 3, 33 with 4).
+// some tiles: 96 sequences of 33 to 2500 tokens of 16 heads of 64 take 30 us, 43 if
+// rows count by their keys alone (31 with 3, 33 with 4); 16 of 20001 to 65536 with 16
+// heads a key head 173, 181 and (170, 173).
 constexpr int kRowCost = 2;
 // With the next call's kernel on the SMs before the join has begun, its CTAs are
-// spread unevenly: 16 sequences of 20001 to 65536 tokens, eight heads a key head, took
-// 172 us a call in a long row of calls where they take 136.
+// spread unevenly: 16 sequences of 20001 to 65536 tokens, four heads a key head, take
+// 149 us a call in a row of calls where they take 111 (eight heads 125 and 120; the 48
+// ragged sequences 40.8 and 41.2).
 constexpr bool kJoinEarly = false;
 constexpr float kJoinWeight = 0x1p-12f;  // a row has fewer than 2^12 parts
 }
@@ -82,12 +85,12 @@ constexpr float kDown = 0x1p-48f;
 // A tile is some blocks of 16 keys.  What a tile costs whatever its size (waits, loads,
 // the maximum) is some 190 instructions, a block's products and conversions are 300 to
 // 400, so larger tiles are faster until the SM waits for their loads: with four heads of
-// 128 tiles of 32 keys take 41 us where 64 take 44 (48 ragged sequences), with eight 31
-// and 34; with one head of 64, 129 where 64 take 108, with 16 of 128, 179 where 64
-// take 175 (16 long ones).
+// 128 tiles of 32 keys take 41 us where 64 take 45 (48 ragged sequences), with eight 31
+// and 34; with two heads of 64, 129 where 64 take 111, with 16 of 128, 181 where 64
+// take 173 (16 long ones).
 // One stage each for keys and values is enough, each filled again as soon as it has been
-// read, as the other is: two stages take 42 us (ragged) and 133 where one takes 124
-// (eight heads, long).
+// read, as the other is: an earlier form took 42 us with two stages where it took 41 with
+// one (ragged), and 133 where 124 (eight heads, long).
 template <int DP, int NT>
 struct Cfg {
     static constexpr int kWords = DP / 64;                  // 16-byte words of a key that a lane has

@@ -159,7 +159,7 @@ def serve8(lens=(200, 57), samples=3, steps=5, turns=(33, 70), seed=0, device="c
         at = torch.cat([torch.arange(a, a + n) for a, n in zip(starts, lens)]).int().to(device)
         return torch.randn(sum(lens), HIDDEN, generator=g).to(device), cu, at
 
-    def rotated(y, at):  # queries and keys stand side by side: one call
+    def rotated(y, at):
         return cf.comp_rope_f32(y, angles, at)
 
     x, cu, at = packed(lens, [0] * len(lens))
